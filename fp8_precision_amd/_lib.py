@@ -50,6 +50,9 @@ _SIGS = {
     "fp8_mx_swiglu_requant": (_i32, [_vp, _i64, _i64, _vp, _vp, _vp]),
     "fp8_mx_quantize_t": (_i32, [_vp, _i64, _i64, _i32, _vp, _vp, _vp]),
     "fp8_mx_quantize_both": (_i32, [_vp, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp]),
+    "fp8_norm_forward": (_i32, [_vp, _i32, _vp, _vp, _vp, ctypes.c_float, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "fp8_norm_backward_workspace": (_i32, [_i64, _i64, _vp]),
+    "fp8_norm_backward": (_i32, [_vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -594,6 +597,116 @@ def mx_gemm_backward(dyq, sdy, dyqt, sdyt, wqt, swt, xqt, sxt, dy_fmt: int = E5M
     _run("fp8_mx_gemm_backward", _lib.fp8_mx_gemm_backward, ts + (dx, dw), _ptr(dyq), _ptr(sdy), _ptr(dyqt),
          _ptr(sdyt), int(dy_fmt), _ptr(wqt), _ptr(swt), _ptr(xqt), _ptr(sxt), _ptr(dx), _ptr(dw), M, N, K)
     return dx, dw
+
+
+def _out(t, name, shape, dtype, device):
+    """An output tensor: the given one, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _dev_tensor(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    return t
+
+
+def _workspace(call, device, *args):
+    """Device memory of the size that the entry point ``call`` names for ``args``
+    on ``device`` (the torch allocator's, so stream-ordered like any tensor)."""
+    size = _i64()
+    with torch.cuda.device(device):
+        _check(call, getattr(_lib, call)(*args, ctypes.byref(size)))
+    return torch.empty(max(16, size.value), dtype=torch.uint8, device=device)
+
+
+_STREAM_TYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _stream_tensor(t, name):
+    _dev_tensor(t, name)
+    if t.dtype not in _STREAM_TYPES:
+        raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [rows, cols]")
+    return t
+
+
+def _like(t, name, other, dtype=None):
+    _dev_tensor(t, name, other.dtype if dtype is None else dtype)
+    if t.shape != other.shape:
+        raise ValueError(f"{name} must have shape {tuple(other.shape)}")
+
+
+def _vector(t, name, n, dtype):
+    _dev_tensor(t, name, dtype)
+    if t.numel() != n:
+        raise ValueError(f"{name} must hold {n} values")
+
+
+def norm(x, weight, bias=None, add=None, eps: float = 1e-5, rms: bool = True, absmax=None, y=None, out_sum=None,
+         mean=None, rstd=None):
+    """Root-mean-square norm (``rms``) or layer norm of the rows of a residual
+    stream x (bf16 or fp32 [rows, cols]), with the previous block's output ``add``
+    (bf16) summed in first: s = x + add, y = norm(s) * weight (+ bias).
+
+    ``absmax`` (fp32 [1], holding +0 or an earlier result) becomes
+    max(absmax, max |y|), the statistic that ``quantize`` of y takes.
+    Returns (y bf16, s in x's type or x itself without ``add``, mean fp32 [rows]
+    or None with ``rms``, rstd fp32 [rows]).
+    """
+    _stream_tensor(x, "x")
+    rows, cols = x.shape
+    _vector(weight, "weight", cols, torch.bfloat16)
+    if bias is not None:
+        _vector(bias, "bias", cols, torch.bfloat16)
+    if add is not None:
+        _like(add, "add", x, torch.bfloat16)
+    elif out_sum is not None:
+        raise ValueError("out_sum is the sum of x and add: give both or neither")
+    if rms and mean is not None:
+        raise ValueError("a root-mean-square norm has no mean")
+    if absmax is not None:
+        _scalar_in(absmax, "absmax")
+    y = _out(y, "y", (rows, cols), torch.bfloat16, x.device)
+    if add is not None:
+        out_sum = _out(out_sum, "out_sum", (rows, cols), x.dtype, x.device)
+    if not rms:
+        mean = _out(mean, "mean", (rows,), torch.float32, x.device)
+    rstd = _out(rstd, "rstd", (rows,), torch.float32, x.device)
+    _run("fp8_norm_forward", _lib.fp8_norm_forward, (x, add, weight, bias, y, out_sum, mean, rstd, absmax),
+         _ptr(x), _STREAM_TYPES[x.dtype], _ptr(add), _ptr(weight), _ptr(bias), eps, 0 if rms else 1, rows, cols, _ptr(y),
+         _ptr(out_sum), _ptr(mean), _ptr(rstd), _ptr(absmax))
+    return y, (x if add is None else out_sum), mean, rstd
+
+
+def norm_backward(dy, s, weight, mean, rstd, dres=None, want_dbias: bool = False, dx=None, dweight=None, dbias=None):
+    """Gradients of ``norm``: dy bf16 [rows, cols], s the forward's sum (bf16 or
+    fp32), mean (None: a root-mean-square norm) and rstd from the forward, ``dres``
+    (s's type) the gradient that reaches s by the residual path.
+
+    Returns (dx in s's type, the gradient of s and so of x and of add, dweight
+    fp32 [cols], dbias fp32 [cols] or None).
+    """
+    _stream_tensor(s, "s")
+    rows, cols = s.shape
+    _like(dy, "dy", s, torch.bfloat16)
+    _vector(weight, "weight", cols, torch.bfloat16)
+    if mean is not None:
+        _vector(mean, "mean", rows, torch.float32)
+    _vector(rstd, "rstd", rows, torch.float32)
+    if dres is not None:
+        _like(dres, "dres", s)
+    want_dbias = want_dbias or dbias is not None
+    if want_dbias and mean is None:
+        raise ValueError("a root-mean-square norm has no bias")
+    dx = _out(dx, "dx", (rows, cols), s.dtype, s.device)
+    dweight = _out(dweight, "dweight", (cols,), torch.float32, s.device)
+    if want_dbias:
+        dbias = _out(dbias, "dbias", (cols,), torch.float32, s.device)
+    ws = _workspace("fp8_norm_backward_workspace", s.device, rows, cols)
+    _run("fp8_norm_backward", _lib.fp8_norm_backward, (dy, s, weight, mean, rstd, dres, dx, dweight, dbias, ws),
+         _ptr(dy), _ptr(s), _STREAM_TYPES[s.dtype], _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dres),
+         1 if mean is not None else 0, rows, cols, _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(ws), ws.numel())
+    return dx, dweight, dbias
 
 
 def stream_copy(src: torch.Tensor, dst: torch.Tensor) -> torch.Tensor:

@@ -591,6 +591,91 @@ fp8_status fp8_mx_gemm_backward(const uint8_t* dyq, const uint8_t* sdy, const ui
     return FP8_OK;
 }
 
+// ---- the operators around the linears: norm, attention, loss
+
+// No output of out[] may overlap an input of in[] or another output.
+static bool outputs_overlap(const Range* out, int n_out, const Range* in, int n_in)
+{
+    for (int a = 0; a < n_out; ++a) {
+        for (int b = a + 1; b < n_out; ++b)
+            if (overlap(out[a].p, out[a].n, out[b].p, out[b].n)) return true;
+        for (int b = 0; b < n_in; ++b)
+            if (overlap(out[a].p, out[a].n, in[b].p, in[b].n)) return true;
+    }
+    return false;
+}
+
+static bool norm_shape_ok(int64_t rows, int64_t cols)
+{
+    return rows >= 1 && rows < ((int64_t)1 << 31) && cols >= 1 && cols <= 16384;
+}
+
+fp8_status fp8_norm_forward(const void* x, fp8_stream_type type, const void* add, const void* weight,
+                            const void* bias, float eps, fp8_norm_kind kind, int64_t rows, int64_t cols, void* y,
+                            void* sum, float* mean, float* rstd, float* absmax, hipStream_t stream)
+{
+    t_last_error.clear();
+    if (type != FP8_STREAM_BF16 && type != FP8_STREAM_F32) return fail(FP8_ERR_INVALID, "fp8_norm_forward: bad stream type");
+    if (kind != FP8_NORM_RMS && kind != FP8_NORM_LAYER) return fail(FP8_ERR_INVALID, "fp8_norm_forward: bad norm kind");
+    const bool rms = kind == FP8_NORM_RMS, f32 = type == FP8_STREAM_F32;
+    if (rows < 1 || cols < 1) return fail(FP8_ERR_INVALID, "fp8_norm_forward: rows and cols must be positive");
+    if (!x || !weight || !y || !rstd || (!rms && !mean)) return fail(FP8_ERR_INVALID, "fp8_norm_forward: null pointer");
+    if (rms && (mean || bias)) return fail(FP8_ERR_INVALID, "fp8_norm_forward: a root-mean-square norm has no mean and no bias");
+    if (!add != !sum) return fail(FP8_ERR_INVALID, "fp8_norm_forward: add and sum go together");
+    if (!(eps >= 0.0f)) return fail(FP8_ERR_INVALID, "fp8_norm_forward: eps must be at least 0");
+    if (!norm_shape_ok(rows, cols)) return fail(FP8_ERR_UNSUPPORTED, "fp8_norm_forward: rows < 2^31 and cols <= 16384");
+    const int64_t n = rows * cols, size = f32 ? 4 : 2;
+    const Range in[] = {{x, n * size}, {add, 2 * n}, {weight, 2 * cols}, {bias, 2 * cols}};
+    const Range out[] = {{y, 2 * n}, {sum, n * size}, {mean, 4 * rows}, {rstd, 4 * rows}, {absmax, 4}};
+    if (outputs_overlap(out, 5, in, 4)) return fail(FP8_ERR_INVALID, "fp8_norm_forward: overlapping buffers");
+    if (!aligned(x, 16) || !aligned(add, 16) || !aligned(weight, 16) || !aligned(bias, 16) || !aligned(y, 16) ||
+        !aligned(sum, 16) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(absmax, 4))
+        return fail(FP8_ERR_UNSUPPORTED, "fp8_norm_forward: misaligned pointer");
+    hipError_t e = fp8k::launch_norm_forward(x, f32, add, weight, bias, eps, rms, rows, cols, y, sum, mean, rstd, absmax, stream);
+    if (e != hipSuccess) return fail_hip("fp8_norm_forward", e);
+    return FP8_OK;
+}
+
+fp8_status fp8_norm_backward_workspace(int64_t rows, int64_t cols, int64_t* bytes)
+{
+    t_last_error.clear();
+    if (!bytes) return fail(FP8_ERR_INVALID, "fp8_norm_backward_workspace: null pointer");
+    if (rows < 1 || cols < 1) return fail(FP8_ERR_INVALID, "fp8_norm_backward_workspace: rows and cols must be positive");
+    if (!norm_shape_ok(rows, cols))
+        return fail(FP8_ERR_UNSUPPORTED, "fp8_norm_backward_workspace: rows < 2^31 and cols <= 16384");
+    *bytes = fp8k::norm_backward_workspace(rows, cols);
+    return FP8_OK;
+}
+
+fp8_status fp8_norm_backward(const void* dy, const void* s, fp8_stream_type type, const void* weight,
+                             const float* mean, const float* rstd, const void* dres, fp8_norm_kind kind,
+                             int64_t rows, int64_t cols, void* dx, float* dweight, float* dbias, void* workspace,
+                             int64_t workspace_bytes, hipStream_t stream)
+{
+    t_last_error.clear();
+    if (type != FP8_STREAM_BF16 && type != FP8_STREAM_F32) return fail(FP8_ERR_INVALID, "fp8_norm_backward: bad stream type");
+    if (kind != FP8_NORM_RMS && kind != FP8_NORM_LAYER) return fail(FP8_ERR_INVALID, "fp8_norm_backward: bad norm kind");
+    const bool rms = kind == FP8_NORM_RMS, f32 = type == FP8_STREAM_F32;
+    if (rows < 1 || cols < 1) return fail(FP8_ERR_INVALID, "fp8_norm_backward: rows and cols must be positive");
+    if (!dy || !s || !weight || !rstd || !dx || !dweight || !workspace || (!rms && !mean))
+        return fail(FP8_ERR_INVALID, "fp8_norm_backward: null pointer");
+    if (rms && (mean || dbias)) return fail(FP8_ERR_INVALID, "fp8_norm_backward: a root-mean-square norm has no mean and no bias");
+    if (!norm_shape_ok(rows, cols)) return fail(FP8_ERR_UNSUPPORTED, "fp8_norm_backward: rows < 2^31 and cols <= 16384");
+    if (workspace_bytes < fp8k::norm_backward_workspace(rows, cols))
+        return fail(FP8_ERR_INVALID, "fp8_norm_backward: workspace too small");
+    const int64_t n = rows * cols, size = f32 ? 4 : 2;
+    const Range in[] = {{dy, 2 * n}, {s, n * size}, {weight, 2 * cols}, {mean, 4 * rows}, {rstd, 4 * rows}, {dres, n * size}};
+    const Range out[] = {{dx, n * size}, {dweight, 4 * cols}, {dbias, 4 * cols}, {workspace, workspace_bytes}};
+    if (outputs_overlap(out, 4, in, 6)) return fail(FP8_ERR_INVALID, "fp8_norm_backward: overlapping buffers");
+    if (!aligned(dy, 16) || !aligned(s, 16) || !aligned(weight, 16) || !aligned(dres, 16) || !aligned(dx, 16) ||
+        !aligned(workspace, 16) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dweight, 4) || !aligned(dbias, 4))
+        return fail(FP8_ERR_UNSUPPORTED, "fp8_norm_backward: misaligned pointer");
+    hipError_t e = fp8k::launch_norm_backward(dy, s, f32, weight, mean, rstd, dres, rms, rows, cols, dx, dweight, dbias,
+                                              static_cast<float*>(workspace), stream);
+    if (e != hipSuccess) return fail_hip("fp8_norm_backward", e);
+    return FP8_OK;
+}
+
 fp8_status fp8_stream_copy(const void* src, void* dst, int64_t bytes, hipStream_t stream)
 {
     t_last_error.clear();

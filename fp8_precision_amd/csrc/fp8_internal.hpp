@@ -128,6 +128,16 @@ hipError_t launch_gemm_tn_pair(const uint8_t* A0, int la0, const uint8_t* B0, in
                                int la1, const uint8_t* B1, int lb1, const float* ia1, const float* ib1, void* out1,
                                int64_t P1, int64_t Q1, int64_t R1, int fmt_a, int fmt_b, hipStream_t stream);
 
+// Row norm of a stream (f32 or bf16), with the residual sum in front, and its
+// gradients (norm.hip); partial holds norm_backward_workspace bytes.
+hipError_t launch_norm_forward(const void* x, bool f32, const void* add, const void* weight, const void* bias,
+                               float eps, bool rms, int64_t rows, int64_t cols, void* y, void* sum, float* mean,
+                               float* rstd, float* absmax, hipStream_t stream);
+int64_t norm_backward_workspace(int64_t rows, int64_t cols);
+hipError_t launch_norm_backward(const void* dy, const void* x, bool f32, const void* weight, const float* mean,
+                                const float* rstd, const void* dres, bool rms, int64_t rows, int64_t cols, void* dx,
+                                float* dw, float* db, float* partial, hipStream_t stream);
+
 // dst[0, bytes) = src[0, bytes): the streaming-copy reference (bytes % 16 == 0, both 16-byte aligned).
 hipError_t launch_stream_copy(const void* src, void* dst, int64_t bytes, hipStream_t stream);
 

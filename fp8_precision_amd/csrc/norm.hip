@@ -1,0 +1,440 @@
+// norm.hip -- root-mean-square and layer norm of the rows of a residual stream,
+// forward (with the residual sum in front and the statistic of the output that
+// the FP8 quantisation takes next) and backward (with the gradients of the
+// weight and the bias), for gfx950.
+//
+//   s = x + a                      (a: the previous block's output; or s = x)
+//   m = mean(s) (layer) or 0 (rms),  r = 1 / sqrt(mean((s - m)^2) + eps)
+//   h = (s - m) r,   y = h w + b
+// and backward, with g = dy w per element and means over the row,
+//   dx = r (g - h mean(g h) - mean(g) [layer only]) + ds
+//   dw = sum over rows of dy h,   db = sum over rows of dy
+// ds is the gradient that reaches s by the residual path around the norm.
+//
+// Everything between a load and a store is held in fp32: the mean, the sum of
+// squared deviations (taken in a second sweep over the registers, so no
+// difference of large sums is formed), the gradient sums; y, s and dx are
+// rounded once, to their own type.
+//
+// Bound by memory: forward reads and writes each element once (the row stays in
+// registers between the sweeps), backward too.  A row is one workgroup of
+// W = ceil(cols / (512 NV)) waves, a lane holding NV groups of 8 consecutive
+// elements; a row's sums are a butterfly in each wave and, for W > 1, one exchange
+// through LDS.  Backward workgroups walk rows with the next row's loads issued
+// before the current row's exchange, so that the exchange does not leave the
+// memory idle, and keep the weight gradient of their rows in registers; they
+// write one partial row each, which a second launch adds up in a fixed order
+// (no atomics: the same bytes every time).
+#include "fp8_device.hpp"
+#include "fp8_internal.hpp"
+
+namespace fp8k {
+
+namespace {
+
+typedef __bf16 nb16x2 __attribute__((ext_vector_type(2)));
+typedef float nf32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kNormMaxWaves = 16;
+
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(nf32x2{a, b}, nb16x2));
+}
+
+// Eight consecutive elements as loaded: 16 bytes of bf16 or 32 of fp32.
+template <bool F32> struct Raw8;
+template <> struct Raw8<false> { uint4 a; };
+template <> struct Raw8<true> { uint4 a, b; };
+
+// Load the 8 elements from column c of a row of `cols`; those past the row's end
+// are zero.  VEC: cols is a multiple of 8, so every group is whole and 16-byte
+// aligned; otherwise the elements are read one by one.
+template <bool F32, bool VEC>
+__device__ __forceinline__ Raw8<F32> load8(const void* row, int c, int cols)
+{
+    Raw8<F32> r{};
+    if (VEC) {
+        if (c < cols) {
+            if constexpr (F32) {
+                const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(row) + c);
+                r.a = p[0];
+                r.b = p[1];
+            } else {
+                r.a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + c);
+            }
+        }
+    } else {
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            w[e] = 0;
+            if (c + e < cols) {
+                if constexpr (F32)
+                    w[e] = __float_as_uint(static_cast<const float*>(row)[c + e]);
+                else
+                    w[e] = static_cast<const uint16_t*>(row)[c + e];
+            }
+        }
+        if constexpr (F32) {
+            r.a = make_uint4(w[0], w[1], w[2], w[3]);
+            r.b = make_uint4(w[4], w[5], w[6], w[7]);
+        } else {
+            r.a = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+        }
+    }
+    return r;
+}
+
+template <bool F32>
+__device__ __forceinline__ void widen(const Raw8<F32>& r, float (&f)[8])
+{
+    if constexpr (F32) {
+        const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(w[e]);
+    } else {
+        const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            f[2 * e] = bf16_lo(w[e]);
+            f[2 * e + 1] = bf16_hi(w[e]);
+        }
+    }
+}
+
+template <bool F32, bool VEC>
+__device__ __forceinline__ void store8(void* row, int c, int cols, const float (&f)[8])
+{
+    if constexpr (F32) {
+        float* p = static_cast<float*>(row) + c;
+        if (VEC) {
+            if (c < cols) {
+                reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+                reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e < cols) p[e] = f[e];
+        }
+    } else {
+        uint16_t* p = static_cast<uint16_t*>(row) + c;
+        const uint4 w = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+        if (VEC) {
+            if (c < cols) *reinterpret_cast<uint4*>(p) = w;
+        } else {
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e < cols) p[e] = (uint16_t)(ww[e >> 1] >> (16 * (e & 1)));
+        }
+    }
+}
+
+__device__ __forceinline__ float wave_sum(float v)
+{
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+    return v;
+}
+
+// Sum over the workgroup's waves of a value already summed in each wave; `part`
+// is an LDS row that no other exchange in flight uses.
+__device__ __forceinline__ float2 block_sum2(float2 v, float2* part, int wave, int waves)
+{
+    if (waves == 1) return v;
+    if ((threadIdx.x & 63) == 0) part[wave] = v;
+    __syncthreads();
+    float2 t = part[0];
+    for (int w = 1; w < waves; ++w) {
+        t.x += part[w].x;
+        t.y += part[w].y;
+    }
+    return t;
+}
+
+}  // namespace
+
+// Forward, one row per workgroup.  Measured on MI355X, 4096 x 4096 bf16 with the
+// residual sum (134 MB): see the table in the launcher's comment.
+template <bool F32, bool VEC, int NV, bool RMS>
+__global__ void __launch_bounds__(kNormMaxWaves * 64)
+norm_forward_kernel(const void* __restrict__ x, const uint16_t* __restrict__ add, const uint16_t* __restrict__ weight,
+                    const uint16_t* __restrict__ bias, float eps, int cols, uint16_t* __restrict__ y,
+                    void* __restrict__ sum, float* __restrict__ mean, float* __restrict__ rstd,
+                    uint32_t* __restrict__ absmax)
+{
+    __shared__ float2 part[2][kNormMaxWaves];
+    const size_t at = (size_t)blockIdx.x * (size_t)cols;
+    const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int col0 = threadIdx.x * 8, step = blockDim.x * 8;
+    const uint8_t* xr = static_cast<const uint8_t*>(x) + at * (F32 ? 4 : 2);
+
+    Raw8<F32> xv[NV];
+    Raw8<false> av[NV], wv[NV], bv[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) xv[v] = load8<F32, VEC>(xr, col0 + v * step, cols);
+    if (add) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) av[v] = load8<false, VEC>(add + at, col0 + v * step, cols);
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) wv[v] = load8<false, VEC>(weight, col0 + v * step, cols);
+    if (bias) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) bv[v] = load8<false, VEC>(bias, col0 + v * step, cols);
+    }
+
+    float s[NV][8];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        widen<F32>(xv[v], s[v]);
+        if (add) {
+            float a[8];
+            widen<false>(av[v], a);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[v][e] += a[e];
+        }
+    }
+    if (sum) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            store8<F32, VEC>(static_cast<uint8_t*>(sum) + at * (F32 ? 4 : 2), col0 + v * step, cols, s[v]);
+    }
+
+    const float inv_n = 1.0f / (float)cols;
+    float m = 0.0f;
+    if (!RMS) {
+        float t = 0.0f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t += s[v][e];      // places past the row's end hold zero
+        m = block_sum2(make_float2(wave_sum(t), 0.0f), part[0], wave, waves).x * inv_n;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                s[v][e] = col0 + v * step + e < cols ? s[v][e] - m : 0.0f;
+    }
+    float q = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q = fmaf(s[v][e], s[v][e], q);
+    const float var = block_sum2(make_float2(wave_sum(q), 0.0f), part[1], wave, waves).x * inv_n;
+    const float r = 1.0f / sqrtf(var + eps);
+    if (threadIdx.x == 0) {
+        rstd[blockIdx.x] = r;
+        if (!RMS) mean[blockIdx.x] = m;
+    }
+
+    uint32_t top = 0;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        float w[8], o[8];
+        widen<false>(wv[v], w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = s[v][e] * r * w[e];
+        if (bias) {
+            float b[8];
+            widen<false>(bv[v], b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] += b[e];
+        }
+        store8<false, VEC>(y + at, col0 + v * step, cols, o);
+        if (absmax) {                                       // of the bf16 values as stored
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                const uint32_t p = pack2(o[e], o[e + 1]);
+                const int c = col0 + v * step + e;
+                if (c < cols) top = max(top, p << 16 & 0x7FFFFFFFu);
+                if (c + 1 < cols) top = max(top, p & 0x7FFF0000u);
+            }
+        }
+    }
+    if (absmax) block_max_to_global(top, absmax);
+}
+
+// Backward over rows blockIdx.x, blockIdx.x + gridDim.x, ...; partial[2][grid][cols]
+// gets the workgroup's sums of dy h and, if asked for, of dy.
+template <bool F32, bool VEC, int NV, bool RMS>
+__global__ void __launch_bounds__(kNormMaxWaves * 64)
+norm_backward_kernel(const uint16_t* __restrict__ dy, const void* __restrict__ x, const uint16_t* __restrict__ weight,
+                     const float* __restrict__ mean, const float* __restrict__ rstd, const void* __restrict__ dres,
+                     int rows, int cols, void* __restrict__ dx, float* __restrict__ partial, int want_db)
+{
+    __shared__ float2 part[2][kNormMaxWaves];
+    constexpr size_t kX = F32 ? 4 : 2;
+    const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int col0 = threadIdx.x * 8, step = blockDim.x * 8;
+    const float inv_n = 1.0f / (float)cols;
+    const uint8_t* xb = static_cast<const uint8_t*>(x);
+    const uint8_t* rb = static_cast<const uint8_t*>(dres);
+
+    float w[NV][8], dw[NV][8], db[NV][8];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        widen<false>(load8<false, VEC>(weight, col0 + v * step, cols), w[v]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[v][e] = db[v][e] = 0.0f;
+    }
+
+    Raw8<false> yv[NV];
+    Raw8<F32> xv[NV], rv[NV];
+    float m = 0.0f, r = 0.0f;
+    auto fetch = [&](int row) {
+        const size_t at = (size_t)row * (size_t)cols;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            yv[v] = load8<false, VEC>(dy + at, col0 + v * step, cols);
+            xv[v] = load8<F32, VEC>(xb + at * kX, col0 + v * step, cols);
+            if (dres) rv[v] = load8<F32, VEC>(rb + at * kX, col0 + v * step, cols);
+        }
+        r = rstd[row];
+        if (!RMS) m = mean[row];
+    };
+
+    int row = blockIdx.x;
+    if (row < rows) fetch(row);
+    for (int turn = 0; row < rows; turn ^= 1) {
+        float g[NV][8], h[NV][8], keep[NV][8];
+        float2 t = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float d[8], xs[8];
+            widen<false>(yv[v], d);
+            widen<F32>(xv[v], xs);
+            if (dres) widen<F32>(rv[v], keep[v]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                // past the row's end dy and w are zero, so whatever h is there adds nothing
+                // (the mean and the reciprocal deviation of a finite row are finite)
+                h[v][e] = (xs[e] - m) * r;
+                g[v][e] = d[e] * w[v][e];
+                dw[v][e] = fmaf(d[e], h[v][e], dw[v][e]);
+                db[v][e] += d[e];
+                t.x = fmaf(g[v][e], h[v][e], t.x);
+                t.y += g[v][e];
+            }
+        }
+        const size_t at = (size_t)row * (size_t)cols;
+        const float rr = r;
+        row += gridDim.x;
+        if (row < rows) fetch(row);
+        t.x = wave_sum(t.x);
+        if (!RMS) t.y = wave_sum(t.y);
+        t = block_sum2(t, part[turn], wave, waves);
+        const float along = t.x * inv_n, flat = RMS ? 0.0f : t.y * inv_n;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                o[e] = rr * (g[v][e] - flat - h[v][e] * along);
+                if (dres) o[e] += keep[v][e];
+            }
+            store8<F32, VEC>(static_cast<uint8_t*>(dx) + at * kX, col0 + v * step, cols, o);
+        }
+    }
+
+    float* pw = partial + (size_t)blockIdx.x * (size_t)cols;
+    float* pb = pw + (size_t)gridDim.x * (size_t)cols;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        store8<true, VEC>(pw, col0 + v * step, cols, dw[v]);
+        if (want_db) store8<true, VEC>(pb, col0 + v * step, cols, db[v]);
+    }
+}
+
+// out[c] = sum over i < parts of partial[i][c], 32 columns per workgroup: 32 lanes of
+// consecutive columns by 32 slices of the parts, the slices joined in LDS in order.
+// blockIdx.y picks the weight's or the bias's sums.
+__global__ void __launch_bounds__(1024)
+norm_join_kernel(const float* __restrict__ partial, int parts, int cols, float* __restrict__ dw, float* __restrict__ db)
+{
+    __shared__ float slice[32][33];
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;
+    const float* p = partial + (size_t)blockIdx.y * (size_t)parts * (size_t)cols;
+    float t = 0.0f;
+    if (c < cols) {
+#pragma unroll 8
+        for (int i = k; i < parts; i += 32) t += p[(size_t)i * (size_t)cols + c];
+    }
+    slice[k][threadIdx.x & 31] = t;
+    __syncthreads();
+    if (k == 0 && c < cols) {
+        t = slice[0][threadIdx.x];
+        for (int i = 1; i < 32; ++i) t += slice[i][threadIdx.x];
+        (blockIdx.y ? db : dw)[c] = t;
+    }
+}
+
+// Lanes per row and groups per lane.  One group of 8 per lane and as many waves as
+// that takes, up to 8192 columns; two above.
+static int norm_waves(int64_t cols, int nv) { return (int)((cols + 512 * nv - 1) / (512 * nv)); }
+static int norm_groups(int64_t cols) { return cols <= 512 * kNormMaxWaves ? 1 : 2; }
+
+// Workgroups of the backward launch: enough to fill the chip (32 waves per CU
+// when rows allow), no more partial rows than rows.
+static int norm_backward_grid(int64_t rows, int64_t cols)
+{
+    const int waves = norm_waves(cols, norm_groups(cols));
+    const int64_t fill = (int64_t)device_cu_count() * std::max(1, 16 / waves);
+    return (int)std::min<int64_t>(rows, fill);
+}
+
+int64_t norm_backward_workspace(int64_t rows, int64_t cols)
+{
+    return (int64_t)norm_backward_grid(rows, cols) * cols * 4 * 2;
+}
+
+namespace {
+
+template <typename Fn>
+hipError_t norm_variant(bool f32, bool vec, int nv, bool rms, Fn&& fn)
+{
+    auto pick_rms = [&](auto f, auto v, auto n) {
+        return rms ? fn(f, v, n, std::true_type{}) : fn(f, v, n, std::false_type{});
+    };
+    auto pick_nv = [&](auto f, auto v) {
+        return nv == 1 ? pick_rms(f, v, std::integral_constant<int, 1>{})
+                       : pick_rms(f, v, std::integral_constant<int, 2>{});
+    };
+    auto pick_vec = [&](auto f) { return vec ? pick_nv(f, std::true_type{}) : pick_nv(f, std::false_type{}); };
+    return f32 ? pick_vec(std::true_type{}) : pick_vec(std::false_type{});
+}
+
+}  // namespace
+
+hipError_t launch_norm_forward(const void* x, bool f32, const void* add, const void* weight, const void* bias,
+                               float eps, bool rms, int64_t rows, int64_t cols, void* y, void* sum, float* mean,
+                               float* rstd, float* absmax, hipStream_t stream)
+{
+    const int nv = norm_groups(cols);
+    return norm_variant(f32, cols % 8 == 0, nv, rms, [&](auto f, auto v, auto n, auto ms) {
+        return launch(norm_forward_kernel<f.value, v.value, n.value, ms.value>, dim3((unsigned)rows),
+                      dim3(64 * norm_waves(cols, n.value)), stream, x, static_cast<const uint16_t*>(add),
+                      static_cast<const uint16_t*>(weight), static_cast<const uint16_t*>(bias), eps, (int)cols,
+                      static_cast<uint16_t*>(y), sum, mean, rstd, reinterpret_cast<uint32_t*>(absmax));
+    });
+}
+
+hipError_t launch_norm_backward(const void* dy, const void* x, bool f32, const void* weight, const float* mean,
+                                const float* rstd, const void* dres, bool rms, int64_t rows, int64_t cols, void* dx,
+                                float* dw, float* db, float* partial, hipStream_t stream)
+{
+    const int nv = norm_groups(cols), grid = norm_backward_grid(rows, cols);
+    const hipError_t e = norm_variant(f32, cols % 8 == 0, nv, rms, [&](auto f, auto v, auto n, auto ms) {
+        return launch(norm_backward_kernel<f.value, v.value, n.value, ms.value>, dim3(grid),
+                      dim3(64 * norm_waves(cols, n.value)), stream, static_cast<const uint16_t*>(dy), x,
+                      static_cast<const uint16_t*>(weight), mean, rstd, dres, (int)rows, (int)cols, dx, partial,
+                      db ? 1 : 0);
+    });
+    if (e != hipSuccess) return e;
+    return launch(norm_join_kernel, dim3((unsigned)((cols + 31) / 32), db ? 2 : 1), dim3(1024), stream,
+                  static_cast<const float*>(partial), grid, (int)cols, dw, db);
+}
+
+}  // namespace fp8k

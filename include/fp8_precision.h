@@ -482,6 +482,70 @@ fp8_status fp8_mx_gemm_backward(const uint8_t* dyq, const uint8_t* sdy, const ui
                                 hipStream_t stream);
 
 /*
+ * The operators around the FP8 linears of a training step: the norm in front of
+ * a linear, attention between the QKV and output projections, and the loss of a
+ * linear head.  They read and write bf16 (the norm's residual stream may be
+ * fp32), hold every sum, statistic and softmax in fp32 and round once to the
+ * output's type.  A call that produces a tensor which the FP8 path quantises
+ * next can fold its statistic into a running absmax (fp8_absmax_accumulate),
+ * saving that call's read of the tensor.  Results do not depend on launch
+ * order (no floating-point atomics): the same inputs give the same bytes.
+ */
+
+/* Type of a residual stream. */
+typedef enum fp8_stream_type { FP8_STREAM_BF16 = 0, FP8_STREAM_F32 = 1 } fp8_stream_type;
+
+/* Which norm: root mean square (no mean, no bias) or layer norm. */
+typedef enum fp8_norm_kind { FP8_NORM_RMS = 0, FP8_NORM_LAYER = 1 } fp8_norm_kind;
+
+/*
+ * Norm of every row of a residual stream, with the residual sum in front:
+ *   s = x + add (or x);  m = mean(s) (layer) or 0 (rms);
+ *   r = 1 / sqrt(mean((s - m)^2) + eps);  y = (s - m) r weight + bias
+ * The norm is taken of the fp32 sum; s is rounded to the stream's type where it
+ * is written.
+ *
+ *   x       stream type [rows, cols]
+ *   add     bf16 [rows, cols] or NULL: the previous block's output
+ *   weight  bf16 [cols];  bias  bf16 [cols] or NULL (NULL for FP8_NORM_RMS)
+ *   eps     >= 0
+ *   y       bf16 [rows, cols]
+ *   sum     stream type [rows, cols]: s; given with add and NULL without it
+ *   mean    fp32 [rows] for FP8_NORM_LAYER, NULL for FP8_NORM_RMS;  rstd  fp32 [rows]
+ *   absmax  fp32 scalar or NULL: becomes max(*absmax, max |y|), y as stored
+ * Constraints: rows in [1, 2^31), cols in [1, 16384].  x and add may be the same
+ * tensor; no output may overlap an input or another output.
+ */
+fp8_status fp8_norm_forward(const void* x, fp8_stream_type type, const void* add, const void* weight,
+                            const void* bias, float eps, fp8_norm_kind kind, int64_t rows, int64_t cols, void* y,
+                            void* sum, float* mean, float* rstd, float* absmax, hipStream_t stream);
+
+/*
+ * Gradients of fp8_norm_forward.  With h = (s - m) r and g = dy weight,
+ *   dx = r (g - h mean(g h) - mean(g) [layer norm only]) + dres
+ *   dweight = sum over rows of dy h,  dbias = sum over rows of dy
+ * dx is the gradient of s, and so of x and of add.
+ *
+ *   dy       bf16 [rows, cols]
+ *   s        stream type [rows, cols]: the forward's sum (x if nothing was added)
+ *   mean, rstd  fp32 [rows] from the forward (mean NULL for FP8_NORM_RMS)
+ *   dres     stream type [rows, cols] or NULL: the gradient that reaches s by the
+ *            residual path around the norm
+ *   dx       stream type [rows, cols]
+ *   dweight  fp32 [cols];  dbias  fp32 [cols] or NULL
+ *   workspace, workspace_bytes   device memory, 16-byte aligned, of at least the
+ *            size that fp8_norm_backward_workspace gives for (rows, cols) on the
+ *            current device; its contents are undefined before and after
+ * Constraints: those of fp8_norm_forward; inputs may be shared, outputs and the
+ * workspace overlap nothing.
+ */
+fp8_status fp8_norm_backward_workspace(int64_t rows, int64_t cols, int64_t* bytes);
+fp8_status fp8_norm_backward(const void* dy, const void* s, fp8_stream_type type, const void* weight,
+                             const float* mean, const float* rstd, const void* dres, fp8_norm_kind kind,
+                             int64_t rows, int64_t cols, void* dx, float* dweight, float* dbias, void* workspace,
+                             int64_t workspace_bytes, hipStream_t stream);
+
+/*
  * Measurement reference, not a step of the FP8 method: a plain device copy
  * dst[0, bytes) = src[0, bytes), built like the streaming kernels above
  * (16-byte vectors, non-temporal loads, the launch shape at which a copy
