@@ -53,6 +53,9 @@ _SIGS = {
     "fp8_norm_forward": (_i32, [_vp, _i32, _vp, _vp, _vp, ctypes.c_float, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),
     "fp8_norm_backward_workspace": (_i32, [_i64, _i64, _vp]),
     "fp8_norm_backward": (_i32, [_vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "fp8_attention_forward": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "fp8_attention_backward_workspace": (_i32, [_vp, _vp]),
+    "fp8_attention_backward": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -707,6 +710,97 @@ def norm_backward(dy, s, weight, mean, rstd, dres=None, want_dbias: bool = False
          _ptr(dy), _ptr(s), _STREAM_TYPES[s.dtype], _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dres),
          1 if mean is not None else 0, rows, cols, _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(ws), ws.numel())
     return dx, dweight, dbias
+
+
+class _HeadTensor(ctypes.Structure):
+    _fields_ = [("data", _vp), ("token_stride", _i64), ("head_stride", _i64)]
+
+
+class _AttentionShape(ctypes.Structure):
+    _fields_ = [("tokens_q", _i64), ("tokens_k", _i64), ("heads_q", _i64), ("heads_k", _i64), ("head_dim", _i64),
+                ("batch", _i64), ("bounds_q", _vp), ("bounds_k", _vp), ("causal", _i32), ("scale", ctypes.c_float)]
+
+
+def _heads(t, name, shape=None):
+    """A bf16 [tokens, heads, head_dim] device tensor whose elements are adjacent
+    within a head; tokens and heads may have any strides."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be " + ("[tokens, heads, head_dim]" if shape is None else f"{tuple(shape)}"))
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must be contiguous along head_dim")
+    return ctypes.byref(_HeadTensor(t.data_ptr(), t.stride(0), t.stride(1)))
+
+
+def _attention_shape(q, k, v, cu_q, cu_k, causal, scale):
+    """The call's shape, checked: (shape struct, q, k, v as head tensors)."""
+    hq, hk = _heads(q, "q"), _heads(k, "k")
+    hv = _heads(v, "v", k.shape)
+    if q.shape[2] != k.shape[2]:
+        raise ValueError("q and k must have one head_dim")
+    if (cu_q is None) != (cu_k is None):
+        raise ValueError("cu_q and cu_k go together")
+    batch = 1
+    if cu_q is not None:
+        _dev_tensor(cu_q, "cu_q", torch.int32)
+        _dev_tensor(cu_k, "cu_k", torch.int32)
+        batch = cu_q.numel() - 1
+        if batch < 1 or cu_k.numel() != batch + 1:
+            raise ValueError("cu_q and cu_k must hold one bound more than there are sequences")
+    shape = _AttentionShape(q.shape[0], k.shape[0], q.shape[1], k.shape[1], q.shape[2], batch, _ptr(cu_q), _ptr(cu_k),
+                            1 if causal else 0, q.shape[2] ** -0.5 if scale is None else scale)
+    return shape, hq, hk, hv
+
+
+def attention(q, k, v, cu_q=None, cu_k=None, causal: bool = False, scale: float | None = None, absmax=None, out=None,
+              lse=None):
+    """Softmax attention over packed sequences: q bf16 [tokens_q, heads_q, head_dim],
+    k and v bf16 [tokens_k, heads_k, head_dim], heads_q a multiple of heads_k,
+    tokens and heads with any strides (slices of one projection's output).
+
+    ``cu_q``, ``cu_k``: int32 device tensors of the sequences' bounds (0, ..., tokens);
+    without them all tokens are one sequence.  ``causal``: query i of a sequence sees
+    keys j <= i + nk - nq.  ``scale``: head_dim ** -0.5 if not given.  ``absmax`` (fp32
+    [1], holding +0 or an earlier result) becomes max(absmax, max |out|).
+    Returns (out as q, lse fp32 [heads_q, tokens_q]); a query that sees no key has
+    out 0 and lse -inf.
+    """
+    shape, hq, hk, hv = _attention_shape(q, k, v, cu_q, cu_k, causal, scale)
+    if absmax is not None:
+        _scalar_in(absmax, "absmax")
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    ho = _heads(out, "out", q.shape)
+    lse = _out(lse, "lse", (q.shape[1], q.shape[0]), torch.float32, q.device)
+    _run("fp8_attention_forward", _lib.fp8_attention_forward, (q, k, v, cu_q, cu_k, out, lse, absmax),
+         ctypes.byref(shape), hq, hk, hv, ho, _ptr(lse), _ptr(absmax))
+    return out, lse
+
+
+def attention_backward(dout, q, k, v, out, lse, cu_q=None, cu_k=None, causal: bool = False,
+                       scale: float | None = None, absmax=None, dq=None, dk=None, dv=None):
+    """Gradients of ``attention``: dout as q, ``out`` and ``lse`` from the forward, the
+    other arguments as there.  dq, dk and dv may be given as slices of one tensor (the
+    gradient of the projection's output); ``absmax`` becomes the largest magnitude of
+    the three and its earlier value.  Returns (dq, dk, dv)."""
+    shape, hq, hk, hv = _attention_shape(q, k, v, cu_q, cu_k, causal, scale)
+    hg, ho = _heads(dout, "dout", q.shape), _heads(out, "out", q.shape)
+    _dev_tensor(lse, "lse", torch.float32)
+    if tuple(lse.shape) != (q.shape[1], q.shape[0]):
+        raise ValueError("lse must be [heads_q, tokens_q]")
+    if absmax is not None:
+        _scalar_in(absmax, "absmax")
+    new = lambda t, like: torch.empty(like.shape, dtype=torch.bfloat16, device=like.device) if t is None else t
+    dq, dk, dv = new(dq, q), new(dk, k), new(dv, v)
+    hdq, hdk, hdv = _heads(dq, "dq", q.shape), _heads(dk, "dk", k.shape), _heads(dv, "dv", v.shape)
+    ws = _workspace("fp8_attention_backward_workspace", q.device, ctypes.byref(shape))
+    _run("fp8_attention_backward", _lib.fp8_attention_backward,
+         (dout, q, k, v, out, lse, cu_q, cu_k, dq, dk, dv, absmax, ws), ctypes.byref(shape), hg, hq, hk, hv, ho,
+         _ptr(lse), hdq, hdk, hdv, _ptr(absmax), _ptr(ws), ws.numel())
+    return dq, dk, dv
 
 
 def stream_copy(src: torch.Tensor, dst: torch.Tensor) -> torch.Tensor:

@@ -676,6 +676,205 @@ fp8_status fp8_norm_backward(const void* dy, const void* s, fp8_stream_type type
     return FP8_OK;
 }
 
+// A tensor of an attention call: its strides checked, and the bytes it spans.
+struct Heads {
+    uint16_t* p = nullptr;
+    int64_t tokens = 0, heads = 0, d = 0, row = 0, head = 0;
+    int64_t row_span() const { return (heads - 1) * head + d; }       // elements of one token's heads
+    Range range() const { return {p, 2 * ((tokens - 1) * row + row_span())}; }
+    // each element has a place of its own
+    bool distinct() const
+    {
+        return (head >= d || heads == 1) && row >= row_span() ? true : row >= d && head >= (tokens - 1) * row + d;
+    }
+};
+
+static fp8_status take_heads(const char* call, const char* name, const fp8_head_tensor* t, int64_t tokens,
+                             int64_t heads, int64_t d, bool written, Heads& h)
+{
+    char msg[160];
+    auto no = [&](fp8_status st, const char* what) {
+        std::snprintf(msg, sizeof(msg), "%s: %s %s", call, name, what);
+        return fail(st, msg);
+    };
+    if (!t || !t->data) return no(FP8_ERR_INVALID, "is a null pointer");
+    h.p = static_cast<uint16_t*>(t->data);
+    h.tokens = tokens;
+    h.heads = heads;
+    h.d = d;
+    h.head = heads == 1 ? 0 : t->head_stride;                          // a single head's or token's stride moves nothing
+    if (h.head < 0 || h.head > ((int64_t)1 << 40)) return no(FP8_ERR_INVALID, "has a bad head stride");
+    h.row = tokens == 1 ? (h.row_span() + 7) / 8 * 8 : t->token_stride;
+    if (tokens > 1 && h.row < d) return no(FP8_ERR_INVALID, "has tokens closer than head_dim");
+    if (tokens > 1 && h.row >= ((int64_t)1 << 22)) return no(FP8_ERR_UNSUPPORTED, "has a token stride of 2^22 or more");
+    if (h.row % 8 || h.head % 8) return no(FP8_ERR_UNSUPPORTED, "has strides that are not multiples of 8");
+    if (!aligned(t->data, 16)) return no(FP8_ERR_UNSUPPORTED, "is not 16-byte aligned");
+    if (written && !h.distinct()) return no(FP8_ERR_INVALID, "overlaps itself");
+    return FP8_OK;
+}
+
+// Two tensors share an element.  Slices of one tensor (the same token stride, each token's
+// heads inside it) interleave without sharing any.
+static bool heads_overlap(const Heads& a, const Heads& b)
+{
+    const Range ra = a.range(), rb = b.range();
+    if (!overlap(ra.p, ra.n, rb.p, rb.n)) return false;
+    if (a.row != b.row || a.row_span() > a.row || b.row_span() > b.row) return true;
+    const int64_t r = 2 * a.row;
+    int64_t off = ((int64_t)(reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p))) % r;
+    if (off < 0) off += r;
+    return off < 2 * a.row_span() || off + 2 * b.row_span() > r;
+}
+
+static bool heads_overlap(const Heads& a, const void* p, int64_t n)
+{
+    const Range r = a.range();
+    return overlap(r.p, r.n, p, n);
+}
+
+static fp8_status attention_shape(const char* call, const fp8_attention_shape* s)
+{
+    char msg[160];
+    auto no = [&](fp8_status st, const char* what) {
+        std::snprintf(msg, sizeof(msg), "%s: %s", call, what);
+        return fail(st, msg);
+    };
+    if (!s) return no(FP8_ERR_INVALID, "null shape");
+    if (s->tokens_q < 1 || s->tokens_k < 1 || s->heads_q < 1 || s->heads_k < 1 || s->batch < 1 || s->head_dim < 1)
+        return no(FP8_ERR_INVALID, "tokens, heads, head_dim and batch must be positive");
+    if (s->tokens_q >= ((int64_t)1 << 31) || s->tokens_k >= ((int64_t)1 << 31) || s->heads_q > 65536 || s->batch > (1 << 24))
+        return no(FP8_ERR_UNSUPPORTED, "more than 2^31 - 1 tokens, 2^16 heads or 2^24 sequences");
+    if (s->heads_q % s->heads_k) return no(FP8_ERR_INVALID, "heads_q must be a multiple of heads_k");
+    if (s->head_dim % 8 || s->head_dim > 128) return no(FP8_ERR_UNSUPPORTED, "head_dim must be a multiple of 8, at most 128");
+    if (!s->bounds_q != !s->bounds_k) return no(FP8_ERR_INVALID, "bounds_q and bounds_k go together");
+    if (!s->bounds_q && s->batch != 1) return no(FP8_ERR_INVALID, "several sequences need bounds");
+    if (!aligned(s->bounds_q, 4) || !aligned(s->bounds_k, 4)) return no(FP8_ERR_UNSUPPORTED, "misaligned bounds");
+    if (s->causal != 0 && s->causal != 1) return no(FP8_ERR_INVALID, "causal must be 0 or 1");
+    if (!(s->scale > 0.0f) || s->scale > 3.0e38f) return no(FP8_ERR_INVALID, "scale must be positive and finite");
+    if (s->tokens_q * s->heads_q / 16 >= 0x7FFFFFFF || !fp8k::attention_grid_ok(s->tokens_q, (int)s->batch, (int)s->heads_q) ||
+        !fp8k::attention_grid_ok(s->tokens_k, (int)s->batch, (int)s->heads_k))
+        return no(FP8_ERR_UNSUPPORTED, "too many rows for one launch");
+    return FP8_OK;
+}
+
+static fp8k::AttentionArgs attention_args(const fp8_attention_shape& s)
+{
+    fp8k::AttentionArgs a{};
+    a.tq = (int)s.tokens_q;
+    a.tk = (int)s.tokens_k;
+    a.hq = (int)s.heads_q;
+    a.hk = (int)s.heads_k;
+    a.d = (int)s.head_dim;
+    a.batch = (int)s.batch;
+    a.cu_q = s.bounds_q;
+    a.cu_k = s.bounds_k;
+    a.causal = s.causal;
+    a.scale = s.scale;
+    return a;
+}
+
+fp8_status fp8_attention_forward(const fp8_attention_shape* shape, const fp8_head_tensor* q,
+                                 const fp8_head_tensor* k, const fp8_head_tensor* v, const fp8_head_tensor* out,
+                                 float* lse, float* absmax, hipStream_t stream)
+{
+    t_last_error.clear();
+    const char* call = "fp8_attention_forward";
+    fp8_status st = attention_shape(call, shape);
+    if (st != FP8_OK) return st;
+    const fp8_attention_shape& s = *shape;
+    Heads h[4];
+    if ((st = take_heads(call, "q", q, s.tokens_q, s.heads_q, s.head_dim, false, h[0])) != FP8_OK ||
+        (st = take_heads(call, "k", k, s.tokens_k, s.heads_k, s.head_dim, false, h[1])) != FP8_OK ||
+        (st = take_heads(call, "v", v, s.tokens_k, s.heads_k, s.head_dim, false, h[2])) != FP8_OK ||
+        (st = take_heads(call, "out", out, s.tokens_q, s.heads_q, s.head_dim, true, h[3])) != FP8_OK)
+        return st;
+    if (!lse) return fail(FP8_ERR_INVALID, "fp8_attention_forward: null lse");
+    if (!aligned(lse, 4) || !aligned(absmax, 4)) return fail(FP8_ERR_UNSUPPORTED, "fp8_attention_forward: misaligned lse or absmax");
+    const Range flat[] = {{lse, 4 * s.heads_q * s.tokens_q}, {absmax, 4}};
+    const Range in[] = {{s.bounds_q, 4 * (s.batch + 1)}, {s.bounds_k, 4 * (s.batch + 1)}};
+    bool bad = outputs_overlap(flat, 2, in, 2);
+    for (int i = 0; i < 4; ++i) {
+        if (i < 3) bad = bad || heads_overlap(h[3], h[i]);
+        for (const Range& r : flat) bad = bad || heads_overlap(h[i], r.p, r.n);
+    }
+    for (const Range& r : in) bad = bad || heads_overlap(h[3], r.p, r.n);
+    if (bad) return fail(FP8_ERR_INVALID, "fp8_attention_forward: overlapping buffers");
+    fp8k::AttentionArgs a = attention_args(s);
+    a.q = h[0].p; a.q_row = h[0].row; a.q_head = h[0].head;
+    a.k = h[1].p; a.k_row = h[1].row; a.k_head = h[1].head;
+    a.v = h[2].p; a.v_row = h[2].row; a.v_head = h[2].head;
+    a.out = h[3].p; a.out_row = h[3].row; a.out_head = h[3].head;
+    a.lse = lse;
+    a.absmax = reinterpret_cast<uint32_t*>(absmax);
+    hipError_t e = fp8k::launch_attention_forward(a, stream);
+    if (e != hipSuccess) return fail_hip(call, e);
+    return FP8_OK;
+}
+
+static int64_t attention_workspace(const fp8_attention_shape& s) { return 2 * 4 * s.heads_q * s.tokens_q; }
+
+fp8_status fp8_attention_backward_workspace(const fp8_attention_shape* shape, int64_t* bytes)
+{
+    t_last_error.clear();
+    fp8_status st = attention_shape("fp8_attention_backward_workspace", shape);
+    if (st != FP8_OK) return st;
+    if (!bytes) return fail(FP8_ERR_INVALID, "fp8_attention_backward_workspace: null pointer");
+    *bytes = attention_workspace(*shape);
+    return FP8_OK;
+}
+
+fp8_status fp8_attention_backward(const fp8_attention_shape* shape, const fp8_head_tensor* dout,
+                                  const fp8_head_tensor* q, const fp8_head_tensor* k, const fp8_head_tensor* v,
+                                  const fp8_head_tensor* out, const float* lse, const fp8_head_tensor* dq,
+                                  const fp8_head_tensor* dk, const fp8_head_tensor* dv, float* absmax,
+                                  void* workspace, int64_t workspace_bytes, hipStream_t stream)
+{
+    t_last_error.clear();
+    const char* call = "fp8_attention_backward";
+    fp8_status st = attention_shape(call, shape);
+    if (st != FP8_OK) return st;
+    const fp8_attention_shape& s = *shape;
+    Heads h[8];                                            // 0-4 read, 5-7 written
+    if ((st = take_heads(call, "dout", dout, s.tokens_q, s.heads_q, s.head_dim, false, h[0])) != FP8_OK ||
+        (st = take_heads(call, "q", q, s.tokens_q, s.heads_q, s.head_dim, false, h[1])) != FP8_OK ||
+        (st = take_heads(call, "k", k, s.tokens_k, s.heads_k, s.head_dim, false, h[2])) != FP8_OK ||
+        (st = take_heads(call, "v", v, s.tokens_k, s.heads_k, s.head_dim, false, h[3])) != FP8_OK ||
+        (st = take_heads(call, "out", out, s.tokens_q, s.heads_q, s.head_dim, false, h[4])) != FP8_OK ||
+        (st = take_heads(call, "dq", dq, s.tokens_q, s.heads_q, s.head_dim, true, h[5])) != FP8_OK ||
+        (st = take_heads(call, "dk", dk, s.tokens_k, s.heads_k, s.head_dim, true, h[6])) != FP8_OK ||
+        (st = take_heads(call, "dv", dv, s.tokens_k, s.heads_k, s.head_dim, true, h[7])) != FP8_OK)
+        return st;
+    if (!lse || !workspace) return fail(FP8_ERR_INVALID, "fp8_attention_backward: null lse or workspace");
+    if (workspace_bytes < attention_workspace(s)) return fail(FP8_ERR_INVALID, "fp8_attention_backward: workspace too small");
+    if (!aligned(lse, 4) || !aligned(absmax, 4) || !aligned(workspace, 16))
+        return fail(FP8_ERR_UNSUPPORTED, "fp8_attention_backward: misaligned lse, absmax or workspace");
+    const Range flat[] = {{absmax, 4}, {workspace, workspace_bytes}};
+    const Range in[] = {{s.bounds_q, 4 * (s.batch + 1)}, {s.bounds_k, 4 * (s.batch + 1)}, {lse, 4 * s.heads_q * s.tokens_q}};
+    bool bad = outputs_overlap(flat, 2, in, 3);
+    for (int i = 0; i < 8; ++i) {
+        for (int j = 5; j < 8; ++j) bad = bad || (i != j && heads_overlap(h[j], h[i]));
+        for (const Range& r : flat) bad = bad || heads_overlap(h[i], r.p, r.n);
+        if (i >= 5)
+            for (const Range& r : in) bad = bad || heads_overlap(h[i], r.p, r.n);
+    }
+    if (bad) return fail(FP8_ERR_INVALID, "fp8_attention_backward: overlapping buffers");
+    fp8k::AttentionArgs a = attention_args(s);
+    a.dout = h[0].p; a.dout_row = h[0].row; a.dout_head = h[0].head;
+    a.q = h[1].p; a.q_row = h[1].row; a.q_head = h[1].head;
+    a.k = h[2].p; a.k_row = h[2].row; a.k_head = h[2].head;
+    a.v = h[3].p; a.v_row = h[3].row; a.v_head = h[3].head;
+    a.out = h[4].p; a.out_row = h[4].row; a.out_head = h[4].head;
+    a.dq = h[5].p; a.dq_row = h[5].row; a.dq_head = h[5].head;
+    a.dk = h[6].p; a.dk_row = h[6].row; a.dk_head = h[6].head;
+    a.dv = h[7].p; a.dv_row = h[7].row; a.dv_head = h[7].head;
+    a.lse = const_cast<float*>(lse);
+    a.stats = static_cast<float*>(workspace);
+    a.absmax = reinterpret_cast<uint32_t*>(absmax);
+    hipError_t e = fp8k::launch_attention_backward(a, stream);
+    if (e != hipSuccess) return fail_hip(call, e);
+    return FP8_OK;
+}
+
 fp8_status fp8_stream_copy(const void* src, void* dst, int64_t bytes, hipStream_t stream)
 {
     t_last_error.clear();

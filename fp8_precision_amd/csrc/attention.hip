@@ -1,0 +1,706 @@
+// attention.hip -- softmax attention over packed sequences, forward and backward,
+// for gfx950.
+//
+// For one sequence of nq queries and nk keys and one query head, with the key head
+// it shares, s = scale q k^T, and a key j seen by query i if j < nk and, causal,
+// j <= i + nk - nq (the last query sees every key):
+//   p = exp(s - lse) over the keys seen, lse = log sum exp(s),   out = p v
+// and backward, which takes p from q, k and lse again instead of keeping it,
+//   delta = rowsum(dout out)          dv = p^T dout
+//   dp = dout v^T                     ds = p (dp - delta)
+//   dq = scale ds k                   dk = scale ds^T q
+// (dk and dv summed over the query heads that share the key head).  A query that
+// sees nothing has out = 0, lse = -inf, and gives no gradient.
+//
+// Bound by the matrix units and, next to them, by the exponentials: 4 d
+// multiply-adds per score against one exponential, a handful of fp32 operations
+// and two roundings.
+//
+// Layout.  Every product runs on v_mfma_f32_32x32x16_bf16, and scores are always
+// computed so that what the workgroup keeps (32 queries per wave in the forward
+// and the dq kernel, 32 keys per wave in the dk/dv kernel) is the product's
+// column: a lane then owns one of them, holds 16 of a block's 32 scores for it,
+// and its partner 32 lanes away the other 16.  So
+//  - a query's maximum and sum are sums over the lane's registers and one swap
+//    with the partner lane;
+//  - the lane's 8 scores of registers 8 c .. 8 c + 7, rounded to bf16, are exactly
+//    the second operand of the next product for 16 of the streamed rows, in the
+//    order 16 c + 8 (e / 4) + 4 (lane / 32) + e % 4: p and ds never leave the
+//    registers;
+//  - the first operand of that product is the streamed tile's transpose in the same
+//    order, which ds_read_b64_tr_b16 delivers from the row-major tile in LDS.
+// Streamed tiles (k and v, or q and dout) go global -> LDS with 16-byte
+// direct-to-LDS buffer loads, two stages; the buffer's size is set to what is left
+// of the sequence, so that rows past its end read as zero, and lanes past the head
+// dimension are given an offset outside it.  16-byte chunk c of tile row r lies at
+// chunk c ^ f(r): with f's low row bits in the high chunk bits, the 4-row pieces
+// of the transposing reads and the 16-row columns of the plain reads both spread
+// over all banks.
+#include "fp8_device.hpp"
+#include "fp8_internal.hpp"
+
+namespace fp8k {
+
+namespace {
+
+typedef __bf16 ab16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 ab16x2 __attribute__((ext_vector_type(2)));
+typedef float af32x2 __attribute__((ext_vector_type(2)));
+typedef float af32x16 __attribute__((ext_vector_type(16)));
+typedef short as16x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int au32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) as16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) au32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) float lds_f32;
+
+constexpr int kAttThreads = 256;
+constexpr int kAttWaves = 4;
+constexpr int kOwn = 128;                 // queries (or keys) a workgroup keeps: 32 per wave
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kInf = __builtin_inff();
+
+union Frag {
+    au32x4 u;
+    ab16x8 b;
+    struct { as16x4 lo, hi; } s;
+    uint32_t w[4];
+};
+
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(af32x2{a, b}, ab16x2));
+}
+
+__device__ __forceinline__ af32x16 mma(const Frag& a, const Frag& b, const af32x16& c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.b, b.b, c, 0, 0, 0);
+}
+
+// The value of the lane 32 away.
+__device__ __forceinline__ float partner(float v)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+}
+
+// Chunk permutation of tile row r (rows of CH 16-byte chunks).
+template <int CH>
+__device__ __forceinline__ int spread(int r)
+{
+    return CH == 16 ? ((r & 3) << 2 | (r >> 2 & 3)) : ((r >> 1 & 1) << 2 | (r >> 2 & 3));
+}
+
+// One 16-byte direct-to-LDS load per lane through a buffer descriptor: lane L reads
+// at base + voff[L] (zero past the descriptor's size) and writes LDS bytes
+// lds + 16 L.  Inline assembly, so that the compiler does not put a wait for every
+// load in flight in front of each LDS read; the kernels wait and synchronise.
+__device__ __forceinline__ void buffer_to_lds(uint32_t voff, const au32x4& desc, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+                 :
+                 : "v"(voff), "s"(desc), "s"(lds)
+                 : "memory", "m0");
+}
+
+__device__ __forceinline__ au32x4 descriptor(const uint8_t* base, int64_t bytes)
+{
+    const uint64_t b = (uint64_t)base;
+    const int64_t n = bytes < 0 ? 0 : bytes > 0x7FFFFFFF ? 0x7FFFFFFF : bytes;
+    au32x4 d;
+    d[0] = __builtin_amdgcn_readfirstlane((uint32_t)b);
+    d[1] = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32) & 0xFFFFu);
+    d[2] = __builtin_amdgcn_readfirstlane((uint32_t)n);
+    d[3] = 0x00020000u;                   // raw buffer, 32-bit elements
+    return d;
+}
+
+// Streams ROWS-row tiles of one head's rows [0, n) of a packed tensor into LDS.
+template <int DT, int ROWS>
+struct Stream {
+    static constexpr int kRow = DT * 2;                        // bytes of a tile row
+    static constexpr int kCh = DT / 8;                         // its 16-byte chunks
+    static constexpr int kPer = 64 / kCh;                      // rows per wave and load
+    static constexpr int kLoads = ROWS / (kPer * kAttWaves);   // loads per wave and tile
+    const uint8_t* base;
+    int64_t stride;                       // bytes between rows
+    int n;
+    uint32_t voff[kLoads];
+
+    __device__ __forceinline__ void init(const uint16_t* p, int64_t row_stride, int rows, int d)
+    {
+        base = reinterpret_cast<const uint8_t*>(p);
+        stride = row_stride * 2;
+        n = rows;
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int r = (wave * kLoads + i) * kPer + lane / kCh;
+            const int c = (lane % kCh) ^ spread<kCh>(r);
+            voff[i] = c * 8 < d ? (uint32_t)(r * stride) + (uint32_t)c * 16u : 0x80000000u;
+        }
+    }
+
+    // rows row0 .. row0 + ROWS - 1 into the ROWS * kRow bytes at LDS address lds
+    __device__ __forceinline__ void issue(int row0, uint32_t lds, int wave) const
+    {
+        const au32x4 desc = descriptor(base + (int64_t)row0 * stride, (int64_t)(n - row0) * stride);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            buffer_to_lds(voff[i], desc, __builtin_amdgcn_readfirstlane(lds + (uint32_t)((wave * kLoads + i) * 1024)));
+    }
+};
+
+// Operand reads from a tile in LDS.  rows(): the tile's rows as the product's rows,
+// the head dimension reduced (chunk c: elements 16 c ..).  cols(): the tile's columns
+// (32 of the head dimension, block db) as the product's rows, 16 of its rows reduced,
+// in the order that the score registers have.
+template <int DT>
+struct Tile {
+    static constexpr int kRow = DT * 2;
+    static constexpr int kCh = DT / 8;
+    uint32_t plain, trans;                // this lane's addresses for c = 0 and for db = 0
+
+    __device__ __forceinline__ void init(uint32_t lds)
+    {
+        const int lane = threadIdx.x & 63, h = lane >> 5;
+        const int r = lane & 31;
+        plain = lds + r * kRow + ((h ^ spread<kCh>(r)) * 16);
+        const int t = 4 * h + ((lane & 15) >> 2);
+        trans = lds + t * kRow + (((2 * (lane >> 4 & 1) + (lane & 3) / 2) ^ spread<kCh>(t)) * 16) + (lane & 1) * 8;
+    }
+    __device__ __forceinline__ Frag rows(uint32_t at, int block, int c) const
+    {
+        Frag f;
+        f.u = *(const lds_u32x4*)(uintptr_t)((plain ^ (uint32_t)(c * 32)) + at + block * 32 * kRow);
+        return f;
+    }
+    __device__ __forceinline__ Frag cols(uint32_t at, int block, int c, int db) const
+    {
+        // 8 rows on, spread() differs in its bit 1 (chunk bit 1: 32 bytes)
+        const uint32_t a = (trans ^ (uint32_t)(db * 64)) + at + (block * 32 + c * 16) * kRow;
+        const uint32_t b = (trans ^ (uint32_t)(db * 64) ^ 32u) + at + (block * 32 + c * 16 + 8) * kRow;
+        Frag f;
+        f.s.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)a);
+        f.s.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)b);
+        return f;
+    }
+};
+
+// 16 scores -> the two operands of 16 reduced rows each.
+__device__ __forceinline__ void to_operands(const af32x16& p, Frag (&f)[2])
+{
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[c].w[e] = bf16_pair(p[8 * c + 2 * e], p[8 * c + 2 * e + 1]);
+}
+
+// A lane's fixed operand: row `row` of a head, chunk c holding elements
+// 16 c + 8 (lane / 32) ..; zero past the head dimension or where !valid.
+template <int DT>
+__device__ __forceinline__ void load_own(Frag (&f)[DT / 16], const uint16_t* row, int d, bool valid)
+{
+    const int h = (threadIdx.x & 63) >> 5;
+#pragma unroll
+    for (int c = 0; c < DT / 16; ++c) {
+        f[c].u = au32x4{0, 0, 0, 0};
+        if (valid && 16 * c + 8 * h < d) f[c].u = *reinterpret_cast<const au32x4*>(row + 16 * c + 8 * h);
+    }
+}
+
+// Store a lane's accumulated row (acc[db][i]: element 32 db + 8 (i / 4) + 4 (lane / 32)
+// + i % 4), times `by`; returns the largest magnitude pattern stored.
+template <int DT>
+__device__ __forceinline__ uint32_t store_own(const af32x16 (&acc)[DT / 32], float by, uint16_t* row, int d, bool valid)
+{
+    const int h = (threadIdx.x & 63) >> 5;
+    uint32_t top = 0;
+    if (!valid) return 0;
+#pragma unroll
+    for (int db = 0; db < DT / 32; ++db)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int at = 32 * db + 8 * b + 4 * h;
+            if (at < d) {
+                uint2 o;
+                o.x = bf16_pair(acc[db][4 * b] * by, acc[db][4 * b + 1] * by);
+                o.y = bf16_pair(acc[db][4 * b + 2] * by, acc[db][4 * b + 3] * by);
+                *reinterpret_cast<uint2*>(row + at) = o;
+                top = max(max(max(top, o.x & 0x7FFF0000u), o.x << 16 & 0x7FFFFFFFu),
+                          max(o.y & 0x7FFF0000u, o.y << 16 & 0x7FFFFFFFu));
+            }
+        }
+    return top;
+}
+
+// Which rows a workgroup keeps: tile `t` of the tiles of all sequences, in order.
+struct Place {
+    int q0, nq, k0, nk;       // the sequence's queries and keys within the packed tensors
+    int first;                // the tile's first row within the sequence
+    bool any;
+};
+
+// The bounds of sequence i, held inside the tensor and in order whatever cu says.
+__device__ __forceinline__ void bounds(const int* cu, int i, int total, int& from, int& count)
+{
+    if (!cu) {
+        from = 0;
+        count = total;
+        return;
+    }
+    const int a = min(max(cu[i], 0), total), b = min(max(cu[i + 1], 0), total);
+    from = a;
+    count = max(b - a, 0);
+}
+
+// Every lane takes a sequence, 64 at a time; a prefix sum over the wave finds the one
+// that holds tile t.  `own` is the side that is tiled (0: queries, 1: keys).
+__device__ __forceinline__ Place find_tile(const AttentionArgs& a, int t, int own)
+{
+    const int lane = threadIdx.x & 63;
+    Place p{};
+    int before = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 64) {
+        int from = 0, count = 0;
+        if (b0 + lane < a.batch) bounds(own ? a.cu_k : a.cu_q, b0 + lane, own ? a.tk : a.tq, from, count);
+        const int tiles = (count + kOwn - 1) / kOwn;
+        int upto = tiles;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int o = __shfl_up(upto, off, 64);
+            if (lane >= off) upto += o;
+        }
+        const uint64_t past = __ballot(before + upto > t);
+        if (past) {
+            const int l = __ffsll((unsigned long long)past) - 1;
+            const int seq = __builtin_amdgcn_readfirstlane(b0 + l);
+            const int tile = t - before - __shfl(upto - tiles, l, 64);
+            p.first = __builtin_amdgcn_readfirstlane(tile * kOwn);
+            bounds(a.cu_q, seq, a.tq, p.q0, p.nq);
+            bounds(a.cu_k, seq, a.tk, p.k0, p.nk);
+            p.q0 = __builtin_amdgcn_readfirstlane(p.q0);
+            p.nq = __builtin_amdgcn_readfirstlane(p.nq);
+            p.k0 = __builtin_amdgcn_readfirstlane(p.k0);
+            p.nk = __builtin_amdgcn_readfirstlane(p.nk);
+            p.any = true;
+            return p;
+        }
+        before += __shfl(upto, 63, 64);
+    }
+    return p;
+}
+
+// Workgroup -> (tile, head).  Workgroups are dealt round-robin to the 8 XCDs: with a
+// multiple of 8 heads each XCD gets whole heads, so that a head's streamed tiles are
+// shared in its L2.
+__device__ __forceinline__ void deal(int b, int heads, int& tile, int& head)
+{
+    if (heads % 8 == 0) {
+        const int per = heads / 8;
+        head = (b % 8) * per + (b / 8) % per;
+        tile = b / heads;
+    } else {
+        head = b % heads;
+        tile = b / heads;
+    }
+}
+
+constexpr int kKeys = 64;                 // keys per streamed tile, forward and dq
+
+}  // namespace
+
+// ---------------------------------------------------------------------- forward
+
+template <int DT>
+__global__ void __launch_bounds__(kAttThreads, 2) attention_forward_kernel(const AttentionArgs a)
+{
+    constexpr int kTile = kKeys * DT * 2;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kTile];
+    int t, head;
+    deal(blockIdx.x, a.hq, t, head);
+    const Place pl = find_tile(a, a.tiles - 1 - t, 0);     // a sequence's last (longest) tiles first
+    if (!pl.any) return;
+    const int lane = threadIdx.x & 63, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+    const int khead = head / (a.hq / a.hk);
+
+    const int q_wave = pl.first + wave * 32, qi = q_wave + (lane & 31);
+    const bool mine = qi < pl.nq;
+    const int shift = pl.nk - pl.nq;
+    // keys seen: by this lane's query, by the wave's first and last, by the workgroup's last
+    const int see = a.causal ? min(pl.nk, qi + shift + 1) : pl.nk;
+    const int see_first = a.causal ? min(pl.nk, q_wave + shift + 1) : pl.nk;
+    const int see_last = a.causal ? min(pl.nk, q_wave + 31 + shift + 1) : pl.nk;
+    const int end = a.causal ? min(pl.nk, min(pl.first + kOwn, pl.nq) + shift) : pl.nk;
+    const int steps = end > 0 ? (end + kKeys - 1) / kKeys : 0;
+
+    Frag q[DT / 16];
+    load_own<DT>(q, a.q + (int64_t)(pl.q0 + qi) * a.q_row + (int64_t)head * a.q_head, a.d, mine);
+
+    Stream<DT, kKeys> ks, vs;
+    ks.init(a.k + (int64_t)pl.k0 * a.k_row + (int64_t)khead * a.k_head, a.k_row, pl.nk, a.d);
+    vs.init(a.v + (int64_t)pl.k0 * a.v_row + (int64_t)khead * a.v_head, a.v_row, pl.nk, a.d);
+    Tile<DT> tile;
+    tile.init(lds0);
+
+    const float c = a.scale * kLog2e;
+    const float far = 8.0f / c;           // scores may pass the running maximum by 2^8 before a rescale
+    af32x16 o[DT / 32];
+#pragma unroll
+    for (int db = 0; db < DT / 32; ++db) o[db] = af32x16{0};
+    float m = -kInf, mc = 0.0f, l = 0.0f;
+
+    if (steps > 0) {
+        ks.issue(0, lds0, wave);
+        vs.issue(0, lds0 + kTile, wave);
+    }
+    for (int s = 0; s < steps; ++s) {
+        const uint32_t at = (uint32_t)(s & 1) * 2 * kTile;
+        __builtin_amdgcn_s_waitcnt(0x0F70);                // this wave's loads of tile s have landed
+        __syncthreads();                                   // everyone's; tile s - 1 is read
+        if (s + 1 < steps) {
+            const uint32_t to = lds0 + (uint32_t)((s + 1) & 1) * 2 * kTile;
+            ks.issue((s + 1) * kKeys, to, wave);
+            vs.issue((s + 1) * kKeys, to + kTile, wave);
+        }
+        const int j0 = s * kKeys;
+        if (j0 >= see_last) continue;                      // nothing of this tile is seen by the wave
+        af32x16 p[2] = {af32x16{0}, af32x16{0}};
+#pragma unroll
+        for (int ch = 0; ch < DT / 16; ++ch)
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) p[kb] = mma(tile.rows(at, kb, ch), q[ch], p[kb]);
+        if (j0 + kKeys > see_first) {
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (j0 + 32 * kb + 8 * (i / 4) + 4 * h + i % 4 >= see) p[kb][i] = -kInf;
+        }
+        float top = -kInf;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, p[kb][i]);
+        top = fmaxf(top, partner(top));
+        if (__any(top > m + far)) {                        // m = -inf: any seen key
+            const float up = fmaxf(m, top);
+            const float use = up == -kInf ? 0.0f : up;
+            const float by = __builtin_amdgcn_exp2f((m - use) * c);
+            m = up;
+            mc = use * c;
+            l *= by;
+#pragma unroll
+            for (int db = 0; db < DT / 32; ++db)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[db][i] *= by;
+        }
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                p[kb][i] = __builtin_amdgcn_exp2f(fmaf(p[kb][i], c, -mc));
+                l += p[kb][i];
+            }
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            Frag f[2];
+            to_operands(p[kb], f);
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+                for (int db = 0; db < DT / 32; ++db)
+                    o[db] = mma(tile.cols(at + kTile, kb, ch, db), f[ch], o[db]);
+        }
+    }
+
+    l += partner(l);
+    const float by = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // a NaN sum stays NaN
+    const uint32_t top = store_own<DT>(o, by, a.out + (int64_t)(pl.q0 + qi) * a.out_row + (int64_t)head * a.out_head,
+                                       a.d, mine);
+    if (mine && h == 0)
+        a.lse[(int64_t)head * a.tq + pl.q0 + qi] = l == 0.0f ? -kInf : (mc + __builtin_amdgcn_logf(l)) * kLn2;
+    if (a.absmax) block_max_to_global(top, a.absmax);
+}
+
+// ---------------------------------------------------------------------- backward
+
+// stats[0][head][token] = lse in powers of two (+inf where the row is empty, so that
+// every p of it is 0), stats[1][head][token] = delta.  16 lanes per (token, head).
+__global__ void __launch_bounds__(256) attention_delta_kernel(const AttentionArgs a)
+{
+    const int64_t unit = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    const int part = threadIdx.x & 15;
+    const int64_t all = (int64_t)a.tq * a.hq;
+    const int token = (int)(unit / a.hq), head = (int)(unit % a.hq);
+    float t = 0.0f;
+    if (unit < all && part * 8 < a.d) {
+        const uint4 o = *reinterpret_cast<const uint4*>(a.out + (int64_t)token * a.out_row + (int64_t)head * a.out_head + part * 8);
+        const uint4 g = *reinterpret_cast<const uint4*>(a.dout + (int64_t)token * a.dout_row + (int64_t)head * a.dout_head + part * 8);
+        const uint32_t ow[4] = {o.x, o.y, o.z, o.w}, gw[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t = fmaf(bf16_lo(ow[i]), bf16_lo(gw[i]), fmaf(bf16_hi(ow[i]), bf16_hi(gw[i]), t));
+    }
+#pragma unroll
+    for (int off = 8; off >= 1; off >>= 1) t += __shfl_xor(t, off, 16);
+    if (unit < all && part == 0) {
+        const int64_t at = (int64_t)head * a.tq + token;
+        const float lse = a.lse[at];
+        a.stats[at] = lse == -kInf ? kInf : lse * kLog2e;
+        a.stats[all + at] = t;
+    }
+}
+
+// dq: 32 queries per wave, keys and values streamed.
+template <int DT>
+__global__ void __launch_bounds__(kAttThreads, 2) attention_dq_kernel(const AttentionArgs a)
+{
+    constexpr int kTile = kKeys * DT * 2;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kTile];
+    int t, head;
+    deal(blockIdx.x, a.hq, t, head);
+    const Place pl = find_tile(a, a.tiles - 1 - t, 0);
+    if (!pl.any) return;
+    const int lane = threadIdx.x & 63, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+    const int khead = head / (a.hq / a.hk);
+
+    const int q_wave = pl.first + wave * 32, qi = q_wave + (lane & 31);
+    const bool mine = qi < pl.nq;
+    const int shift = pl.nk - pl.nq;
+    const int see = a.causal ? min(pl.nk, qi + shift + 1) : pl.nk;
+    const int see_first = a.causal ? min(pl.nk, q_wave + shift + 1) : pl.nk;
+    const int see_last = a.causal ? min(pl.nk, q_wave + 31 + shift + 1) : pl.nk;
+    const int end = a.causal ? min(pl.nk, min(pl.first + kOwn, pl.nq) + shift) : pl.nk;
+    const int steps = end > 0 ? (end + kKeys - 1) / kKeys : 0;
+
+    Frag q[DT / 16], g[DT / 16];
+    load_own<DT>(q, a.q + (int64_t)(pl.q0 + qi) * a.q_row + (int64_t)head * a.q_head, a.d, mine);
+    load_own<DT>(g, a.dout + (int64_t)(pl.q0 + qi) * a.dout_row + (int64_t)head * a.dout_head, a.d, mine);
+    float lse = kInf, delta = 0.0f;
+    if (mine) {
+        const int64_t at = (int64_t)head * a.tq + pl.q0 + qi;
+        lse = a.stats[at];
+        delta = a.stats[(int64_t)a.tq * a.hq + at];
+    }
+
+    Stream<DT, kKeys> ks, vs;
+    ks.init(a.k + (int64_t)pl.k0 * a.k_row + (int64_t)khead * a.k_head, a.k_row, pl.nk, a.d);
+    vs.init(a.v + (int64_t)pl.k0 * a.v_row + (int64_t)khead * a.v_head, a.v_row, pl.nk, a.d);
+    Tile<DT> tile;
+    tile.init(lds0);
+    const float c = a.scale * kLog2e;
+    af32x16 dq[DT / 32];
+#pragma unroll
+    for (int db = 0; db < DT / 32; ++db) dq[db] = af32x16{0};
+
+    if (steps > 0) {
+        ks.issue(0, lds0, wave);
+        vs.issue(0, lds0 + kTile, wave);
+    }
+    for (int s = 0; s < steps; ++s) {
+        const uint32_t at = (uint32_t)(s & 1) * 2 * kTile;
+        __builtin_amdgcn_s_waitcnt(0x0F70);
+        __syncthreads();
+        if (s + 1 < steps) {
+            const uint32_t to = lds0 + (uint32_t)((s + 1) & 1) * 2 * kTile;
+            ks.issue((s + 1) * kKeys, to, wave);
+            vs.issue((s + 1) * kKeys, to + kTile, wave);
+        }
+        const int j0 = s * kKeys;
+        if (j0 >= see_last) continue;
+        const bool masked = j0 + kKeys > see_first;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            af32x16 p = af32x16{0}, dp = af32x16{0};
+#pragma unroll
+            for (int ch = 0; ch < DT / 16; ++ch) {
+                p = mma(tile.rows(at, kb, ch), q[ch], p);
+                dp = mma(tile.rows(at + kTile, kb, ch), g[ch], dp);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                p[i] = __builtin_amdgcn_exp2f(fmaf(p[i], c, -lse));
+                dp[i] = p[i] * (dp[i] - delta);
+            }
+            if (masked) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (j0 + 32 * kb + 8 * (i / 4) + 4 * h + i % 4 >= see) dp[i] = 0.0f;
+            }
+            Frag f[2];
+            to_operands(dp, f);
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+                for (int db = 0; db < DT / 32; ++db) dq[db] = mma(tile.cols(at, kb, ch, db), f[ch], dq[db]);
+        }
+    }
+    const uint32_t top = store_own<DT>(dq, a.scale, a.dq + (int64_t)(pl.q0 + qi) * a.dq_row + (int64_t)head * a.dq_head,
+                                       a.d, mine);
+    if (a.absmax) block_max_to_global(top, a.absmax);
+}
+
+constexpr int kQueries = 32;              // queries per streamed tile, dk/dv
+
+// dk, dv: 32 keys per wave; the queries of every head that shares the key head are
+// streamed, with their dout, lse and delta.  A wave's keys stay in registers; its
+// values are read from a third, fixed tile in LDS (keeping them in registers too
+// would leave the two accumulators no room at two waves per SIMD).
+template <int DT>
+__global__ void __launch_bounds__(kAttThreads, 2) attention_dkv_kernel(const AttentionArgs a)
+{
+    constexpr int kTile = kQueries * DT * 2, kOwnTile = kOwn * DT * 2;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kOwnTile + 4 * kTile];
+    __shared__ float stat[2][2][kQueries];                // [stage][lse, delta][query]
+    int t, khead;
+    deal(blockIdx.x, a.hk, t, khead);
+    const Place pl = find_tile(a, t, 1);                   // a sequence's first keys are seen by most
+    if (!pl.any) return;
+    const int lane = threadIdx.x & 63, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)lds, ring = lds0 + kOwnTile;
+    const int group = a.hq / a.hk;
+
+    const int k_wave = pl.first + wave * 32, ki = k_wave + (lane & 31);
+    const bool mine = ki < pl.nk;
+    const int shift = pl.nk - pl.nq;
+    // the first query that sees this lane's key, the wave's first key, its last, the workgroup's first
+    const int from = a.causal ? max(0, ki - shift) : 0;
+    const int from_first = a.causal ? max(0, k_wave - shift) : 0;
+    const int from_last = a.causal ? max(0, k_wave + 31 - shift) : 0;
+    const int begin = a.causal ? max(0, pl.first - shift) / kQueries : 0;
+    const int last = (pl.nq + kQueries - 1) / kQueries;
+    const int per = max(0, last - begin), steps = per * group;
+
+    Frag k[DT / 16];
+    load_own<DT>(k, a.k + (int64_t)(pl.k0 + ki) * a.k_row + (int64_t)khead * a.k_head, a.d, mine);
+    Tile<DT> own, tile;
+    own.init(lds0 + wave * 32 * DT * 2);
+    tile.init(ring);
+    Stream<DT, kQueries> qs, gs;
+    qs.init(a.q + (int64_t)pl.q0 * a.q_row, a.q_row, pl.nq, a.d);
+    gs.init(a.dout + (int64_t)pl.q0 * a.dout_row, a.dout_row, pl.nq, a.d);
+    const uint8_t* q_base = qs.base;
+    const uint8_t* g_base = gs.base;
+
+    af32x16 dk[DT / 32], dv[DT / 32];
+#pragma unroll
+    for (int db = 0; db < DT / 32; ++db) dk[db] = dv[db] = af32x16{0};
+    const float c = a.scale * kLog2e;
+
+    // step s: query tile begin + s % per of head khead * group + s / per
+    auto issue = [&](int s) {
+        const int head = khead * group + s / per, row0 = (begin + s % per) * kQueries;
+        const uint32_t to = ring + (uint32_t)(s & 1) * 2 * kTile;
+        qs.base = q_base + (int64_t)head * a.q_head * 2;
+        gs.base = g_base + (int64_t)head * a.dout_head * 2;
+        qs.issue(row0, to, wave);
+        gs.issue(row0, to + kTile, wave);
+    };
+    auto fetch_stat = [&](int s) {                         // lanes 0-31: lse, 32-63: delta, of wave 0
+        const int head = khead * group + s / per, row = (begin + s % per) * kQueries + (lane & 31);
+        float v = h ? 0.0f : kInf;
+        if (row < pl.nq) v = a.stats[(int64_t)h * a.tq * a.hq + (int64_t)head * a.tq + pl.q0 + row];
+        return v;
+    };
+
+    float next = 0.0f;
+    if (steps > 0) {
+        Stream<DT, kOwn> vs;
+        vs.init(a.v + (int64_t)pl.k0 * a.v_row + (int64_t)khead * a.v_head, a.v_row, pl.nk, a.d);
+        if (wave == 0) next = fetch_stat(0);
+        vs.issue(pl.first, lds0, wave);
+        issue(0);
+    }
+    for (int s = 0; s < steps; ++s) {
+        const uint32_t at = (uint32_t)(s & 1) * 2 * kTile;
+        if (wave == 0) stat[s & 1][h][lane & 31] = next;
+        __builtin_amdgcn_s_waitcnt(0x0F70);
+        __syncthreads();
+        if (s + 1 < steps) {
+            if (wave == 0) next = fetch_stat(s + 1);
+            issue(s + 1);
+        }
+        const int i0 = (begin + s % per) * kQueries;
+        if (i0 + kQueries <= from_first) continue;         // no query of the tile sees a key of the wave
+        af32x16 p = af32x16{0}, dp = af32x16{0};
+#pragma unroll
+        for (int ch = 0; ch < DT / 16; ++ch) {
+            p = mma(tile.rows(at, 0, ch), k[ch], p);
+            dp = mma(tile.rows(at + kTile, 0, ch), own.rows(0, 0, ch), dp);
+        }
+        const bool masked = i0 < from_last || k_wave + 32 > pl.nk;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const float4 ls = *reinterpret_cast<const float4*>(&stat[s & 1][0][8 * b + 4 * h]);
+            const float4 de = *reinterpret_cast<const float4*>(&stat[s & 1][1][8 * b + 4 * h]);
+            const float lsv[4] = {ls.x, ls.y, ls.z, ls.w}, dev[4] = {de.x, de.y, de.z, de.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 4 * b + e;
+                p[i] = __builtin_amdgcn_exp2f(fmaf(p[i], c, -lsv[e]));
+                dp[i] = p[i] * (dp[i] - dev[e]);
+            }
+        }
+        if (masked) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (!mine || i0 + 8 * (i / 4) + 4 * h + i % 4 < from) p[i] = dp[i] = 0.0f;
+        }
+        Frag f[2], e[2];
+        to_operands(p, f);
+        to_operands(dp, e);
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+            for (int db = 0; db < DT / 32; ++db) {
+                dv[db] = mma(tile.cols(at + kTile, 0, ch, db), f[ch], dv[db]);
+                dk[db] = mma(tile.cols(at, 0, ch, db), e[ch], dk[db]);
+            }
+    }
+    uint32_t top = store_own<DT>(dk, a.scale, a.dk + (int64_t)(pl.k0 + ki) * a.dk_row + (int64_t)khead * a.dk_head, a.d, mine);
+    top = max(top, store_own<DT>(dv, 1.0f, a.dv + (int64_t)(pl.k0 + ki) * a.dv_row + (int64_t)khead * a.dv_head, a.d, mine));
+    if (a.absmax) block_max_to_global(top, a.absmax);
+}
+
+// ---------------------------------------------------------------------- launches
+
+// At most this many tiles: each sequence adds less than one to total / kOwn.
+static int64_t tile_bound(int64_t total, int batch) { return total / kOwn + batch; }
+
+bool attention_grid_ok(int64_t tokens, int batch, int heads)
+{
+    return tile_bound(tokens, batch) * heads <= 0x7FFFFFFF;
+}
+
+hipError_t launch_attention_forward(const AttentionArgs& args, hipStream_t stream)
+{
+    AttentionArgs a = args;
+    a.tiles = (int)tile_bound(a.tq, a.batch);
+    const dim3 grid((unsigned)(a.tiles * a.hq));
+    if (a.d <= 64) return launch(attention_forward_kernel<64>, grid, dim3(kAttThreads), stream, a);
+    return launch(attention_forward_kernel<128>, grid, dim3(kAttThreads), stream, a);
+}
+
+hipError_t launch_attention_backward(const AttentionArgs& args, hipStream_t stream)
+{
+    AttentionArgs a = args;
+    const int64_t units = (int64_t)a.tq * a.hq;
+    hipError_t e = launch(attention_delta_kernel, dim3((unsigned)((units + 15) / 16)), dim3(256), stream, a);
+    if (e != hipSuccess) return e;
+    a.tiles = (int)tile_bound(a.tk, a.batch);
+    const dim3 grid_k((unsigned)(a.tiles * a.hk));
+    e = a.d <= 64 ? launch(attention_dkv_kernel<64>, grid_k, dim3(kAttThreads), stream, a)
+                  : launch(attention_dkv_kernel<128>, grid_k, dim3(kAttThreads), stream, a);
+    if (e != hipSuccess) return e;
+    a.tiles = (int)tile_bound(a.tq, a.batch);
+    const dim3 grid_q((unsigned)(a.tiles * a.hq));
+    if (a.d <= 64) return launch(attention_dq_kernel<64>, grid_q, dim3(kAttThreads), stream, a);
+    return launch(attention_dq_kernel<128>, grid_q, dim3(kAttThreads), stream, a);
+}
+
+}  // namespace fp8k

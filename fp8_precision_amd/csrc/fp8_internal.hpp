@@ -138,6 +138,24 @@ hipError_t launch_norm_backward(const void* dy, const void* x, bool f32, const v
                                 const float* rstd, const void* dres, bool rms, int64_t rows, int64_t cols, void* dx,
                                 float* dw, float* db, float* partial, hipStream_t stream);
 
+// Attention over packed sequences (attention.hip).  Strides in elements: _row between
+// tokens, _head between heads; cu_* int32 [batch + 1] or null (one sequence).
+struct AttentionArgs {
+    const uint16_t *q, *k, *v, *dout;
+    uint16_t *out, *dq, *dk, *dv;         // out is read by the backward pass
+    float* lse;                           // [hq, tq]
+    float* stats;                         // backward: 2 * hq * tq fp32
+    const int *cu_q, *cu_k;
+    uint32_t* absmax;                     // or null
+    int64_t q_row, k_row, v_row, out_row, dout_row, dq_row, dk_row, dv_row;
+    int64_t q_head, k_head, v_head, out_head, dout_head, dq_head, dk_head, dv_head;
+    int tq, tk, hq, hk, d, batch, causal, tiles;
+    float scale;
+};
+bool attention_grid_ok(int64_t tokens, int batch, int heads);
+hipError_t launch_attention_forward(const AttentionArgs& args, hipStream_t stream);
+hipError_t launch_attention_backward(const AttentionArgs& args, hipStream_t stream);
+
 // dst[0, bytes) = src[0, bytes): the streaming-copy reference (bytes % 16 == 0, both 16-byte aligned).
 hipError_t launch_stream_copy(const void* src, void* dst, int64_t bytes, hipStream_t stream);
 

@@ -546,6 +546,71 @@ fp8_status fp8_norm_backward(const void* dy, const void* s, fp8_stream_type type
                              int64_t workspace_bytes, hipStream_t stream);
 
 /*
+ * Attention over packed sequences.  Query token i of a sequence with nq queries
+ * and nk keys sees the keys j < nk and, causal, j <= i + nk - nq (its last query
+ * sees every key).  With s = scale q . k,
+ *   p_ij = exp(s_ij) / sum over the keys seen,  out_i = sum_j p_ij v_j,
+ *   lse_i = log sum_j exp(s_ij)
+ * A query that sees nothing (an empty key side, or causal with fewer keys than
+ * queries) has out = 0, lse = -inf and no gradient.  Query head h uses key head
+ * h / (heads_q / heads_k).
+ *
+ * A tensor is [tokens, heads, head_dim] bf16 with its own strides, so q, k and v
+ * can be the slices of one projection's output, and dq, dk, dv the slices of its
+ * gradient.
+ */
+typedef struct fp8_head_tensor {
+    void* data;            /* 16-byte aligned */
+    int64_t token_stride;  /* elements, a multiple of 8, >= head_dim, < 2^22 */
+    int64_t head_stride;   /* elements, a multiple of 8, >= 0 */
+} fp8_head_tensor;
+
+typedef struct fp8_attention_shape {
+    int64_t tokens_q, tokens_k;         /* packed tokens, 1 .. 2^31 - 1 */
+    int64_t heads_q, heads_k;           /* heads_q a multiple of heads_k */
+    int64_t head_dim;                   /* a multiple of 8, 8 .. 128 */
+    int64_t batch;                      /* sequences; 1 without the bounds below */
+    const int32_t *bounds_q, *bounds_k; /* device int32 [batch + 1]: sequence b is tokens
+                                           bounds[b] .. bounds[b + 1] - 1 (from 0, ascending, ending
+                                           at the token count; equal neighbours: an empty sequence);
+                                           both NULL: one sequence of all tokens */
+    int causal;                         /* 0 or 1 */
+    float scale;                        /* > 0, finite */
+} fp8_attention_shape;
+
+/*
+ *   out     as q;  lse  fp32 [heads_q, tokens_q]
+ *   absmax  fp32 scalar or NULL: becomes max(*absmax, max |out|), out as stored
+ * Rows of out and lse that belong to no sequence are not written.  Bounds outside
+ * [0, tokens] are held to it; no byte outside the tensors is read or written.
+ * Probabilities are rounded to bf16 for the product with v (sums and the softmax
+ * stay in fp32).  A NaN or infinity in v may reach every query of its sequence.
+ */
+fp8_status fp8_attention_forward(const fp8_attention_shape* shape, const fp8_head_tensor* q,
+                                 const fp8_head_tensor* k, const fp8_head_tensor* v, const fp8_head_tensor* out,
+                                 float* lse, float* absmax, hipStream_t stream);
+
+/*
+ * Gradients of q, k and v (of a shared key head: the sum over its query heads).
+ * The probabilities are computed again from q, k and lse.  With
+ *   delta_i = dout_i . out_i,  dp_ij = dout_i . v_j,  ds_ij = p_ij (dp_ij - delta_i):
+ *   dv_j = sum_i p_ij dout_i,  dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i
+ *
+ *   dout    as q;  out, lse  from the forward;  dq, dk, dv  as q, k, v
+ *   absmax  fp32 scalar or NULL: becomes max(*absmax, max |dq|, max |dk|, max |dv|), as stored
+ *   workspace, workspace_bytes   device memory, 16-byte aligned, of at least the size
+ *           that fp8_attention_backward_workspace gives for the shape
+ * No output may overlap an input or another output (outputs may interleave: slices
+ * of one tensor with one token stride).
+ */
+fp8_status fp8_attention_backward_workspace(const fp8_attention_shape* shape, int64_t* bytes);
+fp8_status fp8_attention_backward(const fp8_attention_shape* shape, const fp8_head_tensor* dout,
+                                  const fp8_head_tensor* q, const fp8_head_tensor* k, const fp8_head_tensor* v,
+                                  const fp8_head_tensor* out, const float* lse, const fp8_head_tensor* dq,
+                                  const fp8_head_tensor* dk, const fp8_head_tensor* dv, float* absmax,
+                                  void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/*
  * Measurement reference, not a step of the FP8 method: a plain device copy
  * dst[0, bytes) = src[0, bytes), built like the streaming kernels above
  * (16-byte vectors, non-temporal loads, the launch shape at which a copy
