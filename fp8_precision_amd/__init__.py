@@ -9,5 +9,5 @@ from ._lib import (  # noqa: F401
     gemm_backward,
     gemm_dgrad_mn, gemm_wgrad_mn, gemm_backward_mn, stream_copy, mx_quantize, mx_gemm_fwd,
     mx_swiglu_requant, mx_quantize_t, mx_quantize_both, mx_gemm_backward,
-    norm, norm_backward, attention, attention_backward,
+    norm, norm_backward, attention, attention_backward, linear_cross_entropy, linear_cross_entropy_backward,
 )

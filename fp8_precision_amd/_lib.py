@@ -56,6 +56,10 @@ _SIGS = {
     "fp8_attention_forward": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "fp8_attention_backward_workspace": (_i32, [_vp, _vp]),
     "fp8_attention_backward": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "fp8_linear_cross_entropy_forward_workspace": (_i32, [_i64, _i64, _i64, _vp]),
+    "fp8_linear_cross_entropy_forward": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp]),
+    "fp8_linear_cross_entropy_backward_workspace": (_i32, [_i64, _i64, _i64, _vp]),
+    "fp8_linear_cross_entropy_backward": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -801,6 +805,45 @@ def attention_backward(dout, q, k, v, out, lse, cu_q=None, cu_k=None, causal: bo
          (dout, q, k, v, out, lse, cu_q, cu_k, dq, dk, dv, absmax, ws), ctypes.byref(shape), hg, hq, hk, hv, ho,
          _ptr(lse), hdq, hdk, hdv, _ptr(absmax), _ptr(ws), ws.numel())
     return dq, dk, dv
+
+
+def _head(x, weight, target):
+    """The sizes of a linear head's loss, its inputs checked: (tokens, vocab, dim)."""
+    _dev_tensor(x, "x", torch.bfloat16)
+    _dev_tensor(weight, "weight", torch.bfloat16)
+    if x.dim() != 2 or weight.dim() != 2 or x.shape[1] != weight.shape[1]:
+        raise ValueError("x must be [tokens, dim] and weight [vocab, dim]")
+    _vector(target, "target", x.shape[0], torch.int64)
+    return x.shape[0], weight.shape[0], x.shape[1]
+
+
+def linear_cross_entropy(x, weight, target, loss=None, lse=None):
+    """Cross entropy of the logits x weight^T (x bf16 [tokens, dim], weight bf16
+    [vocab, dim], target int64 [tokens]) without storing them.  A token whose target is
+    outside [0, vocab) has loss 0.  Returns (loss fp32 [tokens], lse fp32 [tokens])."""
+    tokens, vocab, dim = _head(x, weight, target)
+    loss = _out(loss, "loss", (tokens,), torch.float32, x.device)
+    lse = _out(lse, "lse", (tokens,), torch.float32, x.device)
+    ws = _workspace("fp8_linear_cross_entropy_forward_workspace", x.device, tokens, vocab, dim)
+    _run("fp8_linear_cross_entropy_forward", _lib.fp8_linear_cross_entropy_forward, (x, weight, target, loss, lse, ws),
+         _ptr(x), _ptr(weight), _ptr(target), tokens, vocab, dim, _ptr(loss), _ptr(lse), _ptr(ws), ws.numel())
+    return loss, lse
+
+
+def linear_cross_entropy_backward(dloss, x, weight, target, lse, dx=None, dweight=None):
+    """Gradients of ``linear_cross_entropy`` for dloss fp32 [tokens] and the forward's
+    lse: (dx bf16 [tokens, dim], dweight bf16 [vocab, dim]).  The logits are computed
+    again in pieces of the vocabulary; their gradient is held in bf16, a piece at a time."""
+    tokens, vocab, dim = _head(x, weight, target)
+    _vector(dloss, "dloss", tokens, torch.float32)
+    _vector(lse, "lse", tokens, torch.float32)
+    dx = _out(dx, "dx", (tokens, dim), torch.bfloat16, x.device)
+    dweight = _out(dweight, "dweight", (vocab, dim), torch.bfloat16, x.device)
+    ws = _workspace("fp8_linear_cross_entropy_backward_workspace", x.device, tokens, vocab, dim)
+    _run("fp8_linear_cross_entropy_backward", _lib.fp8_linear_cross_entropy_backward,
+         (dloss, x, weight, target, lse, dx, dweight, ws), _ptr(dloss), _ptr(x), _ptr(weight), _ptr(target), _ptr(lse),
+         tokens, vocab, dim, _ptr(dx), _ptr(dweight), _ptr(ws), ws.numel())
+    return dx, dweight
 
 
 def stream_copy(src: torch.Tensor, dst: torch.Tensor) -> torch.Tensor:

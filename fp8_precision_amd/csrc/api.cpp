@@ -875,6 +875,87 @@ fp8_status fp8_attention_backward(const fp8_attention_shape* shape, const fp8_he
     return FP8_OK;
 }
 
+static fp8_status loss_shape(const char* call, int64_t tokens, int64_t vocab, int64_t dim)
+{
+    char msg[160];
+    if (tokens < 1 || vocab < 1 || dim < 1) {
+        std::snprintf(msg, sizeof(msg), "%s: tokens, vocab and dim must be positive", call);
+        return fail(FP8_ERR_INVALID, msg);
+    }
+    if (tokens >= (1 << 24) || vocab >= (1 << 24) || dim > 65536 || dim % 8) {
+        std::snprintf(msg, sizeof(msg), "%s: tokens and vocab below 2^24, dim a multiple of 8 and at most 65536", call);
+        return fail(FP8_ERR_UNSUPPORTED, msg);
+    }
+    return FP8_OK;
+}
+
+fp8_status fp8_linear_cross_entropy_forward_workspace(int64_t tokens, int64_t vocab, int64_t dim, int64_t* bytes)
+{
+    t_last_error.clear();
+    fp8_status st = loss_shape("fp8_linear_cross_entropy_forward_workspace", tokens, vocab, dim);
+    if (st != FP8_OK) return st;
+    if (!bytes) return fail(FP8_ERR_INVALID, "fp8_linear_cross_entropy_forward_workspace: null pointer");
+    *bytes = fp8k::loss_forward_workspace(tokens, vocab);
+    return FP8_OK;
+}
+
+fp8_status fp8_linear_cross_entropy_forward(const void* x, const void* weight, const int64_t* target, int64_t tokens,
+                                            int64_t vocab, int64_t dim, float* loss, float* lse, void* workspace,
+                                            int64_t workspace_bytes, hipStream_t stream)
+{
+    t_last_error.clear();
+    const char* call = "fp8_linear_cross_entropy_forward";
+    fp8_status st = loss_shape(call, tokens, vocab, dim);
+    if (st != FP8_OK) return st;
+    if (!x || !weight || !target || !loss || !lse || !workspace)
+        return fail(FP8_ERR_INVALID, "fp8_linear_cross_entropy_forward: null pointer");
+    if (workspace_bytes < fp8k::loss_forward_workspace(tokens, vocab))
+        return fail(FP8_ERR_INVALID, "fp8_linear_cross_entropy_forward: workspace too small");
+    const Range in[] = {{x, 2 * tokens * dim}, {weight, 2 * vocab * dim}, {target, 8 * tokens}};
+    const Range out[] = {{loss, 4 * tokens}, {lse, 4 * tokens}, {workspace, workspace_bytes}};
+    if (outputs_overlap(out, 3, in, 3)) return fail(FP8_ERR_INVALID, "fp8_linear_cross_entropy_forward: overlapping buffers");
+    if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(target, 8) || !aligned(loss, 4) || !aligned(lse, 4) ||
+        !aligned(workspace, 16))
+        return fail(FP8_ERR_UNSUPPORTED, "fp8_linear_cross_entropy_forward: misaligned pointer");
+    hipError_t e = fp8k::launch_loss_forward(x, weight, target, tokens, vocab, dim, loss, lse, workspace, stream);
+    if (e != hipSuccess) return fail_hip(call, e);
+    return FP8_OK;
+}
+
+fp8_status fp8_linear_cross_entropy_backward_workspace(int64_t tokens, int64_t vocab, int64_t dim, int64_t* bytes)
+{
+    t_last_error.clear();
+    fp8_status st = loss_shape("fp8_linear_cross_entropy_backward_workspace", tokens, vocab, dim);
+    if (st != FP8_OK) return st;
+    if (!bytes) return fail(FP8_ERR_INVALID, "fp8_linear_cross_entropy_backward_workspace: null pointer");
+    *bytes = fp8k::loss_backward_workspace(tokens, vocab, dim);
+    return FP8_OK;
+}
+
+fp8_status fp8_linear_cross_entropy_backward(const float* dloss, const void* x, const void* weight,
+                                             const int64_t* target, const float* lse, int64_t tokens, int64_t vocab,
+                                             int64_t dim, void* dx, void* dweight, void* workspace,
+                                             int64_t workspace_bytes, hipStream_t stream)
+{
+    t_last_error.clear();
+    const char* call = "fp8_linear_cross_entropy_backward";
+    fp8_status st = loss_shape(call, tokens, vocab, dim);
+    if (st != FP8_OK) return st;
+    if (!dloss || !x || !weight || !target || !lse || !dx || !dweight || !workspace)
+        return fail(FP8_ERR_INVALID, "fp8_linear_cross_entropy_backward: null pointer");
+    if (workspace_bytes < fp8k::loss_backward_workspace(tokens, vocab, dim))
+        return fail(FP8_ERR_INVALID, "fp8_linear_cross_entropy_backward: workspace too small");
+    const Range in[] = {{dloss, 4 * tokens}, {x, 2 * tokens * dim}, {weight, 2 * vocab * dim}, {target, 8 * tokens}, {lse, 4 * tokens}};
+    const Range out[] = {{dx, 2 * tokens * dim}, {dweight, 2 * vocab * dim}, {workspace, workspace_bytes}};
+    if (outputs_overlap(out, 3, in, 5)) return fail(FP8_ERR_INVALID, "fp8_linear_cross_entropy_backward: overlapping buffers");
+    if (!aligned(dloss, 4) || !aligned(x, 16) || !aligned(weight, 16) || !aligned(target, 8) || !aligned(lse, 4) ||
+        !aligned(dx, 16) || !aligned(dweight, 16) || !aligned(workspace, 16))
+        return fail(FP8_ERR_UNSUPPORTED, "fp8_linear_cross_entropy_backward: misaligned pointer");
+    hipError_t e = fp8k::launch_loss_backward(dloss, x, weight, target, lse, tokens, vocab, dim, dx, dweight, workspace, stream);
+    if (e != hipSuccess) return fail_hip(call, e);
+    return FP8_OK;
+}
+
 fp8_status fp8_stream_copy(const void* src, void* dst, int64_t bytes, hipStream_t stream)
 {
     t_last_error.clear();

@@ -156,6 +156,15 @@ bool attention_grid_ok(int64_t tokens, int batch, int heads);
 hipError_t launch_attention_forward(const AttentionArgs& args, hipStream_t stream);
 hipError_t launch_attention_backward(const AttentionArgs& args, hipStream_t stream);
 
+// Cross entropy of a linear head (loss.hip): x [T, D], w [V, D].
+int64_t loss_forward_workspace(int64_t T, int64_t V);
+int64_t loss_backward_workspace(int64_t T, int64_t V, int64_t D);
+hipError_t launch_loss_forward(const void* x, const void* w, const int64_t* target, int64_t T, int64_t V, int64_t D,
+                               float* loss, float* lse, void* workspace, hipStream_t stream);
+hipError_t launch_loss_backward(const float* dloss, const void* x, const void* w, const int64_t* target,
+                                const float* lse, int64_t T, int64_t V, int64_t D, void* dx, void* dw,
+                                void* workspace, hipStream_t stream);
+
 // dst[0, bytes) = src[0, bytes): the streaming-copy reference (bytes % 16 == 0, both 16-byte aligned).
 hipError_t launch_stream_copy(const void* src, void* dst, int64_t bytes, hipStream_t stream);
 

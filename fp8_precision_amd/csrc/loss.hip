@@ -1,0 +1,668 @@
+// loss.hip -- cross entropy of a linear head over a large vocabulary, without ever
+// holding the logits, for gfx950.
+//
+// With x [T, D], w [V, D] (bf16), z = x w^T and a target per token,
+//   lse_t = log sum_v exp(z_tv),   loss_t = lse_t - z_t,target(t)
+// and backward, g_tv = dloss_t (exp(z_tv - lse_t) - [v = target(t)]),
+//   dx = g w,   dw = g^T x.
+// A token whose target lies outside [0, V) has no target: loss 0 and no gradient.
+//
+// Forward: the logits' product with the row statistics taken in its epilogue -- the
+// maximum and the sum of exponentials of the wave's columns of each row -- and a
+// second, small launch that joins them.  Backward: the vocabulary is walked in
+// pieces; a piece's logits are computed again, turned into g (bf16) in the epilogue
+// and written to a workspace, from which the piece's dw and its share of dx are
+// taken.  dx is summed over the pieces in fp32.
+//
+// Bound by the matrix units (2 T V D operations forward, 6 T V D backward) except for
+// few tokens, where reading w bounds.  The product kernel: 256 columns by 256, 128 or
+// 64 rows per workgroup of 4 waves, one wave per SIMD; reduction steps of 64
+// elements in two LDS stages filled by 16-byte direct-to-LDS buffer loads issued a
+// step and a half ahead; v_mfma_f32_16x16x32_bf16 with fragments double-buffered in
+// registers across a barrier in the middle of a step; persistent workgroups in an
+// XCD-major walk that load the next tile's first stages before the epilogue.
+// Operands are read along the reduction ("K": x and w for the logits, g for dx) or
+// across it ("MN": w for dx, g and x for dw) through transposing LDS reads, so no
+// transposed copy of anything exists.  Rows, columns and reduction elements past an
+// operand's end read as zero (the buffer's size, or an offset outside it).
+//
+// g is rounded to bf16, as an operand of the matrix units; z, the statistics and every
+// sum stay in fp32.  The sums are formed in a fixed order: no atomics.
+#include "fp8_device.hpp"
+#include "fp8_internal.hpp"
+
+namespace fp8k {
+
+namespace {
+
+typedef __bf16 lb16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 lb16x2 __attribute__((ext_vector_type(2)));
+typedef float lf32x2 __attribute__((ext_vector_type(2)));
+typedef float lf32x4 __attribute__((ext_vector_type(4)));
+typedef short ls16x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int lu32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) ls16x4 lds_ls16x4;
+typedef __attribute__((address_space(3))) lu32x4 lds_lu32x4;
+
+constexpr float kLossLog2e = 1.44269504088896340736f;
+constexpr float kLossLn2 = 0.69314718055994530942f;
+constexpr float kLossInf = __builtin_inff();
+constexpr int kBN = 256;                  // columns of a tile
+constexpr int kStep = 64;                 // reduction elements of a step (128 bytes)
+constexpr int kOutside = (int)0x80000000; // an offset past every buffer's size
+
+// Fragment: 16 rows x 64 reduction elements; u[0] the step's first 32, u[1] the rest.
+union LossFrag {
+    lu32x4 u[2];
+    lb16x8 b[2];
+    ls16x4 s[4];
+};
+
+__device__ __forceinline__ uint32_t loss_pair(float a, float b)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(lf32x2{a, b}, lb16x2));
+}
+
+__device__ __forceinline__ void loss_to_lds(uint32_t voff, const lu32x4& desc, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+                 :
+                 : "v"(voff), "s"(desc), "s"(lds)
+                 : "memory", "m0");
+}
+
+__device__ __forceinline__ lu32x4 loss_desc(const uint8_t* base, int64_t bytes)
+{
+    const uint64_t b = (uint64_t)base;
+    const int64_t n = bytes < 0 ? 0 : bytes > 0x7FFFFFFF ? 0x7FFFFFFF : bytes;
+    lu32x4 d;
+    d[0] = __builtin_amdgcn_readfirstlane((uint32_t)b);
+    d[1] = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32) & 0xFFFFu);
+    d[2] = __builtin_amdgcn_readfirstlane((uint32_t)n);
+    d[3] = 0x00020000u;
+    return d;
+}
+
+// One operand: element (i, r) of the product's row (or column) i and reduction index r
+// at p + i * pitch + r (K) or p + r * pitch + i (MN).
+struct Side {
+    const uint16_t* p;
+    int64_t pitch;
+};
+
+// Loads of one operand's EXT rows (columns) of the tile for one wave.  The LDS image:
+//   K:  EXT rows of 128 bytes, 16-byte chunk c of row r at c ^ (r >> 1 & 7) ^ (r & 1) << 2;
+//   MN: 64 rows (reduction) of 2 EXT bytes, chunk c of row r at
+//       c ^ ((r & 3) << 1 | (r >> 3 & 1) << 3): a transposing read takes 32-byte pieces
+//       of 16 rows, which this spreads over all banks.
+template <bool MN, int EXT>
+struct Feed {
+    static constexpr int kLoads = EXT / 32;                  // 1 KB each
+    const uint8_t* base;
+    int64_t pitch, left;                                     // bytes; of the matrix from base on
+    uint32_t voff[MN ? 4 : 2];
+    int chunk[2];                                            // K: the lane's chunk for even and odd loads
+
+    __device__ __forceinline__ void init(const Side& s, int origin, int extent, int total_r, int r0, int wave, int lane)
+    {
+        pitch = s.pitch * 2;
+        if (!MN) {
+            base = reinterpret_cast<const uint8_t*>(s.p) + (int64_t)origin * pitch + (int64_t)r0 * 2;
+            left = (int64_t)(extent - origin) * pitch - (int64_t)r0 * 2;
+#pragma unroll
+            for (int par = 0; par < 2; ++par) {
+                const int r = wave * (EXT / 4) + par * 8 + (lane >> 3);
+                chunk[par] = (lane & 7) ^ ((r >> 1) & 7) ^ ((r & 1) << 2);
+                voff[par] = (uint32_t)(r * (int)pitch) + (uint32_t)chunk[par] * 16u;
+            }
+        } else {
+            static_assert(!MN || EXT == 256, "the MN image is laid out for 256 columns");
+            base = reinterpret_cast<const uint8_t*>(s.p) + (int64_t)r0 * pitch + (int64_t)origin * 2;
+            left = (int64_t)(total_r - r0) * pitch - (int64_t)origin * 2;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = wave * 16 + (i & 1) * 2 + (i >> 1) * 8 + (lane >> 5);
+                const int c = (lane & 31) ^ ((r & 3) << 1 | (r >> 3 & 1) << 3);
+                voff[i] = origin + c * 8 < extent ? (uint32_t)(r * (int)pitch) + (uint32_t)c * 16u : (uint32_t)kOutside;
+            }
+        }
+    }
+
+    // load ii of step kt (counted from r0); `in_step` elements of the step exist
+    __device__ __forceinline__ void issue(const lu32x4& desc, int ii, int in_step, uint32_t lds) const
+    {
+        uint32_t v;
+        if (!MN) {
+            v = voff[ii & 1] + (uint32_t)((ii >> 1) * 16) * (uint32_t)pitch;
+            v = chunk[ii & 1] * 8 < in_step ? v : (uint32_t)kOutside;
+        } else {
+            v = voff[(ii & 1) | (ii >> 2) << 1] + (uint32_t)((ii >> 1 & 1) * 4) * (uint32_t)pitch;
+            // an offset that is outside stays outside: 4 rows are far less than 2^31 bytes
+        }
+        loss_to_lds(v, desc, lds);
+    }
+    __device__ __forceinline__ lu32x4 desc(int kt) const
+    {
+        const int64_t on = MN ? (int64_t)kt * kStep * pitch : (int64_t)kt * kStep * 2;
+        return loss_desc(base + on, left - on);
+    }
+};
+
+// Rows 16 blk .. of an operand image at LDS address `at`.
+template <bool MN, int EXT>
+__device__ __forceinline__ LossFrag loss_frag(uint32_t at, int blk, int lane)
+{
+    LossFrag f;
+    if (!MN) {
+        const int r = blk * 16 + (lane & 15);
+        const int p = (lane >> 4) ^ ((r >> 1) & 7) ^ ((r & 1) << 2);
+        f.u[0] = *(const lds_lu32x4*)(uintptr_t)(at + r * 128 + p * 16);
+        f.u[1] = *(const lds_lu32x4*)(uintptr_t)(at + r * 128 + (p ^ 4) * 16);
+    } else {
+        constexpr int kRow = EXT * 2;
+        const int g = lane >> 4, l = lane & 15;
+        uint32_t base = at + (8 * g + (l >> 2)) * kRow +
+                        ((((l & 3) >> 1) ^ ((l >> 2) << 1 | (g & 1) << 3)) * 16) + (l & 1) * 8;
+        asm volatile("" : "+v"(base));    // one XOR per block instead of an address held per block
+        const uint32_t a = base ^ (uint32_t)(blk * 32);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f.s[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_ls16x4*)(uintptr_t)(a + ((i & 1) * 4 + (i >> 1) * 32) * kRow));
+    }
+    return f;
+}
+
+// What a launch's epilogue does with the tile's sums.
+enum { kStats = 0, kGrad = 1, kSum = 2, kStore = 3 };
+
+struct LossArgs {
+    Side a, b;
+    int P, Q, R;                          // rows, columns, reduction
+    int tiles_m, tiles_n, units;          // units: tiles * splits
+    int steps, per;                       // reduction steps in all and per split
+    // statistics and gradient
+    const int64_t* target;
+    const float* lse;
+    const float* dloss;
+    float2* stats;                        // [column block][T]: maximum, sum of exponentials
+    float* hit;                           // [T]: the target's logit
+    int v0, vocab;                        // the piece's first column in the vocabulary, and its size
+    // outputs
+    uint16_t* out;                        // bf16, pitch out_pitch: g, dw, or dx once complete
+    int64_t out_pitch;
+    int out_cols;                         // g: columns written (Q rounded up; those past Q get 0)
+    float* sum;                           // [splits][P][Q] fp32 partial dx
+    int first, last;                      // sum: nothing to add to yet; write bf16 to out
+};
+
+struct Unit {
+    int m0, n0, r0, kt, split;
+};
+
+}  // namespace
+
+// MI x NJ blocks of 16 x 16 per wave, GM x GN waves.
+template <int MI, int NJ, int GM, int GN, bool LA, bool LB, int EPI>
+__global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
+{
+    constexpr int BM = 16 * MI * GM;
+    static_assert(16 * NJ * GN == kBN && GM * GN == 4, "four waves cover 256 columns");
+    constexpr int kA = BM * 128, kStage = kA + kBN * 128;
+    constexpr int kLoads = BM / 32 + kBN / 32;
+    constexpr int kEpi = 16 * 16 * NJ * 2;                   // a wave's 16 rows of bf16
+    constexpr int kHalf = MI / 2;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kStage + 4 * kEpi];
+
+    const int G = gridDim.x;
+    int slot = blockIdx.x;
+    if (G % 8 == 0) slot = (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / GN, wn = wave % GN;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
+
+    auto unit_of = [&](int u) {
+        Unit w;
+        const int tiles = g.tiles_m * g.tiles_n;
+        w.split = u / tiles;
+        const int t = u - w.split * tiles;
+        // groups of 8 tile rows, each walked column by column: 32 neighbours are 8 x 4 tiles
+        const int group = t / (8 * g.tiles_n), in = t - group * 8 * g.tiles_n;
+        const int rows = min(8, g.tiles_m - group * 8);
+        w.m0 = (group * 8 + in % rows) * BM;
+        w.n0 = (in / rows) * kBN;
+        const int s0 = w.split * g.per;
+        w.r0 = s0 * kStep;
+        w.kt = min(g.steps - s0, g.per);
+        return w;
+    };
+
+    Feed<LA, BM> fa;
+    Feed<LB, kBN> fb;
+    lf32x4 acc[MI][NJ];
+    LossFrag bq[NJ], alo[kHalf], ahi[kHalf];
+
+    // loads idx of step kt (of the unit that fa, fb stand at) into stage `to`
+    auto issue_one = [&](const lu32x4& da, const lu32x4& db, uint32_t to, int in_step, int idx) {
+        if (idx < BM / 32)
+            fa.issue(da, idx, in_step, __builtin_amdgcn_readfirstlane(to + (wave * (BM / 32) + idx) * 1024));
+        else
+            fb.issue(db, idx - BM / 32, in_step,
+                     __builtin_amdgcn_readfirstlane(to + kA + (wave * (kBN / 32) + idx - BM / 32) * 1024));
+    };
+    auto start = [&](const Unit& w) {
+        fa.init(g.a, w.m0, g.P, g.R, w.r0, wave, lane);
+        fb.init(g.b, w.n0, g.Q, g.R, w.r0, wave, lane);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int kt = min(s, w.kt - 1);
+            const lu32x4 da = fa.desc(kt), db = fb.desc(kt);
+            const int in_step = g.R - w.r0 - kt * kStep;
+#pragma unroll
+            for (int idx = 0; idx < kLoads; ++idx) issue_one(da, db, lds0 + s * kStage, in_step, idx);
+        }
+    };
+    auto fma16 = [&](lf32x4& c, const LossFrag& a, const LossFrag& b) {
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.b[0], a.b[0], c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.b[1], a.b[1], c, 0, 0, 0);
+    };
+    // the first half of a step: A blocks 0 .. kHalf - 1, while the others are read
+    auto half0 = [&](uint32_t at) {
+#pragma unroll
+        for (int t = 0; t < kHalf * NJ; ++t) {
+            const int j = t / kHalf, i = t % kHalf;
+            fma16(acc[i][j], alo[i], bq[j]);
+            if (t % NJ == 1) ahi[t / NJ] = loss_frag<LA, BM>(at, wm * MI + kHalf + t / NJ, lane);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    // the second half: the next step's fragments replace those that are done with, and the
+    // step after next is loaded into this step's stage
+    auto half1 = [&](bool more, uint32_t cur, uint32_t nxt, const lu32x4& da, const lu32x4& db, int in_step) {
+#pragma unroll
+        for (int t = 0; t < kHalf * NJ; ++t) {
+            const int j = t / kHalf, i = t % kHalf;
+            fma16(acc[kHalf + i][j], ahi[i], bq[j]);
+            if (more) {
+                if (i == kHalf - 1) bq[j] = loss_frag<LB, kBN>(nxt + kA, wn * NJ + j, lane);
+                if (t % NJ == 1) alo[t / NJ] = loss_frag<LA, BM>(nxt, wm * MI + t / NJ, lane);
+#pragma unroll
+                for (int x = t * kLoads / (kHalf * NJ); x < (t + 1) * kLoads / (kHalf * NJ); ++x)
+                    issue_one(da, db, cur, in_step, x);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+
+    int u = slot;
+    if (u >= g.units) return;
+    Unit w = unit_of(u);
+    start(w);
+    for (;;) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) acc[i][j] = lf32x4{0, 0, 0, 0};
+        // the first stage has landed once at most the second's loads are in flight
+        if (kLoads == 16) __builtin_amdgcn_s_waitcnt(0x4F70);
+        else if (kLoads == 12) __builtin_amdgcn_s_waitcnt(0x0F7C);
+        else __builtin_amdgcn_s_waitcnt(0x0F7A);
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) bq[j] = loss_frag<LB, kBN>(lds0 + kA, wn * NJ + j, lane);
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i) alo[i] = loss_frag<LA, BM>(lds0, wm * MI + i, lane);
+        half0(lds0);
+        for (int kt = 0; kt + 1 < w.kt; ++kt) {
+            const uint32_t cur = lds0 + (kt & 1) * kStage, nxt = lds0 + ((kt & 1) ^ 1) * kStage;
+            __builtin_amdgcn_s_waitcnt(0x0F70);              // the next step's loads of this wave
+            __syncthreads();                                 // everyone's; this stage is read
+            __builtin_amdgcn_sched_barrier(0);
+            const int ahead = min(kt + 2, w.kt - 1);
+            const lu32x4 da = fa.desc(ahead), db = fb.desc(ahead);
+            half1(true, cur, nxt, da, db, g.R - w.r0 - ahead * kStep);
+            half0(nxt);
+        }
+        __builtin_amdgcn_s_waitcnt(0x0F70);
+        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
+        half1(false, 0, 0, lu32x4{0, 0, 0, 0}, lu32x4{0, 0, 0, 0}, 0);
+        __syncthreads();
+
+        const Unit done = w;
+        u += G;
+        if (u < g.units) {
+            w = unit_of(u);
+            start(w);
+        }
+
+        // lane: row 16 i + lane % 16 of the wave's tile, columns 16 j + 4 (lane / 16) + e
+        int ln = lane;
+        asm volatile("" : "+v"(ln));
+        const int r16 = ln & 15, q4 = ln >> 4;
+        const int m_wave = done.m0 + wm * 16 * MI, n_wave = done.n0 + wn * 16 * NJ;
+        if (EPI == kStats) {
+            if (n_wave < g.Q) {
+#pragma unroll
+                for (int i = 0; i < MI; ++i) {
+                    const int m = m_wave + 16 * i + r16;
+                    float top = -kLossInf;
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (n_wave + 16 * j + 4 * q4 + e >= g.Q) acc[i][j][e] = -kLossInf;
+                            top = fmaxf(top, acc[i][j][e]);
+                        }
+                    top = fmaxf(top, __shfl_xor(top, 16, 64));
+                    top = fmaxf(top, __shfl_xor(top, 32, 64));
+                    const float by = top == -kLossInf ? 0.0f : top * kLossLog2e;
+                    float s = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            s += __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], kLossLog2e, -by));
+                    s += __shfl_xor(s, 16, 64);
+                    s += __shfl_xor(s, 32, 64);
+                    if (m < g.P) {
+                        if (q4 == 0) g.stats[(int64_t)(n_wave / (16 * NJ)) * g.P + m] = make_float2(top, s);
+                        const int64_t at = g.target[m] - n_wave;
+                        if (at >= 0 && at < 16 * NJ && n_wave + at < g.Q) {
+#pragma unroll
+                            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (at == 16 * j + 4 * q4 + e) g.hit[m] = acc[i][j][e];
+                        }
+                    }
+                }
+            }
+        } else if (EPI == kSum) {
+            float* sum = g.sum + (int64_t)done.split * g.P * g.Q;
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                const int m = m_wave + 16 * i + r16;
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    const int n = n_wave + 16 * j + 4 * q4;
+                    if (m < g.P && n < g.Q) {               // Q is a multiple of 8: 4 columns at a time
+                        float4* at = reinterpret_cast<float4*>(sum + (int64_t)m * g.Q + n);
+                        float4 v = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+                        if (!g.first) {
+                            const float4 o = *at;
+                            v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+                        }
+                        if (g.last)
+                            *reinterpret_cast<uint2*>(g.out + (int64_t)m * g.out_pitch + n) =
+                                make_uint2(loss_pair(v.x, v.y), loss_pair(v.z, v.w));
+                        else
+                            *at = v;
+                    }
+                }
+            }
+        } else {
+            // 16 rows at a time through the wave's LDS, written as 16 NJ-column row segments
+            const uint32_t ew = lds0 + 2 * kStage + wave * kEpi;
+            constexpr int kRowB = 32 * NJ, kSeg = 2 * NJ;    // bytes and 16-byte chunks of a row
+            const int cols = EPI == kGrad ? g.out_cols : g.Q;
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                if (EPI == kGrad) {
+                    const int m = m_wave + 16 * i + r16;
+                    float scale = 0.0f, lse2 = 0.0f;
+                    int64_t t = -1;
+                    if (m < g.P) {
+                        t = g.target[m];
+                        if (t >= 0 && t < g.vocab) {
+                            scale = g.dloss[m];
+                            lse2 = g.lse[m] * kLossLog2e;
+                        } else {
+                            t = -1;
+                        }
+                    }
+                    const int64_t at = t - g.v0 - n_wave;    // the target's column within the wave's
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int n = 16 * j + 4 * q4 + e;
+                            float p = __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], kLossLog2e, -lse2));
+                            p = (p - (at == n ? 1.0f : 0.0f)) * scale;
+                            acc[i][j][e] = t < 0 || n_wave + n >= g.Q ? 0.0f : p;
+                        }
+                }
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    const int c = (2 * j + (q4 >> 1)) ^ (r16 & (kSeg - 1));
+                    typedef unsigned int u2 __attribute__((ext_vector_type(2)));
+                    typedef __attribute__((address_space(3))) u2 lds_u2;
+                    *(lds_u2*)(uintptr_t)(ew + r16 * kRowB + c * 16 + (q4 & 1) * 8) =
+                        u2{loss_pair(acc[i][j][0], acc[i][j][1]), loss_pair(acc[i][j][2], acc[i][j][3])};
+                }
+                __builtin_amdgcn_wave_barrier();             // one wave's LDS accesses stay in order
+#pragma unroll
+                for (int k = 0; k < NJ / 2; ++k) {           // 64 lanes x 16 bytes each
+                    const int idx = k * 64 + ln, rr = idx / kSeg, c = idx % kSeg;
+                    const lu32x4 v = *(const lds_lu32x4*)(uintptr_t)(ew + rr * kRowB + ((c ^ (rr & (kSeg - 1))) * 16));
+                    const int m = m_wave + 16 * i + rr, n = n_wave + c * 8;
+                    if (m < g.P && n < cols) *reinterpret_cast<lu32x4*>(g.out + (int64_t)m * g.out_pitch + n) = v;
+                }
+                __builtin_amdgcn_wave_barrier();
+            }
+        }
+        if (u >= g.units) break;
+    }
+}
+
+// lse and loss of 16 rows per workgroup from their column blocks' statistics: 16 lanes
+// take every 16th block of a row, and are joined in order.
+__global__ void __launch_bounds__(256)
+loss_join_kernel(const float2* __restrict__ stats, int blocks, const float* __restrict__ hit,
+                 const int64_t* __restrict__ target, int T, int64_t vocab, float* __restrict__ loss,
+                 float* __restrict__ lse)
+{
+    __shared__ float2 part[16][17];
+    const int r = threadIdx.x & 15, k = threadIdx.x >> 4, m = blockIdx.x * 16 + r;
+    float top = -kLossInf, s = 0.0f;
+    auto join = [&](float2 o) {
+        // a NaN maximum or sum stays NaN
+        const float up = o.x > top ? o.x : top;
+        const float base = up == -kLossInf ? 0.0f : up;
+        s = s * __builtin_amdgcn_exp2f((top - base) * kLossLog2e) + o.y * __builtin_amdgcn_exp2f((o.x - base) * kLossLog2e);
+        top = up;
+    };
+    if (m < T) {
+#pragma unroll 4
+        for (int b = k; b < blocks; b += 16) join(stats[(int64_t)b * T + m]);
+    }
+    part[r][k] = make_float2(top, s);
+    __syncthreads();
+    if (k == 0 && m < T) {
+        top = -kLossInf;
+        s = 0.0f;
+        for (int i = 0; i < 16; ++i) join(part[r][i]);
+        const float z = (top == -kLossInf ? 0.0f : top) + __builtin_amdgcn_logf(s) * kLossLn2;
+        const int64_t t = target[m];
+        lse[m] = z;
+        loss[m] = t >= 0 && t < vocab ? z - hit[m] : 0.0f;
+    }
+}
+
+// dx = the splits' partial sums, added in order and rounded: 4 elements per thread.
+__global__ void __launch_bounds__(256)
+loss_dx_kernel(const float4* __restrict__ sum, int splits, int64_t n4, uint2* __restrict__ dx)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n4) return;
+    float4 t = sum[i];
+    for (int s = 1; s < splits; ++s) {
+        const float4 o = sum[(int64_t)s * n4 + i];
+        t = make_float4(t.x + o.x, t.y + o.y, t.z + o.z, t.w + o.w);
+    }
+    dx[i] = make_uint2(loss_pair(t.x, t.y), loss_pair(t.z, t.w));
+}
+
+// ---------------------------------------------------------------------- plan and launches
+
+namespace {
+
+// Rows of a tile: the fewest that T needs, for few tokens.
+int tile_rows(int64_t T) { return T <= 64 ? 64 : T <= 128 ? 128 : 256; }
+int column_block(int rows) { return rows == 64 ? 64 : 128; }       // a wave's columns
+
+int64_t up_to(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
+
+// The backward pass's pieces of the vocabulary: as many columns as keep g at or under
+// 128 MiB (it stays in the Infinity Cache between the launch that writes it and the two
+// that read it), at least 4096, whole tiles.
+int64_t piece_columns(int64_t T, int64_t V)
+{
+    int64_t c = ((int64_t)128 << 20) / (2 * T) / kBN * kBN;
+    c = std::max<int64_t>(c, 4096);
+    return std::min(c, up_to(V, kBN));
+}
+
+// dx has T / rows x D / 256 tiles; where they would leave CUs idle its reduction over
+// the (first, largest) piece is split among that many workgroups.  Every split has at
+// least one of its reduction steps; those of a smaller last piece may be fewer, and
+// their partial sums then stand as the earlier pieces left them.
+int dx_splits(int64_t T, int64_t D, int64_t piece)
+{
+    const int64_t tiles = (T + tile_rows(T) - 1) / tile_rows(T) * ((D + kBN - 1) / kBN);
+    const int64_t steps = (piece + kStep - 1) / kStep;
+    const int64_t s = std::max<int64_t>(1, std::min<int64_t>(device_cu_count() / tiles, steps / 8));
+    const int64_t per = (steps + s - 1) / s;
+    return (int)((steps + per - 1) / per);
+}
+
+struct Space {                            // the workspace's parts, in bytes from its start
+    int64_t g, sum, total;
+    int64_t piece;
+    int splits;
+};
+
+Space backward_space(int64_t T, int64_t V, int64_t D)
+{
+    Space s;
+    s.piece = piece_columns(T, V);
+    s.splits = dx_splits(T, D, std::min(s.piece, V));
+    s.g = 0;
+    s.sum = up_to(T * s.piece * 2, 256);
+    s.total = s.sum + up_to(T * D * 4 * s.splits, 256);
+    return s;
+}
+
+template <bool LA, bool LB, int EPI>
+hipError_t product(LossArgs g, int rows, int splits, hipStream_t stream)
+{
+    g.tiles_m = (g.P + rows - 1) / rows;
+    g.tiles_n = (g.Q + kBN - 1) / kBN;
+    g.steps = (g.R + kStep - 1) / kStep;
+    g.per = (g.steps + splits - 1) / splits;
+    g.units = g.tiles_m * g.tiles_n * ((g.steps + g.per - 1) / g.per);
+    const dim3 grid((unsigned)std::min(g.units, device_cu_count()));
+    if constexpr (!LA) {
+        if (rows == 64) return launch(loss_product_kernel<4, 4, 1, 4, LA, LB, EPI>, grid, dim3(256), stream, g);
+        if (rows == 128) return launch(loss_product_kernel<4, 8, 2, 2, LA, LB, EPI>, grid, dim3(256), stream, g);
+    }
+    return launch(loss_product_kernel<8, 8, 2, 2, LA, LB, EPI>, grid, dim3(256), stream, g);
+}
+
+}  // namespace
+
+int64_t loss_forward_workspace(int64_t T, int64_t V)
+{
+    const int cb = column_block(tile_rows(T));
+    return up_to((V + cb - 1) / cb * T * 8, 256) + T * 4;
+}
+
+int64_t loss_backward_workspace(int64_t T, int64_t V, int64_t D) { return backward_space(T, V, D).total; }
+
+hipError_t launch_loss_forward(const void* x, const void* w, const int64_t* target, int64_t T, int64_t V, int64_t D,
+                               float* loss, float* lse, void* workspace, hipStream_t stream)
+{
+    const int rows = tile_rows(T), cb = column_block(rows);
+    const int blocks = (int)((V + cb - 1) / cb);
+    LossArgs g{};
+    g.a = {static_cast<const uint16_t*>(x), D};
+    g.b = {static_cast<const uint16_t*>(w), D};
+    g.P = (int)T;
+    g.Q = (int)V;
+    g.R = (int)D;
+    g.target = target;
+    g.vocab = (int)V;
+    g.stats = static_cast<float2*>(workspace);
+    g.hit = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + up_to((int64_t)blocks * T * 8, 256));
+    const hipError_t e = product<false, false, kStats>(g, rows, 1, stream);
+    if (e != hipSuccess) return e;
+    return launch(loss_join_kernel, dim3((unsigned)((T + 15) / 16)), dim3(256), stream,
+                  static_cast<const float2*>(g.stats), blocks, static_cast<const float*>(g.hit), target, (int)T, V, loss,
+                  lse);
+}
+
+hipError_t launch_loss_backward(const float* dloss, const void* x, const void* w, const int64_t* target,
+                                const float* lse, int64_t T, int64_t V, int64_t D, void* dx, void* dw,
+                                void* workspace, hipStream_t stream)
+{
+    const Space sp = backward_space(T, V, D);
+    const int rows = tile_rows(T);
+    uint16_t* gm = static_cast<uint16_t*>(workspace);
+    float* sum = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.sum);
+    const Side xs{static_cast<const uint16_t*>(x), D};
+    int splits = sp.splits;
+    for (int64_t v0 = 0; v0 < V; v0 += sp.piece) {
+        const int64_t n = std::min(sp.piece, V - v0);
+        const Side ws{static_cast<const uint16_t*>(w) + v0 * D, D}, gs{gm, sp.piece};
+        LossArgs g{};
+        g.a = xs;
+        g.b = ws;
+        g.P = (int)T;
+        g.Q = (int)n;
+        g.R = (int)D;
+        g.target = target;
+        g.lse = lse;
+        g.dloss = dloss;
+        g.v0 = (int)v0;
+        g.vocab = (int)V;
+        g.out = gm;
+        g.out_pitch = sp.piece;
+        g.out_cols = (int)up_to(n, 8);
+        hipError_t e = product<false, false, kGrad>(g, rows, 1, stream);
+        if (e != hipSuccess) return e;
+
+        LossArgs d{};
+        d.a = gs;
+        d.b = ws;
+        d.P = (int)T;
+        d.Q = (int)D;
+        d.R = (int)n;
+        d.sum = sum;
+        d.out = static_cast<uint16_t*>(dx);
+        d.out_pitch = D;
+        d.first = v0 == 0;
+        d.last = splits == 1 && v0 + n == V;
+        e = product<false, true, kSum>(d, rows, splits, stream);
+        if (e != hipSuccess) return e;
+
+        LossArgs h{};
+        h.a = gs;
+        h.b = xs;
+        h.P = (int)n;
+        h.Q = (int)D;
+        h.R = (int)T;
+        h.out = static_cast<uint16_t*>(dw) + v0 * D;
+        h.out_pitch = D;
+        e = product<true, true, kStore>(h, 256, 1, stream);
+        if (e != hipSuccess) return e;
+    }
+    if (splits > 1) {
+        const int64_t n4 = T * D / 4;
+        return launch(loss_dx_kernel, dim3((unsigned)((n4 + 255) / 256)), dim3(256), stream,
+                      reinterpret_cast<const float4*>(sum), splits, n4, static_cast<uint2*>(dx));
+    }
+    return hipSuccess;
+}
+
+}  // namespace fp8k

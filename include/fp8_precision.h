@@ -611,6 +611,43 @@ fp8_status fp8_attention_backward(const fp8_attention_shape* shape, const fp8_he
                                   void* workspace, int64_t workspace_bytes, hipStream_t stream);
 
 /*
+ * Cross entropy of a linear head over a large vocabulary, from the hidden states and
+ * the head's weight; the logits z = x w^T are never stored.
+ *   lse_t = log sum_v exp(z_tv),  loss_t = lse_t - z_t,target(t)
+ * A token whose target is outside [0, vocab) (such as -100) has no target: its loss
+ * is 0 and it gives no gradient.
+ *
+ *   x       bf16 [tokens, dim];  weight  bf16 [vocab, dim]
+ *   target  int64 [tokens], 8-byte aligned
+ *   loss, lse   fp32 [tokens]
+ *   workspace, workspace_bytes   device memory, 16-byte aligned, of at least the size
+ *           that the workspace call gives for the sizes on the current device
+ * Constraints: dim a multiple of 8, at most 65536; tokens and vocab in [1, 2^24).
+ * No output may overlap an input, another output or the workspace.
+ */
+fp8_status fp8_linear_cross_entropy_forward_workspace(int64_t tokens, int64_t vocab, int64_t dim, int64_t* bytes);
+fp8_status fp8_linear_cross_entropy_forward(const void* x, const void* weight, const int64_t* target, int64_t tokens,
+                                            int64_t vocab, int64_t dim, float* loss, float* lse, void* workspace,
+                                            int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Its gradients: with g_tv = dloss_t (exp(z_tv - lse_t) - [v = target(t)]),
+ *   dx = g w,  dweight = g^T x
+ * The vocabulary is walked in pieces: a piece's logits are computed again, its g is
+ * rounded to bf16 in the workspace, and both products are taken from there (dx is
+ * summed over the pieces in fp32).
+ *
+ *   dloss   fp32 [tokens] (for the mean over n tokens: 1 / n);  lse  from the forward
+ *   dx      bf16 [tokens, dim];  dweight  bf16 [vocab, dim]  (written, not added to)
+ * Constraints and workspace as for the forward.
+ */
+fp8_status fp8_linear_cross_entropy_backward_workspace(int64_t tokens, int64_t vocab, int64_t dim, int64_t* bytes);
+fp8_status fp8_linear_cross_entropy_backward(const float* dloss, const void* x, const void* weight,
+                                             const int64_t* target, const float* lse, int64_t tokens, int64_t vocab,
+                                             int64_t dim, void* dx, void* dweight, void* workspace,
+                                             int64_t workspace_bytes, hipStream_t stream);
+
+/*
  * Measurement reference, not a step of the FP8 method: a plain device copy
  * dst[0, bytes) = src[0, bytes), built like the streaming kernels above
  * (16-byte vectors, non-temporal loads, the launch shape at which a copy
