@@ -85,20 +85,30 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle by device index, without building a Stream object
+# around it (a microsecond a call) where this torch has the accessor.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _run(call: str, fn, tensors, *args) -> None:
     """Call entry point ``fn`` with ``args`` and the stream.  Every tensor of the
     call must be on one device; that device is made current for the call (the
     library acts on the current HIP device) and its current stream is passed."""
-    dev = None
+    first = None
     for t in tensors:
         if t is None:
             continue
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{call}: all tensors must be on one device (got {dev} and {t.device})")
-    with torch.cuda.device(dev):
-        _check(call, fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+        i = t.get_device()
+        if first is None:
+            first, index = t, i
+        elif i != index or (i < 0 and t.device != first.device):
+            raise ValueError(f"{call}: all tensors must be on one device (got {first.device} and {t.device})")
+    if index >= 0 and index == torch.cuda.current_device():
+        _check(call, fn(*args, _raw_stream(index)))
+        return
+    with torch.cuda.device(first.device):
+        _check(call, fn(*args, torch.cuda.current_stream(first.device).cuda_stream))
 
 
 def _dev_tensor(t, name, dtype=None):
@@ -611,7 +621,7 @@ def _out(t, name, shape, dtype, device):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
     _dev_tensor(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}")
     return t
 
@@ -620,8 +630,11 @@ def _workspace(call, device, *args):
     """Device memory of the size that the entry point ``call`` names for ``args``
     on ``device`` (the torch allocator's, so stream-ordered like any tensor)."""
     size = _i64()
-    with torch.cuda.device(device):
+    if device.index == torch.cuda.current_device():
         _check(call, getattr(_lib, call)(*args, ctypes.byref(size)))
+    else:
+        with torch.cuda.device(device):
+            _check(call, getattr(_lib, call)(*args, ctypes.byref(size)))
     return torch.empty(max(16, size.value), dtype=torch.uint8, device=device)
 
 

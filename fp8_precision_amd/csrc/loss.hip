@@ -47,7 +47,6 @@ typedef __attribute__((address_space(3))) lu32x4 lds_lu32x4;
 constexpr float kLossLog2e = 1.44269504088896340736f;
 constexpr float kLossLn2 = 0.69314718055994530942f;
 constexpr float kLossInf = __builtin_inff();
-constexpr int kBN = 256;                  // columns of a tile
 constexpr int kStep = 64;                 // reduction elements of a step (128 bytes)
 constexpr int kOutside = (int)0x80000000; // an offset past every buffer's size
 
@@ -173,6 +172,9 @@ __device__ __forceinline__ LossFrag loss_frag(uint32_t at, int blk, int lane)
     return f;
 }
 
+// s_waitcnt immediate: at most n vector memory operations in flight.
+constexpr int wait_loads(int n) { return 0x0F70 | (n & 15) | (n >> 4) << 14; }
+
 // What a launch's epilogue does with the tile's sums.
 enum { kStats = 0, kGrad = 1, kSum = 2, kStore = 3 };
 
@@ -203,16 +205,16 @@ struct Unit {
 }  // namespace
 
 // MI x NJ blocks of 16 x 16 per wave, GM x GN waves.
-template <int MI, int NJ, int GM, int GN, bool LA, bool LB, int EPI>
+template <int MI, int NJ, int GM, int GN, int NS, bool LA, bool LB, int EPI>
 __global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
 {
-    constexpr int BM = 16 * MI * GM;
-    static_assert(16 * NJ * GN == kBN && GM * GN == 4, "four waves cover 256 columns");
-    constexpr int kA = BM * 128, kStage = kA + kBN * 128;
-    constexpr int kLoads = BM / 32 + kBN / 32;
+    constexpr int BM = 16 * MI * GM, BN = 16 * NJ * GN;
+    static_assert(GM * GN == 4, "four waves");
+    constexpr int kA = BM * 128, kStage = kA + BN * 128;
+    constexpr int kLoads = BM / 32 + BN / 32;
     constexpr int kEpi = 16 * 16 * NJ * 2;                   // a wave's 16 rows of bf16
     constexpr int kHalf = MI / 2;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kStage + 4 * kEpi];
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * kStage + 4 * kEpi];
 
     const int G = gridDim.x;
     int slot = blockIdx.x;
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
         const int group = t / (8 * g.tiles_n), in = t - group * 8 * g.tiles_n;
         const int rows = min(8, g.tiles_m - group * 8);
         w.m0 = (group * 8 + in % rows) * BM;
-        w.n0 = (in / rows) * kBN;
+        w.n0 = (in / rows) * BN;
         const int s0 = w.split * g.per;
         w.r0 = s0 * kStep;
         w.kt = min(g.steps - s0, g.per);
@@ -239,7 +241,7 @@ __global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
     };
 
     Feed<LA, BM> fa;
-    Feed<LB, kBN> fb;
+    Feed<LB, BN> fb;
     lf32x4 acc[MI][NJ];
     LossFrag bq[NJ], alo[kHalf], ahi[kHalf];
 
@@ -249,13 +251,13 @@ __global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
             fa.issue(da, idx, in_step, __builtin_amdgcn_readfirstlane(to + (wave * (BM / 32) + idx) * 1024));
         else
             fb.issue(db, idx - BM / 32, in_step,
-                     __builtin_amdgcn_readfirstlane(to + kA + (wave * (kBN / 32) + idx - BM / 32) * 1024));
+                     __builtin_amdgcn_readfirstlane(to + kA + (wave * (BN / 32) + idx - BM / 32) * 1024));
     };
     auto start = [&](const Unit& w) {
         fa.init(g.a, w.m0, g.P, g.R, w.r0, wave, lane);
         fb.init(g.b, w.n0, g.Q, g.R, w.r0, wave, lane);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < NS; ++s) {
             const int kt = min(s, w.kt - 1);
             const lu32x4 da = fa.desc(kt), db = fb.desc(kt);
             const int in_step = g.R - w.r0 - kt * kStep;
@@ -278,14 +280,14 @@ __global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
         }
     };
     // the second half: the next step's fragments replace those that are done with, and the
-    // step after next is loaded into this step's stage
+    // step NS ahead is loaded into this step's stage
     auto half1 = [&](bool more, uint32_t cur, uint32_t nxt, const lu32x4& da, const lu32x4& db, int in_step) {
 #pragma unroll
         for (int t = 0; t < kHalf * NJ; ++t) {
             const int j = t / kHalf, i = t % kHalf;
             fma16(acc[kHalf + i][j], ahi[i], bq[j]);
             if (more) {
-                if (i == kHalf - 1) bq[j] = loss_frag<LB, kBN>(nxt + kA, wn * NJ + j, lane);
+                if (i == kHalf - 1) bq[j] = loss_frag<LB, BN>(nxt + kA, wn * NJ + j, lane);
                 if (t % NJ == 1) alo[t / NJ] = loss_frag<LA, BM>(nxt, wm * MI + t / NJ, lane);
 #pragma unroll
                 for (int x = t * kLoads / (kHalf * NJ); x < (t + 1) * kLoads / (kHalf * NJ); ++x)
@@ -304,27 +306,29 @@ __global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
         for (int i = 0; i < MI; ++i)
 #pragma unroll
             for (int j = 0; j < NJ; ++j) acc[i][j] = lf32x4{0, 0, 0, 0};
-        // the first stage has landed once at most the second's loads are in flight
-        if (kLoads == 16) __builtin_amdgcn_s_waitcnt(0x4F70);
-        else if (kLoads == 12) __builtin_amdgcn_s_waitcnt(0x0F7C);
-        else __builtin_amdgcn_s_waitcnt(0x0F7A);
+        // the first stage has landed once at most the later ones' loads are in flight
+        __builtin_amdgcn_s_waitcnt(wait_loads((NS - 1) * kLoads));
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) bq[j] = loss_frag<LB, kBN>(lds0 + kA, wn * NJ + j, lane);
+        for (int j = 0; j < NJ; ++j) bq[j] = loss_frag<LB, BN>(lds0 + kA, wn * NJ + j, lane);
 #pragma unroll
         for (int i = 0; i < kHalf; ++i) alo[i] = loss_frag<LA, BM>(lds0, wm * MI + i, lane);
         half0(lds0);
+        uint32_t cur = lds0;
         for (int kt = 0; kt + 1 < w.kt; ++kt) {
-            const uint32_t cur = lds0 + (kt & 1) * kStage, nxt = lds0 + ((kt & 1) ^ 1) * kStage;
-            __builtin_amdgcn_s_waitcnt(0x0F70);              // the next step's loads of this wave
+            const uint32_t nxt = cur + kStage == lds0 + NS * kStage ? lds0 : cur + kStage;
+            __builtin_amdgcn_s_waitcnt(wait_loads((NS - 2) * kLoads));   // the next step's loads of this wave
             __syncthreads();                                 // everyone's; this stage is read
             __builtin_amdgcn_sched_barrier(0);
-            const int ahead = min(kt + 2, w.kt - 1);
+            // (past the last step its loads are repeated into stages that are read no more,
+            // so that the count of loads in flight stays the same)
+            const int ahead = min(kt + NS, w.kt - 1);
             const lu32x4 da = fa.desc(ahead), db = fb.desc(ahead);
             half1(true, cur, nxt, da, db, g.R - w.r0 - ahead * kStep);
             half0(nxt);
+            cur = nxt;
         }
-        __builtin_amdgcn_s_waitcnt(0x0F70);
+        __builtin_amdgcn_s_waitcnt(wait_loads(0));
         __syncthreads();
         __builtin_amdgcn_sched_barrier(0);
         half1(false, 0, 0, lu32x4{0, 0, 0, 0}, lu32x4{0, 0, 0, 0}, 0);
@@ -404,7 +408,7 @@ __global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
             }
         } else {
             // 16 rows at a time through the wave's LDS, written as 16 NJ-column row segments
-            const uint32_t ew = lds0 + 2 * kStage + wave * kEpi;
+            const uint32_t ew = lds0 + NS * kStage + wave * kEpi;
             constexpr int kRowB = 32 * NJ, kSeg = 2 * NJ;    // bytes and 16-byte chunks of a row
             const int cols = EPI == kGrad ? g.out_cols : g.Q;
 #pragma unroll
@@ -456,14 +460,14 @@ __global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
     }
 }
 
-// lse and loss of 16 rows per workgroup from their column blocks' statistics: 16 lanes
-// take every 16th block of a row, and are joined in order.
-__global__ void __launch_bounds__(256)
+// lse and loss of 16 rows per workgroup from their column blocks' statistics: 64 lanes
+// take every 64th block of a row; 8, then the last lane join them in order.
+__global__ void __launch_bounds__(1024)
 loss_join_kernel(const float2* __restrict__ stats, int blocks, const float* __restrict__ hit,
                  const int64_t* __restrict__ target, int T, int64_t vocab, float* __restrict__ loss,
                  float* __restrict__ lse)
 {
-    __shared__ float2 part[16][17];
+    __shared__ float2 part[64][16];
     const int r = threadIdx.x & 15, k = threadIdx.x >> 4, m = blockIdx.x * 16 + r;
     float top = -kLossInf, s = 0.0f;
     auto join = [&](float2 o) {
@@ -475,14 +479,20 @@ loss_join_kernel(const float2* __restrict__ stats, int blocks, const float* __re
     };
     if (m < T) {
 #pragma unroll 4
-        for (int b = k; b < blocks; b += 16) join(stats[(int64_t)b * T + m]);
+        for (int b = k; b < blocks; b += 64) join(stats[(int64_t)b * T + m]);
     }
-    part[r][k] = make_float2(top, s);
-    __syncthreads();
-    if (k == 0 && m < T) {
+    part[k][r] = make_float2(top, s);
+    for (int left = 64; left > 1; left /= 8) {
+        const int n = left / 8;
+        __syncthreads();
         top = -kLossInf;
         s = 0.0f;
-        for (int i = 0; i < 16; ++i) join(part[r][i]);
+        if (k < n)
+            for (int i = 0; i < 8; ++i) join(part[k * 8 + i][r]);
+        __syncthreads();
+        if (k < n) part[k][r] = make_float2(top, s);
+    }
+    if (k == 0 && m < T) {
         const float z = (top == -kLossInf ? 0.0f : top) + __builtin_amdgcn_logf(s) * kLossLn2;
         const int64_t t = target[m];
         lse[m] = z;
@@ -510,7 +520,7 @@ namespace {
 
 // Rows of a tile: the fewest that T needs, for few tokens.
 int tile_rows(int64_t T) { return T <= 64 ? 64 : T <= 128 ? 128 : 256; }
-int column_block(int rows) { return rows == 64 ? 64 : 128; }       // a wave's columns
+int column_block(int rows) { return rows == 64 ? 32 : 128; }       // a wave's columns of the logits
 
 int64_t up_to(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 
@@ -519,9 +529,9 @@ int64_t up_to(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 // that read it), at least 4096, whole tiles.
 int64_t piece_columns(int64_t T, int64_t V)
 {
-    int64_t c = ((int64_t)128 << 20) / (2 * T) / kBN * kBN;
+    int64_t c = ((int64_t)128 << 20) / (2 * T) / 256 * 256;
     c = std::max<int64_t>(c, 4096);
-    return std::min(c, up_to(V, kBN));
+    return std::min(c, up_to(V, 256));
 }
 
 // dx has T / rows x D / 256 tiles; where they would leave CUs idle its reduction over
@@ -530,7 +540,7 @@ int64_t piece_columns(int64_t T, int64_t V)
 // their partial sums then stand as the earlier pieces left them.
 int dx_splits(int64_t T, int64_t D, int64_t piece)
 {
-    const int64_t tiles = (T + tile_rows(T) - 1) / tile_rows(T) * ((D + kBN - 1) / kBN);
+    const int64_t tiles = (T + tile_rows(T) - 1) / tile_rows(T) * ((D + 255) / 256);
     const int64_t steps = (piece + kStep - 1) / kStep;
     const int64_t s = std::max<int64_t>(1, std::min<int64_t>(device_cu_count() / tiles, steps / 8));
     const int64_t per = (steps + s - 1) / s;
@@ -558,16 +568,22 @@ template <bool LA, bool LB, int EPI>
 hipError_t product(LossArgs g, int rows, int splits, hipStream_t stream)
 {
     g.tiles_m = (g.P + rows - 1) / rows;
-    g.tiles_n = (g.Q + kBN - 1) / kBN;
+    const bool narrow = !LA && !LB && rows == 64;
+    const int cols = narrow ? 128 : 256;
+    g.tiles_n = (g.Q + cols - 1) / cols;
     g.steps = (g.R + kStep - 1) / kStep;
     g.per = (g.steps + splits - 1) / splits;
     g.units = g.tiles_m * g.tiles_n * ((g.steps + g.per - 1) / g.per);
     const dim3 grid((unsigned)std::min(g.units, device_cu_count()));
     if constexpr (!LA) {
-        if (rows == 64) return launch(loss_product_kernel<4, 4, 1, 4, LA, LB, EPI>, grid, dim3(256), stream, g);
-        if (rows == 128) return launch(loss_product_kernel<4, 8, 2, 2, LA, LB, EPI>, grid, dim3(256), stream, g);
+        if constexpr (!LB) {
+            if (narrow) return launch(loss_product_kernel<4, 2, 1, 4, 6, LA, LB, EPI>, grid, dim3(256), stream, g);
+        } else {
+            if (rows == 64) return launch(loss_product_kernel<4, 4, 1, 4, 3, LA, LB, EPI>, grid, dim3(256), stream, g);
+        }
+        if (rows == 128) return launch(loss_product_kernel<4, 8, 2, 2, 3, LA, LB, EPI>, grid, dim3(256), stream, g);
     }
-    return launch(loss_product_kernel<8, 8, 2, 2, LA, LB, EPI>, grid, dim3(256), stream, g);
+    return launch(loss_product_kernel<8, 8, 2, 2, 2, LA, LB, EPI>, grid, dim3(256), stream, g);
 }
 
 }  // namespace
@@ -597,7 +613,7 @@ hipError_t launch_loss_forward(const void* x, const void* w, const int64_t* targ
     g.hit = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + up_to((int64_t)blocks * T * 8, 256));
     const hipError_t e = product<false, false, kStats>(g, rows, 1, stream);
     if (e != hipSuccess) return e;
-    return launch(loss_join_kernel, dim3((unsigned)((T + 15) / 16)), dim3(256), stream,
+    return launch(loss_join_kernel, dim3((unsigned)((T + 15) / 16)), dim3(1024), stream,
                   static_cast<const float2*>(g.stats), blocks, static_cast<const float*>(g.hit), target, (int)T, V, loss,
                   lse);
 }
