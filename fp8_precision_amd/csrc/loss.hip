@@ -18,8 +18,10 @@
 // few tokens, where reading w bounds.  The product kernel: 256 columns by 256, 128 or
 // 64 rows per workgroup of 4 waves, one wave per SIMD; reduction steps of 64
 // elements in two LDS stages filled by 16-byte direct-to-LDS buffer loads issued a
-// step and a half ahead; v_mfma_f32_16x16x32_bf16 with fragments double-buffered in
-// registers across a barrier in the middle of a step; persistent workgroups in an
+// step and a half ahead; v_mfma_f32_32x32x16_bf16 (its 32 cycles leave room for the
+// reads and loads issued beside it: with 16x16x32 the kernel was bound by instruction
+// issue, 1250 TFLOP/s) with fragments double-buffered in registers across a barrier in
+// the middle of a step; persistent workgroups in an
 // XCD-major walk that load the next tile's first stages before the epilogue.
 // Operands are read along the reduction ("K": x and w for the logits, g for dx) or
 // across it ("MN": w for dx, g and x for dw) through transposing LDS reads, so no
@@ -50,11 +52,11 @@ constexpr float kLossInf = __builtin_inff();
 constexpr int kStep = 64;                 // reduction elements of a step (128 bytes)
 constexpr int kOutside = (int)0x80000000; // an offset past every buffer's size
 
-// Fragment: 16 rows x 64 reduction elements; u[0] the step's first 32, u[1] the rest.
+// Fragment: 16 rows x 32 reduction elements, 8 per lane.
 union LossFrag {
-    lu32x4 u[2];
-    lb16x8 b[2];
-    ls16x4 s[4];
+    lu32x4 u;
+    lb16x8 b;
+    ls16x4 s[2];
 };
 
 __device__ __forceinline__ uint32_t loss_pair(float a, float b)
@@ -92,14 +94,15 @@ struct Side {
 // Loads of one operand's EXT rows (columns) of the tile for one wave.  The LDS image:
 //   K:  EXT rows of 128 bytes, 16-byte chunk c of row r at c ^ (r >> 1 & 7) ^ (r & 1) << 2;
 //   MN: 64 rows (reduction) of 2 EXT bytes, chunk c of row r at
-//       c ^ ((r & 3) << 1 | (r >> 3 & 1) << 3): a transposing read takes 32-byte pieces
-//       of 16 rows, which this spreads over all banks.
+//       c ^ ((r & 3) << 1 | (r >> 3 & 1) << 3):
+// so that the 16 rows of a plain read, and the 32-byte pieces of 8 rows that half a
+// wave's transposing read takes, spread over all banks.
 template <bool MN, int EXT>
 struct Feed {
     static constexpr int kLoads = EXT / 32;                  // 1 KB each
     const uint8_t* base;
     int64_t pitch, left;                                     // bytes; of the matrix from base on
-    uint32_t voff[MN ? 4 : 2];
+    uint32_t voff[kLoads];
     int chunk[2];                                            // K: the lane's chunk for even and odd loads
 
     __device__ __forceinline__ void init(const Side& s, int origin, int extent, int total_r, int r0, int wave, int lane)
@@ -109,36 +112,33 @@ struct Feed {
             base = reinterpret_cast<const uint8_t*>(s.p) + (int64_t)origin * pitch + (int64_t)r0 * 2;
             left = (int64_t)(extent - origin) * pitch - (int64_t)r0 * 2;
 #pragma unroll
-            for (int par = 0; par < 2; ++par) {
-                const int r = wave * (EXT / 4) + par * 8 + (lane >> 3);
-                chunk[par] = (lane & 7) ^ ((r >> 1) & 7) ^ ((r & 1) << 2);
-                voff[par] = (uint32_t)(r * (int)pitch) + (uint32_t)chunk[par] * 16u;
+            for (int ii = 0; ii < kLoads; ++ii) {
+                const int r = wave * (EXT / 4) + ii * 8 + (lane >> 3);
+                chunk[ii & 1] = (lane & 7) ^ ((r >> 1) & 7) ^ ((r & 1) << 2);
+                voff[ii] = (uint32_t)(r * (int)pitch) + (uint32_t)chunk[ii & 1] * 16u;
             }
         } else {
             static_assert(!MN || EXT == 256, "the MN image is laid out for 256 columns");
             base = reinterpret_cast<const uint8_t*>(s.p) + (int64_t)r0 * pitch + (int64_t)origin * 2;
             left = (int64_t)(total_r - r0) * pitch - (int64_t)origin * 2;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = wave * 16 + (i & 1) * 2 + (i >> 1) * 8 + (lane >> 5);
+            for (int ii = 0; ii < kLoads; ++ii) {
+                const int r = wave * 16 + ii * 2 + (lane >> 5);
                 const int c = (lane & 31) ^ ((r & 3) << 1 | (r >> 3 & 1) << 3);
-                voff[i] = origin + c * 8 < extent ? (uint32_t)(r * (int)pitch) + (uint32_t)c * 16u : (uint32_t)kOutside;
+                voff[ii] = origin + c * 8 < extent ? (uint32_t)(r * (int)pitch) + (uint32_t)c * 16u : (uint32_t)kOutside;
             }
         }
     }
 
-    // load ii of step kt (counted from r0); `in_step` elements of the step exist
-    __device__ __forceinline__ void issue(const lu32x4& desc, int ii, int in_step, uint32_t lds) const
+    // From here on every load is of the reduction's last step, which has in_step < kStep
+    // elements: lanes past them read zero.
+    __device__ __forceinline__ void trim(int in_step)
     {
-        uint32_t v;
         if (!MN) {
-            v = voff[ii & 1] + (uint32_t)((ii >> 1) * 16) * (uint32_t)pitch;
-            v = chunk[ii & 1] * 8 < in_step ? v : (uint32_t)kOutside;
-        } else {
-            v = voff[(ii & 1) | (ii >> 2) << 1] + (uint32_t)((ii >> 1 & 1) * 4) * (uint32_t)pitch;
-            // an offset that is outside stays outside: 4 rows are far less than 2^31 bytes
+#pragma unroll
+            for (int ii = 0; ii < kLoads; ++ii)
+                if (chunk[ii & 1] * 8 >= in_step) voff[ii] = (uint32_t)kOutside;
         }
-        loss_to_lds(v, desc, lds);
     }
     __device__ __forceinline__ lu32x4 desc(int kt) const
     {
@@ -147,33 +147,54 @@ struct Feed {
     }
 };
 
-// Rows 16 blk .. of an operand image at LDS address `at`.
-template <bool MN, int EXT>
-__device__ __forceinline__ LossFrag loss_frag(uint32_t at, int blk, int lane)
-{
-    LossFrag f;
-    if (!MN) {
-        const int r = blk * 16 + (lane & 15);
-        const int p = (lane >> 4) ^ ((r >> 1) & 7) ^ ((r & 1) << 2);
-        f.u[0] = *(const lds_lu32x4*)(uintptr_t)(at + r * 128 + p * 16);
-        f.u[1] = *(const lds_lu32x4*)(uintptr_t)(at + r * 128 + (p ^ 4) * 16);
-    } else {
-        constexpr int kRow = EXT * 2;
+// This lane's addresses in an operand image of the first stage, for the wave's 16-row
+// blocks from `first` on; block i and reduction elements 32 k .. are at
+//   K:  at[k] + 2048 i;   MN:  at[i] + 32 k rows, and 4 rows on.
+template <bool MN, int EXT, int N>
+struct Reader {
+    uint32_t at[MN ? N : 2];
+    __device__ __forceinline__ void init(uint32_t image, int first, int lane)
+    {
         const int g = lane >> 4, l = lane & 15;
-        uint32_t base = at + (8 * g + (l >> 2)) * kRow +
-                        ((((l & 3) >> 1) ^ ((l >> 2) << 1 | (g & 1) << 3)) * 16) + (l & 1) * 8;
-        asm volatile("" : "+v"(base));    // one XOR per block instead of an address held per block
-        const uint32_t a = base ^ (uint32_t)(blk * 32);
+        if (!MN) {
+            const int f = ((l >> 1) & 7) ^ ((l & 1) << 2);
+            at[0] = image + (first * 16 + l) * 128 + ((g ^ f) * 16);
+            at[1] = image + (first * 16 + l) * 128 + ((g ^ f ^ 4) * 16);
+        } else {
+            const int f = (l >> 2) << 1 | (g & 1) << 3;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            f.s[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_ls16x4*)(uintptr_t)(a + ((i & 1) * 4 + (i >> 1) * 32) * kRow));
+            for (int i = 0; i < N; ++i)
+                at[MN ? i : 0] = image + (8 * g + (l >> 2)) * (EXT * 2) + (((2 * (first + i) + (l & 3) / 2) ^ f) * 16) +
+                                 (l & 1) * 8;
+        }
     }
-    return f;
-}
+    __device__ __forceinline__ LossFrag read(uint32_t stage, int i, int k) const
+    {
+        LossFrag f;
+        if (!MN) {
+            f.u = *((const lds_lu32x4*)(uintptr_t)(at[k] + stage) + i * 128);
+        } else {
+            lds_ls16x4* p = (lds_ls16x4*)(uintptr_t)(at[MN ? i : 0] + stage) + k * (32 * EXT / 4);
+            f.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
+            f.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p + EXT);
+        }
+        return f;
+    }
+};
 
 // s_waitcnt immediate: at most n vector memory operations in flight.
 constexpr int wait_loads(int n) { return 0x0F70 | (n & 15) | (n >> 4) << 14; }
+
+// A barrier that waits for nothing but the waves themselves: what a wave has to have done
+// before it is waited for explicitly.  No LDS access is moved over it.
+__device__ __forceinline__ void lds_barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+}
 
 // What a launch's epilogue does with the tile's sums.
 enum { kStats = 0, kGrad = 1, kSum = 2, kStore = 3 };
@@ -204,7 +225,7 @@ struct Unit {
 
 }  // namespace
 
-// MI x NJ blocks of 16 x 16 per wave, GM x GN waves.
+// MI x NJ blocks of 16 x 16 per wave, GM x GN waves, NS stages.
 template <int MI, int NJ, int GM, int GN, int NS, bool LA, bool LB, int EPI>
 __global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
 {
@@ -212,9 +233,12 @@ __global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
     static_assert(GM * GN == 4, "four waves");
     constexpr int kA = BM * 128, kStage = kA + BN * 128;
     constexpr int kLoads = BM / 32 + BN / 32;
-    constexpr int kEpi = 16 * 16 * NJ * 2;                   // a wave's 16 rows of bf16
+    constexpr int kEpi = EPI == kGrad || EPI == kStore ? 16 * 16 * NJ * 2 : 0;   // a wave's 16 rows of bf16
     constexpr int kHalf = MI / 2;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * kStage + 4 * kEpi];
+    // the tile's rows: target (-1: none), dloss, lse in powers of two
+    __shared__ int row_target[BM];
+    __shared__ float row_scale[BM], row_lse[BM];
 
     const int G = gridDim.x;
     int slot = blockIdx.x;
@@ -242,16 +266,20 @@ __global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
 
     Feed<LA, BM> fa;
     Feed<LB, BN> fb;
+    Reader<LA, BM, MI> ra;
+    Reader<LB, BN, NJ> rb;
+    ra.init(lds0, wm * MI, lane);
+    rb.init(lds0 + kA, wn * NJ, lane);
     lf32x4 acc[MI][NJ];
-    LossFrag bq[NJ], alo[kHalf], ahi[kHalf];
+    LossFrag bq[NJ][2], alo[kHalf][2], ahi[kHalf][2];
 
-    // loads idx of step kt (of the unit that fa, fb stand at) into stage `to`
-    auto issue_one = [&](const lu32x4& da, const lu32x4& db, uint32_t to, int in_step, int idx) {
-        if (idx < BM / 32)
-            fa.issue(da, idx, in_step, __builtin_amdgcn_readfirstlane(to + (wave * (BM / 32) + idx) * 1024));
-        else
-            fb.issue(db, idx - BM / 32, in_step,
-                     __builtin_amdgcn_readfirstlane(to + kA + (wave * (BN / 32) + idx - BM / 32) * 1024));
+    // before the first load of step kt: if it is the reduction's last and not a whole one
+    auto trim = [&](const Unit& w, int kt) {
+        const int in_step = g.R - w.r0 - kt * kStep;
+        if (in_step < kStep) {
+            fa.trim(in_step);
+            fb.trim(in_step);
+        }
     };
     auto start = [&](const Unit& w) {
         fa.init(g.a, w.m0, g.P, g.R, w.r0, wave, lane);
@@ -259,47 +287,102 @@ __global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
             const int kt = min(s, w.kt - 1);
+            trim(w, kt);
             const lu32x4 da = fa.desc(kt), db = fb.desc(kt);
-            const int in_step = g.R - w.r0 - kt * kStep;
 #pragma unroll
-            for (int idx = 0; idx < kLoads; ++idx) issue_one(da, db, lds0 + s * kStage, in_step, idx);
+            for (int x = 0; x < BM / 32; ++x)
+                loss_to_lds(fa.voff[x], da,
+                            __builtin_amdgcn_readfirstlane(lds0 + s * kStage + (wave * (BM / 32) + x) * 1024));
+#pragma unroll
+            for (int x = 0; x < BN / 32; ++x)
+                loss_to_lds(fb.voff[x], db,
+                            __builtin_amdgcn_readfirstlane(lds0 + s * kStage + kA + (wave * (BN / 32) + x) * 1024));
         }
     };
-    auto fma16 = [&](lf32x4& c, const LossFrag& a, const LossFrag& b) {
-        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.b[0], a.b[0], c, 0, 0, 0);
-        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.b[1], a.b[1], c, 0, 0, 0);
-    };
-    // the first half of a step: A blocks 0 .. kHalf - 1, while the others are read
-    auto half0 = [&](uint32_t at) {
+    // Instruction t of a half step: B block t / (2 kHalf), A block t / 2 % kHalf, the first or
+    // second 32 of the 64 reduction elements (one accumulator's two instructions in a row
+    // measured 2% faster than kHalf apart).  An instruction takes 16 cycles and the wave
+    // issues another at most every 4, so reads and loads are dealt over the slots one at a
+    // time, and the loads over the whole step: a CU takes a 1 KB load every 16 cycles, and
+    // all 64 of a step in one half of it made every instruction behind them wait.
+    constexpr int kSlots = 2 * kHalf * NJ, kFree = kSlots / 4;
+    constexpr int kLoadsA = BM / 32, kLoadsB = BN / 32;
+    // The first half of a step: A blocks 0 .. kHalf - 1, while the others are read.  B was
+    // read in the half before; once every wave has it (slot kFree), B of the step NS ahead is
+    // loaded into its place.
+    auto half0 = [&](uint32_t cur, const lu32x4& db) {
 #pragma unroll
-        for (int t = 0; t < kHalf * NJ; ++t) {
-            const int j = t / kHalf, i = t % kHalf;
-            fma16(acc[i][j], alo[i], bq[j]);
-            if (t % NJ == 1) ahi[t / NJ] = loss_frag<LA, BM>(at, wm * MI + kHalf + t / NJ, lane);
+        for (int t = 0; t < kSlots; ++t) {
+            const int j = t / (2 * kHalf), k = t % 2, i = t / 2 % kHalf;
+            if (t == kFree) {
+                __builtin_amdgcn_s_waitcnt(0xC07F);          // this wave's reads
+                lds_barrier();
+            }
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bq[j][k].b, alo[i][k].b, acc[i][j], 0, 0, 0);
+#pragma unroll
+            for (int x = 0; x < 2 * kHalf; ++x)
+                if (t == x * kSlots * 3 / (8 * kHalf)) ahi[x / 2][x % 2] = ra.read(cur, kHalf + x / 2, x % 2);
+#pragma unroll
+            for (int x = 0; x < kLoadsB; ++x)
+                if (t == kFree + x * (kSlots - kFree) / kLoadsB)
+                    loss_to_lds(fb.voff[x], db,
+                                __builtin_amdgcn_readfirstlane(lds0 + cur + kA + (wave * kLoadsB + x) * 1024));
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    // the second half: the next step's fragments replace those that are done with, and the
-    // step NS ahead is loaded into this step's stage
-    auto half1 = [&](bool more, uint32_t cur, uint32_t nxt, const lu32x4& da, const lu32x4& db, int in_step) {
+    // The second half: the next step's fragments replace those that are done with, and A of
+    // the step NS ahead is loaded into this step's place.
+    auto half1 = [&](bool more, uint32_t cur, uint32_t nxt, const lu32x4& da) {
 #pragma unroll
-        for (int t = 0; t < kHalf * NJ; ++t) {
-            const int j = t / kHalf, i = t % kHalf;
-            fma16(acc[kHalf + i][j], ahi[i], bq[j]);
+        for (int t = 0; t < kSlots; ++t) {
+            const int j = t / (2 * kHalf), k = t % 2, i = t / 2 % kHalf;
+            acc[kHalf + i][j] =
+                __builtin_amdgcn_mfma_f32_16x16x32_bf16(bq[j][k].b, ahi[i][k].b, acc[kHalf + i][j], 0, 0, 0);
             if (more) {
-                if (i == kHalf - 1) bq[j] = loss_frag<LB, BN>(nxt + kA, wn * NJ + j, lane);
-                if (t % NJ == 1) alo[t / NJ] = loss_frag<LA, BM>(nxt, wm * MI + t / NJ, lane);
+                if (i == kHalf - 1) bq[j][k] = rb.read(nxt, j, k);
 #pragma unroll
-                for (int x = t * kLoads / (kHalf * NJ); x < (t + 1) * kLoads / (kHalf * NJ); ++x)
-                    issue_one(da, db, cur, in_step, x);
+                for (int x = 0; x < 2 * kHalf; ++x)
+                    if (t == x * kSlots / (2 * kHalf)) alo[x / 2][x % 2] = ra.read(nxt, x / 2, x % 2);
+#pragma unroll
+                for (int x = 0; x < kLoadsA; ++x)
+                    if (t == x * kSlots / kLoadsA + 1)
+                        loss_to_lds(fa.voff[x], da,
+                                    __builtin_amdgcn_readfirstlane(lds0 + cur + (wave * kLoadsA + x) * 1024));
             }
             __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+
+    // The rows' values are loaded before the tile's first operand loads and stored to LDS
+    // before the next tile's, so that waiting for them never waits for a prefetch.
+    int my_target = -1;
+    float my_scale = 0.0f, my_lse = 0.0f;
+    auto fetch_rows = [&](const Unit& w) {
+        if (EPI != kStats && EPI != kGrad) return;
+        const int m = w.m0 + (int)threadIdx.x;
+        my_target = -1;
+        if ((int)threadIdx.x < BM && m < g.P) {
+            const int64_t t = g.target[m];
+            if (t >= 0 && t < g.vocab) my_target = (int)t;
+            if (EPI == kGrad) {
+                my_scale = g.dloss[m];
+                my_lse = g.lse[m];
+            }
+        }
+    };
+    auto keep_rows = [&]() {
+        if ((EPI != kStats && EPI != kGrad) || (int)threadIdx.x >= BM) return;
+        row_target[threadIdx.x] = my_target;
+        if (EPI == kGrad) {
+            row_scale[threadIdx.x] = my_target < 0 ? 0.0f : my_scale;
+            row_lse[threadIdx.x] = my_target < 0 ? 0.0f : my_lse * kLossLog2e;
         }
     };
 
     int u = slot;
     if (u >= g.units) return;
     Unit w = unit_of(u);
+    fetch_rows(w);
     start(w);
     for (;;) {
 #pragma unroll
@@ -310,34 +393,41 @@ __global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
         __builtin_amdgcn_s_waitcnt(wait_loads((NS - 1) * kLoads));
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) bq[j] = loss_frag<LB, BN>(lds0 + kA, wn * NJ + j, lane);
+        for (int k = 0; k < 2; ++k) {
 #pragma unroll
-        for (int i = 0; i < kHalf; ++i) alo[i] = loss_frag<LA, BM>(lds0, wm * MI + i, lane);
-        half0(lds0);
-        uint32_t cur = lds0;
+            for (int j = 0; j < NJ; ++j) bq[j][k] = rb.read(0, j, k);
+#pragma unroll
+            for (int i = 0; i < kHalf; ++i) alo[i][k] = ra.read(0, i, k);
+        }
+        uint32_t cur = 0;                                    // the stage, in bytes from the first
+        // (past the last step its loads are repeated into places that are read no more, so
+        // that the count of loads in flight stays the same)
+        int ahead = min(NS, w.kt - 1);
+        trim(w, ahead);
+        half0(cur, fb.desc(ahead));
         for (int kt = 0; kt + 1 < w.kt; ++kt) {
-            const uint32_t nxt = cur + kStage == lds0 + NS * kStage ? lds0 : cur + kStage;
-            __builtin_amdgcn_s_waitcnt(wait_loads((NS - 2) * kLoads));   // the next step's loads of this wave
-            __syncthreads();                                 // everyone's; this stage is read
-            __builtin_amdgcn_sched_barrier(0);
-            // (past the last step its loads are repeated into stages that are read no more,
-            // so that the count of loads in flight stays the same)
-            const int ahead = min(kt + NS, w.kt - 1);
-            const lu32x4 da = fa.desc(ahead), db = fb.desc(ahead);
-            half1(true, cur, nxt, da, db, g.R - w.r0 - ahead * kStep);
-            half0(nxt);
+            const uint32_t nxt = cur + kStage == NS * kStage ? 0 : cur + kStage;
+            // the next step's loads of this wave (later: whole steps and one B), and its reads
+            __builtin_amdgcn_s_waitcnt(wait_loads((NS - 2) * kLoads + kLoadsB) & 0xF0FF);
+            lds_barrier();                                   // everyone's; this step's A is read
+            half1(true, cur, nxt, fa.desc(ahead));
+            ahead = min(kt + 1 + NS, w.kt - 1);
+            trim(w, ahead);
+            half0(nxt, fb.desc(ahead));
             cur = nxt;
         }
         __builtin_amdgcn_s_waitcnt(wait_loads(0));
         __syncthreads();
         __builtin_amdgcn_sched_barrier(0);
-        half1(false, 0, 0, lu32x4{0, 0, 0, 0}, lu32x4{0, 0, 0, 0}, 0);
+        half1(false, 0, 0, lu32x4{0, 0, 0, 0});
+        keep_rows();
         __syncthreads();
 
         const Unit done = w;
         u += G;
         if (u < g.units) {
             w = unit_of(u);
+            fetch_rows(w);
             start(w);
         }
 
@@ -352,13 +442,17 @@ __global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
                 for (int i = 0; i < MI; ++i) {
                     const int m = m_wave + 16 * i + r16;
                     float top = -kLossInf;
+                    if (n_wave + 16 * NJ > g.Q) {            // only a row's last block
+#pragma unroll
+                        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (n_wave + 16 * j + 4 * q4 + e >= g.Q) acc[i][j][e] = -kLossInf;
+                    }
 #pragma unroll
                     for (int j = 0; j < NJ; ++j)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if (n_wave + 16 * j + 4 * q4 + e >= g.Q) acc[i][j][e] = -kLossInf;
-                            top = fmaxf(top, acc[i][j][e]);
-                        }
+                        for (int e = 0; e < 4; ++e) top = fmaxf(top, acc[i][j][e]);
                     top = fmaxf(top, __shfl_xor(top, 16, 64));
                     top = fmaxf(top, __shfl_xor(top, 32, 64));
                     const float by = top == -kLossInf ? 0.0f : top * kLossLog2e;
@@ -372,8 +466,8 @@ __global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
                     s += __shfl_xor(s, 32, 64);
                     if (m < g.P) {
                         if (q4 == 0) g.stats[(int64_t)(n_wave / (16 * NJ)) * g.P + m] = make_float2(top, s);
-                        const int64_t at = g.target[m] - n_wave;
-                        if (at >= 0 && at < 16 * NJ && n_wave + at < g.Q) {
+                        const int at = row_target[m - done.m0] - n_wave;
+                        if (at >= 0 && at < 16 * NJ) {
 #pragma unroll
                             for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -414,28 +508,31 @@ __global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
                 if (EPI == kGrad) {
-                    const int m = m_wave + 16 * i + r16;
-                    float scale = 0.0f, lse2 = 0.0f;
-                    int64_t t = -1;
-                    if (m < g.P) {
-                        t = g.target[m];
-                        if (t >= 0 && t < g.vocab) {
-                            scale = g.dloss[m];
-                            lse2 = g.lse[m] * kLossLog2e;
-                        } else {
-                            t = -1;
-                        }
-                    }
-                    const int64_t at = t - g.v0 - n_wave;    // the target's column within the wave's
+                    const int row = m_wave - done.m0 + 16 * i + r16, t = row_target[row];
+                    const float scale = row_scale[row], lse2 = row_lse[row];
+                    // p dloss, 0 for a token without a target (whatever its logits are)
 #pragma unroll
                     for (int j = 0; j < NJ; ++j)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int n = 16 * j + 4 * q4 + e;
-                            float p = __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], kLossLog2e, -lse2));
-                            p = (p - (at == n ? 1.0f : 0.0f)) * scale;
-                            acc[i][j][e] = t < 0 || n_wave + n >= g.Q ? 0.0f : p;
+                            const float p = scale * __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], kLossLog2e, -lse2));
+                            acc[i][j][e] = t < 0 ? 0.0f : p;
                         }
+                    const int at = t < 0 ? -1 : t - g.v0 - n_wave;   // the target's column within the wave's
+                    if (__any(at >= 0 && at < 16 * NJ)) {
+#pragma unroll
+                        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (at == 16 * j + 4 * q4 + e) acc[i][j][e] -= scale;
+                    }
+                    if (n_wave + 16 * NJ > g.Q) {
+#pragma unroll
+                        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (n_wave + 16 * j + 4 * q4 + e >= g.Q) acc[i][j][e] = 0.0f;
+                    }
                 }
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) {
@@ -581,7 +678,7 @@ hipError_t product(LossArgs g, int rows, int splits, hipStream_t stream)
         } else {
             if (rows == 64) return launch(loss_product_kernel<4, 4, 1, 4, 3, LA, LB, EPI>, grid, dim3(256), stream, g);
         }
-        if (rows == 128) return launch(loss_product_kernel<4, 8, 2, 2, 3, LA, LB, EPI>, grid, dim3(256), stream, g);
+        if (rows == 128) return launch(loss_product_kernel<4, 8, 2, 2, 2, LA, LB, EPI>, grid, dim3(256), stream, g);
     }
     return launch(loss_product_kernel<8, 8, 2, 2, 2, LA, LB, EPI>, grid, dim3(256), stream, g);
 }
