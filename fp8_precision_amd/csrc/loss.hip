@@ -18,11 +18,12 @@
 // few tokens, where reading w bounds.  The product kernel: 256 columns by 256, 128 or
 // 64 rows per workgroup of 4 waves, one wave per SIMD; reduction steps of 64
 // elements in two LDS stages filled by 16-byte direct-to-LDS buffer loads issued a
-// step and a half ahead; v_mfma_f32_32x32x16_bf16 (its 32 cycles leave room for the
-// reads and loads issued beside it: with 16x16x32 the kernel was bound by instruction
-// issue, 1250 TFLOP/s) with fragments double-buffered in registers across a barrier in
-// the middle of a step; persistent workgroups in an
-// XCD-major walk that load the next tile's first stages before the epilogue.
+// step and more ahead; fragments double-buffered in registers across two barriers per
+// step; persistent workgroups in an XCD-major walk that load the next tile's first
+// stages before the epilogue.  The chip runs these products at its power limit, so the
+// instruction matters: v_mfma_f32_16x16x32_bf16; 32x32x16 kept the matrix units 65%
+// busy instead of 58% at the same stage of this kernel and yet ran 3% slower, its clock
+// at 1.88 GHz instead of 2.26.
 // Operands are read along the reduction ("K": x and w for the logits, g for dx) or
 // across it ("MN": w for dx, g and x for dw) through transposing LDS reads, so no
 // transposed copy of anything exists.  Rows, columns and reduction elements past an
@@ -118,13 +119,13 @@ struct Feed {
                 voff[ii] = (uint32_t)(r * (int)pitch) + (uint32_t)chunk[ii & 1] * 16u;
             }
         } else {
-            static_assert(!MN || EXT == 256, "the MN image is laid out for 256 columns");
+            constexpr int kRowLanes = EXT / 8, kRows = 64 / kRowLanes;   // lanes per row, rows per load
             base = reinterpret_cast<const uint8_t*>(s.p) + (int64_t)r0 * pitch + (int64_t)origin * 2;
             left = (int64_t)(total_r - r0) * pitch - (int64_t)origin * 2;
 #pragma unroll
             for (int ii = 0; ii < kLoads; ++ii) {
-                const int r = wave * 16 + ii * 2 + (lane >> 5);
-                const int c = (lane & 31) ^ ((r & 3) << 1 | (r >> 3 & 1) << 3);
+                const int r = wave * 16 + ii * kRows + lane / kRowLanes;
+                const int c = (lane % kRowLanes) ^ ((r & 3) << 1 | (r >> 3 & 1) << 3);
                 voff[ii] = origin + c * 8 < extent ? (uint32_t)(r * (int)pitch) + (uint32_t)c * 16u : (uint32_t)kOutside;
             }
         }
@@ -204,6 +205,8 @@ struct LossArgs {
     int P, Q, R;                          // rows, columns, reduction
     int tiles_m, tiles_n, units;          // units: tiles * splits
     int steps, per;                       // reduction steps in all and per split
+    int first, halves;                    // halves: this launch's units are the two 128-row halves of
+                                          // the 256-row units from `first` on
     // statistics and gradient
     const int64_t* target;
     const float* lse;
@@ -216,7 +219,7 @@ struct LossArgs {
     int64_t out_pitch;
     int out_cols;                         // g: columns written (Q rounded up; those past Q get 0)
     float* sum;                           // [splits][P][Q] fp32 partial dx
-    int first, last;                      // sum: nothing to add to yet; write bf16 to out
+    int fresh, last;                      // sum: nothing to add to yet; write bf16 to out
 };
 
 struct Unit {
@@ -225,9 +228,14 @@ struct Unit {
 
 }  // namespace
 
+namespace {
+// Workgroups per CU: two where the accumulators are small.
+constexpr int loss_per_cu(int mi, int nj) { return mi * nj <= 16 ? 2 : 1; }
+}  // namespace
+
 // MI x NJ blocks of 16 x 16 per wave, GM x GN waves, NS stages.
 template <int MI, int NJ, int GM, int GN, int NS, bool LA, bool LB, int EPI>
-__global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
+__global__ void __launch_bounds__(256, loss_per_cu(MI, NJ)) loss_product_kernel(const LossArgs g)
 {
     constexpr int BM = 16 * MI * GM, BN = 16 * NJ * GN;
     static_assert(GM * GN == 4, "four waves");
@@ -250,13 +258,14 @@ __global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
 
     auto unit_of = [&](int u) {
         Unit w;
-        const int tiles = g.tiles_m * g.tiles_n;
-        w.split = u / tiles;
-        const int t = u - w.split * tiles;
+        const int tiles = g.tiles_m * g.tiles_n, id = g.halves ? g.first + u / 2 : u;
+        w.split = id / tiles;
+        const int t = id - w.split * tiles;
         // groups of 8 tile rows, each walked column by column: 32 neighbours are 8 x 4 tiles
         const int group = t / (8 * g.tiles_n), in = t - group * 8 * g.tiles_n;
         const int rows = min(8, g.tiles_m - group * 8);
         w.m0 = (group * 8 + in % rows) * BM;
+        if (g.halves) w.m0 = 2 * w.m0 + (u & 1) * BM;
         w.n0 = (in / rows) * BN;
         const int s0 = w.split * g.per;
         w.r0 = s0 * kStep;
@@ -282,8 +291,10 @@ __global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
         }
     };
     auto start = [&](const Unit& w) {
-        fa.init(g.a, w.m0, g.P, g.R, w.r0, wave, lane);
-        fb.init(g.b, w.n0, g.Q, g.R, w.r0, wave, lane);
+        int ln = lane;
+        asm volatile("" : "+v"(ln));      // what follows from the lane is computed per tile, not held across them
+        fa.init(g.a, w.m0, g.P, g.R, w.r0, wave, ln);
+        fb.init(g.b, w.n0, g.Q, g.R, w.r0, wave, ln);
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
             const int kt = min(s, w.kt - 1);
@@ -431,6 +442,18 @@ __global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
             start(w);
         }
 
+        // Sums of rows i and up stay in accumulation registers until row i is taken: moved
+        // earlier (as the compiler would) they spill what the next tile's loads need.
+        auto hold = [&](int i) {
+            if constexpr (MI * NJ == 64) {
+#pragma unroll
+                for (int x = 0; x < MI; ++x)
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j)
+                        if (x >= i) asm volatile("" : "+a"(acc[x][j]));
+            }
+        };
+        hold(0);
         // lane: row 16 i + lane % 16 of the wave's tile, columns 16 j + 4 (lane / 16) + e
         int ln = lane;
         asm volatile("" : "+v"(ln));
@@ -440,6 +463,7 @@ __global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
             if (n_wave < g.Q) {
 #pragma unroll
                 for (int i = 0; i < MI; ++i) {
+                    hold(i);
                     const int m = m_wave + 16 * i + r16;
                     float top = -kLossInf;
                     if (n_wave + 16 * NJ > g.Q) {            // only a row's last block
@@ -481,6 +505,7 @@ __global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
             float* sum = g.sum + (int64_t)done.split * g.P * g.Q;
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
+                hold(i);
                 const int m = m_wave + 16 * i + r16;
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) {
@@ -488,7 +513,7 @@ __global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
                     if (m < g.P && n < g.Q) {               // Q is a multiple of 8: 4 columns at a time
                         float4* at = reinterpret_cast<float4*>(sum + (int64_t)m * g.Q + n);
                         float4 v = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
-                        if (!g.first) {
+                        if (!g.fresh) {
                             const float4 o = *at;
                             v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
                         }
@@ -507,6 +532,7 @@ __global__ void __launch_bounds__(256, 1) loss_product_kernel(const LossArgs g)
             const int cols = EPI == kGrad ? g.out_cols : g.Q;
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
+                hold(i);
                 if (EPI == kGrad) {
                     const int row = m_wave - done.m0 + 16 * i + r16, t = row_target[row];
                     const float scale = row_scale[row], lse2 = row_lse[row];
@@ -621,14 +647,15 @@ int column_block(int rows) { return rows == 64 ? 32 : 128; }       // a wave's c
 
 int64_t up_to(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 
-// The backward pass's pieces of the vocabulary: as many columns as keep g at or under
-// 128 MiB (it stays in the Infinity Cache between the launch that writes it and the two
-// that read it), at least 4096, whole tiles.
+// The backward pass's pieces of the vocabulary: as few as keep a piece's g at or under
+// 256 MiB (or 4096 columns), of one size, whole tiles.  Fewer pieces read and write the
+// fp32 sums of dx less often: 8192 tokens, 65521 x 5120, in pieces of 128 / 256 / 512 MiB
+// took 12.56 / 12.19 / 12.07 ms; the workspace is what larger ones cost.
 int64_t piece_columns(int64_t T, int64_t V)
 {
-    int64_t c = ((int64_t)128 << 20) / (2 * T) / 256 * 256;
-    c = std::max<int64_t>(c, 4096);
-    return std::min(c, up_to(V, 256));
+    const int64_t most = std::max<int64_t>(4096, ((int64_t)256 << 20) / (2 * T));
+    const int64_t pieces = (V + most - 1) / most;
+    return up_to((V + pieces - 1) / pieces, 256);
 }
 
 // dx has T / rows x D / 256 tiles; where they would leave CUs idle its reduction over
@@ -661,26 +688,50 @@ Space backward_space(int64_t T, int64_t V, int64_t D)
     return s;
 }
 
+template <int MI, int NJ, int GM, int GN, int NS, bool LA, bool LB, int EPI>
+hipError_t launch_product(const LossArgs& g, hipStream_t stream)
+{
+    const int grid = std::min(g.units, device_cu_count() * loss_per_cu(MI, NJ));
+    return launch(loss_product_kernel<MI, NJ, GM, GN, NS, LA, LB, EPI>, dim3((unsigned)grid), dim3(256), stream, g);
+}
+
+// Which tiles a product runs on.  Few rows (64 or 128) take tiles of as many.  256-row
+// tiles run in rounds of one per CU; when those past the last full round would fill at
+// most half of one, they run as halves in a launch of their own (8192 x 8192 x 5120, 640
+// tiles: 2.5 rounds instead of 3).
 template <bool LA, bool LB, int EPI>
 hipError_t product(LossArgs g, int rows, int splits, hipStream_t stream)
 {
+    const bool narrow = !LB && rows == 64;               // logits of few tokens: 64 x 128
+    const bool shallow = LA && rows == 128;              // dw of few tokens: 128 x 128
+    const int cols = narrow || shallow ? 128 : 256;
     g.tiles_m = (g.P + rows - 1) / rows;
-    const bool narrow = !LA && !LB && rows == 64;
-    const int cols = narrow ? 128 : 256;
     g.tiles_n = (g.Q + cols - 1) / cols;
     g.steps = (g.R + kStep - 1) / kStep;
     g.per = (g.steps + splits - 1) / splits;
     g.units = g.tiles_m * g.tiles_n * ((g.steps + g.per - 1) / g.per);
-    const dim3 grid((unsigned)std::min(g.units, device_cu_count()));
     if constexpr (!LA) {
         if constexpr (!LB) {
-            if (narrow) return launch(loss_product_kernel<4, 2, 1, 4, 6, LA, LB, EPI>, grid, dim3(256), stream, g);
+            if (rows == 64) return launch_product<4, 2, 1, 4, 3, LA, LB, EPI>(g, stream);
         } else {
-            if (rows == 64) return launch(loss_product_kernel<4, 4, 1, 4, 3, LA, LB, EPI>, grid, dim3(256), stream, g);
+            if (rows == 64) return launch_product<4, 4, 1, 4, 2, LA, LB, EPI>(g, stream);
         }
-        if (rows == 128) return launch(loss_product_kernel<4, 8, 2, 2, 2, LA, LB, EPI>, grid, dim3(256), stream, g);
+        if (rows == 128) return launch_product<4, 8, 2, 2, 2, LA, LB, EPI>(g, stream);
+    } else {
+        if (rows == 128) return launch_product<4, 4, 2, 2, 2, LA, LB, EPI>(g, stream);
     }
-    return launch(loss_product_kernel<8, 8, 2, 2, 2, LA, LB, EPI>, grid, dim3(256), stream, g);
+    const int cus = device_cu_count(), tail = g.units % cus;
+    const bool split = tail > 0 && 2 * tail <= cus;
+    const int whole = split ? g.units - tail : g.units;
+    if (whole > 0) {
+        g.units = whole;
+        const hipError_t e = launch_product<8, 8, 2, 2, 2, LA, LB, EPI>(g, stream);
+        if (e != hipSuccess || !split) return e;
+    }
+    g.first = whole;
+    g.halves = 1;
+    g.units = 2 * tail;
+    return launch_product<4, 8, 2, 2, 2, LA, LB, EPI>(g, stream);
 }
 
 }  // namespace
@@ -754,7 +805,7 @@ hipError_t launch_loss_backward(const float* dloss, const void* x, const void* w
         d.sum = sum;
         d.out = static_cast<uint16_t*>(dx);
         d.out_pitch = D;
-        d.first = v0 == 0;
+        d.fresh = v0 == 0;
         d.last = splits == 1 && v0 + n == V;
         e = product<false, true, kSum>(d, rows, splits, stream);
         if (e != hipSuccess) return e;
@@ -767,7 +818,7 @@ hipError_t launch_loss_backward(const float* dloss, const void* x, const void* w
         h.R = (int)T;
         h.out = static_cast<uint16_t*>(dw) + v0 * D;
         h.out_pitch = D;
-        e = product<true, true, kStore>(h, 256, 1, stream);
+        e = product<true, true, kStore>(h, T <= kStep ? 128 : 256, 1, stream);
         if (e != hipSuccess) return e;
     }
     if (splits > 1) {
