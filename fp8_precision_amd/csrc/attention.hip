@@ -151,38 +151,46 @@ struct Stream {
     }
 };
 
-// Operand reads from a tile in LDS.  rows(): the tile's rows as the product's rows,
-// the head dimension reduced (chunk c: elements 16 c ..).  cols(): the tile's columns
-// (32 of the head dimension, block db) as the product's rows, 16 of its rows reduced,
-// in the order that the score registers have.
+// Operand reads from tiles in LDS.  rows(): a tile's rows as the product's rows, the
+// head dimension reduced (chunk c: elements 16 c ..).  cols(): its columns (32 of the
+// head dimension, block db) as the product's rows, 16 of its rows reduced, in the
+// order that the score registers have.  A lane keeps one address per c and per (db,
+// half), relative to which every tile, stage and block is a constant: the tiles of a
+// kernel lie within the 64 KB that an LDS instruction's offset reaches.
 template <int DT>
 struct Tile {
     static constexpr int kRow = DT * 2;
     static constexpr int kCh = DT / 8;
-    uint32_t plain, trans;                // this lane's addresses for c = 0 and for db = 0
+    uint32_t plain[DT / 16], trans[DT / 32][2];
 
     __device__ __forceinline__ void init(uint32_t lds)
     {
         const int lane = threadIdx.x & 63, h = lane >> 5;
         const int r = lane & 31;
-        plain = lds + r * kRow + ((h ^ spread<kCh>(r)) * 16);
+#pragma unroll
+        for (int c = 0; c < DT / 16; ++c) plain[c] = lds + r * kRow + (((2 * c + h) ^ spread<kCh>(r)) * 16);
         const int t = 4 * h + ((lane & 15) >> 2);
-        trans = lds + t * kRow + (((2 * (lane >> 4 & 1) + (lane & 3) / 2) ^ spread<kCh>(t)) * 16) + (lane & 1) * 8;
+#pragma unroll
+        for (int db = 0; db < DT / 32; ++db)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                trans[db][i] = lds + (t + 8 * i) * kRow +
+                               (((4 * db + 2 * (lane >> 4 & 1) + (lane & 3) / 2) ^ spread<kCh>(t + 8 * i)) * 16) +
+                               (lane & 1) * 8;
     }
-    __device__ __forceinline__ Frag rows(uint32_t at, int block, int c) const
+    // at: the tile's constant offset
+    __device__ __forceinline__ Frag rows(int at, int block, int c) const
     {
         Frag f;
-        f.u = *(const lds_u32x4*)(uintptr_t)((plain ^ (uint32_t)(c * 32)) + at + block * 32 * kRow);
+        f.u = *((const lds_u32x4*)(uintptr_t)plain[c] + (at + block * 32 * kRow) / 16);
         return f;
     }
-    __device__ __forceinline__ Frag cols(uint32_t at, int block, int c, int db) const
+    __device__ __forceinline__ Frag cols(int at, int block, int c, int db) const
     {
-        // 8 rows on, spread() differs in its bit 1 (chunk bit 1: 32 bytes)
-        const uint32_t a = (trans ^ (uint32_t)(db * 64)) + at + (block * 32 + c * 16) * kRow;
-        const uint32_t b = (trans ^ (uint32_t)(db * 64) ^ 32u) + at + (block * 32 + c * 16 + 8) * kRow;
+        const int off = (at + (block * 32 + c * 16) * kRow) / 8;
         Frag f;
-        f.s.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)a);
-        f.s.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)b);
+        f.s.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)trans[db][0] + off);
+        f.s.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)trans[db][1] + off);
         return f;
     }
 };
@@ -356,34 +364,38 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_forward_kernel(const
         ks.issue(0, lds0, wave);
         vs.issue(0, lds0 + kTile, wave);
     }
-    for (int s = 0; s < steps; ++s) {
-        const uint32_t at = (uint32_t)(s & 1) * 2 * kTile;
+    auto step = [&](auto stage, int s) {
+        constexpr int at = stage.value * 2 * kTile, to = (2 - stage.value * 2) * kTile;
         __builtin_amdgcn_s_waitcnt(0x0F70);                // this wave's loads of tile s have landed
         __syncthreads();                                   // everyone's; tile s - 1 is read
         if (s + 1 < steps) {
-            const uint32_t to = lds0 + (uint32_t)((s + 1) & 1) * 2 * kTile;
-            ks.issue((s + 1) * kKeys, to, wave);
-            vs.issue((s + 1) * kKeys, to + kTile, wave);
+            ks.issue((s + 1) * kKeys, lds0 + to, wave);
+            vs.issue((s + 1) * kKeys, lds0 + to + kTile, wave);
         }
         const int j0 = s * kKeys;
-        if (j0 >= see_last) continue;                      // nothing of this tile is seen by the wave
+        if (j0 >= see_last) return;                        // nothing of this tile is seen by the wave
         af32x16 p[2] = {af32x16{0}, af32x16{0}};
 #pragma unroll
         for (int ch = 0; ch < DT / 16; ++ch)
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) p[kb] = mma(tile.rows(at, kb, ch), q[ch], p[kb]);
         if (j0 + kKeys > see_first) {
+            const int see0 = see - j0 - 4 * h;             // register i: key 32 kb + 8 (i / 4) + i % 4 of what is left
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    if (j0 + 32 * kb + 8 * (i / 4) + 4 * h + i % 4 >= see) p[kb][i] = -kInf;
+                    if (32 * kb + 8 * (i / 4) + i % 4 >= see0) p[kb][i] = -kInf;
         }
-        float top = -kInf;
+        float tops[4];
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
+        for (int x = 0; x < 4; ++x) {
+            tops[x] = fmaxf(p[x / 2][8 * (x % 2)], p[x / 2][8 * (x % 2) + 1]);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, p[kb][i]);
+            for (int i = 2; i < 8; i += 2)
+                tops[x] = fmaxf(fmaxf(tops[x], p[x / 2][8 * (x % 2) + i]), p[x / 2][8 * (x % 2) + i + 1]);
+        }
+        float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
         top = fmaxf(top, partner(top));
         if (__any(top > m + far)) {                        // m = -inf: any seen key
             const float up = fmaxf(m, top);
@@ -397,15 +409,14 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_forward_kernel(const
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[db][i] *= by;
         }
+        float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
+        for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 p[kb][i] = __builtin_amdgcn_exp2f(fmaf(p[kb][i], c, -mc));
-                l += p[kb][i];
+                sums[i % 4] += p[kb][i];
             }
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
             Frag f[2];
             to_operands(p[kb], f);
 #pragma unroll
@@ -414,6 +425,11 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_forward_kernel(const
                 for (int db = 0; db < DT / 32; ++db)
                     o[db] = mma(tile.cols(at + kTile, kb, ch, db), f[ch], o[db]);
         }
+        l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+    };
+    for (int s = 0; s < steps; s += 2) {
+        step(std::integral_constant<int, 0>{}, s);
+        if (s + 1 < steps) step(std::integral_constant<int, 1>{}, s + 1);
     }
 
     l += partner(l);
@@ -501,17 +517,16 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dq_kernel(const Atte
         ks.issue(0, lds0, wave);
         vs.issue(0, lds0 + kTile, wave);
     }
-    for (int s = 0; s < steps; ++s) {
-        const uint32_t at = (uint32_t)(s & 1) * 2 * kTile;
+    auto step = [&](auto stage, int s) {
+        constexpr int at = stage.value * 2 * kTile, to = (2 - stage.value * 2) * kTile;
         __builtin_amdgcn_s_waitcnt(0x0F70);
         __syncthreads();
         if (s + 1 < steps) {
-            const uint32_t to = lds0 + (uint32_t)((s + 1) & 1) * 2 * kTile;
-            ks.issue((s + 1) * kKeys, to, wave);
-            vs.issue((s + 1) * kKeys, to + kTile, wave);
+            ks.issue((s + 1) * kKeys, lds0 + to, wave);
+            vs.issue((s + 1) * kKeys, lds0 + to + kTile, wave);
         }
         const int j0 = s * kKeys;
-        if (j0 >= see_last) continue;
+        if (j0 >= see_last) return;
         const bool masked = j0 + kKeys > see_first;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
@@ -527,9 +542,10 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dq_kernel(const Atte
                 dp[i] = p[i] * (dp[i] - delta);
             }
             if (masked) {
+                const int see0 = see - j0 - 4 * h;
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    if (j0 + 32 * kb + 8 * (i / 4) + 4 * h + i % 4 >= see) dp[i] = 0.0f;
+                    if (32 * kb + 8 * (i / 4) + i % 4 >= see0) dp[i] = 0.0f;
             }
             Frag f[2];
             to_operands(dp, f);
@@ -538,6 +554,10 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dq_kernel(const Atte
 #pragma unroll
                 for (int db = 0; db < DT / 32; ++db) dq[db] = mma(tile.cols(at, kb, ch, db), f[ch], dq[db]);
         }
+    };
+    for (int s = 0; s < steps; s += 2) {
+        step(std::integral_constant<int, 0>{}, s);
+        if (s + 1 < steps) step(std::integral_constant<int, 1>{}, s + 1);
     }
     const uint32_t top = store_own<DT>(dq, a.scale, a.dq + (int64_t)(pl.q0 + qi) * a.dq_row + (int64_t)head * a.dq_head,
                                        a.d, mine);
@@ -578,9 +598,9 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dkv_kernel(const Att
 
     Frag k[DT / 16];
     load_own<DT>(k, a.k + (int64_t)(pl.k0 + ki) * a.k_row + (int64_t)khead * a.k_head, a.d, mine);
-    Tile<DT> own, tile;
-    own.init(lds0 + wave * 32 * DT * 2);
-    tile.init(ring);
+    Tile<DT> tile;
+    tile.init(lds0);
+    const uint32_t own = (uint32_t)(wave * 32 * DT * 2);   // the wave's values within the fixed tile
     Stream<DT, kQueries> qs, gs;
     qs.init(a.q + (int64_t)pl.q0 * a.q_row, a.q_row, pl.nq, a.d);
     gs.init(a.dout + (int64_t)pl.q0 * a.dout_row, a.dout_row, pl.nq, a.d);
@@ -616,9 +636,9 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dkv_kernel(const Att
         vs.issue(pl.first, lds0, wave);
         issue(0);
     }
-    for (int s = 0; s < steps; ++s) {
-        const uint32_t at = (uint32_t)(s & 1) * 2 * kTile;
-        if (wave == 0) stat[s & 1][h][lane & 31] = next;
+    auto step = [&](auto stage, int s) {
+        constexpr int at = kOwnTile + stage.value * 2 * kTile;
+        if (wave == 0) stat[stage.value][h][lane & 31] = next;
         __builtin_amdgcn_s_waitcnt(0x0F70);
         __syncthreads();
         if (s + 1 < steps) {
@@ -626,18 +646,20 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dkv_kernel(const Att
             issue(s + 1);
         }
         const int i0 = (begin + s % per) * kQueries;
-        if (i0 + kQueries <= from_first) continue;         // no query of the tile sees a key of the wave
+        if (i0 + kQueries <= from_first) return;           // no query of the tile sees a key of the wave
         af32x16 p = af32x16{0}, dp = af32x16{0};
 #pragma unroll
         for (int ch = 0; ch < DT / 16; ++ch) {
+            Frag v;
+            v.u = *(const lds_u32x4*)(uintptr_t)(tile.plain[ch] + own);
             p = mma(tile.rows(at, 0, ch), k[ch], p);
-            dp = mma(tile.rows(at + kTile, 0, ch), own.rows(0, 0, ch), dp);
+            dp = mma(tile.rows(at + kTile, 0, ch), v, dp);
         }
         const bool masked = i0 < from_last || k_wave + 32 > pl.nk;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const float4 ls = *reinterpret_cast<const float4*>(&stat[s & 1][0][8 * b + 4 * h]);
-            const float4 de = *reinterpret_cast<const float4*>(&stat[s & 1][1][8 * b + 4 * h]);
+            const float4 ls = *reinterpret_cast<const float4*>(&stat[stage.value][0][8 * b + 4 * h]);
+            const float4 de = *reinterpret_cast<const float4*>(&stat[stage.value][1][8 * b + 4 * h]);
             const float lsv[4] = {ls.x, ls.y, ls.z, ls.w}, dev[4] = {de.x, de.y, de.z, de.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -647,9 +669,10 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dkv_kernel(const Att
             }
         }
         if (masked) {
+            const int from0 = mine ? from - i0 - 4 * h : kQueries;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                if (!mine || i0 + 8 * (i / 4) + 4 * h + i % 4 < from) p[i] = dp[i] = 0.0f;
+                if (8 * (i / 4) + i % 4 < from0) p[i] = dp[i] = 0.0f;
         }
         Frag f[2], e[2];
         to_operands(p, f);
@@ -661,6 +684,10 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dkv_kernel(const Att
                 dv[db] = mma(tile.cols(at + kTile, 0, ch, db), f[ch], dv[db]);
                 dk[db] = mma(tile.cols(at, 0, ch, db), e[ch], dk[db]);
             }
+    };
+    for (int s = 0; s < steps; s += 2) {
+        step(std::integral_constant<int, 0>{}, s);
+        if (s + 1 < steps) step(std::integral_constant<int, 1>{}, s + 1);
     }
     uint32_t top = store_own<DT>(dk, a.scale, a.dk + (int64_t)(pl.k0 + ki) * a.dk_row + (int64_t)khead * a.dk_head, a.d, mine);
     top = max(top, store_own<DT>(dv, 1.0f, a.dv + (int64_t)(pl.k0 + ki) * a.dv_row + (int64_t)khead * a.dv_head, a.d, mine));
