@@ -811,7 +811,11 @@ fp8_status fp8_attention_forward(const fp8_attention_shape* shape, const fp8_hea
     return FP8_OK;
 }
 
-static int64_t attention_workspace(const fp8_attention_shape& s) { return 2 * 4 * s.heads_q * s.tokens_q; }
+static int64_t attention_workspace(const fp8_attention_shape& s)
+{
+    return fp8k::attention_backward_workspace(s.tokens_q, s.tokens_k, (int)s.heads_q, (int)s.heads_k, (int)s.head_dim,
+                                              (int)s.batch);
+}
 
 fp8_status fp8_attention_backward_workspace(const fp8_attention_shape* shape, int64_t* bytes)
 {

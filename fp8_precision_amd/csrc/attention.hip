@@ -36,6 +36,8 @@
 // chunk c ^ f(r): with f's low row bits in the high chunk bits, the 4-row pieces
 // of the transposing reads and the 16-row columns of the plain reads both spread
 // over all banks.
+#include <algorithm>
+
 #include "fp8_device.hpp"
 #include "fp8_internal.hpp"
 
@@ -51,11 +53,12 @@ typedef short as16x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int au32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) as16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) au32x4 lds_u32x4;
-typedef __attribute__((address_space(3))) float lds_f32;
+typedef float af32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) af32x4 lds_f32x4;
 
 constexpr int kAttThreads = 256;
 constexpr int kAttWaves = 4;
-constexpr int kOwn = 128;                 // queries (or keys) a workgroup keeps: 32 per wave
+constexpr int kOwn = 128;                 // queries a workgroup keeps: 32 per wave
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kInf = __builtin_inff();
@@ -103,6 +106,18 @@ __device__ __forceinline__ void buffer_to_lds(uint32_t voff, const au32x4& desc,
                  : "memory", "m0");
 }
 
+// The same with 4 bytes per lane (LDS bytes lds + 4 L).
+__device__ __forceinline__ void buffer4_to_lds(uint32_t voff, const au32x4& desc, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dword %0, %1, 0 offen lds"
+                 :
+                 : "v"(voff), "s"(desc), "s"(lds)
+                 : "memory", "m0");
+}
+
+// s_waitcnt immediate: at most n vector memory operations in flight.
+constexpr int wait_loads(int n) { return 0x0F70 | (n & 15) | (n >> 4) << 14; }
+
 __device__ __forceinline__ au32x4 descriptor(const uint8_t* base, int64_t bytes)
 {
     const uint64_t b = (uint64_t)base;
@@ -116,12 +131,13 @@ __device__ __forceinline__ au32x4 descriptor(const uint8_t* base, int64_t bytes)
 }
 
 // Streams ROWS-row tiles of one head's rows [0, n) of a packed tensor into LDS.
-template <int DT, int ROWS>
+template <int DT, int ROWS, int WAVES = kAttWaves>
 struct Stream {
     static constexpr int kRow = DT * 2;                        // bytes of a tile row
     static constexpr int kCh = DT / 8;                         // its 16-byte chunks
     static constexpr int kPer = 64 / kCh;                      // rows per wave and load
-    static constexpr int kLoads = ROWS / (kPer * kAttWaves);   // loads per wave and tile
+    static constexpr int kLoads = ROWS / (kPer * WAVES);       // loads per wave and tile
+    static_assert(kLoads * kPer * WAVES == ROWS, "whole loads");
     const uint8_t* base;
     int64_t stride;                       // bytes between rows
     int n;
@@ -242,6 +258,23 @@ __device__ __forceinline__ uint32_t store_own(const af32x16 (&acc)[DT / 32], flo
     return top;
 }
 
+// The same row as fp32 partial sums.
+template <int DT>
+__device__ __forceinline__ void store_partial(const af32x16 (&acc)[DT / 32], float* row, int d, bool valid)
+{
+    const int h = (threadIdx.x & 63) >> 5;
+    if (!valid) return;
+#pragma unroll
+    for (int db = 0; db < DT / 32; ++db)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int at = 32 * db + 8 * b + 4 * h;
+            if (at < d)
+                *reinterpret_cast<float4*>(row + at) =
+                    make_float4(acc[db][4 * b], acc[db][4 * b + 1], acc[db][4 * b + 2], acc[db][4 * b + 3]);
+        }
+}
+
 // Which rows a workgroup keeps: tile `t` of the tiles of all sequences, in order.
 struct Place {
     int q0, nq, k0, nk;       // the sequence's queries and keys within the packed tensors
@@ -264,7 +297,7 @@ __device__ __forceinline__ void bounds(const int* cu, int i, int total, int& fro
 
 // Every lane takes a sequence, 64 at a time; a prefix sum over the wave finds the one
 // that holds tile t.  `own` is the side that is tiled (0: queries, 1: keys).
-__device__ __forceinline__ Place find_tile(const AttentionArgs& a, int t, int own)
+__device__ __forceinline__ Place find_tile(const AttentionArgs& a, int t, int own, int rows = kOwn)
 {
     const int lane = threadIdx.x & 63;
     Place p{};
@@ -272,7 +305,7 @@ __device__ __forceinline__ Place find_tile(const AttentionArgs& a, int t, int ow
     for (int b0 = 0; b0 < a.batch; b0 += 64) {
         int from = 0, count = 0;
         if (b0 + lane < a.batch) bounds(own ? a.cu_k : a.cu_q, b0 + lane, own ? a.tk : a.tq, from, count);
-        const int tiles = (count + kOwn - 1) / kOwn;
+        const int tiles = (count + rows - 1) / rows;
         int upto = tiles;
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1) {
@@ -284,7 +317,7 @@ __device__ __forceinline__ Place find_tile(const AttentionArgs& a, int t, int ow
             const int l = __ffsll((unsigned long long)past) - 1;
             const int seq = __builtin_amdgcn_readfirstlane(b0 + l);
             const int tile = t - before - __shfl(upto - tiles, l, 64);
-            p.first = __builtin_amdgcn_readfirstlane(tile * kOwn);
+            p.first = __builtin_amdgcn_readfirstlane(tile * rows);
             bounds(a.cu_q, seq, a.tq, p.q0, p.nq);
             bounds(a.cu_k, seq, a.tk, p.k0, p.nk);
             p.q0 = __builtin_amdgcn_readfirstlane(p.q0);
@@ -443,33 +476,9 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_forward_kernel(const
 
 // ---------------------------------------------------------------------- backward
 
-// stats[0][head][token] = lse in powers of two (+inf where the row is empty, so that
-// every p of it is 0), stats[1][head][token] = delta.  16 lanes per (token, head).
-__global__ void __launch_bounds__(256) attention_delta_kernel(const AttentionArgs a)
-{
-    const int64_t unit = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-    const int part = threadIdx.x & 15;
-    const int64_t all = (int64_t)a.tq * a.hq;
-    const int token = (int)(unit / a.hq), head = (int)(unit % a.hq);
-    float t = 0.0f;
-    if (unit < all && part * 8 < a.d) {
-        const uint4 o = *reinterpret_cast<const uint4*>(a.out + (int64_t)token * a.out_row + (int64_t)head * a.out_head + part * 8);
-        const uint4 g = *reinterpret_cast<const uint4*>(a.dout + (int64_t)token * a.dout_row + (int64_t)head * a.dout_head + part * 8);
-        const uint32_t ow[4] = {o.x, o.y, o.z, o.w}, gw[4] = {g.x, g.y, g.z, g.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) t = fmaf(bf16_lo(ow[i]), bf16_lo(gw[i]), fmaf(bf16_hi(ow[i]), bf16_hi(gw[i]), t));
-    }
-#pragma unroll
-    for (int off = 8; off >= 1; off >>= 1) t += __shfl_xor(t, off, 16);
-    if (unit < all && part == 0) {
-        const int64_t at = (int64_t)head * a.tq + token;
-        const float lse = a.lse[at];
-        a.stats[at] = lse == -kInf ? kInf : lse * kLog2e;
-        a.stats[all + at] = t;
-    }
-}
-
-// dq: 32 queries per wave, keys and values streamed.
+// dq: 32 queries per wave, keys and values streamed.  A wave first takes its queries'
+// delta and leaves it for the dk/dv kernel: stats[0][head][token] = lse in powers of two
+// (+inf where the row is empty, so that every p of it is 0), stats[1][head][token] = delta.
 template <int DT>
 __global__ void __launch_bounds__(kAttThreads, 2) attention_dq_kernel(const AttentionArgs a)
 {
@@ -497,10 +506,21 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dq_kernel(const Atte
     load_own<DT>(q, a.q + (int64_t)(pl.q0 + qi) * a.q_row + (int64_t)head * a.q_head, a.d, mine);
     load_own<DT>(g, a.dout + (int64_t)(pl.q0 + qi) * a.dout_row + (int64_t)head * a.dout_head, a.d, mine);
     float lse = kInf, delta = 0.0f;
-    if (mine) {
-        const int64_t at = (int64_t)head * a.tq + pl.q0 + qi;
-        lse = a.stats[at];
-        delta = a.stats[(int64_t)a.tq * a.hq + at];
+    {
+        Frag o[DT / 16];
+        load_own<DT>(o, a.out + (int64_t)(pl.q0 + qi) * a.out_row + (int64_t)head * a.out_head, a.d, mine);
+#pragma unroll
+        for (int ch = 0; ch < DT / 16; ++ch)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                delta = fmaf(bf16_lo(o[ch].w[i]), bf16_lo(g[ch].w[i]), fmaf(bf16_hi(o[ch].w[i]), bf16_hi(g[ch].w[i]), delta));
+        delta += partner(delta);
+        if (mine) {
+            const int64_t at = (int64_t)head * a.tq + pl.q0 + qi;
+            lse = a.lse[at];
+            lse = lse == -kInf ? kInf : lse * kLog2e;
+            a.stats[(h ? (int64_t)a.tq * a.hq : 0) + at] = h ? delta : lse;
+        }
     }
 
     Stream<DT, kKeys> ks, vs;
@@ -565,24 +585,34 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dq_kernel(const Atte
 }
 
 constexpr int kQueries = 32;              // queries per streamed tile, dk/dv
+constexpr int kRing = 4;                  // stages of them
+constexpr int keys_waves(int dt) { return dt == 128 ? 8 : 4; }
 
 // dk, dv: 32 keys per wave; the queries of every head that shares the key head are
-// streamed, with their dout, lse and delta.  A wave's keys stay in registers; its
-// values are read from a third, fixed tile in LDS (keeping them in registers too
-// would leave the two accumulators no room at two waves per SIMD).
+// streamed, with their dout, lse and delta, three tiles ahead.  A wave's keys stay in
+// registers; its values are read from a fixed tile in LDS (keeping them in registers too
+// would leave the two accumulators no room at two waves per SIMD).  At head dimension 128
+// a workgroup is 8 waves: they share each streamed tile, and the LDS of two workgroups of
+// 4 makes room for the ring (with two stages of it, and a barrier to each 32 queries, the
+// waves waited for their loads for half of the time).
+// chunks > 1: the steps are dealt over that many workgroups, each of which leaves fp32
+// partial sums [chunk][dk, dv][token][head][d].
 template <int DT>
-__global__ void __launch_bounds__(kAttThreads, 2) attention_dkv_kernel(const AttentionArgs a)
+__global__ void __launch_bounds__(64 * keys_waves(DT), 2) attention_dkv_kernel(const AttentionArgs a)
 {
-    constexpr int kTile = kQueries * DT * 2, kOwnTile = kOwn * DT * 2;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[kOwnTile + 4 * kTile];
-    __shared__ float stat[2][2][kQueries];                // [stage][lse, delta][query]
-    int t, khead;
-    deal(blockIdx.x, a.hk, t, khead);
-    const Place pl = find_tile(a, t, 1);                   // a sequence's first keys are seen by most
+    constexpr int WAVES = keys_waves(DT), kMine = 32 * WAVES;
+    constexpr int kTile = kQueries * DT * 2, kOwnTile = kMine * DT * 2, kStat = 512;
+    using Q = Stream<DT, kQueries, WAVES>;
+    constexpr int kLoads = 2 * Q::kLoads + 1;              // per wave and step
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing * 2 * kTile + kOwnTile + kRing * kStat];
+    int t, unit;
+    deal(blockIdx.x, a.hk * a.chunks, t, unit);
+    const int khead = unit / a.chunks, chunk = unit % a.chunks;
+    const Place pl = find_tile(a, t, 1, kMine);            // a sequence's first keys are seen by most
     if (!pl.any) return;
     const int lane = threadIdx.x & 63, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t lds0 = (uint32_t)(uintptr_t)lds, ring = lds0 + kOwnTile;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)lds, stat0 = lds0 + kRing * 2 * kTile + kOwnTile;
     const int group = a.hq / a.hk;
 
     const int k_wave = pl.first + wave * 32, ki = k_wave + (lane & 31);
@@ -594,59 +624,52 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dkv_kernel(const Att
     const int from_last = a.causal ? max(0, k_wave + 31 - shift) : 0;
     const int begin = a.causal ? max(0, pl.first - shift) / kQueries : 0;
     const int last = (pl.nq + kQueries - 1) / kQueries;
-    const int per = max(0, last - begin), steps = per * group;
+    const int per = max(0, last - begin);
+    const int64_t all = (int64_t)per * group;
+    const int s_begin = (int)(all * chunk / a.chunks), s_end = (int)(all * (chunk + 1) / a.chunks);
 
     Frag k[DT / 16];
     load_own<DT>(k, a.k + (int64_t)(pl.k0 + ki) * a.k_row + (int64_t)khead * a.k_head, a.d, mine);
     Tile<DT> tile;
     tile.init(lds0);
-    const uint32_t own = (uint32_t)(wave * 32 * DT * 2);   // the wave's values within the fixed tile
-    Stream<DT, kQueries> qs, gs;
+    const uint32_t own = (uint32_t)(kRing * 2 * kTile + wave * 32 * DT * 2);   // the wave's values
+    Q qs, gs;
     qs.init(a.q + (int64_t)pl.q0 * a.q_row, a.q_row, pl.nq, a.d);
     gs.init(a.dout + (int64_t)pl.q0 * a.dout_row, a.dout_row, pl.nq, a.d);
     const uint8_t* q_base = qs.base;
     const uint8_t* g_base = gs.base;
+    const uint32_t stat_off = lane < 32 ? lane * 4u : 0x80000000u;
+    // even waves bring the tile's lse, odd ones its delta (the same bytes each)
+    const float* stat_base = a.stats + (wave & 1 ? (int64_t)a.tq * a.hq : 0) + pl.q0;
 
     af32x16 dk[DT / 32], dv[DT / 32];
 #pragma unroll
     for (int db = 0; db < DT / 32; ++db) dk[db] = dv[db] = af32x16{0};
     const float c = a.scale * kLog2e;
 
-    // step s: query tile begin + s % per of head khead * group + s / per
-    auto issue = [&](int s) {
+    // step s: query tile begin + s % per of head khead * group + s / per.  Past the last step
+    // its loads are repeated, into a stage that is read no more, so that the count of loads
+    // in flight stays the same.
+    auto issue = [&](int s, int stage) __attribute__((always_inline)) {
+        s = min(s, s_end - 1);
         const int head = khead * group + s / per, row0 = (begin + s % per) * kQueries;
-        const uint32_t to = ring + (uint32_t)(s & 1) * 2 * kTile;
+        const uint32_t to = lds0 + (uint32_t)stage * 2 * kTile;
         qs.base = q_base + (int64_t)head * a.q_head * 2;
         gs.base = g_base + (int64_t)head * a.dout_head * 2;
         qs.issue(row0, to, wave);
         gs.issue(row0, to + kTile, wave);
-    };
-    auto fetch_stat = [&](int s) {                         // lanes 0-31: lse, 32-63: delta, of wave 0
-        const int head = khead * group + s / per, row = (begin + s % per) * kQueries + (lane & 31);
-        float v = h ? 0.0f : kInf;
-        if (row < pl.nq) v = a.stats[(int64_t)h * a.tq * a.hq + (int64_t)head * a.tq + pl.q0 + row];
-        return v;
+        const au32x4 desc = descriptor(reinterpret_cast<const uint8_t*>(stat_base + (int64_t)head * a.tq + row0),
+                                       (int64_t)(pl.nq - row0) * 4);
+        buffer4_to_lds(stat_off, desc, __builtin_amdgcn_readfirstlane(stat0 + (uint32_t)(stage * kStat + (wave & 1) * 256)));
     };
 
-    float next = 0.0f;
-    if (steps > 0) {
-        Stream<DT, kOwn> vs;
-        vs.init(a.v + (int64_t)pl.k0 * a.v_row + (int64_t)khead * a.v_head, a.v_row, pl.nk, a.d);
-        if (wave == 0) next = fetch_stat(0);
-        vs.issue(pl.first, lds0, wave);
-        issue(0);
-    }
-    auto step = [&](auto stage, int s) {
-        constexpr int at = kOwnTile + stage.value * 2 * kTile;
-        if (wave == 0) stat[stage.value][h][lane & 31] = next;
-        __builtin_amdgcn_s_waitcnt(0x0F70);
-        __syncthreads();
-        if (s + 1 < steps) {
-            if (wave == 0) next = fetch_stat(s + 1);
-            issue(s + 1);
-        }
+    auto step = [&](auto stage, int s) __attribute__((always_inline)) {
+        constexpr int at = stage.value * 2 * kTile;
+        __builtin_amdgcn_s_waitcnt(wait_loads((kRing - 2) * kLoads));     // this wave's loads of step s
+        __syncthreads();                                   // everyone's; step s - 1 is read
+        issue(s + kRing - 1, (stage.value + kRing - 1) % kRing);
         const int i0 = (begin + s % per) * kQueries;
-        if (i0 + kQueries <= from_first) return;           // no query of the tile sees a key of the wave
+        if (i0 + kQueries <= from_first || k_wave >= pl.nk) return;   // no query of the tile sees a key of the wave
         af32x16 p = af32x16{0}, dp = af32x16{0};
 #pragma unroll
         for (int ch = 0; ch < DT / 16; ++ch) {
@@ -656,16 +679,15 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dkv_kernel(const Att
             dp = mma(tile.rows(at + kTile, 0, ch), v, dp);
         }
         const bool masked = i0 < from_last || k_wave + 32 > pl.nk;
+        const lds_f32x4* stat = (const lds_f32x4*)(uintptr_t)(stat0 + stage.value * kStat + 16 * h);
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const float4 ls = *reinterpret_cast<const float4*>(&stat[stage.value][0][8 * b + 4 * h]);
-            const float4 de = *reinterpret_cast<const float4*>(&stat[stage.value][1][8 * b + 4 * h]);
-            const float lsv[4] = {ls.x, ls.y, ls.z, ls.w}, dev[4] = {de.x, de.y, de.z, de.w};
+            const af32x4 ls = stat[2 * b], de = stat[2 * b + 16];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int i = 4 * b + e;
-                p[i] = __builtin_amdgcn_exp2f(fmaf(p[i], c, -lsv[e]));
-                dp[i] = p[i] * (dp[i] - dev[e]);
+                p[i] = __builtin_amdgcn_exp2f(fmaf(p[i], c, -ls[e]));
+                dp[i] = p[i] * (dp[i] - de[e]);
             }
         }
         if (masked) {
@@ -685,29 +707,102 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dkv_kernel(const Att
                 dk[db] = mma(tile.cols(at, 0, ch, db), e[ch], dk[db]);
             }
     };
-    for (int s = 0; s < steps; s += 2) {
-        step(std::integral_constant<int, 0>{}, s);
-        if (s + 1 < steps) step(std::integral_constant<int, 1>{}, s + 1);
+    if (s_begin < s_end) {
+        Stream<DT, kMine, WAVES> vs;
+        vs.init(a.v + (int64_t)pl.k0 * a.v_row + (int64_t)khead * a.v_head, a.v_row, pl.nk, a.d);
+        vs.issue(pl.first, lds0 + kRing * 2 * kTile, wave);
+#pragma unroll
+        for (int i = 0; i < kRing - 1; ++i) issue(s_begin + i, i);
+        for (int s = s_begin; s < s_end; s += kRing) {
+            step(std::integral_constant<int, 0>{}, s);
+            if (s + 1 < s_end) step(std::integral_constant<int, 1>{}, s + 1);
+            if (s + 2 < s_end) step(std::integral_constant<int, 2>{}, s + 2);
+            if (s + 3 < s_end) step(std::integral_constant<int, 3>{}, s + 3);
+        }
+        __builtin_amdgcn_s_waitcnt(wait_loads(0));         // no load outlives the workgroup's LDS
+    }
+    if (a.chunks > 1) {
+        const int64_t row = ((int64_t)(pl.k0 + ki) * a.hk + khead) * a.d, whole = (int64_t)a.tk * a.hk * a.d;
+        store_partial<DT>(dk, a.partial + (int64_t)(2 * chunk) * whole + row, a.d, mine);
+        store_partial<DT>(dv, a.partial + (int64_t)(2 * chunk + 1) * whole + row, a.d, mine);
+        return;
     }
     uint32_t top = store_own<DT>(dk, a.scale, a.dk + (int64_t)(pl.k0 + ki) * a.dk_row + (int64_t)khead * a.dk_head, a.d, mine);
     top = max(top, store_own<DT>(dv, 1.0f, a.dv + (int64_t)(pl.k0 + ki) * a.dv_row + (int64_t)khead * a.dv_head, a.d, mine));
     if (a.absmax) block_max_to_global(top, a.absmax);
 }
 
+// dk and dv from the chunks' partial sums, added in order: 8 elements per thread.
+__global__ void __launch_bounds__(256) attention_join_kernel(const AttentionArgs a)
+{
+    const int per_row = a.d / 8;
+    const int64_t whole = (int64_t)a.tk * a.hk * a.d, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int which = blockIdx.y;
+    int64_t row = i / per_row;
+    const int c = (int)(i % per_row) * 8, head = (int)(row % a.hk), token = (int)(row / a.hk);
+    int from = 0, upto = a.tk;            // the tokens that belong to a sequence
+    if (a.cu_k) {
+        from = min(max(a.cu_k[0], 0), a.tk);
+        upto = min(max(a.cu_k[a.batch], 0), a.tk);
+    }
+    uint32_t top = 0;
+    if (i < whole / 8 && token >= from && token < upto) {
+        const float* p = a.partial + which * whole + row * a.d + c;
+        float t[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int s = 0; s < a.chunks; ++s, p += 2 * whole) {
+            const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
+            const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] += v[e];
+        }
+        const float by = which ? 1.0f : a.scale;
+        uint16_t* out = which ? a.dv + (int64_t)token * a.dv_row + (int64_t)head * a.dv_head
+                              : a.dk + (int64_t)token * a.dk_row + (int64_t)head * a.dk_head;
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            w[e] = bf16_pair(t[2 * e] * by, t[2 * e + 1] * by);
+            top = max(max(top, w[e] & 0x7FFF0000u), w[e] << 16 & 0x7FFFFFFFu);
+        }
+        *reinterpret_cast<uint4*>(out + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    if (a.absmax) block_max_to_global(top, a.absmax);
+}
+
 // ---------------------------------------------------------------------- launches
 
-// At most this many tiles: each sequence adds less than one to total / kOwn.
-static int64_t tile_bound(int64_t total, int batch) { return total / kOwn + batch; }
+// At most this many tiles: each sequence adds less than one to total / rows.
+static int64_t tile_bound(int64_t total, int batch, int rows) { return total / rows + batch; }
+
+static int key_rows(int d) { return 32 * keys_waves(d <= 64 ? 64 : 128); }
 
 bool attention_grid_ok(int64_t tokens, int batch, int heads)
 {
-    return tile_bound(tokens, batch) * heads <= 0x7FFFFFFF;
+    return tile_bound(tokens, batch, kOwn) * heads <= 0x7FFFFFFF / 8;
+}
+
+// Workgroups that share the steps of one tile of keys.  With less than two tiles per CU
+// (few key heads, or short sequences of many queries) the causal mask leaves the first
+// tiles' workgroups running alone: their steps are then split, at 32 or more to a chunk
+// (8192 causal tokens, 40 query and 8 key heads of 128: 264 workgroups).
+static int key_chunks(int64_t tq, int64_t tk, int hq, int hk, int d, int batch)
+{
+    const int64_t tiles = tile_bound(tk, batch, key_rows(d)) * hk, want = 2 * (int64_t)device_cu_count();
+    const int64_t steps = (tq / batch + kQueries - 1) / kQueries * (hq / hk);   // of a sequence of average length
+    return (int)std::max<int64_t>(1, std::min<int64_t>({(want + tiles - 1) / tiles, steps / 32, 8}));
+}
+
+int64_t attention_backward_workspace(int64_t tq, int64_t tk, int hq, int hk, int d, int batch)
+{
+    const int chunks = key_chunks(tq, tk, hq, hk, d, batch);
+    const int64_t stats = (2 * tq * hq + 3) / 4 * 4;        // fp32 values; what follows is 16-byte aligned
+    return 4 * (stats + (chunks > 1 ? 2 * chunks * tk * hk * d : 0));
 }
 
 hipError_t launch_attention_forward(const AttentionArgs& args, hipStream_t stream)
 {
     AttentionArgs a = args;
-    a.tiles = (int)tile_bound(a.tq, a.batch);
+    a.tiles = (int)tile_bound(a.tq, a.batch, kOwn);
     const dim3 grid((unsigned)(a.tiles * a.hq));
     if (a.d <= 64) return launch(attention_forward_kernel<64>, grid, dim3(kAttThreads), stream, a);
     return launch(attention_forward_kernel<128>, grid, dim3(kAttThreads), stream, a);
@@ -716,18 +811,20 @@ hipError_t launch_attention_forward(const AttentionArgs& args, hipStream_t strea
 hipError_t launch_attention_backward(const AttentionArgs& args, hipStream_t stream)
 {
     AttentionArgs a = args;
-    const int64_t units = (int64_t)a.tq * a.hq;
-    hipError_t e = launch(attention_delta_kernel, dim3((unsigned)((units + 15) / 16)), dim3(256), stream, a);
-    if (e != hipSuccess) return e;
-    a.tiles = (int)tile_bound(a.tk, a.batch);
-    const dim3 grid_k((unsigned)(a.tiles * a.hk));
-    e = a.d <= 64 ? launch(attention_dkv_kernel<64>, grid_k, dim3(kAttThreads), stream, a)
-                  : launch(attention_dkv_kernel<128>, grid_k, dim3(kAttThreads), stream, a);
-    if (e != hipSuccess) return e;
-    a.tiles = (int)tile_bound(a.tq, a.batch);
+    a.chunks = key_chunks(a.tq, a.tk, a.hq, a.hk, a.d, a.batch);
+    a.partial = a.stats + (2 * (int64_t)a.tq * a.hq + 3) / 4 * 4;
+    a.tiles = (int)tile_bound(a.tq, a.batch, kOwn);
     const dim3 grid_q((unsigned)(a.tiles * a.hq));
-    if (a.d <= 64) return launch(attention_dq_kernel<64>, grid_q, dim3(kAttThreads), stream, a);
-    return launch(attention_dq_kernel<128>, grid_q, dim3(kAttThreads), stream, a);
+    hipError_t e = a.d <= 64 ? launch(attention_dq_kernel<64>, grid_q, dim3(kAttThreads), stream, a)
+                             : launch(attention_dq_kernel<128>, grid_q, dim3(kAttThreads), stream, a);
+    if (e != hipSuccess) return e;
+    a.tiles = (int)tile_bound(a.tk, a.batch, key_rows(a.d));
+    const dim3 grid_k((unsigned)(a.tiles * a.hk * a.chunks));
+    e = a.d <= 64 ? launch(attention_dkv_kernel<64>, grid_k, dim3(64 * keys_waves(64)), stream, a)
+                  : launch(attention_dkv_kernel<128>, grid_k, dim3(64 * keys_waves(128)), stream, a);
+    if (e != hipSuccess || a.chunks == 1) return e;
+    const int64_t units = (int64_t)a.tk * a.hk * a.d / 8;
+    return launch(attention_join_kernel, dim3((unsigned)((units + 255) / 256), 2), dim3(256), stream, a);
 }
 
 }  // namespace fp8k
