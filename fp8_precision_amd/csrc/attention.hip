@@ -231,6 +231,10 @@ __device__ __forceinline__ void load_own(Frag (&f)[DT / 16], const uint16_t* row
         f[c].u = au32x4{0, 0, 0, 0};
         if (valid && 16 * c + 8 * h < d) f[c].u = *reinterpret_cast<const au32x4*>(row + 16 * c + 8 * h);
     }
+    // Waited for here: at its first use, in the loop, the compiler's wait (it does not see
+    // the direct-to-LDS loads) would be one for every tile in flight, in every step.
+#pragma unroll
+    for (int c = 0; c < DT / 16; ++c) asm volatile("" : "+v"(f[c].u));
 }
 
 // Store a lane's accumulated row (acc[db][i]: element 32 db + 8 (i / 4) + 4 (lane / 32)
@@ -407,11 +411,25 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_forward_kernel(const
         }
         const int j0 = s * kKeys;
         if (j0 >= see_last) return;                        // nothing of this tile is seen by the wave
+        // The tile's matrix instructions in order -- the scores' (two blocks of keys by the
+        // chunks of the head dimension), then the values' -- each with its operand read
+        // from LDS kAhead instructions before it; the first values are read before the
+        // softmax.
+        constexpr int kS = DT / 8, kAll = kS + DT / 8, kAhead = 4;
+        Frag r[kAhead];
+        auto fetch = [&](int t) __attribute__((always_inline)) {
+            if (t < kS) r[t % kAhead] = tile.rows(at, t % 2, t / 2);
+            else if (t < kAll) r[t % kAhead] = tile.cols(at + kTile, (t - kS) / (DT / 16), (t - kS) / (DT / 32) % 2, (t - kS) % (DT / 32));
+        };
+#pragma unroll
+        for (int t = 0; t < kAhead; ++t) fetch(t);
         af32x16 p[2] = {af32x16{0}, af32x16{0}};
 #pragma unroll
-        for (int ch = 0; ch < DT / 16; ++ch)
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) p[kb] = mma(tile.rows(at, kb, ch), q[ch], p[kb]);
+        for (int t = 0; t < kS; ++t) {
+            p[t % 2] = mma(r[t % kAhead], q[t / 2], p[t % 2]);
+            fetch(t + kAhead);
+            __builtin_amdgcn_sched_barrier(0);
+        }
         if (j0 + kKeys > see_first) {
             const int see0 = see - j0 - 4 * h;             // register i: key 32 kb + 8 (i / 4) + i % 4 of what is left
 #pragma unroll
@@ -443,6 +461,7 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_forward_kernel(const
                 for (int i = 0; i < 16; ++i) o[db][i] *= by;
         }
         float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        Frag f[2][2];
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
@@ -450,13 +469,14 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_forward_kernel(const
                 p[kb][i] = __builtin_amdgcn_exp2f(fmaf(p[kb][i], c, -mc));
                 sums[i % 4] += p[kb][i];
             }
-            Frag f[2];
-            to_operands(p[kb], f);
+            to_operands(p[kb], f[kb]);
 #pragma unroll
-            for (int ch = 0; ch < 2; ++ch)
-#pragma unroll
-                for (int db = 0; db < DT / 32; ++db)
-                    o[db] = mma(tile.cols(at + kTile, kb, ch, db), f[ch], o[db]);
+            for (int t = kS + kb * (DT / 16); t < kS + (kb + 1) * (DT / 16); ++t) {
+                const int db = (t - kS) % (DT / 32);
+                o[db] = mma(r[t % kAhead], f[kb][(t - kS) / (DT / 32) % 2], o[db]);
+                fetch(t + kAhead);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
         l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
     };
@@ -519,6 +539,7 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dq_kernel(const Atte
             const int64_t at = (int64_t)head * a.tq + pl.q0 + qi;
             lse = a.lse[at];
             lse = lse == -kInf ? kInf : lse * kLog2e;
+            asm volatile("" : "+v"(lse));
             a.stats[(h ? (int64_t)a.tq * a.hq : 0) + at] = h ? delta : lse;
         }
     }
@@ -548,13 +569,28 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dq_kernel(const Atte
         const int j0 = s * kKeys;
         if (j0 >= see_last) return;
         const bool masked = j0 + kKeys > see_first;
+        // as in the forward: per block of 32 keys the scores and dp (k and v rows in turn),
+        // then dq (k columns)
+        constexpr int kS = DT / 8, kB = kS + DT / 16, kAll = 2 * kB, kAhead = 4;
+        Frag r[kAhead];
+        auto fetch = [&](int t) __attribute__((always_inline)) {
+            const int kb = t / kB, x = t % kB;
+            if (t >= kAll) return;
+            if (x < kS) r[t % kAhead] = tile.rows(at + x % 2 * kTile, kb, x / 2);
+            else r[t % kAhead] = tile.cols(at, kb, (x - kS) / (DT / 32), (x - kS) % (DT / 32));
+        };
+#pragma unroll
+        for (int t = 0; t < kAhead; ++t) fetch(t);
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             af32x16 p = af32x16{0}, dp = af32x16{0};
 #pragma unroll
-            for (int ch = 0; ch < DT / 16; ++ch) {
-                p = mma(tile.rows(at, kb, ch), q[ch], p);
-                dp = mma(tile.rows(at + kTile, kb, ch), g[ch], dp);
+            for (int x = 0; x < kS; ++x) {
+                const int t = kb * kB + x;
+                if (x % 2 == 0) p = mma(r[t % kAhead], q[x / 2], p);
+                else dp = mma(r[t % kAhead], g[x / 2], dp);
+                fetch(t + kAhead);
+                __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -570,9 +606,12 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dq_kernel(const Atte
             Frag f[2];
             to_operands(dp, f);
 #pragma unroll
-            for (int ch = 0; ch < 2; ++ch)
-#pragma unroll
-                for (int db = 0; db < DT / 32; ++db) dq[db] = mma(tile.cols(at, kb, ch, db), f[ch], dq[db]);
+            for (int x = kS; x < kB; ++x) {
+                const int t = kb * kB + x, db = (x - kS) % (DT / 32);
+                dq[db] = mma(r[t % kAhead], f[(x - kS) / (DT / 32)], dq[db]);
+                fetch(t + kAhead);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
     };
     for (int s = 0; s < steps; s += 2) {
@@ -670,13 +709,28 @@ __global__ void __launch_bounds__(64 * keys_waves(DT), 2) attention_dkv_kernel(c
         issue(s + kRing - 1, (stage.value + kRing - 1) % kRing);
         const int i0 = (begin + s % per) * kQueries;
         if (i0 + kQueries <= from_first || k_wave >= pl.nk) return;   // no query of the tile sees a key of the wave
+        // as in the forward: the scores and dp (q and dout rows in turn), then dv and dk
+        // (dout and q columns in turn)
+        constexpr int kS = DT / 8, kAll = kS + DT / 8, kAhead = 2;   // 4 spill
+        Frag r[kAhead], v[2];
+        auto fetch = [&](int t) __attribute__((always_inline)) {
+            if (t < kS) {
+                r[t % kAhead] = tile.rows(at + t % 2 * kTile, 0, t / 2);
+                if (t % 2) v[t / 2 % 2].u = *(const lds_u32x4*)(uintptr_t)(tile.plain[t / 2] + own);
+            } else if (t < kAll) {
+                const int x = t - kS;
+                r[t % kAhead] = tile.cols(at + (1 - x % 2) * kTile, 0, x / 2 / (DT / 32), x / 2 % (DT / 32));
+            }
+        };
+#pragma unroll
+        for (int t = 0; t < kAhead; ++t) fetch(t);
         af32x16 p = af32x16{0}, dp = af32x16{0};
 #pragma unroll
-        for (int ch = 0; ch < DT / 16; ++ch) {
-            Frag v;
-            v.u = *(const lds_u32x4*)(uintptr_t)(tile.plain[ch] + own);
-            p = mma(tile.rows(at, 0, ch), k[ch], p);
-            dp = mma(tile.rows(at + kTile, 0, ch), v, dp);
+        for (int t = 0; t < kS; ++t) {
+            if (t % 2 == 0) p = mma(r[t % kAhead], k[t / 2], p);
+            else dp = mma(r[t % kAhead], v[t / 2 % 2], dp);
+            fetch(t + kAhead);
+            __builtin_amdgcn_sched_barrier(0);
         }
         const bool masked = i0 < from_last || k_wave + 32 > pl.nk;
         const lds_f32x4* stat = (const lds_f32x4*)(uintptr_t)(stat0 + stage.value * kStat + 16 * h);
@@ -700,12 +754,13 @@ __global__ void __launch_bounds__(64 * keys_waves(DT), 2) attention_dkv_kernel(c
         to_operands(p, f);
         to_operands(dp, e);
 #pragma unroll
-        for (int ch = 0; ch < 2; ++ch)
-#pragma unroll
-            for (int db = 0; db < DT / 32; ++db) {
-                dv[db] = mma(tile.cols(at + kTile, 0, ch, db), f[ch], dv[db]);
-                dk[db] = mma(tile.cols(at, 0, ch, db), e[ch], dk[db]);
-            }
+        for (int t = kS; t < kAll; ++t) {
+            const int x = t - kS, ch = x / 2 / (DT / 32), db = x / 2 % (DT / 32);
+            if (x % 2 == 0) dv[db] = mma(r[t % kAhead], f[ch], dv[db]);
+            else dk[db] = mma(r[t % kAhead], e[ch], dk[db]);
+            fetch(t + kAhead);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     };
     if (s_begin < s_end) {
         Stream<DT, kMine, WAVES> vs;
