@@ -536,12 +536,10 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dq_kernel(const Atte
                 delta = fmaf(bf16_lo(o[ch].w[i]), bf16_lo(g[ch].w[i]), fmaf(bf16_hi(o[ch].w[i]), bf16_hi(g[ch].w[i]), delta));
         delta += partner(delta);
         if (mine) {
-            const int64_t at = (int64_t)head * a.tq + pl.q0 + qi;
-            lse = a.lse[at];
+            lse = a.lse[(int64_t)head * a.tq + pl.q0 + qi];
             lse = lse == -kInf ? kInf : lse * kLog2e;
-            asm volatile("" : "+v"(lse));
-            a.stats[(h ? (int64_t)a.tq * a.hq : 0) + at] = h ? delta : lse;
         }
+        asm volatile("" : "+v"(lse));
     }
 
     Stream<DT, kKeys> ks, vs;
@@ -554,7 +552,41 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dq_kernel(const Atte
 #pragma unroll
     for (int db = 0; db < DT / 32; ++db) dq[db] = af32x16{0};
 
-    if (steps > 0) {
+    // Where at most two tiles of keys are seen, delta is taken again as the sum of p dp:
+    // out is rounded to bf16, which weighs most where it is the average of few values (in
+    // a causal sequence's first rows, whose gradients are its largest).
+    if (steps == 1 || steps == 2) {
+        for (int s = 0; s < steps; ++s) {
+            ks.issue(s * kKeys, lds0 + s * 2 * kTile, wave);
+            vs.issue(s * kKeys, lds0 + s * 2 * kTile + kTile, wave);
+        }
+        __builtin_amdgcn_s_waitcnt(wait_loads(0));
+        __syncthreads();
+        float sum = 0.0f;
+        for (int u = 0; u < 2 * steps && 32 * u < see_last; ++u) {
+            const uint32_t at = (uint32_t)(u / 2 * 2 * kTile + u % 2 * 32 * DT * 2);
+            af32x16 p = af32x16{0}, dp = af32x16{0};
+#pragma unroll
+            for (int ch = 0; ch < DT / 16; ++ch) {
+                Frag x, y;
+                x.u = *(const lds_u32x4*)(uintptr_t)(tile.plain[ch] + at);
+                y.u = *(const lds_u32x4*)(uintptr_t)(tile.plain[ch] + at + kTile);
+                p = mma(x, q[ch], p);
+                dp = mma(y, g[ch], dp);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float x = __builtin_amdgcn_exp2f(fmaf(p[i], c, -lse)) * dp[i];
+                sum += 32 * u + 8 * (i / 4) + 4 * h + i % 4 < see ? x : 0.0f;
+            }
+        }
+        delta = sum + partner(sum);
+    }
+    if (mine)
+        a.stats[(h ? (int64_t)a.tq * a.hq : 0) + (int64_t)head * a.tq + pl.q0 + qi] = h ? delta : lse;
+
+    const bool loaded = steps <= 2;       // with their tiles in LDS already
+    if (!loaded) {
         ks.issue(0, lds0, wave);
         vs.issue(0, lds0 + kTile, wave);
     }
@@ -562,7 +594,7 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dq_kernel(const Atte
         constexpr int at = stage.value * 2 * kTile, to = (2 - stage.value * 2) * kTile;
         __builtin_amdgcn_s_waitcnt(0x0F70);
         __syncthreads();
-        if (s + 1 < steps) {
+        if (s + 1 < steps && !loaded) {
             ks.issue((s + 1) * kKeys, lds0 + to, wave);
             vs.issue((s + 1) * kKeys, lds0 + to + kTile, wave);
         }

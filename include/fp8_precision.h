@@ -593,8 +593,11 @@ fp8_status fp8_attention_forward(const fp8_attention_shape* shape, const fp8_hea
 /*
  * Gradients of q, k and v (of a shared key head: the sum over its query heads).
  * The probabilities are computed again from q, k and lse.  With
- *   delta_i = dout_i . out_i,  dp_ij = dout_i . v_j,  ds_ij = p_ij (dp_ij - delta_i):
+ *   dp_ij = dout_i . v_j,  delta_i = sum_j p_ij dp_ij,  ds_ij = p_ij (dp_ij - delta_i):
  *   dv_j = sum_i p_ij dout_i,  dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i
+ *
+ * (delta is taken as dout_i . out_i, the same sum, where a tile of queries sees more
+ * than 128 keys).
  *
  *   dout    as q;  out, lse  from the forward;  dq, dk, dv  as q, k, v
  *   absmax  fp32 scalar or NULL: becomes max(*absmax, max |dq|, max |dk|, max |dv|), as stored

@@ -6,9 +6,11 @@ Tolerances, elementwise, from the roundings (u = 2^-8, bf16's unit):
    plus the exponential and the sum over the keys);
  - out and dv are sums with p rounded once (u) and are rounded once themselves (u);
  - ds = p (dp - delta) is rounded once (u) and carries p's e and fp32 errors of dp and
-   delta (2^-16 of their sums of magnitudes); dq and dk are sums of it, rounded once.
-The backward call is checked as a function of the out and lse that it is given, and
-the whole gradient against differences.
+   delta (2^-16 of their sums of magnitudes); dq and dk are sums of it, rounded once;
+ - delta is the sum of p dp.  Over more than 128 keys it may be taken as dout . out, and
+   then carries out's two roundings (u of |dout| . |out| and of |dout| . sum p |v|).
+The backward call is checked for the lse that it is given, and the whole gradient
+against differences.
 """
 import itertools
 
@@ -85,10 +87,12 @@ def check_backward(dout, q, k, v, out, lse, dq, dk, dv, lq, lk, causal, scale):
         seen = visible(len(a), len(b), causal)
         z = lse[h, qs].to(F64)[:, None]
         p = torch.where(seen, torch.exp(a @ b.t() * scale - torch.where(z.isinf(), 0.0, z)), 0.0)
-        delta = (g * o).sum(1, keepdim=True)
         dp = g @ c.t()
+        delta = (p * dp).sum(1, keepdim=True)
         ds = p * (dp - delta)
         err = (U + E) * ds.abs() + p * 2.0 ** -16 * (g.abs() @ c.abs().t() + (g * o).abs().sum(1, keepdim=True))
+        if len(b) > 128:
+            err = err + p * U * (g.abs() * (o.abs() + p @ c.abs())).sum(1, keepdim=True)
         want["dv"][ks, kh] += p.t() @ g
         slack["dv"][ks, kh] += (U + 2 * E) * (p.t() @ g.abs())
         want["dq"][qs, h] = scale * (ds @ b)
