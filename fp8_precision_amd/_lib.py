@@ -53,7 +53,8 @@ _SIGS = {
     "fp8_norm_forward": (_i32, [_vp, _i32, _vp, _vp, _vp, ctypes.c_float, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),
     "fp8_norm_backward_workspace": (_i32, [_i64, _i64, _vp]),
     "fp8_norm_backward": (_i32, [_vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _vp]),
-    "fp8_attention_forward": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "fp8_attention_forward_workspace": (_i32, [_vp, _vp]),
+    "fp8_attention_forward": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
     "fp8_attention_backward_workspace": (_i32, [_vp, _vp]),
     "fp8_attention_backward": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
     "fp8_linear_cross_entropy_forward_workspace": (_i32, [_i64, _i64, _i64, _vp]),
@@ -628,14 +629,15 @@ def _out(t, name, shape, dtype, device):
 
 def _workspace(call, device, *args):
     """Device memory of the size that the entry point ``call`` names for ``args``
-    on ``device`` (the torch allocator's, so stream-ordered like any tensor)."""
+    on ``device`` (the torch allocator's, so stream-ordered like any tensor); None
+    where none is needed."""
     size = _i64()
     if device.index == torch.cuda.current_device():
         _check(call, getattr(_lib, call)(*args, ctypes.byref(size)))
     else:
         with torch.cuda.device(device):
             _check(call, getattr(_lib, call)(*args, ctypes.byref(size)))
-    return torch.empty(max(16, size.value), dtype=torch.uint8, device=device)
+    return torch.empty(size.value, dtype=torch.uint8, device=device) if size.value else None
 
 
 _STREAM_TYPES = {torch.bfloat16: 0, torch.float32: 1}
@@ -792,8 +794,9 @@ def attention(q, k, v, cu_q=None, cu_k=None, causal: bool = False, scale: float 
         out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
     ho = _heads(out, "out", q.shape)
     lse = _out(lse, "lse", (q.shape[1], q.shape[0]), torch.float32, q.device)
-    _run("fp8_attention_forward", _lib.fp8_attention_forward, (q, k, v, cu_q, cu_k, out, lse, absmax),
-         ctypes.byref(shape), hq, hk, hv, ho, _ptr(lse), _ptr(absmax))
+    ws = _workspace("fp8_attention_forward_workspace", q.device, ctypes.byref(shape))
+    _run("fp8_attention_forward", _lib.fp8_attention_forward, (q, k, v, cu_q, cu_k, out, lse, absmax, ws),
+         ctypes.byref(shape), hq, hk, hv, ho, _ptr(lse), _ptr(absmax), _ptr(ws), 0 if ws is None else ws.numel())
     return out, lse
 
 

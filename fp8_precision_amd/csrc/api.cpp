@@ -773,9 +773,25 @@ static fp8k::AttentionArgs attention_args(const fp8_attention_shape& s)
     return a;
 }
 
+static int64_t attention_forward_bytes(const fp8_attention_shape& s)
+{
+    return fp8k::attention_forward_workspace(s.tokens_q, s.tokens_k, (int)s.heads_q, (int)s.head_dim, (int)s.batch);
+}
+
+fp8_status fp8_attention_forward_workspace(const fp8_attention_shape* shape, int64_t* bytes)
+{
+    t_last_error.clear();
+    fp8_status st = attention_shape("fp8_attention_forward_workspace", shape);
+    if (st != FP8_OK) return st;
+    if (!bytes) return fail(FP8_ERR_INVALID, "fp8_attention_forward_workspace: null pointer");
+    *bytes = attention_forward_bytes(*shape);
+    return FP8_OK;
+}
+
 fp8_status fp8_attention_forward(const fp8_attention_shape* shape, const fp8_head_tensor* q,
                                  const fp8_head_tensor* k, const fp8_head_tensor* v, const fp8_head_tensor* out,
-                                 float* lse, float* absmax, hipStream_t stream)
+                                 float* lse, float* absmax, void* workspace, int64_t workspace_bytes,
+                                 hipStream_t stream)
 {
     t_last_error.clear();
     const char* call = "fp8_attention_forward";
@@ -789,10 +805,14 @@ fp8_status fp8_attention_forward(const fp8_attention_shape* shape, const fp8_hea
         (st = take_heads(call, "out", out, s.tokens_q, s.heads_q, s.head_dim, true, h[3])) != FP8_OK)
         return st;
     if (!lse) return fail(FP8_ERR_INVALID, "fp8_attention_forward: null lse");
-    if (!aligned(lse, 4) || !aligned(absmax, 4)) return fail(FP8_ERR_UNSUPPORTED, "fp8_attention_forward: misaligned lse or absmax");
-    const Range flat[] = {{lse, 4 * s.heads_q * s.tokens_q}, {absmax, 4}};
+    const int64_t need = attention_forward_bytes(s);
+    if (need > 0 && !workspace) return fail(FP8_ERR_INVALID, "fp8_attention_forward: null workspace");
+    if (workspace_bytes < need) return fail(FP8_ERR_INVALID, "fp8_attention_forward: workspace too small");
+    if (!aligned(lse, 4) || !aligned(absmax, 4) || !aligned(workspace, 16))
+        return fail(FP8_ERR_UNSUPPORTED, "fp8_attention_forward: misaligned lse, absmax or workspace");
+    const Range flat[] = {{lse, 4 * s.heads_q * s.tokens_q}, {absmax, 4}, {workspace, workspace_bytes}};
     const Range in[] = {{s.bounds_q, 4 * (s.batch + 1)}, {s.bounds_k, 4 * (s.batch + 1)}};
-    bool bad = outputs_overlap(flat, 2, in, 2);
+    bool bad = outputs_overlap(flat, 3, in, 2);
     for (int i = 0; i < 4; ++i) {
         if (i < 3) bad = bad || heads_overlap(h[3], h[i]);
         for (const Range& r : flat) bad = bad || heads_overlap(h[i], r.p, r.n);
@@ -806,7 +826,7 @@ fp8_status fp8_attention_forward(const fp8_attention_shape* shape, const fp8_hea
     a.out = h[3].p; a.out_row = h[3].row; a.out_head = h[3].head;
     a.lse = lse;
     a.absmax = reinterpret_cast<uint32_t*>(absmax);
-    hipError_t e = fp8k::launch_attention_forward(a, stream);
+    hipError_t e = fp8k::launch_attention_forward(a, workspace, stream);
     if (e != hipSuccess) return fail_hip(call, e);
     return FP8_OK;
 }

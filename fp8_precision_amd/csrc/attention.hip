@@ -362,8 +362,9 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_forward_kernel(const
 {
     constexpr int kTile = kKeys * DT * 2;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kTile];
-    int t, head;
-    deal(blockIdx.x, a.hq, t, head);
+    int t, unit;
+    deal(blockIdx.x, a.hq * a.splits, t, unit);
+    const int head = unit / a.splits, split = unit % a.splits;
     const Place pl = find_tile(a, a.tiles - 1 - t, 0);     // a sequence's last (longest) tiles first
     if (!pl.any) return;
     const int lane = threadIdx.x & 63, h = lane >> 5;
@@ -379,7 +380,8 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_forward_kernel(const
     const int see_first = a.causal ? min(pl.nk, q_wave + shift + 1) : pl.nk;
     const int see_last = a.causal ? min(pl.nk, q_wave + 31 + shift + 1) : pl.nk;
     const int end = a.causal ? min(pl.nk, min(pl.first + kOwn, pl.nq) + shift) : pl.nk;
-    const int steps = end > 0 ? (end + kKeys - 1) / kKeys : 0;
+    const int all = end > 0 ? (end + kKeys - 1) / kKeys : 0;
+    const int s_begin = (int)((int64_t)all * split / a.splits), s_end = (int)((int64_t)all * (split + 1) / a.splits);
 
     Frag q[DT / 16];
     load_own<DT>(q, a.q + (int64_t)(pl.q0 + qi) * a.q_row + (int64_t)head * a.q_head, a.d, mine);
@@ -397,15 +399,15 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_forward_kernel(const
     for (int db = 0; db < DT / 32; ++db) o[db] = af32x16{0};
     float m = -kInf, mc = 0.0f, l = 0.0f;
 
-    if (steps > 0) {
-        ks.issue(0, lds0, wave);
-        vs.issue(0, lds0 + kTile, wave);
+    if (s_begin < s_end) {
+        ks.issue(s_begin * kKeys, lds0, wave);
+        vs.issue(s_begin * kKeys, lds0 + kTile, wave);
     }
     auto step = [&](auto stage, int s) {
         constexpr int at = stage.value * 2 * kTile, to = (2 - stage.value * 2) * kTile;
         __builtin_amdgcn_s_waitcnt(0x0F70);                // this wave's loads of tile s have landed
         __syncthreads();                                   // everyone's; tile s - 1 is read
-        if (s + 1 < steps) {
+        if (s + 1 < s_end) {
             ks.issue((s + 1) * kKeys, lds0 + to, wave);
             vs.issue((s + 1) * kKeys, lds0 + to + kTile, wave);
         }
@@ -480,17 +482,64 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_forward_kernel(const
         }
         l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
     };
-    for (int s = 0; s < steps; s += 2) {
+    for (int s = s_begin; s < s_end; s += 2) {
         step(std::integral_constant<int, 0>{}, s);
-        if (s + 1 < steps) step(std::integral_constant<int, 1>{}, s + 1);
+        if (s + 1 < s_end) step(std::integral_constant<int, 1>{}, s + 1);
     }
 
     l += partner(l);
+    if (a.splits > 1) {
+        const int64_t row = ((int64_t)split * a.hq + head) * a.tq + pl.q0 + qi;
+        store_partial<DT>(o, a.partial + row * a.d, a.d, mine);
+        if (mine && h == 0) a.tops[row] = make_float2(m == -kInf ? -kInf : mc, l);
+        return;
+    }
     const float by = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // a NaN sum stays NaN
     const uint32_t top = store_own<DT>(o, by, a.out + (int64_t)(pl.q0 + qi) * a.out_row + (int64_t)head * a.out_head,
                                        a.d, mine);
     if (mine && h == 0)
         a.lse[(int64_t)head * a.tq + pl.q0 + qi] = l == 0.0f ? -kInf : (mc + __builtin_amdgcn_logf(l)) * kLn2;
+    if (a.absmax) block_max_to_global(top, a.absmax);
+}
+
+// out and lse of one (token, head) per d / 8 threads, from its splits' unnormalised sums,
+// their maxima (in powers of two) and totals.
+__global__ void __launch_bounds__(256) attention_forward_join_kernel(const AttentionArgs a)
+{
+    const int per_row = a.d / 8;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, rows = (int64_t)a.tq * a.hq, row = i / per_row;
+    const int c = (int)(i % per_row) * 8, head = (int)(row / a.tq), token = (int)(row % a.tq);
+    int from = 0, upto = a.tq;            // the tokens that belong to a sequence
+    if (a.cu_q) {
+        from = min(max(a.cu_q[0], 0), a.tq);
+        upto = min(max(a.cu_q[a.batch], 0), a.tq);
+    }
+    uint32_t top = 0;
+    if (row < rows && token >= from && token < upto) {
+        float m = -kInf, l = 0.0f, t[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int s = 0; s < a.splits; ++s) m = fmaxf(m, a.tops[s * rows + row].x);
+        const float use = m == -kInf ? 0.0f : m;
+        for (int s = 0; s < a.splits; ++s) {
+            const float2 x = a.tops[s * rows + row];
+            const float by = __builtin_amdgcn_exp2f(x.x - use);
+            const float4* p = reinterpret_cast<const float4*>(a.partial + (s * rows + row) * a.d + c);
+            const float4 u = p[0], v = p[1];
+            const float e[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+            l = fmaf(x.y, by, l);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) t[k] = fmaf(e[k], by, t[k]);
+        }
+        const float by = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            w[k] = bf16_pair(t[2 * k] * by, t[2 * k + 1] * by);
+            top = max(max(top, w[k] & 0x7FFF0000u), w[k] << 16 & 0x7FFFFFFFu);
+        }
+        *reinterpret_cast<uint4*>(a.out + (int64_t)token * a.out_row + (int64_t)head * a.out_head + c) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+        if (c == 0) a.lse[row] = l == 0.0f ? -kInf : (use + __builtin_amdgcn_logf(l)) * kLn2;
+    }
     if (a.absmax) block_max_to_global(top, a.absmax);
 }
 
@@ -504,8 +553,9 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dq_kernel(const Atte
 {
     constexpr int kTile = kKeys * DT * 2;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kTile];
-    int t, head;
-    deal(blockIdx.x, a.hq, t, head);
+    int t, unit;
+    deal(blockIdx.x, a.hq * a.splits, t, unit);
+    const int head = unit / a.splits, split = unit % a.splits;
     const Place pl = find_tile(a, a.tiles - 1 - t, 0);
     if (!pl.any) return;
     const int lane = threadIdx.x & 63, h = lane >> 5;
@@ -563,6 +613,7 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dq_kernel(const Atte
         __builtin_amdgcn_s_waitcnt(wait_loads(0));
         __syncthreads();
         float sum = 0.0f;
+#pragma unroll 1
         for (int u = 0; u < 2 * steps && 32 * u < see_last; ++u) {
             const uint32_t at = (uint32_t)(u / 2 * 2 * kTile + u % 2 * 32 * DT * 2);
             af32x16 p = af32x16{0}, dp = af32x16{0};
@@ -582,19 +633,22 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dq_kernel(const Atte
         }
         delta = sum + partner(sum);
     }
-    if (mine)
+    if (mine && split == 0)
         a.stats[(h ? (int64_t)a.tq * a.hq : 0) + (int64_t)head * a.tq + pl.q0 + qi] = h ? delta : lse;
 
-    const bool loaded = steps <= 2;       // with their tiles in LDS already
-    if (!loaded) {
-        ks.issue(0, lds0, wave);
-        vs.issue(0, lds0 + kTile, wave);
+    const bool loaded = steps <= 2;       // with their tiles in LDS already, in place (no split then)
+    const int s_begin = loaded ? 0 : (int)((int64_t)steps * split / a.splits);
+    const int s_end = !loaded ? (int)((int64_t)steps * (split + 1) / a.splits) : split == 0 ? steps : 0;
+    const int load_end = loaded ? 0 : s_end;
+    if (s_begin < load_end) {
+        ks.issue(s_begin * kKeys, lds0, wave);
+        vs.issue(s_begin * kKeys, lds0 + kTile, wave);
     }
     auto step = [&](auto stage, int s) {
         constexpr int at = stage.value * 2 * kTile, to = (2 - stage.value * 2) * kTile;
         __builtin_amdgcn_s_waitcnt(0x0F70);
         __syncthreads();
-        if (s + 1 < steps && !loaded) {
+        if (s + 1 < load_end) {
             ks.issue((s + 1) * kKeys, lds0 + to, wave);
             vs.issue((s + 1) * kKeys, lds0 + to + kTile, wave);
         }
@@ -646,9 +700,14 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dq_kernel(const Atte
             }
         }
     };
-    for (int s = 0; s < steps; s += 2) {
+    for (int s = s_begin; s < s_end; s += 2) {
         step(std::integral_constant<int, 0>{}, s);
-        if (s + 1 < steps) step(std::integral_constant<int, 1>{}, s + 1);
+        if (s + 1 < s_end) step(std::integral_constant<int, 1>{}, s + 1);
+    }
+    if (a.splits > 1) {
+        const int64_t row = ((int64_t)split * a.tq + pl.q0 + qi) * a.hq + head;
+        store_partial<DT>(dq, a.partial + row * a.d, a.d, mine);
+        return;
     }
     const uint32_t top = store_own<DT>(dq, a.scale, a.dq + (int64_t)(pl.q0 + qi) * a.dq_row + (int64_t)head * a.dq_head,
                                        a.d, mine);
@@ -819,32 +878,35 @@ __global__ void __launch_bounds__(64 * keys_waves(DT), 2) attention_dkv_kernel(c
     if (a.absmax) block_max_to_global(top, a.absmax);
 }
 
-// dk and dv from the chunks' partial sums, added in order: 8 elements per thread.
-__global__ void __launch_bounds__(256) attention_join_kernel(const AttentionArgs a)
+// Gradients from their partial sums [part][which][token][head][d], added in order: 8
+// elements per thread.  dq (one tensor, a.splits parts), or dk and dv (a.chunks parts).
+__global__ void __launch_bounds__(256) attention_join_kernel(const AttentionArgs a, int queries)
 {
-    const int per_row = a.d / 8;
-    const int64_t whole = (int64_t)a.tk * a.hk * a.d, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int which = blockIdx.y;
-    int64_t row = i / per_row;
-    const int c = (int)(i % per_row) * 8, head = (int)(row % a.hk), token = (int)(row / a.hk);
-    int from = 0, upto = a.tk;            // the tokens that belong to a sequence
-    if (a.cu_k) {
-        from = min(max(a.cu_k[0], 0), a.tk);
-        upto = min(max(a.cu_k[a.batch], 0), a.tk);
+    const int tokens = queries ? a.tq : a.tk, heads = queries ? a.hq : a.hk, parts = queries ? a.splits : a.chunks;
+    const int per_row = a.d / 8, which = blockIdx.y, tensors = gridDim.y;
+    const int64_t whole = (int64_t)tokens * heads * a.d, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t row = i / per_row;
+    const int c = (int)(i % per_row) * 8, head = (int)(row % heads), token = (int)(row / heads);
+    const int* cu = queries ? a.cu_q : a.cu_k;
+    int from = 0, upto = tokens;          // the tokens that belong to a sequence
+    if (cu) {
+        from = min(max(cu[0], 0), tokens);
+        upto = min(max(cu[a.batch], 0), tokens);
     }
     uint32_t top = 0;
     if (i < whole / 8 && token >= from && token < upto) {
         const float* p = a.partial + which * whole + row * a.d + c;
         float t[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int s = 0; s < a.chunks; ++s, p += 2 * whole) {
+        for (int s = 0; s < parts; ++s, p += tensors * whole) {
             const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
             const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int e = 0; e < 8; ++e) t[e] += v[e];
         }
-        const float by = which ? 1.0f : a.scale;
-        uint16_t* out = which ? a.dv + (int64_t)token * a.dv_row + (int64_t)head * a.dv_head
-                              : a.dk + (int64_t)token * a.dk_row + (int64_t)head * a.dk_head;
+        const float by = which ? 1.0f : a.scale;          // dq and dk carry the scale
+        uint16_t* out = queries ? a.dq + (int64_t)token * a.dq_row + (int64_t)head * a.dq_head
+                        : which ? a.dv + (int64_t)token * a.dv_row + (int64_t)head * a.dv_head
+                                : a.dk + (int64_t)token * a.dk_row + (int64_t)head * a.dk_head;
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -879,39 +941,72 @@ static int key_chunks(int64_t tq, int64_t tk, int hq, int hk, int d, int batch)
     return (int)std::max<int64_t>(1, std::min<int64_t>({(want + tiles - 1) / tiles, steps / 32, 8}));
 }
 
-int64_t attention_backward_workspace(int64_t tq, int64_t tk, int hq, int hk, int d, int batch)
+// Workgroups that share the keys of one tile of queries, in the forward and for dq: where
+// the tiles leave more than half of the CUs idle and the keys are many, at 4 or more
+// streamed tiles (256 keys) each.  Unsplit / split, MI355X, heads of 128: 100 queries of 8
+// heads on 4000 keys, forward 72 / 25 us, backward 110 / 48; one query of 32 heads on 16384
+// keys 274 / 49 and 378 / 107; 512 queries of 4 heads on 4096 keys 73 / 28 and 128 / 69.
+static int query_splits(int64_t tq, int64_t tk, int hq, int batch)
 {
-    const int chunks = key_chunks(tq, tk, hq, hk, d, batch);
-    const int64_t stats = (2 * tq * hq + 3) / 4 * 4;        // fp32 values; what follows is 16-byte aligned
-    return 4 * (stats + (chunks > 1 ? 2 * chunks * tk * hk * d : 0));
+    const int64_t tiles = tile_bound(tq, batch, kOwn) * hq, cus = device_cu_count();
+    if (2 * tiles > cus) return 1;
+    const int64_t steps = tk / batch / kKeys;             // of a sequence of average length
+    return (int)std::max<int64_t>(1, std::min<int64_t>({cus / tiles, steps / 4, 32}));
 }
 
-hipError_t launch_attention_forward(const AttentionArgs& args, hipStream_t stream)
+static int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }   // fp32 values, so that what follows is 16-byte aligned
+
+int64_t attention_forward_workspace(int64_t tq, int64_t tk, int hq, int d, int batch)
+{
+    const int64_t splits = query_splits(tq, tk, hq, batch);
+    return splits > 1 ? 4 * splits * (up4(2 * tq * hq) + tq * hq * d) : 0;
+}
+
+int64_t attention_backward_workspace(int64_t tq, int64_t tk, int hq, int hk, int d, int batch)
+{
+    const int64_t chunks = key_chunks(tq, tk, hq, hk, d, batch), splits = query_splits(tq, tk, hq, batch);
+    // the partial sums of dq are joined before those of dk and dv are written
+    return 4 * (up4(2 * tq * hq) + std::max(chunks > 1 ? 2 * chunks * tk * hk * d : 0, splits > 1 ? splits * tq * hq * d : 0));
+}
+
+hipError_t launch_attention_forward(const AttentionArgs& args, void* workspace, hipStream_t stream)
 {
     AttentionArgs a = args;
+    a.splits = query_splits(a.tq, a.tk, a.hq, a.batch);
+    a.tops = static_cast<float2*>(workspace);
+    a.partial = static_cast<float*>(workspace) + a.splits * up4(2 * (int64_t)a.tq * a.hq);
     a.tiles = (int)tile_bound(a.tq, a.batch, kOwn);
-    const dim3 grid((unsigned)(a.tiles * a.hq));
-    if (a.d <= 64) return launch(attention_forward_kernel<64>, grid, dim3(kAttThreads), stream, a);
-    return launch(attention_forward_kernel<128>, grid, dim3(kAttThreads), stream, a);
+    const dim3 grid((unsigned)(a.tiles * a.hq * a.splits));
+    const hipError_t e = a.d <= 64 ? launch(attention_forward_kernel<64>, grid, dim3(kAttThreads), stream, a)
+                                   : launch(attention_forward_kernel<128>, grid, dim3(kAttThreads), stream, a);
+    if (e != hipSuccess || a.splits == 1) return e;
+    const int64_t units = (int64_t)a.tq * a.hq * a.d / 8;
+    return launch(attention_forward_join_kernel, dim3((unsigned)((units + 255) / 256)), dim3(256), stream, a);
 }
 
 hipError_t launch_attention_backward(const AttentionArgs& args, hipStream_t stream)
 {
     AttentionArgs a = args;
     a.chunks = key_chunks(a.tq, a.tk, a.hq, a.hk, a.d, a.batch);
-    a.partial = a.stats + (2 * (int64_t)a.tq * a.hq + 3) / 4 * 4;
+    a.splits = query_splits(a.tq, a.tk, a.hq, a.batch);
+    a.partial = a.stats + up4(2 * (int64_t)a.tq * a.hq);
+    auto join = [&](int queries) {
+        const int64_t units = (queries ? (int64_t)a.tq * a.hq : (int64_t)a.tk * a.hk) * a.d / 8;
+        return launch(attention_join_kernel, dim3((unsigned)((units + 255) / 256), queries ? 1 : 2), dim3(256), stream,
+                      a, queries);
+    };
     a.tiles = (int)tile_bound(a.tq, a.batch, kOwn);
-    const dim3 grid_q((unsigned)(a.tiles * a.hq));
+    const dim3 grid_q((unsigned)(a.tiles * a.hq * a.splits));
     hipError_t e = a.d <= 64 ? launch(attention_dq_kernel<64>, grid_q, dim3(kAttThreads), stream, a)
                              : launch(attention_dq_kernel<128>, grid_q, dim3(kAttThreads), stream, a);
+    if (e == hipSuccess && a.splits > 1) e = join(1);
     if (e != hipSuccess) return e;
     a.tiles = (int)tile_bound(a.tk, a.batch, key_rows(a.d));
     const dim3 grid_k((unsigned)(a.tiles * a.hk * a.chunks));
     e = a.d <= 64 ? launch(attention_dkv_kernel<64>, grid_k, dim3(64 * keys_waves(64)), stream, a)
                   : launch(attention_dkv_kernel<128>, grid_k, dim3(64 * keys_waves(128)), stream, a);
     if (e != hipSuccess || a.chunks == 1) return e;
-    const int64_t units = (int64_t)a.tk * a.hk * a.d / 8;
-    return launch(attention_join_kernel, dim3((unsigned)((units + 255) / 256), 2), dim3(256), stream, a);
+    return join(0);
 }
 
 }  // namespace fp8k

@@ -145,17 +145,19 @@ struct AttentionArgs {
     uint16_t *out, *dq, *dk, *dv;         // out is read by the backward pass
     float* lse;                           // [hq, tq]
     float* stats;                         // backward: 2 * hq * tq fp32, then the partial sums
-    float* partial;
+    float* partial;                       // fp32 partial sums of split work
+    float2* tops;                         // forward, split: maxima and totals [split][hq][tq]
     const int *cu_q, *cu_k;
     uint32_t* absmax;                     // or null
     int64_t q_row, k_row, v_row, out_row, dout_row, dq_row, dk_row, dv_row;
     int64_t q_head, k_head, v_head, out_head, dout_head, dq_head, dk_head, dv_head;
-    int tq, tk, hq, hk, d, batch, causal, tiles, chunks;
+    int tq, tk, hq, hk, d, batch, causal, tiles, chunks, splits;
     float scale;
 };
 bool attention_grid_ok(int64_t tokens, int batch, int heads);
 int64_t attention_backward_workspace(int64_t tq, int64_t tk, int hq, int hk, int d, int batch);
-hipError_t launch_attention_forward(const AttentionArgs& args, hipStream_t stream);
+int64_t attention_forward_workspace(int64_t tq, int64_t tk, int hq, int d, int batch);
+hipError_t launch_attention_forward(const AttentionArgs& args, void* workspace, hipStream_t stream);
 hipError_t launch_attention_backward(const AttentionArgs& args, hipStream_t stream);
 
 // Cross entropy of a linear head (loss.hip): x [T, D], w [V, D].

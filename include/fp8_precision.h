@@ -581,14 +581,19 @@ typedef struct fp8_attention_shape {
 /*
  *   out     as q;  lse  fp32 [heads_q, tokens_q]
  *   absmax  fp32 scalar or NULL: becomes max(*absmax, max |out|), out as stored
+ *   workspace, workspace_bytes   device memory, 16-byte aligned, of at least the size
+ *           that fp8_attention_forward_workspace gives for the shape (0 for most: few
+ *           queries on many keys are split over the keys and joined; NULL then)
  * Rows of out and lse that belong to no sequence are not written.  Bounds outside
  * [0, tokens] are held to it; no byte outside the tensors is read or written.
  * Probabilities are rounded to bf16 for the product with v (sums and the softmax
  * stay in fp32).  A NaN or infinity in v may reach every query of its sequence.
  */
+fp8_status fp8_attention_forward_workspace(const fp8_attention_shape* shape, int64_t* bytes);
 fp8_status fp8_attention_forward(const fp8_attention_shape* shape, const fp8_head_tensor* q,
                                  const fp8_head_tensor* k, const fp8_head_tensor* v, const fp8_head_tensor* out,
-                                 float* lse, float* absmax, hipStream_t stream);
+                                 float* lse, float* absmax, void* workspace, int64_t workspace_bytes,
+                                 hipStream_t stream);
 
 /*
  * Gradients of q, k and v (of a shared key head: the sum over its query heads).

@@ -121,6 +121,11 @@ CASES = [
     ([2000], [2000], 8, 8, 128, True),
     ([1000], [1500], 8, 1, 64, True),
     ([300, 17] * 40, [300, 17] * 40, 2, 1, 64, True),   # more than 64 sequences
+    # few queries on many keys: the keys split over workgroups and joined
+    ([1], [5001], 4, 2, 128, True),
+    ([90], [3000], 2, 1, 80, False),
+    ([3, 100, 40], [2500, 90, 0], 4, 4, 64, True),      # some splits, and some sequences, have nothing to do
+    ([130], [8000], 1, 1, 128, True),
 ]
 
 
@@ -196,6 +201,25 @@ def test_rows_outside_every_sequence_are_left_alone(fp8):
     assert (out[:20] == 3).all() and (out[180:] == 3).all() and (lse[:, :20] == 5).all() and (lse[:, 180:] == 5).all()
     for t, w in zip(grads, want):
         assert torch.equal(t[20:180], w) and (t[:20] == 3).all() and (t[180:] == 3).all()
+
+
+def test_rows_outside_every_sequence_are_left_alone_by_split_work(fp8):
+    d, h = 64, 1
+    q, k, v, dout = make([60], [4000], h, h, d, 15)
+    cu_q, cu_k = (torch.tensor(b, dtype=torch.int32, device="cuda") for b in ([10, 50], [100, 3900]))
+    out, lse = torch.full_like(q, 3.0), torch.full((h, 60), 5.0, device="cuda")
+    fp8.attention(q, k, v, cu_q, cu_k, out=out, lse=lse)
+    grads = [torch.full_like(t, 3.0) for t in (q, k, v)]
+    fp8.attention_backward(dout, q, k, v, out, lse, cu_q, cu_k, dq=grads[0], dk=grads[1], dv=grads[2])
+    qs, ks = slice(10, 50), slice(100, 3900)
+    check_forward(q[qs], k[ks], v[ks], out[qs], lse[:, qs], [40], [3800], False, d ** -0.5)
+    check_backward(dout[qs], q[qs], k[ks], v[ks], out[qs], lse[:, qs], grads[0][qs], grads[1][ks], grads[2][ks], [40],
+                   [3800], False, d ** -0.5)
+    for t, keep in ((out, qs), (grads[0], qs), (grads[1], ks), (grads[2], ks)):
+        rest = torch.ones(len(t), dtype=torch.bool, device="cuda")
+        rest[keep] = False
+        assert (t[rest] == 3).all()
+    assert (lse[:, :10] == 5).all() and (lse[:, 50:] == 5).all()
 
 
 def test_bounds_out_of_range_are_held_to_the_tensor(fp8):
