@@ -29,8 +29,10 @@
 // transposed copy of anything exists.  Rows, columns and reduction elements past an
 // operand's end read as zero (the buffer's size, or an offset outside it).
 //
-// g is rounded to bf16, as an operand of the matrix units; z, the statistics and every
-// sum stay in fp32.  The sums are formed in a fixed order: no atomics.
+// g is rounded to bf16, as an operand of the matrix units -- divided by the largest
+// |dloss|, which the products' epilogues multiply in again: with one dloss for all tokens
+// (the mean), its own rounding would be a common error of every gradient, up to 2^-8.
+// z, the statistics and every sum stay in fp32.  The sums are formed in a fixed order: no atomics.
 #include "fp8_device.hpp"
 #include "fp8_internal.hpp"
 
@@ -211,6 +213,7 @@ struct LossArgs {
     const int64_t* target;
     const float* lse;
     const float* dloss;
+    const float* unit;                    // the largest |dloss|, which g leaves to its products' epilogues
     float2* stats;                        // [column block][T]: maximum, sum of exponentials
     float* hit;                           // [T]: the target's logit
     int v0, vocab;                        // the piece's first column in the vocabulary, and its size
@@ -381,11 +384,12 @@ __global__ void __launch_bounds__(256, loss_per_cu(MI, NJ)) loss_product_kernel(
             }
         }
     };
+    const float by = EPI == kStats ? 1.0f : *g.unit;
     auto keep_rows = [&]() {
         if ((EPI != kStats && EPI != kGrad) || (int)threadIdx.x >= BM) return;
         row_target[threadIdx.x] = my_target;
         if (EPI == kGrad) {
-            row_scale[threadIdx.x] = my_target < 0 ? 0.0f : my_scale;
+            row_scale[threadIdx.x] = my_target < 0 ? 0.0f : my_scale / by;
             row_lse[threadIdx.x] = my_target < 0 ? 0.0f : my_lse * kLossLog2e;
         }
     };
@@ -519,7 +523,7 @@ __global__ void __launch_bounds__(256, loss_per_cu(MI, NJ)) loss_product_kernel(
                         }
                         if (g.last)
                             *reinterpret_cast<uint2*>(g.out + (int64_t)m * g.out_pitch + n) =
-                                make_uint2(loss_pair(v.x, v.y), loss_pair(v.z, v.w));
+                                make_uint2(loss_pair(v.x * by, v.y * by), loss_pair(v.z * by, v.w * by));
                         else
                             *at = v;
                     }
@@ -566,7 +570,9 @@ __global__ void __launch_bounds__(256, loss_per_cu(MI, NJ)) loss_product_kernel(
                     typedef unsigned int u2 __attribute__((ext_vector_type(2)));
                     typedef __attribute__((address_space(3))) u2 lds_u2;
                     *(lds_u2*)(uintptr_t)(ew + r16 * kRowB + c * 16 + (q4 & 1) * 8) =
-                        u2{loss_pair(acc[i][j][0], acc[i][j][1]), loss_pair(acc[i][j][2], acc[i][j][3])};
+                        EPI == kGrad ? u2{loss_pair(acc[i][j][0], acc[i][j][1]), loss_pair(acc[i][j][2], acc[i][j][3])}
+                                     : u2{loss_pair(acc[i][j][0] * by, acc[i][j][1] * by),
+                                          loss_pair(acc[i][j][2] * by, acc[i][j][3] * by)};
                 }
                 __builtin_amdgcn_wave_barrier();             // one wave's LDS accesses stay in order
 #pragma unroll
@@ -625,7 +631,8 @@ loss_join_kernel(const float2* __restrict__ stats, int blocks, const float* __re
 
 // dx = the splits' partial sums, added in order and rounded: 4 elements per thread.
 __global__ void __launch_bounds__(256)
-loss_dx_kernel(const float4* __restrict__ sum, int splits, int64_t n4, uint2* __restrict__ dx)
+loss_dx_kernel(const float4* __restrict__ sum, int splits, int64_t n4, const float* __restrict__ unit,
+               uint2* __restrict__ dx)
 {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n4) return;
@@ -634,7 +641,26 @@ loss_dx_kernel(const float4* __restrict__ sum, int splits, int64_t n4, uint2* __
         const float4 o = sum[(int64_t)s * n4 + i];
         t = make_float4(t.x + o.x, t.y + o.y, t.z + o.z, t.w + o.w);
     }
-    dx[i] = make_uint2(loss_pair(t.x, t.y), loss_pair(t.z, t.w));
+    const float by = *unit;
+    dx[i] = make_uint2(loss_pair(t.x * by, t.y * by), loss_pair(t.z * by, t.w * by));
+}
+
+// The largest finite |dloss|; 1 if there is none above 0.
+__global__ void __launch_bounds__(1024) loss_unit_kernel(const float* __restrict__ dloss, int T, float* __restrict__ unit)
+{
+    __shared__ uint32_t part[16];
+    uint32_t top = 0;
+    for (int i = threadIdx.x; i < T; i += 1024) {
+        const uint32_t v = __float_as_uint(dloss[i]) & 0x7FFFFFFFu;
+        if (v < 0x7F800000u) top = max(top, v);
+    }
+    top = wave_max_u32(top);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < 16; ++i) top = max(top, part[i]);
+        *unit = top == 0 ? 1.0f : __uint_as_float(top);
+    }
 }
 
 // ---------------------------------------------------------------------- plan and launches
@@ -672,7 +698,7 @@ int dx_splits(int64_t T, int64_t D, int64_t piece)
 }
 
 struct Space {                            // the workspace's parts, in bytes from its start
-    int64_t g, sum, total;
+    int64_t g, sum, unit, total;
     int64_t piece;
     int splits;
 };
@@ -684,7 +710,8 @@ Space backward_space(int64_t T, int64_t V, int64_t D)
     s.splits = dx_splits(T, D, std::min(s.piece, V));
     s.g = 0;
     s.sum = up_to(T * s.piece * 2, 256);
-    s.total = s.sum + up_to(T * D * 4 * s.splits, 256);
+    s.unit = s.sum + up_to(T * D * 4 * s.splits, 256);
+    s.total = s.unit + 256;
     return s;
 }
 
@@ -774,6 +801,9 @@ hipError_t launch_loss_backward(const float* dloss, const void* x, const void* w
     const int rows = tile_rows(T);
     uint16_t* gm = static_cast<uint16_t*>(workspace);
     float* sum = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.sum);
+    float* unit = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.unit);
+    hipError_t e = launch(loss_unit_kernel, dim3(1), dim3(1024), stream, dloss, (int)T, unit);
+    if (e != hipSuccess) return e;
     const Side xs{static_cast<const uint16_t*>(x), D};
     int splits = sp.splits;
     for (int64_t v0 = 0; v0 < V; v0 += sp.piece) {
@@ -788,12 +818,13 @@ hipError_t launch_loss_backward(const float* dloss, const void* x, const void* w
         g.target = target;
         g.lse = lse;
         g.dloss = dloss;
+        g.unit = unit;
         g.v0 = (int)v0;
         g.vocab = (int)V;
         g.out = gm;
         g.out_pitch = sp.piece;
         g.out_cols = (int)up_to(n, 8);
-        hipError_t e = product<false, false, kGrad>(g, rows, 1, stream);
+        e = product<false, false, kGrad>(g, rows, 1, stream);
         if (e != hipSuccess) return e;
 
         LossArgs d{};
@@ -803,6 +834,7 @@ hipError_t launch_loss_backward(const float* dloss, const void* x, const void* w
         d.Q = (int)D;
         d.R = (int)n;
         d.sum = sum;
+        d.unit = unit;
         d.out = static_cast<uint16_t*>(dx);
         d.out_pitch = D;
         d.fresh = v0 == 0;
@@ -816,6 +848,7 @@ hipError_t launch_loss_backward(const float* dloss, const void* x, const void* w
         h.P = (int)n;
         h.Q = (int)D;
         h.R = (int)T;
+        h.unit = unit;
         h.out = static_cast<uint16_t*>(dw) + v0 * D;
         h.out_pitch = D;
         e = product<true, true, kStore>(h, T <= kStep ? 128 : 256, 1, stream);
@@ -824,7 +857,7 @@ hipError_t launch_loss_backward(const float* dloss, const void* x, const void* w
     if (splits > 1) {
         const int64_t n4 = T * D / 4;
         return launch(loss_dx_kernel, dim3((unsigned)((n4 + 255) / 256)), dim3(256), stream,
-                      reinterpret_cast<const float4*>(sum), splits, n4, static_cast<uint2*>(dx));
+                      reinterpret_cast<const float4*>(sum), splits, n4, static_cast<const float*>(unit), static_cast<uint2*>(dx));
     }
     return hipSuccess;
 }

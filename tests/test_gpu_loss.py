@@ -98,6 +98,22 @@ def test_backward_in_several_pieces(fp8, T, V, D):
     check_gradients(x, w, t, d, dx, dw)
 
 
+@pytest.mark.parametrize("T,V,D", [(255, 2048, 256), (17, 4096, 128), (1023, 1000, 64)])
+def test_a_mean_is_not_rounded_into_every_gradient(fp8, T, V, D):
+    """1 / T next to the middle between two bf16 values: as a factor of g it would be off by
+    2^-8 for every token alike.  The roundings left are the results' own (an rms of at
+    most 2^-8 / sqrt 3, uniform in the last place) and g's, where a target's p - 1 rounds to
+    -1 (p, about 1 / V at these logits, up to e^1 of it)."""
+    x, w, t, d = make(T, V, D, 3, sigma=0.1 * D ** -0.5)
+    d = torch.full_like(d, 1.0 / T)
+    _, lse = fp8.linear_cross_entropy(x, w, t)
+    dx, dw = fp8.linear_cross_entropy_backward(d, x, w, t, lse)
+    *_, g, _ = reference(x, w, t, d)
+    for got, want in ((dx, g @ w.to(F64)), (dw, g.t() @ x.to(F64))):
+        off = float((got.to(F64) - want).norm() / want.norm())
+        assert off <= 2.0 ** -8 / 3 ** 0.5 + 2.72 / V, off
+
+
 def test_gradient_against_differences(fp8):
     T, V, D = 3, 11, 8
     x, w, t, d = make(T, V, D, 4, sigma=1.0)
