@@ -47,6 +47,12 @@ template <bool F32> struct Raw8;
 template <> struct Raw8<false> { uint4 a; };
 template <> struct Raw8<true> { uint4 a, b; };
 
+// What follows from these bits is computed from here on, not kept from before.
+__device__ __forceinline__ void opaque(uint4& v)
+{
+    asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w));
+}
+
 // Load the 8 elements from column c of a row of `cols`; those past the row's end
 // are zero.  VEC: cols is a multiple of 8, so every group is whole and 16-byte
 // aligned; otherwise the elements are read one by one.
@@ -273,54 +279,104 @@ norm_backward_kernel(const uint16_t* __restrict__ dy, const void* __restrict__ x
     const uint8_t* xb = static_cast<const uint8_t*>(x);
     const uint8_t* rb = static_cast<const uint8_t*>(dres);
 
-    float w[NV][8], dw[NV][8], db[NV][8];
+    // Two groups per lane leave the registers no room for the weight's and the bias's sums,
+    // which then lie in LDS (each lane its own), nor for what the second sweep needs in fp32,
+    // which is formed again from the row as loaded; an fp32 dres is loaded in between.
+    constexpr bool kAgain = NV > 1, kLate = NV > 1 && F32;
+    constexpr int kSums = RMS ? 1 : 2;
+    __shared__ float4 sums[kAgain ? kSums * NV * 2 : 1][kAgain ? kNormMaxWaves * 64 : 1];
+    Raw8<false> wv[NV];
+    float dw[NV][8], db[NV][8];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        widen<false>(load8<false, VEC>(weight, col0 + v * step, cols), w[v]);
+        wv[v] = load8<false, VEC>(weight, col0 + v * step, cols);
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[v][e] = db[v][e] = 0.0f;
     }
-
-    Raw8<false> yv[NV];
-    Raw8<F32> xv[NV], rv[NV];
-    float m = 0.0f, r = 0.0f;
-    auto fetch = [&](int row) {
+    if (kAgain)
+        for (int i = 0; i < kSums * NV * 2; ++i) sums[i][threadIdx.x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    Raw8<false> yv[NV], yn[NV];
+    Raw8<F32> xv[NV], xn[NV], rv[NV], rn[NV];
+    float m = 0.0f, r = 0.0f, mn = 0.0f, rstd_n = 0.0f;
+    auto fetch = [&](int row) __attribute__((always_inline)) {
         const size_t at = (size_t)row * (size_t)cols;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            yv[v] = load8<false, VEC>(dy + at, col0 + v * step, cols);
-            xv[v] = load8<F32, VEC>(xb + at * kX, col0 + v * step, cols);
-            if (dres) rv[v] = load8<F32, VEC>(rb + at * kX, col0 + v * step, cols);
+            yn[v] = load8<false, VEC>(dy + at, col0 + v * step, cols);
+            xn[v] = load8<F32, VEC>(xb + at * kX, col0 + v * step, cols);
+            if (!kLate && dres) rn[v] = load8<F32, VEC>(rb + at * kX, col0 + v * step, cols);
         }
-        r = rstd[row];
-        if (!RMS) m = mean[row];
+        rstd_n = rstd[row];
+        if (!RMS) mn = mean[row];
     };
 
     int row = blockIdx.x;
     if (row < rows) fetch(row);
     for (int turn = 0; row < rows; turn ^= 1) {
         float g[NV][8], h[NV][8], keep[NV][8];
-        float2 t = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            float d[8], xs[8];
+        // h and g of group v; past the row's end dy and w are zero, so whatever h is there
+        // adds nothing (the mean and the reciprocal deviation of a finite row are finite)
+        auto form = [&](int v, float (&d)[8]) __attribute__((always_inline)) {
+            float xs[8], w[8];
             widen<false>(yv[v], d);
             widen<F32>(xv[v], xs);
-            if (dres) widen<F32>(rv[v], keep[v]);
+            widen<false>(wv[v], w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                // past the row's end dy and w are zero, so whatever h is there adds nothing
-                // (the mean and the reciprocal deviation of a finite row are finite)
                 h[v][e] = (xs[e] - m) * r;
-                g[v][e] = d[e] * w[v][e];
-                dw[v][e] = fmaf(d[e], h[v][e], dw[v][e]);
-                db[v][e] += d[e];
+                g[v][e] = d[e] * w[e];
+            }
+        };
+        float2 t = make_float2(0.0f, 0.0f);
+        m = mn;
+        r = rstd_n;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            yv[v] = yn[v];
+            xv[v] = xn[v];
+            if (!kLate) rv[v] = rn[v];
+            if (kAgain) __builtin_amdgcn_sched_barrier(0);   // one group's values at a time
+            float d[8];
+            form(v, d);
+            if (!kAgain && dres) widen<F32>(rv[v], keep[v]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
                 t.x = fmaf(g[v][e], h[v][e], t.x);
                 t.y += g[v][e];
             }
+            if (kAgain) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float4* p = &sums[2 * v + k][threadIdx.x];
+                    float4 a = *p;
+                    a.x = fmaf(d[4 * k], h[v][4 * k], a.x);
+                    a.y = fmaf(d[4 * k + 1], h[v][4 * k + 1], a.y);
+                    a.z = fmaf(d[4 * k + 2], h[v][4 * k + 2], a.z);
+                    a.w = fmaf(d[4 * k + 3], h[v][4 * k + 3], a.w);
+                    *p = a;
+                    if (!RMS) {
+                        p = &sums[2 * (NV + v) + k][threadIdx.x];
+                        a = *p;
+                        a.x += d[4 * k];
+                        a.y += d[4 * k + 1];
+                        a.z += d[4 * k + 2];
+                        a.w += d[4 * k + 3];
+                        *p = a;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    dw[v][e] = fmaf(d[e], h[v][e], dw[v][e]);
+                    db[v][e] += d[e];
+                }
+            }
         }
         const size_t at = (size_t)row * (size_t)cols;
-        const float rr = r;
+        if (kLate && dres) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) rv[v] = load8<F32, VEC>(rb + at * kX, col0 + v * step, cols);
+        }
         row += gridDim.x;
         if (row < rows) fetch(row);
         t.x = wave_sum(t.x);
@@ -329,10 +385,20 @@ norm_backward_kernel(const uint16_t* __restrict__ dy, const void* __restrict__ x
         const float along = t.x * inv_n, flat = RMS ? 0.0f : t.y * inv_n;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            float o[8];
+            float o[8], d[8];
+            if (kAgain) {
+                __builtin_amdgcn_sched_barrier(0);
+                opaque(yv[v].a);
+                opaque(xv[v].a);
+                if constexpr (F32) opaque(xv[v].b);
+                opaque(wv[v].a);
+                if (dres) opaque(rv[v].a);
+                form(v, d);
+                if (dres) widen<F32>(rv[v], keep[v]);
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                o[e] = rr * (g[v][e] - flat - h[v][e] * along);
+                o[e] = r * (g[v][e] - flat - h[v][e] * along);
                 if (dres) o[e] += keep[v][e];
             }
             store8<F32, VEC>(static_cast<uint8_t*>(dx) + at * kX, col0 + v * step, cols, o);
@@ -343,8 +409,16 @@ norm_backward_kernel(const uint16_t* __restrict__ dy, const void* __restrict__ x
     float* pb = pw + (size_t)gridDim.x * (size_t)cols;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
+        if (kAgain) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float4 a = sums[2 * v + k][threadIdx.x], b = sums[RMS ? 0 : 2 * (NV + v) + k][threadIdx.x];
+                dw[v][4 * k] = a.x, dw[v][4 * k + 1] = a.y, dw[v][4 * k + 2] = a.z, dw[v][4 * k + 3] = a.w;
+                db[v][4 * k] = b.x, db[v][4 * k + 1] = b.y, db[v][4 * k + 2] = b.z, db[v][4 * k + 3] = b.w;
+            }
+        }
         store8<true, VEC>(pw, col0 + v * step, cols, dw[v]);
-        if (want_db) store8<true, VEC>(pb, col0 + v * step, cols, db[v]);
+        if (!RMS && want_db) store8<true, VEC>(pb, col0 + v * step, cols, db[v]);
     }
 }
 
