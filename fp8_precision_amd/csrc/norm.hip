@@ -53,9 +53,15 @@ __device__ __forceinline__ void opaque(uint4& v)
     asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w));
 }
 
+// 16 bytes at an address that is only a multiple of an element's size: one instruction
+// too, as the hardware takes global accesses of any alignment.  Rows that are no multiple
+// of 8 elements (2048 x 9001 bf16, backward) took 99 us element by element, 57 so.
+typedef uint32_t Loose16 __attribute__((ext_vector_type(4), aligned(2)));
+__device__ __forceinline__ uint4 strict(const Loose16& v) { return make_uint4(v.x, v.y, v.z, v.w); }
+
 // Load the 8 elements from column c of a row of `cols`; those past the row's end
 // are zero.  VEC: cols is a multiple of 8, so every group is whole and 16-byte
-// aligned; otherwise the elements are read one by one.
+// aligned; otherwise a row's last group is read element by element.
 template <bool F32, bool VEC>
 __device__ __forceinline__ Raw8<F32> load8(const void* row, int c, int cols)
 {
@@ -70,7 +76,15 @@ __device__ __forceinline__ Raw8<F32> load8(const void* row, int c, int cols)
                 r.a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + c);
             }
         }
-    } else {
+    } else if (c + 8 <= cols) {
+        if constexpr (F32) {
+            const Loose16* p = reinterpret_cast<const Loose16*>(static_cast<const float*>(row) + c);
+            r.a = strict(p[0]);
+            r.b = strict(p[1]);
+        } else {
+            r.a = strict(*reinterpret_cast<const Loose16*>(static_cast<const uint16_t*>(row) + c));
+        }
+    } else if (c < cols) {
         uint32_t w[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -112,29 +126,29 @@ __device__ __forceinline__ void widen(const Raw8<F32>& r, float (&f)[8])
 template <bool F32, bool VEC>
 __device__ __forceinline__ void store8(void* row, int c, int cols, const float (&f)[8])
 {
-    if constexpr (F32) {
-        float* p = static_cast<float*>(row) + c;
-        if (VEC) {
-            if (c < cols) {
-                reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-                reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-            }
-        } else {
+    if (c >= cols) return;
+    constexpr int kWords = F32 ? 8 : 4, kSize = F32 ? 4 : 2;
+    uint8_t* p = static_cast<uint8_t*>(row) + (size_t)c * kSize;
+    uint32_t w[kWords];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (c + e < cols) p[e] = f[e];
-        }
-    } else {
-        uint16_t* p = static_cast<uint16_t*>(row) + c;
-        const uint4 w = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
-        if (VEC) {
-            if (c < cols) *reinterpret_cast<uint4*>(p) = w;
-        } else {
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+    for (int i = 0; i < kWords; ++i) w[i] = F32 ? __float_as_uint(f[i]) : pack2(f[2 * i & 7], f[(2 * i + 1) & 7]);
+    if (VEC || c + 8 <= cols) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (c + e < cols) p[e] = (uint16_t)(ww[e >> 1] >> (16 * (e & 1)));
+        for (int i = 0; i < kWords; i += 4) {
+            if (VEC)
+                *reinterpret_cast<uint4*>(p + 4 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+            else
+                *reinterpret_cast<Loose16*>(p + 4 * i) = Loose16{w[i], w[i + 1], w[i + 2], w[i + 3]};
         }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        if (c + e >= cols) continue;
+        if (F32)
+            reinterpret_cast<uint32_t*>(p)[e] = w[e & (kWords - 1)];
+        else
+            reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
     }
 }
 
