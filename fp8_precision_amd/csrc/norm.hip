@@ -20,7 +20,7 @@
 // registers between the sweeps), backward too.  A row is one workgroup of
 // W = ceil(cols / (512 NV)) waves, a lane holding NV groups of 8 consecutive
 // elements; a row's sums are a butterfly in each wave and, for W > 1, one exchange
-// through LDS.  Backward workgroups walk rows with the next row's loads issued
+// through LDS.  Narrow rows share a workgroup.  Backward workgroups walk rows with the next row's loads issued
 // before the current row's exchange, so that the exchange does not leave the
 // memory idle, and keep the weight gradient of their rows in registers; they
 // write one partial row each, which a second launch adds up in a fixed order
@@ -36,6 +36,7 @@ typedef __bf16 nb16x2 __attribute__((ext_vector_type(2)));
 typedef float nf32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kNormMaxWaves = 16;
+constexpr int kNarrow = 256;              // threads of a workgroup that takes several rows
 
 __device__ __forceinline__ uint32_t pack2(float a, float b)
 {
@@ -152,10 +153,12 @@ __device__ __forceinline__ void store8(void* row, int c, int cols, const float (
     }
 }
 
-__device__ __forceinline__ float wave_sum(float v)
+// Sum over the `lanes` (a power of two) neighbouring lanes of a row.
+template <int lanes>
+__device__ __forceinline__ float lane_sum(float v)
 {
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+    for (int off = lanes / 2; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
     return v;
 }
 
@@ -176,19 +179,24 @@ __device__ __forceinline__ float2 block_sum2(float2 v, float2* part, int wave, i
 
 }  // namespace
 
-// Forward, one row per workgroup.  Measured on MI355X, 4096 x 4096 bf16 with the
-// residual sum (134 MB): see the table in the launcher's comment.
-template <bool F32, bool VEC, int NV, bool RMS>
-__global__ void __launch_bounds__(kNormMaxWaves * 64)
+// Forward.  L = 0: a row per workgroup; else L lanes per row, several rows per workgroup.
+// 4096 x 4096 bf16 with the residual sum (134 MB): 23.6 us, 5.7 TB/s (a large copy on the
+// same chip: 5.8); a single row is bound by the call.
+template <bool F32, bool VEC, int NV, int L, bool RMS>
+__global__ void __launch_bounds__(L ? kNarrow : kNormMaxWaves * 64)
 norm_forward_kernel(const void* __restrict__ x, const uint16_t* __restrict__ add, const uint16_t* __restrict__ weight,
-                    const uint16_t* __restrict__ bias, float eps, int cols, uint16_t* __restrict__ y,
+                    const uint16_t* __restrict__ bias, float eps, uint32_t rows, int cols, uint16_t* __restrict__ y,
                     void* __restrict__ sum, float* __restrict__ mean, float* __restrict__ rstd,
                     uint32_t* __restrict__ absmax)
 {
     __shared__ float2 part[2][kNormMaxWaves];
-    const size_t at = (size_t)blockIdx.x * (size_t)cols;
-    const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-    const int col0 = threadIdx.x * 8, step = blockDim.x * 8;
+    constexpr int kLanes = L ? L : 64;
+    const uint32_t row = L ? blockIdx.x * (kNarrow / kLanes) + threadIdx.x / kLanes : blockIdx.x;   // rows < 2^31
+    const bool have = !L || row < rows;
+    const size_t at = have ? (size_t)row * (size_t)cols : 0;
+    const int wave = threadIdx.x >> 6, waves = L ? 1 : blockDim.x >> 6;
+    const int lane = L ? threadIdx.x % kLanes : threadIdx.x;
+    const int col0 = have ? lane * 8 : cols, step = L ? 0 : blockDim.x * 8;
     const uint8_t* xr = static_cast<const uint8_t*>(x) + at * (F32 ? 4 : 2);
 
     Raw8<F32> xv[NV];
@@ -231,7 +239,7 @@ norm_forward_kernel(const void* __restrict__ x, const uint16_t* __restrict__ add
         for (int v = 0; v < NV; ++v)
 #pragma unroll
             for (int e = 0; e < 8; ++e) t += s[v][e];      // places past the row's end hold zero
-        m = block_sum2(make_float2(wave_sum(t), 0.0f), part[0], wave, waves).x * inv_n;
+        m = block_sum2(make_float2(lane_sum<kLanes>(t), 0.0f), part[0], wave, waves).x * inv_n;
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -243,11 +251,11 @@ norm_forward_kernel(const void* __restrict__ x, const uint16_t* __restrict__ add
     for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int e = 0; e < 8; ++e) q = fmaf(s[v][e], s[v][e], q);
-    const float var = block_sum2(make_float2(wave_sum(q), 0.0f), part[1], wave, waves).x * inv_n;
+    const float var = block_sum2(make_float2(lane_sum<kLanes>(q), 0.0f), part[1], wave, waves).x * inv_n;
     const float r = 1.0f / sqrtf(var + eps);
-    if (threadIdx.x == 0) {
-        rstd[blockIdx.x] = r;
-        if (!RMS) mean[blockIdx.x] = m;
+    if (lane == 0 && have) {
+        rstd[row] = r;
+        if (!RMS) mean[row] = m;
     }
 
     uint32_t top = 0;
@@ -277,18 +285,21 @@ norm_forward_kernel(const void* __restrict__ x, const uint16_t* __restrict__ add
     if (absmax) block_max_to_global(top, absmax);
 }
 
-// Backward over rows blockIdx.x, blockIdx.x + gridDim.x, ...; partial[2][grid][cols]
+// Backward over every gridDim.x-th row (L = 0) or set of rows; partial[2][grid][cols]
 // gets the workgroup's sums of dy h and, if asked for, of dy.
-template <bool F32, bool VEC, int NV, bool RMS>
-__global__ void __launch_bounds__(kNormMaxWaves * 64)
+// 8192 x 5120 bf16 with dres (336 MB): 64 us, 5.2 TB/s, the sums' launch included (3 us);
+// more workgroups read no faster and write more partial rows.
+template <bool F32, bool VEC, int NV, int L, bool RMS>
+__global__ void __launch_bounds__(L ? kNarrow : kNormMaxWaves * 64)
 norm_backward_kernel(const uint16_t* __restrict__ dy, const void* __restrict__ x, const uint16_t* __restrict__ weight,
                      const float* __restrict__ mean, const float* __restrict__ rstd, const void* __restrict__ dres,
-                     int rows, int cols, void* __restrict__ dx, float* __restrict__ partial, int want_db)
+                     uint32_t rows, int cols, void* __restrict__ dx, float* __restrict__ partial, int want_db)
 {
     __shared__ float2 part[2][kNormMaxWaves];
     constexpr size_t kX = F32 ? 4 : 2;
-    const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-    const int col0 = threadIdx.x * 8, step = blockDim.x * 8;
+    constexpr int kLanes = L ? L : 64, kRows = L ? kNarrow / kLanes : 1;
+    const int wave = threadIdx.x >> 6, waves = L ? 1 : blockDim.x >> 6;
+    const int col0 = (L ? threadIdx.x % kLanes : threadIdx.x) * 8, step = L ? 0 : blockDim.x * 8;
     const float inv_n = 1.0f / (float)cols;
     const uint8_t* xb = static_cast<const uint8_t*>(x);
     const uint8_t* rb = static_cast<const uint8_t*>(dres);
@@ -312,7 +323,7 @@ norm_backward_kernel(const uint16_t* __restrict__ dy, const void* __restrict__ x
     Raw8<false> yv[NV], yn[NV];
     Raw8<F32> xv[NV], xn[NV], rv[NV], rn[NV];
     float m = 0.0f, r = 0.0f, mn = 0.0f, rstd_n = 0.0f;
-    auto fetch = [&](int row) __attribute__((always_inline)) {
+    auto fetch = [&](uint32_t row) __attribute__((always_inline)) {
         const size_t at = (size_t)row * (size_t)cols;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -324,7 +335,7 @@ norm_backward_kernel(const uint16_t* __restrict__ dy, const void* __restrict__ x
         if (!RMS) mn = mean[row];
     };
 
-    int row = blockIdx.x;
+    uint32_t row = L ? blockIdx.x * kRows + threadIdx.x / kLanes : blockIdx.x;
     if (row < rows) fetch(row);
     for (int turn = 0; row < rows; turn ^= 1) {
         float g[NV][8], h[NV][8], keep[NV][8];
@@ -391,10 +402,10 @@ norm_backward_kernel(const uint16_t* __restrict__ dy, const void* __restrict__ x
 #pragma unroll
             for (int v = 0; v < NV; ++v) rv[v] = load8<F32, VEC>(rb + at * kX, col0 + v * step, cols);
         }
-        row += gridDim.x;
+        row += gridDim.x * kRows;
         if (row < rows) fetch(row);
-        t.x = wave_sum(t.x);
-        if (!RMS) t.y = wave_sum(t.y);
+        t.x = lane_sum<kLanes>(t.x);
+        if (!RMS) t.y = lane_sum<kLanes>(t.y);
         t = block_sum2(t, part[turn], wave, waves);
         const float along = t.x * inv_n, flat = RMS ? 0.0f : t.y * inv_n;
 #pragma unroll
@@ -419,6 +430,29 @@ norm_backward_kernel(const uint16_t* __restrict__ dy, const void* __restrict__ x
         }
     }
 
+    if (L) {                                                 // the workgroup's rows, in order
+        __shared__ float join[L ? kNarrow / 64 : 1][2][L ? kLanes * 8 : 1];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+#pragma unroll
+            for (int off = kLanes; off < 64; off <<= 1) {
+                dw[0][e] += __shfl_xor(dw[0][e], off, 64);
+                if (!RMS) db[0][e] += __shfl_xor(db[0][e], off, 64);
+            }
+            if ((int)(threadIdx.x & 63) < kLanes) {
+                join[wave][0][col0 + e] = dw[0][e];
+                if (!RMS) join[wave][1][col0 + e] = db[0][e];
+            }
+        }
+        __syncthreads();
+        if ((int)threadIdx.x >= kLanes) return;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            for (int k = 1; k < kNarrow / 64; ++k) {
+                dw[0][e] += join[k][0][col0 + e];
+                if (!RMS) db[0][e] += join[k][1][col0 + e];
+            }
+    }
     float* pw = partial + (size_t)blockIdx.x * (size_t)cols;
     float* pb = pw + (size_t)gridDim.x * (size_t)cols;
 #pragma unroll
@@ -459,18 +493,32 @@ norm_join_kernel(const float* __restrict__ partial, int parts, int cols, float* 
     }
 }
 
-// Lanes per row and groups per lane.  One group of 8 per lane and as many waves as
-// that takes, up to 8192 columns; two above.
-static int norm_waves(int64_t cols, int nv) { return (int)((cols + 512 * nv - 1) / (512 * nv)); }
-static int norm_groups(int64_t cols) { return cols <= 512 * kNormMaxWaves ? 1 : 2; }
+// How a row is laid over lanes.  Up to 512 columns: the fewest of 16, 32 or 64 lanes that
+// hold it 8 elements each, 256 threads taking several rows: 131072 rows of 128 bf16 (one
+// norm per head), forward 39.7 us with a wave per row and 24.2 so, backward 54 and 29.6;
+// 327680 of 64: 86 and 31, 109 and 38; 32768 of 512: 23.4 and 24.1, 36 and 30.  Above, a
+// workgroup of as many waves as it takes, up to 8192 columns; two groups per lane above that.
+struct NormLayout {
+    int lanes, groups, threads, rows;     // lanes 0: the workgroup's; rows of a workgroup
+};
 
-// Workgroups of the backward launch: enough to fill the chip (32 waves per CU
+static NormLayout norm_layout(int64_t cols)
+{
+    if (cols <= 512) {
+        const int lanes = cols <= 128 ? 16 : cols <= 256 ? 32 : 64;
+        return {lanes, 1, kNarrow, kNarrow / lanes};
+    }
+    const int groups = cols <= 512 * kNormMaxWaves ? 1 : 2;
+    return {0, groups, 64 * (int)((cols + 512 * groups - 1) / (512 * groups)), 1};
+}
+
+// Workgroups of the backward launch: enough to fill the chip (16 waves per CU
 // when rows allow), no more partial rows than rows.
 static int norm_backward_grid(int64_t rows, int64_t cols)
 {
-    const int waves = norm_waves(cols, norm_groups(cols));
-    const int64_t fill = (int64_t)device_cu_count() * std::max(1, 16 / waves);
-    return (int)std::min<int64_t>(rows, fill);
+    const NormLayout l = norm_layout(cols);
+    const int64_t fill = (int64_t)device_cu_count() * std::max(1, 1024 / l.threads);
+    return (int)std::min<int64_t>((rows + l.rows - 1) / l.rows, fill);
 }
 
 int64_t norm_backward_workspace(int64_t rows, int64_t cols)
@@ -481,16 +529,24 @@ int64_t norm_backward_workspace(int64_t rows, int64_t cols)
 namespace {
 
 template <typename Fn>
-hipError_t norm_variant(bool f32, bool vec, int nv, bool rms, Fn&& fn)
+hipError_t norm_variant(bool f32, bool vec, const NormLayout& l, bool rms, Fn&& fn)
 {
-    auto pick_rms = [&](auto f, auto v, auto n) {
-        return rms ? fn(f, v, n, std::true_type{}) : fn(f, v, n, std::false_type{});
+    auto pick_rms = [&](auto f, auto v, auto n, auto lanes) {
+        return rms ? fn(f, v, n, lanes, std::true_type{}) : fn(f, v, n, lanes, std::false_type{});
     };
-    auto pick_nv = [&](auto f, auto v) {
-        return nv == 1 ? pick_rms(f, v, std::integral_constant<int, 1>{})
-                       : pick_rms(f, v, std::integral_constant<int, 2>{});
+    auto pick_layout = [&](auto f, auto v) {
+        using One = std::integral_constant<int, 1>;
+        if (l.groups == 2) return pick_rms(f, v, std::integral_constant<int, 2>{}, std::integral_constant<int, 0>{});
+        switch (l.lanes) {
+        case 16: return pick_rms(f, v, One{}, std::integral_constant<int, 16>{});
+        case 32: return pick_rms(f, v, One{}, std::integral_constant<int, 32>{});
+        case 64: return pick_rms(f, v, One{}, std::integral_constant<int, 64>{});
+        default: return pick_rms(f, v, One{}, std::integral_constant<int, 0>{});
+        }
     };
-    auto pick_vec = [&](auto f) { return vec ? pick_nv(f, std::true_type{}) : pick_nv(f, std::false_type{}); };
+    auto pick_vec = [&](auto f) {
+        return vec ? pick_layout(f, std::true_type{}) : pick_layout(f, std::false_type{});
+    };
     return f32 ? pick_vec(std::true_type{}) : pick_vec(std::false_type{});
 }
 
@@ -500,11 +556,12 @@ hipError_t launch_norm_forward(const void* x, bool f32, const void* add, const v
                                float eps, bool rms, int64_t rows, int64_t cols, void* y, void* sum, float* mean,
                                float* rstd, float* absmax, hipStream_t stream)
 {
-    const int nv = norm_groups(cols);
-    return norm_variant(f32, cols % 8 == 0, nv, rms, [&](auto f, auto v, auto n, auto ms) {
-        return launch(norm_forward_kernel<f.value, v.value, n.value, ms.value>, dim3((unsigned)rows),
-                      dim3(64 * norm_waves(cols, n.value)), stream, x, static_cast<const uint16_t*>(add),
-                      static_cast<const uint16_t*>(weight), static_cast<const uint16_t*>(bias), eps, (int)cols,
+    const NormLayout l = norm_layout(cols);
+    return norm_variant(f32, cols % 8 == 0, l, rms, [&](auto f, auto v, auto n, auto lanes, auto ms) {
+        return launch(norm_forward_kernel<f.value, v.value, n.value, lanes.value, ms.value>,
+                      dim3((unsigned)((rows + l.rows - 1) / l.rows)), dim3(l.threads), stream, x,
+                      static_cast<const uint16_t*>(add), static_cast<const uint16_t*>(weight),
+                      static_cast<const uint16_t*>(bias), eps, (uint32_t)rows, (int)cols,
                       static_cast<uint16_t*>(y), sum, mean, rstd, reinterpret_cast<uint32_t*>(absmax));
     });
 }
@@ -513,11 +570,12 @@ hipError_t launch_norm_backward(const void* dy, const void* x, bool f32, const v
                                 const float* rstd, const void* dres, bool rms, int64_t rows, int64_t cols, void* dx,
                                 float* dw, float* db, float* partial, hipStream_t stream)
 {
-    const int nv = norm_groups(cols), grid = norm_backward_grid(rows, cols);
-    const hipError_t e = norm_variant(f32, cols % 8 == 0, nv, rms, [&](auto f, auto v, auto n, auto ms) {
-        return launch(norm_backward_kernel<f.value, v.value, n.value, ms.value>, dim3(grid),
-                      dim3(64 * norm_waves(cols, n.value)), stream, static_cast<const uint16_t*>(dy), x,
-                      static_cast<const uint16_t*>(weight), mean, rstd, dres, (int)rows, (int)cols, dx, partial,
+    const NormLayout l = norm_layout(cols);
+    const int grid = norm_backward_grid(rows, cols);
+    const hipError_t e = norm_variant(f32, cols % 8 == 0, l, rms, [&](auto f, auto v, auto n, auto lanes, auto ms) {
+        return launch(norm_backward_kernel<f.value, v.value, n.value, lanes.value, ms.value>, dim3(grid),
+                      dim3(l.threads), stream, static_cast<const uint16_t*>(dy), x,
+                      static_cast<const uint16_t*>(weight), mean, rstd, dres, (uint32_t)rows, (int)cols, dx, partial,
                       db ? 1 : 0);
     });
     if (e != hipSuccess) return e;

@@ -107,6 +107,19 @@ def test_backward(fp8, rows, cols, rms, f32, joined):
         assert ((db.to(F64) - dy.sum(0)).abs() <= dy.abs().sum(0) * col + 1e-30).all()
 
 
+# Rows narrow enough that a workgroup takes several: one per head of a projection, as many
+# as make its workgroups walk, and counts that leave the last set of rows ragged.
+NARROW = [(16, 16), (17, 128), (5, 129), (9, 250), (1001, 64), (33, 300), (70, 480), (40003, 128), (20011, 200)]
+
+
+@pytest.mark.parametrize("rows,cols", NARROW)
+@pytest.mark.parametrize("rms,f32,joined", [(True, False, False), (False, False, True), (True, True, True),
+                                            (False, True, False)])
+def test_narrow_rows(fp8, rows, cols, rms, f32, joined):
+    test_forward(fp8, rows, cols, rms, f32, joined)
+    test_backward(fp8, rows, cols, rms, f32, joined)
+
+
 @pytest.mark.parametrize("rms", [True, False])
 def test_gradient_against_differences(fp8, rms):
     """dx, dweight and dbias against central differences of the float64 forward."""
