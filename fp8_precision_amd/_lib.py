@@ -751,18 +751,25 @@ def _heads(t, name, shape=None):
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3 or (shape is not None and t.shape != shape):
+    size, step = t.shape, t.stride()
+    if len(size) != 3 or (shape is not None and size != shape):
         raise ValueError(f"{name} must be " + ("[tokens, heads, head_dim]" if shape is None else f"{tuple(shape)}"))
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    if step[2] != 1 and size[2] > 1:
         raise ValueError(f"{name} must be contiguous along head_dim")
-    return ctypes.byref(_HeadTensor(t.data_ptr(), t.stride(0), t.stride(1)))
+    return ctypes.byref(_HeadTensor(t.data_ptr(), step[0], step[1]))
+
+
+def _new_heads(like):
+    """A new contiguous tensor of ``like``'s shape, type and device."""
+    return torch.empty_like(like, memory_format=torch.contiguous_format)
 
 
 def _attention_shape(q, k, v, cu_q, cu_k, causal, scale):
     """The call's shape, checked: (shape struct, q, k, v as head tensors)."""
     hq, hk = _heads(q, "q"), _heads(k, "k")
-    hv = _heads(v, "v", k.shape)
-    if q.shape[2] != k.shape[2]:
+    size_q, size_k = q.shape, k.shape
+    hv = _heads(v, "v", size_k)
+    if size_q[2] != size_k[2]:
         raise ValueError("q and k must have one head_dim")
     if (cu_q is None) != (cu_k is None):
         raise ValueError("cu_q and cu_k go together")
@@ -773,8 +780,8 @@ def _attention_shape(q, k, v, cu_q, cu_k, causal, scale):
         batch = cu_q.numel() - 1
         if batch < 1 or cu_k.numel() != batch + 1:
             raise ValueError("cu_q and cu_k must hold one bound more than there are sequences")
-    shape = _AttentionShape(q.shape[0], k.shape[0], q.shape[1], k.shape[1], q.shape[2], batch, _ptr(cu_q), _ptr(cu_k),
-                            1 if causal else 0, q.shape[2] ** -0.5 if scale is None else scale)
+    shape = _AttentionShape(size_q[0], size_k[0], size_q[1], size_k[1], size_q[2], batch, _ptr(cu_q), _ptr(cu_k),
+                            1 if causal else 0, size_q[2] ** -0.5 if scale is None else scale)
     return shape, hq, hk, hv
 
 
@@ -795,7 +802,7 @@ def attention(q, k, v, cu_q=None, cu_k=None, causal: bool = False, scale: float 
     if absmax is not None:
         _scalar_in(absmax, "absmax")
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        out = _new_heads(q)
     ho = _heads(out, "out", q.shape)
     lse = _out(lse, "lse", (q.shape[1], q.shape[0]), torch.float32, q.device)
     ws = _workspace("fp8_attention_forward_workspace", q.device, ctypes.byref(shape))
@@ -811,15 +818,17 @@ def attention_backward(dout, q, k, v, out, lse, cu_q=None, cu_k=None, causal: bo
     gradient of the projection's output); ``absmax`` becomes the largest magnitude of
     the three and its earlier value.  Returns (dq, dk, dv)."""
     shape, hq, hk, hv = _attention_shape(q, k, v, cu_q, cu_k, causal, scale)
-    hg, ho = _heads(dout, "dout", q.shape), _heads(out, "out", q.shape)
+    size_q, size_k = q.shape, k.shape
+    hg, ho = _heads(dout, "dout", size_q), _heads(out, "out", size_q)
     _dev_tensor(lse, "lse", torch.float32)
-    if tuple(lse.shape) != (q.shape[1], q.shape[0]):
+    if lse.shape != (size_q[1], size_q[0]):
         raise ValueError("lse must be [heads_q, tokens_q]")
     if absmax is not None:
         _scalar_in(absmax, "absmax")
-    new = lambda t, like: torch.empty(like.shape, dtype=torch.bfloat16, device=like.device) if t is None else t
-    dq, dk, dv = new(dq, q), new(dk, k), new(dv, v)
-    hdq, hdk, hdv = _heads(dq, "dq", q.shape), _heads(dk, "dk", k.shape), _heads(dv, "dv", v.shape)
+    dq = _new_heads(q) if dq is None else dq
+    dk = _new_heads(k) if dk is None else dk
+    dv = _new_heads(v) if dv is None else dv
+    hdq, hdk, hdv = _heads(dq, "dq", size_q), _heads(dk, "dk", size_k), _heads(dv, "dv", size_k)
     ws = _workspace("fp8_attention_backward_workspace", q.device, ctypes.byref(shape))
     _run("fp8_attention_backward", _lib.fp8_attention_backward,
          (dout, q, k, v, out, lse, cu_q, cu_k, dq, dk, dv, absmax, ws), ctypes.byref(shape), hg, hq, hk, hv, ho,

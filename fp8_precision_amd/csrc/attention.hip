@@ -932,13 +932,16 @@ bool attention_grid_ok(int64_t tokens, int batch, int heads)
 
 // Workgroups that share the steps of one tile of keys.  With less than two tiles per CU
 // (few key heads, or short sequences of many queries) the causal mask leaves the first
-// tiles' workgroups running alone: their steps are then split, at 32 or more to a chunk
-// (8192 causal tokens, 40 query and 8 key heads of 128: 264 workgroups).
+// tiles' workgroups running alone: their steps are then split, at 8 or more to a chunk
+// (8192 causal tokens, 40 query and 8 key heads of 128: 264 workgroups).  The backward at
+// 32 or more to a chunk and at 8, MI355X, heads of 128: 1024 tokens of 8 query and 2 key
+// heads 92 / 62 us, 512 of 16 and 4 84 / 58, 2048 of 8 and 8 121 / 118; at 4, 1024 tokens
+// of 16 and 16 heads took 86 instead of 71.
 static int key_chunks(int64_t tq, int64_t tk, int hq, int hk, int d, int batch)
 {
     const int64_t tiles = tile_bound(tk, batch, key_rows(d)) * hk, want = 2 * (int64_t)device_cu_count();
     const int64_t steps = (tq / batch + kQueries - 1) / kQueries * (hq / hk);   // of a sequence of average length
-    return (int)std::max<int64_t>(1, std::min<int64_t>({(want + tiles - 1) / tiles, steps / 32, 8}));
+    return (int)std::max<int64_t>(1, std::min<int64_t>({(want + tiles - 1) / tiles, steps / 8, 16}));
 }
 
 // Workgroups that share the keys of one tile of queries, in the forward and for dq: where

@@ -98,6 +98,12 @@ def test_backward_in_several_pieces(fp8, T, V, D):
     check_gradients(x, w, t, d, dx, dw)
 
 
+@pytest.mark.parametrize("T,V,D", [(5000, 300, 136), (2049, 1, 8), (4096, 256, 264), (1500, 1700, 1032)])
+def test_backward_of_a_small_vocabulary(fp8, T, V, D):
+    """dweight's sum over the tokens is split over workgroups."""
+    test_backward(fp8, T, V, D)
+
+
 @pytest.mark.parametrize("T,V,D", [(255, 2048, 256), (17, 4096, 128), (1023, 1000, 64)])
 def test_a_mean_is_not_rounded_into_every_gradient(fp8, T, V, D):
     """1 / T next to the middle between two bf16 values: as a factor of g it would be off by
