@@ -672,6 +672,15 @@ namespace {
 
 // Rows of a tile: the fewest that T needs, for few tokens.
 int tile_rows(int64_t T) { return T <= 64 ? 64 : T <= 128 ? 128 : 256; }
+
+// The same for the logits, which take the smallest tiles (64 x 128) also where these are
+// no more than the CUs.  MI355X, forward, larger tiles / these: 298 tokens, 1933 x 2960
+// 38.6 / 21.4 us; 100, 4000 x 4096 48.8 / 25.2; 128, 8000 x 1024 20.3 / 14.6.  With two to
+// a CU they lose: 200, 16000 x 4096 53.6 / 113.8.
+int logit_rows(int64_t T, int64_t V)
+{
+    return (T + 63) / 64 * ((V + 127) / 128) <= device_cu_count() ? 64 : tile_rows(T);
+}
 int column_block(int rows) { return rows == 64 ? 32 : 128; }       // a wave's columns of the logits
 
 int64_t up_to(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
@@ -702,8 +711,8 @@ int dx_splits(int64_t T, int64_t D, int64_t piece)
 
 // dw of a small vocabulary likewise: where the vocabulary is one piece and its tiles fill at
 // most half of the CUs, its reduction over the tokens is split (8 or more steps each) and
-// the partial sums are joined.  Unsplit / split, the backward, MI355X: 8039 tokens,
-// 1246 x 272, 131 / 78 us; 8192, 256 x 4096: 169 / 123.
+// the partial sums are joined.  The split saves 56 us of 131 with 8039 tokens, 1246 x 272,
+// and 46 of 169 with 8192, 256 x 4096 (MI355X).
 int dw_splits(int64_t T, int64_t V, int64_t D, int64_t piece)
 {
     const int64_t tiles = (V + 255) / 256 * ((D + 255) / 256), steps = (T + kStep - 1) / kStep;
@@ -784,7 +793,7 @@ hipError_t product(LossArgs g, int rows, int splits, hipStream_t stream)
 
 int64_t loss_forward_workspace(int64_t T, int64_t V)
 {
-    const int cb = column_block(tile_rows(T));
+    const int cb = column_block(logit_rows(T, V));
     return up_to((V + cb - 1) / cb * T * 8, 256) + T * 4;
 }
 
@@ -793,7 +802,7 @@ int64_t loss_backward_workspace(int64_t T, int64_t V, int64_t D) { return backwa
 hipError_t launch_loss_forward(const void* x, const void* w, const int64_t* target, int64_t T, int64_t V, int64_t D,
                                float* loss, float* lse, void* workspace, hipStream_t stream)
 {
-    const int rows = tile_rows(T), cb = column_block(rows);
+    const int rows = logit_rows(T, V), cb = column_block(rows);
     const int blocks = (int)((V + cb - 1) / cb);
     LossArgs g{};
     g.a = {static_cast<const uint16_t*>(x), D};
@@ -845,7 +854,7 @@ hipError_t launch_loss_backward(const float* dloss, const void* x, const void* w
         g.out = gm;
         g.out_pitch = sp.piece;
         g.out_cols = (int)up_to(n, 8);
-        e = product<false, false, kGrad>(g, rows, 1, stream);
+        e = product<false, false, kGrad>(g, logit_rows(T, n), 1, stream);
         if (e != hipSuccess) return e;
 
         LossArgs d{};
