@@ -227,6 +227,7 @@ struct LossArgs {
 
 struct Unit {
     int m0, n0, r0, kt, split;
+    int turn;                             // the reduction step it begins with
 };
 
 }  // namespace
@@ -246,6 +247,12 @@ __global__ void __launch_bounds__(256, loss_per_cu(MI, NJ)) loss_product_kernel(
     constexpr int kLoads = BM / 32 + BN / 32;
     constexpr int kEpi = EPI == kGrad || EPI == kStore ? 16 * 16 * NJ * 2 : 0;   // a wave's 16 rows of bf16
     constexpr int kHalf = MI / 2;
+    // Few rows: bound by reading w, whose rows are often a power of two apart; workgroups
+    // that all begin with a row's start would then read the same few of the memory's
+    // channels at any one time, so each begins with another step of the reduction (16
+    // tokens, 32000 x 4096, the weight in memory: 64 us with one beginning, 51 so; 128
+    // tokens, 50000 x 2048: 57.6 and 46.5; with tiles of 256 rows it loses, 87 and 94).
+    constexpr bool kTurn = BM <= 128 && !LA && !LB;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * kStage + 4 * kEpi];
     // the tile's rows: target (-1: none), dloss, lse in powers of two
     __shared__ int row_target[BM];
@@ -273,7 +280,13 @@ __global__ void __launch_bounds__(256, loss_per_cu(MI, NJ)) loss_product_kernel(
         const int s0 = w.split * g.per;
         w.r0 = s0 * kStep;
         w.kt = min(g.steps - s0, g.per);
+        w.turn = kTurn && !g.halves && g.R % kStep == 0 ? w.n0 / BN % w.kt : 0;
         return w;
+    };
+    // step kt of the unit, and the load descriptors' step
+    auto turned = [&](const Unit& w, int kt) {
+        kt += w.turn;
+        return kTurn && kt >= w.kt ? kt - w.kt : kt;
     };
 
     Feed<LA, BM> fa;
@@ -302,7 +315,7 @@ __global__ void __launch_bounds__(256, loss_per_cu(MI, NJ)) loss_product_kernel(
         for (int s = 0; s < NS; ++s) {
             const int kt = min(s, w.kt - 1);
             trim(w, kt);
-            const lu32x4 da = fa.desc(kt), db = fb.desc(kt);
+            const lu32x4 da = fa.desc(turned(w, kt)), db = fb.desc(turned(w, kt));
 #pragma unroll
             for (int x = 0; x < BM / 32; ++x)
                 loss_to_lds(fa.voff[x], da,
@@ -419,16 +432,16 @@ __global__ void __launch_bounds__(256, loss_per_cu(MI, NJ)) loss_product_kernel(
         // that the count of loads in flight stays the same)
         int ahead = min(NS, w.kt - 1);
         trim(w, ahead);
-        half0(cur, fb.desc(ahead));
+        half0(cur, fb.desc(turned(w, ahead)));
         for (int kt = 0; kt + 1 < w.kt; ++kt) {
             const uint32_t nxt = cur + kStage == NS * kStage ? 0 : cur + kStage;
             // the next step's loads of this wave (later: whole steps and one B), and its reads
             __builtin_amdgcn_s_waitcnt(wait_loads((NS - 2) * kLoads + kLoadsB) & 0xF0FF);
             lds_barrier();                                   // everyone's; this step's A is read
-            half1(true, cur, nxt, fa.desc(ahead));
+            half1(true, cur, nxt, fa.desc(turned(w, ahead)));
             ahead = min(kt + 1 + NS, w.kt - 1);
             trim(w, ahead);
-            half0(nxt, fb.desc(ahead));
+            half0(nxt, fb.desc(turned(w, ahead)));
             cur = nxt;
         }
         __builtin_amdgcn_s_waitcnt(wait_loads(0));
