@@ -287,8 +287,7 @@ norm_forward_kernel(const void* __restrict__ x, const uint16_t* __restrict__ add
 
 // Backward over every gridDim.x-th row (L = 0) or set of rows; partial[2][grid][cols]
 // gets the workgroup's sums of dy h and, if asked for, of dy.
-// 8192 x 5120 bf16 with dres (336 MB): 64 us, 5.2 TB/s, the sums' launch included (3 us);
-// more workgroups read no faster and write more partial rows.
+// 8192 x 5120 bf16 with dres (336 MB): 64 us, 5.2 TB/s, the sums' launch (4 us) included.
 template <bool F32, bool VEC, int NV, int L, bool RMS>
 __global__ void __launch_bounds__(L ? kNarrow : kNormMaxWaves * 64)
 norm_backward_kernel(const uint16_t* __restrict__ dy, const void* __restrict__ x, const uint16_t* __restrict__ weight,
@@ -512,13 +511,16 @@ static NormLayout norm_layout(int64_t cols)
     return {0, groups, 64 * (int)((cols + 512 * groups - 1) / (512 * groups)), 1};
 }
 
-// Workgroups of the backward launch: enough to fill the chip (16 waves per CU
-// when rows allow), no more partial rows than rows.
+// Workgroups of the backward launch: enough to fill the chip (16 waves per CU when rows
+// allow), but beyond one per CU only with four or more of its rows (or sets of rows) for
+// each: every one costs a partial row to write and to add.  With a row or more, four or
+// more, eight or more, bf16: 4096 x 1024 17.7 / 14.3 / 15.2 us, 2048 x 2048 15.5 / 13.0 / 14.9;
+// 1537 x 1000 fp32 with a bias 17.6 / 13.0 / 15.0; 300 x 640 is fastest spread out, 5.9 / 7.9 / 10.9.
 static int norm_backward_grid(int64_t rows, int64_t cols)
 {
     const NormLayout l = norm_layout(cols);
-    const int64_t fill = (int64_t)device_cu_count() * std::max(1, 1024 / l.threads);
-    return (int)std::min<int64_t>((rows + l.rows - 1) / l.rows, fill);
+    const int64_t cus = device_cu_count(), fill = cus * std::max(1, 1024 / l.threads), sets = (rows + l.rows - 1) / l.rows;
+    return (int)std::min<int64_t>(fill, std::max<int64_t>((sets + 3) / 4, std::min<int64_t>(sets, cus)));
 }
 
 int64_t norm_backward_workspace(int64_t rows, int64_t cols)
