@@ -775,7 +775,8 @@ static fp8k::AttentionArgs attention_args(const fp8_attention_shape& s)
 
 static int64_t attention_forward_bytes(const fp8_attention_shape& s)
 {
-    return fp8k::attention_forward_workspace(s.tokens_q, s.tokens_k, (int)s.heads_q, (int)s.head_dim, (int)s.batch);
+    return fp8k::attention_forward_workspace(s.tokens_q, s.tokens_k, (int)s.heads_q, (int)s.heads_k, (int)s.head_dim,
+                                              (int)s.batch);
 }
 
 fp8_status fp8_attention_forward_workspace(const fp8_attention_shape* shape, int64_t* bytes)

@@ -301,7 +301,7 @@ __device__ __forceinline__ void bounds(const int* cu, int i, int total, int& fro
 
 // Every lane takes a sequence, 64 at a time; a prefix sum over the wave finds the one
 // that holds tile t.  `own` is the side that is tiled (0: queries, 1: keys).
-__device__ __forceinline__ Place find_tile(const AttentionArgs& a, int t, int own, int rows = kOwn)
+__device__ __forceinline__ Place find_tile(const AttentionArgs& a, int t, int own, int rows = kOwn, int group = 1)
 {
     const int lane = threadIdx.x & 63;
     Place p{};
@@ -309,7 +309,7 @@ __device__ __forceinline__ Place find_tile(const AttentionArgs& a, int t, int ow
     for (int b0 = 0; b0 < a.batch; b0 += 64) {
         int from = 0, count = 0;
         if (b0 + lane < a.batch) bounds(own ? a.cu_k : a.cu_q, b0 + lane, own ? a.tk : a.tq, from, count);
-        const int tiles = (count + rows - 1) / rows;
+        const int tiles = (int)(((int64_t)count * group + rows - 1) / rows);
         int upto = tiles;
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1) {
@@ -357,7 +357,9 @@ constexpr int kKeys = 64;                 // keys per streamed tile, forward and
 
 // ---------------------------------------------------------------------- forward
 
-// 32 queries per wave; 64 keys a step, with one running maximum and sum per query.  Operands
+// 32 rows per wave, a row being a query of one head, or, where the queries are few, of one of
+// the `group` heads that share a key head, which then read its keys once; 64 keys a step,
+// with one running maximum and sum per row.  Operands
 // are read from LDS four instructions ahead of the matrix instruction that takes them.
 // MI355X, causal, heads of 128: 4096 tokens, 32 heads 148 us (0.93 PFLOP/s); 8192 packed
 // tokens, 40 query and 8 key heads 262 us (0.92).  Bound by the two products and the
@@ -371,23 +373,26 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_forward_kernel(const
     constexpr int kTile = kKeys * DT * 2;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kTile];
     int t, unit;
-    deal(blockIdx.x, a.hq * a.splits, t, unit);
-    const int head = unit / a.splits, split = unit % a.splits;
-    const Place pl = find_tile(a, a.tiles - 1 - t, 0);     // a sequence's last (longest) tiles first
+    deal(blockIdx.x, a.hq / a.group * a.splits, t, unit);
+    const int split = unit % a.splits, head0 = unit / a.splits * a.group;
+    const Place pl = find_tile(a, a.tiles - 1 - t, 0, kOwn, a.group);   // a sequence's last (longest) tiles first
     if (!pl.any) return;
     const int lane = threadIdx.x & 63, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
-    const int khead = head / (a.hq / a.hk);
+    const int khead = head0 / (a.hq / a.hk);
 
-    const int q_wave = pl.first + wave * 32, qi = q_wave + (lane & 31);
-    const bool mine = qi < pl.nq;
+    // row r of the sequence: query r / group, head head0 + r % group
+    const int rows = pl.nq * a.group, r_wave = pl.first + wave * 32, ri = r_wave + (lane & 31);
+    const int q_wave = r_wave / a.group, q_last = (r_wave + 31) / a.group;
+    const int qi = ri / a.group, head = head0 + ri - qi * a.group;
+    const bool mine = ri < rows;
     const int shift = pl.nk - pl.nq;
     // keys seen: by this lane's query, by the wave's first and last, by the workgroup's last
     const int see = a.causal ? min(pl.nk, qi + shift + 1) : pl.nk;
     const int see_first = a.causal ? min(pl.nk, q_wave + shift + 1) : pl.nk;
-    const int see_last = a.causal ? min(pl.nk, q_wave + 31 + shift + 1) : pl.nk;
-    const int end = a.causal ? min(pl.nk, min(pl.first + kOwn, pl.nq) + shift) : pl.nk;
+    const int see_last = r_wave >= rows ? 0 : a.causal ? min(pl.nk, q_last + shift + 1) : pl.nk;
+    const int end = a.causal ? min(pl.nk, min((pl.first + kOwn - 1) / a.group + 1, pl.nq) + shift) : pl.nk;
     const int all = end > 0 ? (end + kKeys - 1) / kKeys : 0;
     const int s_begin = (int)((int64_t)all * split / a.splits), s_end = (int)((int64_t)all * (split + 1) / a.splits);
 
@@ -510,39 +515,57 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_forward_kernel(const
     if (a.absmax) block_max_to_global(top, a.absmax);
 }
 
-// out and lse of one (token, head) per d / 8 threads, from its splits' unnormalised sums,
-// their maxima (in powers of two) and totals.
+// out and lse of one (token, head) per workgroup, from its splits' unnormalised sums, their
+// maxima (in powers of two) and totals: 8 elements per thread, the splits dealt over as
+// many groups of d / 8 threads as there are, which are then added in order.  (With one
+// group per row, whose threads walk all splits, one query of 40 heads on 16384 keys of 8
+// took 51 us at 64 splits, longer than the work that is split; so, 21 us.)
 __global__ void __launch_bounds__(256) attention_forward_join_kernel(const AttentionArgs a)
 {
-    const int per_row = a.d / 8;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, rows = (int64_t)a.tq * a.hq, row = i / per_row;
-    const int c = (int)(i % per_row) * 8, head = (int)(row / a.tq), token = (int)(row % a.tq);
-    int from = 0, upto = a.tq;            // the tokens that belong to a sequence
-    if (a.cu_q) {
-        from = min(max(a.cu_q[0], 0), a.tq);
-        upto = min(max(a.cu_q[a.batch], 0), a.tq);
+    __shared__ float4 part[256][2];
+    const int64_t rows = (int64_t)a.tq * a.hq, row = blockIdx.x;
+    const int head = (int)(row / a.tq), token = (int)(row % a.tq);
+    if (a.cu_q && (token < a.cu_q[0] || token >= a.cu_q[a.batch])) return;   // of no sequence
+    const int per = a.d / 8, groups = 256 / per, k = threadIdx.x / per, c = threadIdx.x % per * 8;
+    float m = -kInf, l = 0.0f;
+    for (int s = threadIdx.x & 63; s < a.splits; s += 64) m = fmaxf(m, a.tops[s * rows + row].x);
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+    const float use = m == -kInf ? 0.0f : m;
+    for (int s = threadIdx.x & 63; s < a.splits; s += 64) {
+        const float2 x = a.tops[s * rows + row];
+        l = fmaf(x.y, __builtin_amdgcn_exp2f(x.x - use), l);
     }
-    uint32_t top = 0;
-    if (row < rows && token >= from && token < upto) {
-        float m = -kInf, l = 0.0f, t[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int s = 0; s < a.splits; ++s) m = fmaxf(m, a.tops[s * rows + row].x);
-        const float use = m == -kInf ? 0.0f : m;
-        for (int s = 0; s < a.splits; ++s) {
-            const float2 x = a.tops[s * rows + row];
-            const float by = __builtin_amdgcn_exp2f(x.x - use);
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) l += __shfl_xor(l, off, 64);
+    float t[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (k < groups)
+#pragma unroll 4
+        for (int s = k; s < a.splits; s += groups) {
+            const float by = __builtin_amdgcn_exp2f(a.tops[s * rows + row].x - use);
             const float4* p = reinterpret_cast<const float4*>(a.partial + (s * rows + row) * a.d + c);
             const float4 u = p[0], v = p[1];
             const float e[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-            l = fmaf(x.y, by, l);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) t[k] = fmaf(e[k], by, t[k]);
+            for (int i = 0; i < 8; ++i) t[i] = fmaf(e[i], by, t[i]);
+        }
+    part[threadIdx.x][0] = make_float4(t[0], t[1], t[2], t[3]);
+    part[threadIdx.x][1] = make_float4(t[4], t[5], t[6], t[7]);
+    __syncthreads();
+    uint32_t top = 0;
+    if (k == 0) {
+        for (int g = 1; g < groups; ++g) {
+            const float4 u = part[g * per + threadIdx.x][0], v = part[g * per + threadIdx.x][1];
+            const float e[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[i] += e[i];
         }
         const float by = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
         uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            w[k] = bf16_pair(t[2 * k] * by, t[2 * k + 1] * by);
-            top = max(max(top, w[k] & 0x7FFF0000u), w[k] << 16 & 0x7FFFFFFFu);
+        for (int i = 0; i < 4; ++i) {
+            w[i] = bf16_pair(t[2 * i] * by, t[2 * i + 1] * by);
+            top = max(max(top, w[i] & 0x7FFF0000u), w[i] << 16 & 0x7FFFFFFFu);
         }
         *reinterpret_cast<uint4*>(a.out + (int64_t)token * a.out_row + (int64_t)head * a.out_head + c) =
             make_uint4(w[0], w[1], w[2], w[3]);
@@ -955,29 +978,40 @@ static int key_chunks(int64_t tq, int64_t tk, int hq, int hk, int d, int batch)
 }
 
 // Workgroups that share the keys of one tile of queries, in the forward and for dq: where
-// the tiles leave more than half of the CUs idle and the keys are many, at 4 or more
-// streamed tiles (256 keys) each.  Unsplit / split, MI355X, heads of 128: 100 queries of 8
-// heads on 4000 keys, forward 72 / 25 us, backward 110 / 48; one query of 32 heads on 16384
-// keys 274 / 49 and 378 / 107; 512 queries of 4 heads on 4096 keys 73 / 28 and 128 / 69.
-static int query_splits(int64_t tq, int64_t tk, int hq, int batch)
+// there are fewer tiles than CUs and the keys are many, up to two workgroups per CU, at 4 or
+// more streamed tiles (256 keys) each.  Unsplit / split, MI355X, heads of 128: 100 queries
+// of 8 heads on 4000 keys, forward 72 / 19 us, backward 107 / 46; one query of 32 heads on
+// 16384 keys 270 / 47 and 493 / 231; 512 queries of 4 heads on 4096 keys 73 / 28 and 124 / 63.
+static int query_splits(int64_t tq, int64_t tk, int hq, int batch, int group)
 {
-    const int64_t tiles = tile_bound(tq, batch, kOwn) * hq, cus = device_cu_count();
-    if (2 * tiles > cus) return 1;
+    const int64_t tiles = tile_bound(tq * group, batch, kOwn) * (hq / group), cus = device_cu_count();
+    if (tiles > cus) return 1;
     const int64_t steps = tk / batch / kKeys;             // of a sequence of average length
-    return (int)std::max<int64_t>(1, std::min<int64_t>({cus / tiles, steps / 4, 32}));
+    return (int)std::max<int64_t>(1, std::min<int64_t>({2 * cus / tiles, steps / 4, 128}));
+}
+
+// Query heads that share a tile of the forward: all that share a key head, where a
+// sequence's queries are few (half a tile on average); else each has tiles of its own.
+// MI355X, one query per sequence, heads of 128, apart / together: 64 sequences of 4096 keys,
+// 32 and 8 heads 394 / 193 us (1.07 GB of keys and values, 5.6 TB/s); 8 of 8192, 40 and 8
+// 157 / 61; one of 16384, 40 and 8 36 / 21.
+static int tile_group(int64_t tq, int hq, int hk, int batch)
+{
+    const int group = hq / hk;
+    return tq / batch <= kOwn / 2 && tq * group < 0x7FFFFF00 ? group : 1;   // rows of a sequence are counted in int
 }
 
 static int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }   // fp32 values, so that what follows is 16-byte aligned
 
-int64_t attention_forward_workspace(int64_t tq, int64_t tk, int hq, int d, int batch)
+int64_t attention_forward_workspace(int64_t tq, int64_t tk, int hq, int hk, int d, int batch)
 {
-    const int64_t splits = query_splits(tq, tk, hq, batch);
+    const int64_t splits = query_splits(tq, tk, hq, batch, tile_group(tq, hq, hk, batch));
     return splits > 1 ? 4 * splits * (up4(2 * tq * hq) + tq * hq * d) : 0;
 }
 
 int64_t attention_backward_workspace(int64_t tq, int64_t tk, int hq, int hk, int d, int batch)
 {
-    const int64_t chunks = key_chunks(tq, tk, hq, hk, d, batch), splits = query_splits(tq, tk, hq, batch);
+    const int64_t chunks = key_chunks(tq, tk, hq, hk, d, batch), splits = query_splits(tq, tk, hq, batch, 1);
     // the partial sums of dq are joined before those of dk and dv are written
     return 4 * (up4(2 * tq * hq) + std::max(chunks > 1 ? 2 * chunks * tk * hk * d : 0, splits > 1 ? splits * tq * hq * d : 0));
 }
@@ -985,23 +1019,23 @@ int64_t attention_backward_workspace(int64_t tq, int64_t tk, int hq, int hk, int
 hipError_t launch_attention_forward(const AttentionArgs& args, void* workspace, hipStream_t stream)
 {
     AttentionArgs a = args;
-    a.splits = query_splits(a.tq, a.tk, a.hq, a.batch);
+    a.group = tile_group(a.tq, a.hq, a.hk, a.batch);
+    a.splits = query_splits(a.tq, a.tk, a.hq, a.batch, a.group);
     a.tops = static_cast<float2*>(workspace);
     a.partial = static_cast<float*>(workspace) + a.splits * up4(2 * (int64_t)a.tq * a.hq);
-    a.tiles = (int)tile_bound(a.tq, a.batch, kOwn);
-    const dim3 grid((unsigned)(a.tiles * a.hq * a.splits));
+    a.tiles = (int)tile_bound((int64_t)a.tq * a.group, a.batch, kOwn);
+    const dim3 grid((unsigned)(a.tiles * (a.hq / a.group) * a.splits));
     const hipError_t e = a.d <= 64 ? launch(attention_forward_kernel<64>, grid, dim3(kAttThreads), stream, a)
                                    : launch(attention_forward_kernel<128>, grid, dim3(kAttThreads), stream, a);
     if (e != hipSuccess || a.splits == 1) return e;
-    const int64_t units = (int64_t)a.tq * a.hq * a.d / 8;
-    return launch(attention_forward_join_kernel, dim3((unsigned)((units + 255) / 256)), dim3(256), stream, a);
+    return launch(attention_forward_join_kernel, dim3((unsigned)((int64_t)a.tq * a.hq)), dim3(256), stream, a);
 }
 
 hipError_t launch_attention_backward(const AttentionArgs& args, hipStream_t stream)
 {
     AttentionArgs a = args;
     a.chunks = key_chunks(a.tq, a.tk, a.hq, a.hk, a.d, a.batch);
-    a.splits = query_splits(a.tq, a.tk, a.hq, a.batch);
+    a.splits = query_splits(a.tq, a.tk, a.hq, a.batch, 1);
     a.partial = a.stats + up4(2 * (int64_t)a.tq * a.hq);
     auto join = [&](int queries) {
         const int64_t units = (queries ? (int64_t)a.tq * a.hq : (int64_t)a.tk * a.hk) * a.d / 8;

@@ -152,11 +152,12 @@ struct AttentionArgs {
     int64_t q_row, k_row, v_row, out_row, dout_row, dq_row, dk_row, dv_row;
     int64_t q_head, k_head, v_head, out_head, dout_head, dq_head, dk_head, dv_head;
     int tq, tk, hq, hk, d, batch, causal, tiles, chunks, splits;
+    int group;                            // forward: query heads that share a tile
     float scale;
 };
 bool attention_grid_ok(int64_t tokens, int batch, int heads);
 int64_t attention_backward_workspace(int64_t tq, int64_t tk, int hq, int hk, int d, int batch);
-int64_t attention_forward_workspace(int64_t tq, int64_t tk, int hq, int d, int batch);
+int64_t attention_forward_workspace(int64_t tq, int64_t tk, int hq, int hk, int d, int batch);
 hipError_t launch_attention_forward(const AttentionArgs& args, void* workspace, hipStream_t stream);
 hipError_t launch_attention_backward(const AttentionArgs& args, hipStream_t stream);
 

@@ -146,6 +146,19 @@ def test_forward_and_backward(fp8, case):
     check_backward(dout, q, k, v, out, lse, dq, dk, dv, lq, lk, causal, scale)
 
 
+# Few queries: the heads that share a key head share tiles, whose rows then are queries of
+# several heads; with many keys, split over them.
+FEW = [([1] * 70, [37 * i % 130 for i in range(70)], 10, 2, 128, True), ([1, 3, 2], [5000, 0, 4097], 8, 1, 128, True),
+       ([2, 64, 0, 61], [1, 300, 5, 40], 12, 4, 64, True), ([1], [20000], 40, 8, 128, False),
+       ([5, 130, 1], [700, 130, 9], 6, 2, 72, False), ([63, 1, 40], [10, 2000, 41], 14, 2, 40, True),
+       ([1, 1], [1, 0], 200, 1, 8, True)]
+
+
+@pytest.mark.parametrize("case", FEW, ids=lambda c: f"{len(c[0])}x{c[0][0]}-{c[1][0]}-{c[2]}h{c[3]}-d{c[4]}")
+def test_few_queries(fp8, case):
+    test_forward_and_backward(fp8, case)
+
+
 def test_slices_of_one_projection(fp8):
     """q, k, v as slices of one tensor, and the gradients written as slices of one."""
     lens, hq, hk, d = [70, 200], 10, 2, 128
