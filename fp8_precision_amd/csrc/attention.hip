@@ -930,6 +930,7 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AttentionArgs
     if (i < whole / 8 && token >= from && token < upto) {
         const float* p = a.partial + which * whole + row * a.d + c;
         float t[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
         for (int s = 0; s < parts; ++s, p += tensors * whole) {
             const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
             const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};

@@ -657,6 +657,7 @@ loss_add_kernel(const float4* __restrict__ sum, int splits, int64_t n4, const fl
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n4) return;
     float4 t = sum[i];
+#pragma unroll 8
     for (int s = 1; s < splits; ++s) {
         const float4 o = sum[(int64_t)s * n4 + i];
         t = make_float4(t.x + o.x, t.y + o.y, t.z + o.z, t.w + o.w);
