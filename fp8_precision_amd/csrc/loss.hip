@@ -213,7 +213,7 @@ struct LossArgs {
     const int64_t* target;
     const float* lse;
     const float* dloss;
-    const float* unit;                    // the largest |dloss|, which g leaves to its products' epilogues
+    float* unit;                          // the largest |dloss|, found with g and left to its products' epilogues
     float2* stats;                        // [column block][T]: maximum, sum of exponentials
     float* hit;                           // [T]: the target's logit
     int v0, vocab;                        // the piece's first column in the vocabulary, and its size
@@ -401,7 +401,26 @@ __global__ void __launch_bounds__(256, loss_per_cu(MI, NJ)) loss_product_kernel(
             }
         }
     };
-    const float by = EPI == kStats ? 1.0f : *g.unit;
+    // The largest finite |dloss| (1 if there is none above 0).  g's launches find it, every
+    // workgroup for itself (a launch of its own took 2 to 5 us), and leave it in memory.
+    float by = 1.0f;
+    if (EPI == kGrad) {
+        __shared__ uint32_t part[4];
+        uint32_t top = 0;
+#pragma unroll 8
+        for (int i = threadIdx.x; i < g.P; i += 256) {
+            const uint32_t v = __float_as_uint(g.dloss[i]) & 0x7FFFFFFFu;
+            top = max(top, v < 0x7F800000u ? v : 0u);
+        }
+        top = wave_max_u32(top);
+        if (lane == 0) part[wave] = top;
+        __syncthreads();
+        top = max(max(part[0], part[1]), max(part[2], part[3]));
+        if (top != 0) by = __uint_as_float(top);
+        if (blockIdx.x == 0 && threadIdx.x == 0) *g.unit = by;
+    } else if (EPI != kStats) {
+        by = *g.unit;
+    }
     auto keep_rows = [&]() {
         if ((EPI != kStats && EPI != kGrad) || (int)threadIdx.x >= BM) return;
         row_target[threadIdx.x] = my_target;
@@ -666,24 +685,6 @@ loss_add_kernel(const float4* __restrict__ sum, int splits, int64_t n4, const fl
     out[i] = make_uint2(loss_pair(t.x * by, t.y * by), loss_pair(t.z * by, t.w * by));
 }
 
-// The largest finite |dloss|; 1 if there is none above 0.
-__global__ void __launch_bounds__(1024) loss_unit_kernel(const float* __restrict__ dloss, int T, float* __restrict__ unit)
-{
-    __shared__ uint32_t part[16];
-    uint32_t top = 0;
-    for (int i = threadIdx.x; i < T; i += 1024) {
-        const uint32_t v = __float_as_uint(dloss[i]) & 0x7FFFFFFFu;
-        if (v < 0x7F800000u) top = max(top, v);
-    }
-    top = wave_max_u32(top);
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < 16; ++i) top = max(top, part[i]);
-        *unit = top == 0 ? 1.0f : __uint_as_float(top);
-    }
-}
-
 // ---------------------------------------------------------------------- plan and launches
 
 namespace {
@@ -850,8 +851,7 @@ hipError_t launch_loss_backward(const float* dloss, const void* x, const void* w
     float* sum = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.sum);
     float* unit = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.unit);
     float* wsum = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.wsum);
-    hipError_t e = launch(loss_unit_kernel, dim3(1), dim3(1024), stream, dloss, (int)T, unit);
-    if (e != hipSuccess) return e;
+    hipError_t e = hipSuccess;
     const Side xs{static_cast<const uint16_t*>(x), D};
     int splits = sp.splits;
     for (int64_t v0 = 0; v0 < V; v0 += sp.piece) {
