@@ -220,6 +220,16 @@ __device__ __forceinline__ void to_operands(const af32x16& p, Frag (&f)[2])
         for (int e = 0; e < 4; ++e) f[c].w[e] = bf16_pair(p[8 * c + 2 * e], p[8 * c + 2 * e + 1]);
 }
 
+// What their rounding left off, as further operands of the same rows.
+__device__ __forceinline__ void to_residuals(const af32x16& p, const Frag (&f)[2], Frag (&l)[2])
+{
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            l[c].w[e] = bf16_pair(p[8 * c + 2 * e] - bf16_lo(f[c].w[e]), p[8 * c + 2 * e + 1] - bf16_hi(f[c].w[e]));
+}
+
 // A lane's fixed operand: row `row` of a head, chunk c holding elements
 // 16 c + 8 (lane / 32) ..; zero past the head dimension or where !valid.
 template <int DT>
@@ -676,7 +686,7 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dq_kernel(const Atte
         ks.issue(s_begin * kKeys, lds0, wave);
         vs.issue(s_begin * kKeys, lds0 + kTile, wave);
     }
-    auto step = [&](auto stage, int s) {
+    auto step = [&](auto stage, auto fine, int s) {
         constexpr int at = stage.value * 2 * kTile, to = (2 - stage.value * 2) * kTile;
         __builtin_amdgcn_s_waitcnt(0x0F70);
         __syncthreads();
@@ -721,20 +731,31 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dq_kernel(const Atte
                 for (int i = 0; i < 16; ++i)
                     if (32 * kb + 8 * (i / 4) + i % 4 >= see0) dp[i] = 0.0f;
             }
-            Frag f[2];
+            Frag f[2], l[2];
             to_operands(dp, f);
+            if (fine.value) to_residuals(dp, f, l);
 #pragma unroll
             for (int x = kS; x < kB; ++x) {
                 const int t = kb * kB + x, db = (x - kS) % (DT / 32);
                 dq[db] = mma(r[t % kAhead], f[(x - kS) / (DT / 32)], dq[db]);
+                if (fine.value) dq[db] = mma(r[t % kAhead], l[(x - kS) / (DT / 32)], dq[db]);
                 fetch(t + kAhead);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
     };
-    for (int s = s_begin; s < s_end; s += 2) {
-        step(std::integral_constant<int, 0>{}, s);
-        if (s + 1 < s_end) step(std::integral_constant<int, 1>{}, s + 1);
+    // Where few keys are seen, single ds make up the result, and their rounding adds as much
+    // to its error as its own does (2.4e-3 of the gradients' norm instead of 1.7e-3): what
+    // the rounding leaves off is then taken as a further operand.  Over more keys it would
+    // cost a fifth of the kernel's products.
+    if (loaded) {
+        if (s_begin < s_end) step(std::integral_constant<int, 0>{}, std::true_type{}, s_begin);
+        if (s_begin + 1 < s_end) step(std::integral_constant<int, 1>{}, std::true_type{}, s_begin + 1);
+    } else {
+        for (int s = s_begin; s < s_end; s += 2) {
+            step(std::integral_constant<int, 0>{}, std::false_type{}, s);
+            if (s + 1 < s_end) step(std::integral_constant<int, 1>{}, std::false_type{}, s + 1);
+        }
     }
     if (a.splits > 1) {
         const int64_t row = ((int64_t)split * a.tq + pl.q0 + qi) * a.hq + head;
@@ -750,6 +771,8 @@ constexpr int kQueries = 32;              // queries per streamed tile, dk/dv
 constexpr int kRing = 4;                  // stages of them
 constexpr int keys_waves(int dt) { return dt == 128 ? 8 : 4; }
 
+// (The workgroups of sequences of at most 128 keys take, like dq's, what the rounding of p and
+// ds leaves off; the loop for it is compiled apart, as the main one has no register to spare.)
 // dk, dv: 32 keys per wave; the queries of every head that shares the key head are
 // streamed, with their dout, lse and delta, three tiles ahead.  A wave's keys stay in
 // registers; its values are read from a fixed tile in LDS (keeping them in registers too
@@ -761,7 +784,7 @@ constexpr int keys_waves(int dt) { return dt == 128 ? 8 : 4; }
 // chunks > 1: the steps are dealt over that many workgroups, each of which leaves fp32
 // partial sums [chunk][dk, dv][token][head][d].
 template <int DT>
-__global__ void __launch_bounds__(64 * keys_waves(DT), 2) attention_dkv_kernel(const AttentionArgs a)
+__global__ void __launch_bounds__(64 * keys_waves(DT), DT == 64 ? 3 : 2) attention_dkv_kernel(const AttentionArgs a)
 {
     constexpr int WAVES = keys_waves(DT), kMine = 32 * WAVES;
     constexpr int kTile = kQueries * DT * 2, kOwnTile = kMine * DT * 2, kStat = 512;
@@ -782,7 +805,7 @@ __global__ void __launch_bounds__(64 * keys_waves(DT), 2) attention_dkv_kernel(c
     const bool mine = ki < pl.nk;
     const int shift = pl.nk - pl.nq;
     // the first query that sees this lane's key, the wave's first key, its last, the workgroup's first
-    const int from = a.causal ? max(0, ki - shift) : 0;
+    const int lane_from = (a.causal ? max(0, ki - shift) : 0) - 4 * h;   // (4 h: its first row of a block)
     const int from_first = a.causal ? max(0, k_wave - shift) : 0;
     const int from_last = a.causal ? max(0, k_wave + 31 - shift) : 0;
     const int begin = a.causal ? max(0, pl.first - shift) / kQueries : 0;
@@ -826,7 +849,7 @@ __global__ void __launch_bounds__(64 * keys_waves(DT), 2) attention_dkv_kernel(c
         buffer4_to_lds(stat_off, desc, __builtin_amdgcn_readfirstlane(stat0 + (uint32_t)(stage * kStat + (wave & 1) * 256)));
     };
 
-    auto step = [&](auto stage, int s) __attribute__((always_inline)) {
+    auto step = [&](auto stage, auto fine, int s) __attribute__((always_inline)) {
         constexpr int at = stage.value * 2 * kTile;
         __builtin_amdgcn_s_waitcnt(wait_loads((kRing - 2) * kLoads));     // this wave's loads of step s
         __syncthreads();                                   // everyone's; step s - 1 is read
@@ -856,7 +879,8 @@ __global__ void __launch_bounds__(64 * keys_waves(DT), 2) attention_dkv_kernel(c
             fetch(t + kAhead);
             __builtin_amdgcn_sched_barrier(0);
         }
-        const bool masked = i0 < from_last || k_wave + 32 > pl.nk;
+        // (keys past the sequence's end are columns of their own, which are not stored)
+        const bool masked = i0 < from_last;
         const lds_f32x4* stat = (const lds_f32x4*)(uintptr_t)(stat0 + stage.value * kStat + 16 * h);
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
@@ -869,19 +893,27 @@ __global__ void __launch_bounds__(64 * keys_waves(DT), 2) attention_dkv_kernel(c
             }
         }
         if (masked) {
-            const int from0 = mine ? from - i0 - 4 * h : kQueries;
+            const int from0 = lane_from - i0;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 if (8 * (i / 4) + i % 4 < from0) p[i] = dp[i] = 0.0f;
         }
-        Frag f[2], e[2];
+        Frag f[2], e[2], fl[2], el[2];
         to_operands(p, f);
         to_operands(dp, e);
+        if (fine.value) {
+            to_residuals(p, f, fl);
+            to_residuals(dp, e, el);
+        }
 #pragma unroll
         for (int t = kS; t < kAll; ++t) {
             const int x = t - kS, ch = x / 2 / (DT / 32), db = x / 2 % (DT / 32);
             if (x % 2 == 0) dv[db] = mma(r[t % kAhead], f[ch], dv[db]);
             else dk[db] = mma(r[t % kAhead], e[ch], dk[db]);
+            if (fine.value) {
+                if (x % 2 == 0) dv[db] = mma(r[t % kAhead], fl[ch], dv[db]);
+                else dk[db] = mma(r[t % kAhead], el[ch], dk[db]);
+            }
             fetch(t + kAhead);
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -892,12 +924,17 @@ __global__ void __launch_bounds__(64 * keys_waves(DT), 2) attention_dkv_kernel(c
         vs.issue(pl.first, lds0 + kRing * 2 * kTile, wave);
 #pragma unroll
         for (int i = 0; i < kRing - 1; ++i) issue(s_begin + i, i);
-        for (int s = s_begin; s < s_end; s += kRing) {
-            step(std::integral_constant<int, 0>{}, s);
-            if (s + 1 < s_end) step(std::integral_constant<int, 1>{}, s + 1);
-            if (s + 2 < s_end) step(std::integral_constant<int, 2>{}, s + 2);
-            if (s + 3 < s_end) step(std::integral_constant<int, 3>{}, s + 3);
-        }
+        auto walk = [&](auto fine) __attribute__((always_inline)) {
+            for (int s = s_begin; s < s_end; s += kRing) {
+                step(std::integral_constant<int, 0>{}, fine, s);
+                if (s + 1 < s_end) step(std::integral_constant<int, 1>{}, fine, s + 1);
+                if (s + 2 < s_end) step(std::integral_constant<int, 2>{}, fine, s + 2);
+                if (s + 3 < s_end) step(std::integral_constant<int, 3>{}, fine, s + 3);
+            }
+        };
+        // as for dq: with few keys, what the rounding of p and ds leaves off is taken too
+        if (pl.nk <= 2 * kKeys) walk(std::true_type{});
+        else walk(std::false_type{});
         __builtin_amdgcn_s_waitcnt(wait_loads(0));         // no load outlives the workgroup's LDS
     }
     if (a.chunks > 1) {

@@ -602,7 +602,8 @@ fp8_status fp8_attention_forward(const fp8_attention_shape* shape, const fp8_hea
  *   dv_j = sum_i p_ij dout_i,  dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i
  *
  * (delta is taken as dout_i . out_i, the same sum, where a tile of queries sees more
- * than 128 keys).
+ * than 128 keys).  p and ds are rounded to bf16 for these products; with at most 128 keys
+ * (of the tile of queries for dq, of the sequence for dk and dv) to twice its precision.
  *
  *   dout    as q;  out, lse  from the forward;  dq, dk, dv  as q, k, v
  *   absmax  fp32 scalar or NULL: becomes max(*absmax, max |dq|, max |dk|, max |dv|), as stored

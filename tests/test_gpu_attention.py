@@ -159,6 +159,31 @@ def test_few_queries(fp8, case):
     test_forward_and_backward(fp8, case)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hk,d", [(4, 4, 128), (10, 2, 64), (6, 1, 40)])
+def test_gradients_of_short_sequences_carry_their_own_rounding_alone(fp8, hq, hk, d, causal):
+    """At most 128 keys: the error's norm is that of one rounding, at most 2^-8 / sqrt 3 of the
+    gradient's (uniform in the last place, at the shortest mantissa), and 2^-14 for the rest."""
+    lens = [128, 37, 5, 1, 64, 100]
+    q, k, v, dout = make(lens, lens, hq, hk, d, 11)
+    cu = bounds(lens)
+    out, lse = fp8.attention(q, k, v, cu, cu, causal=causal)
+    got = fp8.attention_backward(dout, q, k, v, out, lse, cu, cu, causal=causal)
+    want = [torch.zeros(t.shape, dtype=F64, device="cuda") for t in (q, k, v)]
+    scale = d ** -0.5
+    for qs, ks, h in pieces(lens, lens, hq):
+        a, b, c, g = (t.to(F64) for t in (q[qs, h], k[ks, h * hk // hq], v[ks, h * hk // hq], dout[qs, h]))
+        s = (a @ b.t() * scale).masked_fill(~visible(len(a), len(b), causal), -float("inf"))
+        p = torch.softmax(s, 1)
+        dp = g @ c.t()
+        ds = p * (dp - (p * dp).sum(1, keepdim=True)) * scale
+        want[0][qs, h] = ds @ b
+        want[1][ks, h * hk // hq] += ds.t() @ a
+        want[2][ks, h * hk // hq] += p.t() @ g
+    for x, y in zip(got, want):
+        assert float((x.to(F64) - y).norm() / y.norm()) <= 2.0 ** -8 / 3 ** 0.5 + 2.0 ** -14
+
+
 def test_slices_of_one_projection(fp8):
     """q, k, v as slices of one tensor, and the gradients written as slices of one."""
     lens, hq, hk, d = [70, 200], 10, 2, 128
