@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "fp8_internal.hpp"
+#include "head_tensor.hpp"
 
 namespace {
 
@@ -677,16 +678,9 @@ fp8_status fp8_norm_backward(const void* dy, const void* s, fp8_stream_type type
 }
 
 // A tensor of an attention call: its strides checked, and the bytes it spans.
-struct Heads {
+struct Heads : fp8k::HeadLayout {
     uint16_t* p = nullptr;
-    int64_t tokens = 0, heads = 0, d = 0, row = 0, head = 0;
-    int64_t row_span() const { return (heads - 1) * head + d; }       // elements of one token's heads
-    Range range() const { return {p, 2 * ((tokens - 1) * row + row_span())}; }
-    // each element has a place of its own
-    bool distinct() const
-    {
-        return (head >= d || heads == 1) && row >= row_span() ? true : row >= d && head >= (tokens - 1) * row + d;
-    }
+    Range range() const { return {p, 2 * span()}; }
 };
 
 static fp8_status take_heads(const char* call, const char* name, const fp8_head_tensor* t, int64_t tokens,
@@ -704,9 +698,9 @@ static fp8_status take_heads(const char* call, const char* name, const fp8_head_
     h.d = d;
     h.head = heads == 1 ? 0 : t->head_stride;                          // a single head's or token's stride moves nothing
     if (h.head < 0 || h.head > ((int64_t)1 << 40)) return no(FP8_ERR_INVALID, "has a bad head stride");
-    h.row = tokens == 1 ? (h.row_span() + 7) / 8 * 8 : t->token_stride;
-    if (tokens > 1 && h.row < d) return no(FP8_ERR_INVALID, "has tokens closer than head_dim");
-    if (tokens > 1 && h.row >= ((int64_t)1 << 22)) return no(FP8_ERR_UNSUPPORTED, "has a token stride of 2^22 or more");
+    h.row = fp8k::kernel_row(tokens, d, t->token_stride);
+    if (h.row < d) return no(FP8_ERR_INVALID, "has tokens closer than head_dim");
+    if (h.row >= fp8k::kMaxRow) return no(FP8_ERR_UNSUPPORTED, "has a token stride of 2^22 or more");
     if (h.row % 8 || h.head % 8) return no(FP8_ERR_UNSUPPORTED, "has strides that are not multiples of 8");
     if (!aligned(t->data, 16)) return no(FP8_ERR_UNSUPPORTED, "is not 16-byte aligned");
     if (written && !h.distinct()) return no(FP8_ERR_INVALID, "overlaps itself");

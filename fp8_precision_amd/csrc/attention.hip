@@ -40,6 +40,7 @@
 
 #include "fp8_device.hpp"
 #include "fp8_internal.hpp"
+#include "head_tensor.hpp"
 
 namespace fp8k {
 
@@ -118,10 +119,9 @@ __device__ __forceinline__ void buffer4_to_lds(uint32_t voff, const au32x4& desc
 // s_waitcnt immediate: at most n vector memory operations in flight.
 constexpr int wait_loads(int n) { return 0x0F70 | (n & 15) | (n >> 4) << 14; }
 
-__device__ __forceinline__ au32x4 descriptor(const uint8_t* base, int64_t bytes)
+__device__ __forceinline__ au32x4 descriptor(const uint8_t* base, int64_t n)
 {
     const uint64_t b = (uint64_t)base;
-    const int64_t n = bytes < 0 ? 0 : bytes > 0x7FFFFFFF ? 0x7FFFFFFF : bytes;
     au32x4 d;
     d[0] = __builtin_amdgcn_readfirstlane((uint32_t)b);
     d[1] = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32) & 0xFFFFu);
@@ -153,14 +153,14 @@ struct Stream {
         for (int i = 0; i < kLoads; ++i) {
             const int r = (wave * kLoads + i) * kPer + lane / kCh;
             const int c = (lane % kCh) ^ spread<kCh>(r);
-            voff[i] = c * 8 < d ? (uint32_t)(r * stride) + (uint32_t)c * 16u : 0x80000000u;
+            voff[i] = stream_offset(r, c, stride, d);
         }
     }
 
     // rows row0 .. row0 + ROWS - 1 into the ROWS * kRow bytes at LDS address lds
     __device__ __forceinline__ void issue(int row0, uint32_t lds, int wave) const
     {
-        const au32x4 desc = descriptor(base + (int64_t)row0 * stride, (int64_t)(n - row0) * stride);
+        const au32x4 desc = descriptor(base + (int64_t)row0 * stride, stream_bytes(n - row0, stride));
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
             buffer_to_lds(voff[i], desc, __builtin_amdgcn_readfirstlane(lds + (uint32_t)((wave * kLoads + i) * 1024)));
@@ -824,7 +824,7 @@ __global__ void __launch_bounds__(64 * keys_waves(DT), DT == 64 ? 3 : 2) attenti
     gs.init(a.dout + (int64_t)pl.q0 * a.dout_row, a.dout_row, pl.nq, a.d);
     const uint8_t* q_base = qs.base;
     const uint8_t* g_base = gs.base;
-    const uint32_t stat_off = lane < 32 ? lane * 4u : 0x80000000u;
+    const uint32_t stat_off = lane < 32 ? lane * 4u : kPastBuffer;
     // even waves bring the tile's lse, odd ones its delta (the same bytes each)
     const float* stat_base = a.stats + (wave & 1 ? (int64_t)a.tq * a.hq : 0) + pl.q0;
 
@@ -845,7 +845,7 @@ __global__ void __launch_bounds__(64 * keys_waves(DT), DT == 64 ? 3 : 2) attenti
         qs.issue(row0, to, wave);
         gs.issue(row0, to + kTile, wave);
         const au32x4 desc = descriptor(reinterpret_cast<const uint8_t*>(stat_base + (int64_t)head * a.tq + row0),
-                                       (int64_t)(pl.nq - row0) * 4);
+                                       stream_bytes(pl.nq - row0, 4));
         buffer4_to_lds(stat_off, desc, __builtin_amdgcn_readfirstlane(stat0 + (uint32_t)(stage * kStat + (wave & 1) * 256)));
     };
 

@@ -561,8 +561,8 @@ fp8_status fp8_norm_backward(const void* dy, const void* s, fp8_stream_type type
  */
 typedef struct fp8_head_tensor {
     void* data;            /* 16-byte aligned */
-    int64_t token_stride;  /* elements, a multiple of 8, >= head_dim, < 2^22 */
-    int64_t head_stride;   /* elements, a multiple of 8, >= 0 */
+    int64_t token_stride;  /* elements, a multiple of 8, >= head_dim, < 2^22; one token: any */
+    int64_t head_stride;   /* elements, a multiple of 8, 0 .. 2^40; one head: any */
 } fp8_head_tensor;
 
 typedef struct fp8_attention_shape {
