@@ -707,17 +707,10 @@ static fp8_status take_heads(const char* call, const char* name, const fp8_head_
     return FP8_OK;
 }
 
-// Two tensors share an element.  Slices of one tensor (the same token stride, each token's
-// heads inside it) interleave without sharing any.
 static bool heads_overlap(const Heads& a, const Heads& b)
 {
-    const Range ra = a.range(), rb = b.range();
-    if (!overlap(ra.p, ra.n, rb.p, rb.n)) return false;
-    if (a.row != b.row || a.row_span() > a.row || b.row_span() > b.row) return true;
-    const int64_t r = 2 * a.row;
-    int64_t off = ((int64_t)(reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p))) % r;
-    if (off < 0) off += r;
-    return off < 2 * a.row_span() || off + 2 * b.row_span() > r;
+    const intptr_t off = reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p);
+    return fp8k::share_element(a, b, off / 2);             // both are 16-byte aligned
 }
 
 static bool heads_overlap(const Heads& a, const void* p, int64_t n)

@@ -18,6 +18,31 @@ struct HeadLayout {
     }
 };
 
+// Two tensors of one head dimension share an element, b's first lying `off` elements after
+// a's.  Exact where both strides agree (slices of one tensor, in whatever order its axes
+// lie); with other strides between heads a token's heads count as one block, and with
+// other strides between tokens the whole tensor does.
+inline bool share_element(const HeadLayout& a, const HeadLayout& b, int64_t off)
+{
+    if (off >= a.span() || -off >= b.span()) return false;
+    // the stride of a single token or head leads nowhere: it is whatever the other's is
+    const int64_t row = a.tokens > 1 ? a.row : b.row, head = a.heads > 1 ? a.head : b.head;
+    if (a.tokens > 1 && b.tokens > 1 && a.row != b.row) return true;
+    if (a.heads > 1 && b.heads > 1 && a.head != b.head) {
+        if (a.row_span() > row || b.row_span() > row) return true;
+        const int64_t m = (off % row + row) % row;
+        return m < a.row_span() || m + b.row_span() > row;
+    }
+    // a head of b, y heads and x tokens after one of a's: x the least that is not too far before it
+    for (int64_t y = 1 - a.heads; y < b.heads; ++y) {
+        const int64_t at = off + y * head, need = 1 - b.d - at;        // x row >= need
+        int64_t x = need > 0 ? (need + row - 1) / row : -(-need / row);
+        if (x < 1 - a.tokens) x = 1 - a.tokens;
+        if (x < b.tokens && at + x * row < a.d) return true;
+    }
+    return false;
+}
+
 // The stride between tokens that the kernels are given.  A single token's own may be
 // anything (its heads may lie gigabytes apart) and leads nowhere; a tile's rows past the
 // only one need no more than to lie past the buffer's end.  Of several tokens it is below

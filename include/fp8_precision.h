@@ -609,8 +609,9 @@ fp8_status fp8_attention_forward(const fp8_attention_shape* shape, const fp8_hea
  *   absmax  fp32 scalar or NULL: becomes max(*absmax, max |dq|, max |dk|, max |dv|), as stored
  *   workspace, workspace_bytes   device memory, 16-byte aligned, of at least the size
  *           that fp8_attention_backward_workspace gives for the shape
- * No output may overlap an input or another output (outputs may interleave: slices
- * of one tensor with one token stride).
+ * No output may share an element with an input or another output.  They may interleave
+ * with them: slices of one tensor that have its token and head strides, such as those of
+ * [tokens, heads, 3, head_dim], or whose heads lie within a token in blocks apart.
  */
 fp8_status fp8_attention_backward_workspace(const fp8_attention_shape* shape, int64_t* bytes);
 fp8_status fp8_attention_backward(const fp8_attention_shape* shape, const fp8_head_tensor* dout,
