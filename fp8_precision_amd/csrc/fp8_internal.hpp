@@ -27,6 +27,9 @@ inline hipError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, hipStream_
     return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, ptrs, 0, stream);
 }
 
+// Most workgroups of so many threads that one launch takes: its threads are counted in 32 bits.
+constexpr int64_t max_workgroups(int threads) { return 0xFFFFFFFFll / threads; }
+
 // Number of compute units of the current device (cached per device).
 int device_cu_count();
 

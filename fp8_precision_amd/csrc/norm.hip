@@ -559,13 +559,22 @@ hipError_t launch_norm_forward(const void* x, bool f32, const void* add, const v
                                float* rstd, float* absmax, hipStream_t stream)
 {
     const NormLayout l = norm_layout(cols);
-    return norm_variant(f32, cols % 8 == 0, l, rms, [&](auto f, auto v, auto n, auto lanes, auto ms) {
-        return launch(norm_forward_kernel<f.value, v.value, n.value, lanes.value, ms.value>,
-                      dim3((unsigned)((rows + l.rows - 1) / l.rows)), dim3(l.threads), stream, x,
-                      static_cast<const uint16_t*>(add), static_cast<const uint16_t*>(weight),
-                      static_cast<const uint16_t*>(bias), eps, (uint32_t)rows, (int)cols,
-                      static_cast<uint16_t*>(y), sum, mean, rstd, reinterpret_cast<uint32_t*>(absmax));
-    });
+    const int64_t most = max_workgroups(l.threads) * l.rows, size = f32 ? 4 : 2;   // rows of one launch; bytes
+    auto after = [](auto* p, int64_t n) { return p ? p + n : p; };
+    for (int64_t from = 0; from < rows; from += most) {
+        const int64_t part = std::min(most, rows - from), at = from * cols;
+        const hipError_t e = norm_variant(f32, cols % 8 == 0, l, rms, [&](auto f, auto v, auto n, auto lanes, auto ms) {
+            return launch(norm_forward_kernel<f.value, v.value, n.value, lanes.value, ms.value>,
+                          dim3((unsigned)((part + l.rows - 1) / l.rows)), dim3(l.threads), stream,
+                          static_cast<const void*>(static_cast<const uint8_t*>(x) + at * size),
+                          after(static_cast<const uint16_t*>(add), at), static_cast<const uint16_t*>(weight),
+                          static_cast<const uint16_t*>(bias), eps, (uint32_t)part, (int)cols,
+                          static_cast<uint16_t*>(y) + at, static_cast<void*>(after(static_cast<uint8_t*>(sum), at * size)),
+                          after(mean, from), rstd + from, reinterpret_cast<uint32_t*>(absmax));
+        });
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_norm_backward(const void* dy, const void* x, bool f32, const void* weight, const float* mean,
