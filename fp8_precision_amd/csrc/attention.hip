@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_forward_kernel(const
     int t, unit;
     deal(blockIdx.x, a.hq / a.group * a.splits, t, unit);
     const int split = unit % a.splits, head0 = unit / a.splits * a.group;
-    const Place pl = find_tile(a, a.tiles - 1 - t, 0, kOwn, a.group);   // a sequence's last (longest) tiles first
+    const Place pl = find_tile(a, a.tiles - 1 - a.tile0 - t, 0, kOwn, a.group);   // a sequence's last (longest) tiles first
     if (!pl.any) return;
     const int lane = threadIdx.x & 63, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_dq_kernel(const Atte
     int t, unit;
     deal(blockIdx.x, a.hq * a.splits, t, unit);
     const int head = unit / a.splits, split = unit % a.splits;
-    const Place pl = find_tile(a, a.tiles - 1 - t, 0);
+    const Place pl = find_tile(a, a.tiles - 1 - a.tile0 - t, 0);
     if (!pl.any) return;
     const int lane = threadIdx.x & 63, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -794,7 +794,7 @@ __global__ void __launch_bounds__(64 * keys_waves(DT), DT == 64 ? 3 : 2) attenti
     int t, unit;
     deal(blockIdx.x, a.hk * a.chunks, t, unit);
     const int khead = unit / a.chunks, chunk = unit % a.chunks;
-    const Place pl = find_tile(a, t, 1, kMine);            // a sequence's first keys are seen by most
+    const Place pl = find_tile(a, a.tile0 + t, 1, kMine);            // a sequence's first keys are seen by most
     if (!pl.any) return;
     const int lane = threadIdx.x & 63, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -1054,6 +1054,18 @@ int64_t attention_backward_workspace(int64_t tq, int64_t tk, int hq, int hk, int
     return 4 * (up4(2 * tq * hq) + std::max(chunks > 1 ? 2 * chunks * tk * hk * d : 0, splits > 1 ? splits * tq * hq * d : 0));
 }
 
+// `units` workgroups of each of the a.tiles tiles, in as many launches as their threads take.
+static hipError_t launch_tiles(void (*kernel)(AttentionArgs), AttentionArgs a, int64_t units, int threads, hipStream_t stream)
+{
+    const int64_t most = max_workgroups(threads) / units;
+    for (int64_t first = 0; first < a.tiles; first += most) {
+        a.tile0 = (int)first;
+        const hipError_t e = launch(kernel, dim3((unsigned)(std::min(most, a.tiles - first) * units)), dim3(threads), stream, a);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 hipError_t launch_attention_forward(const AttentionArgs& args, void* workspace, hipStream_t stream)
 {
     AttentionArgs a = args;
@@ -1062,9 +1074,8 @@ hipError_t launch_attention_forward(const AttentionArgs& args, void* workspace, 
     a.tops = static_cast<float2*>(workspace);
     a.partial = static_cast<float*>(workspace) + a.splits * up4(2 * (int64_t)a.tq * a.hq);
     a.tiles = (int)tile_bound((int64_t)a.tq * a.group, a.batch, kOwn);
-    const dim3 grid((unsigned)(a.tiles * (a.hq / a.group) * a.splits));
-    const hipError_t e = a.d <= 64 ? launch(attention_forward_kernel<64>, grid, dim3(kAttThreads), stream, a)
-                                   : launch(attention_forward_kernel<128>, grid, dim3(kAttThreads), stream, a);
+    const hipError_t e = launch_tiles(a.d <= 64 ? attention_forward_kernel<64> : attention_forward_kernel<128>, a,
+                                      (int64_t)(a.hq / a.group) * a.splits, kAttThreads, stream);
     if (e != hipSuccess || a.splits == 1) return e;
     return launch(attention_forward_join_kernel, dim3((unsigned)((int64_t)a.tq * a.hq)), dim3(256), stream, a);
 }
@@ -1081,15 +1092,13 @@ hipError_t launch_attention_backward(const AttentionArgs& args, hipStream_t stre
                       a, queries);
     };
     a.tiles = (int)tile_bound(a.tq, a.batch, kOwn);
-    const dim3 grid_q((unsigned)(a.tiles * a.hq * a.splits));
-    hipError_t e = a.d <= 64 ? launch(attention_dq_kernel<64>, grid_q, dim3(kAttThreads), stream, a)
-                             : launch(attention_dq_kernel<128>, grid_q, dim3(kAttThreads), stream, a);
+    hipError_t e = launch_tiles(a.d <= 64 ? attention_dq_kernel<64> : attention_dq_kernel<128>, a, (int64_t)a.hq * a.splits,
+                                kAttThreads, stream);
     if (e == hipSuccess && a.splits > 1) e = join(1);
     if (e != hipSuccess) return e;
     a.tiles = (int)tile_bound(a.tk, a.batch, key_rows(a.d));
-    const dim3 grid_k((unsigned)(a.tiles * a.hk * a.chunks));
-    e = a.d <= 64 ? launch(attention_dkv_kernel<64>, grid_k, dim3(64 * keys_waves(64)), stream, a)
-                  : launch(attention_dkv_kernel<128>, grid_k, dim3(64 * keys_waves(128)), stream, a);
+    e = a.d <= 64 ? launch_tiles(attention_dkv_kernel<64>, a, (int64_t)a.hk * a.chunks, 64 * keys_waves(64), stream)
+                  : launch_tiles(attention_dkv_kernel<128>, a, (int64_t)a.hk * a.chunks, 64 * keys_waves(128), stream);
     if (e != hipSuccess || a.chunks == 1) return e;
     return join(0);
 }

@@ -156,6 +156,7 @@ struct AttentionArgs {
     int64_t q_head, k_head, v_head, out_head, dout_head, dq_head, dk_head, dv_head;
     int tq, tk, hq, hk, d, batch, causal, tiles, chunks, splits;
     int group;                            // forward: query heads that share a tile
+    int tile0;                            // the launch's first tile
     float scale;
 };
 bool attention_grid_ok(int64_t tokens, int batch, int heads);

@@ -567,9 +567,10 @@ typedef struct fp8_head_tensor {
 
 typedef struct fp8_attention_shape {
     int64_t tokens_q, tokens_k;         /* packed tokens, 1 .. 2^31 - 1 */
-    int64_t heads_q, heads_k;           /* heads_q a multiple of heads_k */
+    int64_t heads_q, heads_k;           /* heads_q a multiple of heads_k, at most 2^16; of either side
+                                           (tokens / 128 + batch) heads below 2^28 */
     int64_t head_dim;                   /* a multiple of 8, 8 .. 128 */
-    int64_t batch;                      /* sequences; 1 without the bounds below */
+    int64_t batch;                      /* sequences, at most 2^24; 1 without the bounds below */
     const int32_t *bounds_q, *bounds_k; /* device int32 [batch + 1]: sequence b is tokens
                                            bounds[b] .. bounds[b + 1] - 1 (from 0, ascending, ending
                                            at the token count; equal neighbours: an empty sequence);
