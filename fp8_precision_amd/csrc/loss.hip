@@ -5,7 +5,9 @@
 //   lse_t = log sum_v exp(z_tv),   loss_t = lse_t - z_t,target(t)
 // and backward, g_tv = dloss_t (exp(z_tv - lse_t) - [v = target(t)]),
 //   dx = g w,   dw = g^T x.
-// A token whose target lies outside [0, V) has no target: loss 0 and no gradient.
+// A token whose target lies outside [0, V) has no target: loss 0 and no gradient, whatever its
+// x: g's launch leaves a bit per token, by which dw's loads pass over its row (4096 tokens,
+// 32000 x 4096, all three products: 2254 us without, 2273 so).
 //
 // Forward: the logits' product with the row statistics taken in its epilogue -- the
 // maximum and the sum of exponentials of the wave's columns of each row -- and a
@@ -133,6 +135,17 @@ struct Feed {
         }
     }
 
+    // Load ii's offset, past the buffer where the reduction row's bit is not in `live` (of
+    // the step's 64 rows): the row then reads as zero.  `dead` is dead_rows(live).
+    __device__ __forceinline__ static uint32_t dead_rows(uint64_t live, int wave, int lane)
+    {
+        return (uint32_t)(~live >> (wave * 16)) >> (lane / (EXT / 8));
+    }
+    __device__ __forceinline__ uint32_t offset(int ii, uint32_t dead) const
+    {
+        return voff[ii] | (dead << (31 - ii * (512 / EXT)) & (uint32_t)kOutside);
+    }
+
     // From here on every load is of the reduction's last step, which has in_step < kStep
     // elements: lanes past them read zero.
     __device__ __forceinline__ void trim(int in_step)
@@ -199,6 +212,9 @@ __device__ __forceinline__ void lds_barrier()
     asm volatile("" ::: "memory");
 }
 
+// Memory that nothing writes while the kernel runs, read through the scalar cache.
+typedef const __attribute__((address_space(4))) uint64_t* ScalarWords;
+
 // What a launch's epilogue does with the tile's sums.
 enum { kStats = 0, kGrad = 1, kSum = 2, kStore = 3 };
 
@@ -216,6 +232,7 @@ struct LossArgs {
     float* unit;                          // the largest |dloss|, found with g and left to its products' epilogues
     float2* stats;                        // [column block][T]: maximum, sum of exponentials
     float* hit;                           // [T]: the target's logit
+    uint64_t* live;                       // a bit per token: it has a target (found with g, for dw)
     int v0, vocab;                        // the piece's first column in the vocabulary, and its size
     // outputs
     uint16_t* out;                        // bf16, pitch out_pitch: g, dw, or dx once complete
@@ -257,6 +274,9 @@ __global__ void __launch_bounds__(256, loss_per_cu(MI, NJ)) loss_product_kernel(
     // tokens, 32000 x 4096, the weight in memory: 64 us with one beginning, 51 so; 128
     // tokens, 50000 x 2048: 57.6 and 46.5; with tiles of 256 rows it loses, 87 and 94).
     constexpr bool kTurn = BM <= 128 && !LA && !LB;
+    // dw: the reduction runs over the tokens.  g is 0 for those without a target, but their x
+    // may be anything, and 0 times an infinity is not 0: their rows of x are not read.
+    constexpr bool kLive = LA;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * kStage + 4 * kEpi];
     // the tile's rows: target (-1: none), dloss, lse in powers of two
     __shared__ int row_target[BM];
@@ -310,6 +330,9 @@ __global__ void __launch_bounds__(256, loss_per_cu(MI, NJ)) loss_product_kernel(
             fb.trim(in_step);
         }
     };
+    auto live_rows = [&](const Unit& w, int kt) -> uint64_t {
+        return ((ScalarWords)(uintptr_t)g.live)[__builtin_amdgcn_readfirstlane(w.r0 / kStep + kt)];
+    };
     auto start = [&](const Unit& w) {
         int ln = lane;
         asm volatile("" : "+v"(ln));      // what follows from the lane is computed per tile, not held across them
@@ -320,13 +343,14 @@ __global__ void __launch_bounds__(256, loss_per_cu(MI, NJ)) loss_product_kernel(
             const int kt = min(s, w.kt - 1);
             trim(w, kt);
             const lu32x4 da = fa.desc(turned(w, kt)), db = fb.desc(turned(w, kt));
+            const uint32_t dead = kLive ? fb.dead_rows(live_rows(w, kt), wave, ln) : 0;
 #pragma unroll
             for (int x = 0; x < BM / 32; ++x)
                 loss_to_lds(fa.voff[x], da,
                             __builtin_amdgcn_readfirstlane(lds0 + s * kStage + (wave * (BM / 32) + x) * 1024));
 #pragma unroll
             for (int x = 0; x < BN / 32; ++x)
-                loss_to_lds(fb.voff[x], db,
+                loss_to_lds(kLive ? fb.offset(x, dead) : fb.voff[x], db,
                             __builtin_amdgcn_readfirstlane(lds0 + s * kStage + kA + (wave * (BN / 32) + x) * 1024));
         }
     };
@@ -341,13 +365,18 @@ __global__ void __launch_bounds__(256, loss_per_cu(MI, NJ)) loss_product_kernel(
     // The first half of a step: A blocks 0 .. kHalf - 1, while the others are read.  B was
     // read in the half before; once every wave has it (slot kFree), B of the step NS ahead is
     // loaded into its place.
-    auto half0 = [&](uint32_t cur, const lu32x4& db) {
+    // Their rows' word was read in the half0 before, after a wait for LDS reads and ahead of
+    // the next: a scalar load in flight makes every wait for an LDS read one for all.
+    uint64_t live = 0;
+    auto half0 = [&](uint32_t cur, const lu32x4& db, const Unit& w, int next) {
+        const uint32_t dead = kLive ? fb.dead_rows(live, wave, lane) : 0;
 #pragma unroll
         for (int t = 0; t < kSlots; ++t) {
             const int j = t / (2 * kHalf), k = t % 2, i = t / 2 % kHalf;
             if (t == kFree) {
                 __builtin_amdgcn_s_waitcnt(0xC07F);          // this wave's reads
                 lds_barrier();
+                if (kLive) live = live_rows(w, next);
             }
             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bq[j][k].b, alo[i][k].b, acc[i][j], 0, 0, 0);
 #pragma unroll
@@ -356,7 +385,7 @@ __global__ void __launch_bounds__(256, loss_per_cu(MI, NJ)) loss_product_kernel(
 #pragma unroll
             for (int x = 0; x < kLoadsB; ++x)
                 if (t == kFree + x * (kSlots - kFree) / kLoadsB)
-                    loss_to_lds(fb.voff[x], db,
+                    loss_to_lds(kLive ? fb.offset(x, dead) : fb.voff[x], db,
                                 __builtin_amdgcn_readfirstlane(lds0 + cur + kA + (wave * kLoadsB + x) * 1024));
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -421,8 +450,12 @@ __global__ void __launch_bounds__(256, loss_per_cu(MI, NJ)) loss_product_kernel(
     } else if (EPI != kStats) {
         by = *g.unit;
     }
-    auto keep_rows = [&]() {
+    auto keep_rows = [&](const Unit& w) {
         if ((EPI != kStats && EPI != kGrad) || (int)threadIdx.x >= BM) return;
+        if (EPI == kGrad && w.n0 == 0 && w.m0 + wave * 64 < g.P) {
+            const uint64_t has = __ballot(my_target >= 0);
+            if (lane == 0) g.live[w.m0 / 64 + wave] = has;
+        }
         row_target[threadIdx.x] = my_target;
         if (EPI == kGrad) {
             row_scale[threadIdx.x] = my_target < 0 ? 0.0f : my_scale / by;
@@ -455,7 +488,8 @@ __global__ void __launch_bounds__(256, loss_per_cu(MI, NJ)) loss_product_kernel(
         // that the count of loads in flight stays the same)
         int ahead = min(NS, w.kt - 1);
         trim(w, ahead);
-        half0(cur, fb.desc(turned(w, ahead)));
+        if (kLive) live = live_rows(w, ahead);
+        half0(cur, fb.desc(turned(w, ahead)), w, min(NS + 1, w.kt - 1));
         for (int kt = 0; kt + 1 < w.kt; ++kt) {
             const uint32_t nxt = cur + kStage == NS * kStage ? 0 : cur + kStage;
             // the next step's loads of this wave (later: whole steps and one B), and its reads
@@ -464,14 +498,14 @@ __global__ void __launch_bounds__(256, loss_per_cu(MI, NJ)) loss_product_kernel(
             half1(true, cur, nxt, fa.desc(turned(w, ahead)));
             ahead = min(kt + 1 + NS, w.kt - 1);
             trim(w, ahead);
-            half0(nxt, fb.desc(turned(w, ahead)));
+            half0(nxt, fb.desc(turned(w, ahead)), w, min(kt + 2 + NS, w.kt - 1));
             cur = nxt;
         }
         __builtin_amdgcn_s_waitcnt(wait_loads(0));
         __syncthreads();
         __builtin_amdgcn_sched_barrier(0);
         half1(false, 0, 0, lu32x4{0, 0, 0, 0});
-        keep_rows();
+        keep_rows(w);
         __syncthreads();
 
         const Unit done = w;
@@ -742,7 +776,7 @@ int dw_splits(int64_t T, int64_t V, int64_t D, int64_t piece)
 }
 
 struct Space {                            // the workspace's parts, in bytes from its start
-    int64_t g, sum, unit, wsum, total;
+    int64_t g, sum, unit, live, wsum, total;
     int64_t piece;
     int splits, wsplits;                  // of dx, of dw
 };
@@ -756,7 +790,8 @@ Space backward_space(int64_t T, int64_t V, int64_t D)
     s.sum = up_to(T * s.piece * 2, 256);
     s.unit = s.sum + up_to(T * D * 4 * s.splits, 256);
     s.wsplits = dw_splits(T, V, D, s.piece);
-    s.wsum = s.unit + 256;
+    s.live = s.unit + 256;
+    s.wsum = s.live + up_to((T + 63) / 64 * 8, 256);
     s.total = s.wsum + (s.wsplits > 1 ? V * D * 4 * s.wsplits : 0);
     return s;
 }
@@ -850,6 +885,7 @@ hipError_t launch_loss_backward(const float* dloss, const void* x, const void* w
     uint16_t* gm = static_cast<uint16_t*>(workspace);
     float* sum = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.sum);
     float* unit = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.unit);
+    uint64_t* live = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(workspace) + sp.live);
     float* wsum = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.wsum);
     hipError_t e = hipSuccess;
     const Side xs{static_cast<const uint16_t*>(x), D};
@@ -867,6 +903,7 @@ hipError_t launch_loss_backward(const float* dloss, const void* x, const void* w
         g.lse = lse;
         g.dloss = dloss;
         g.unit = unit;
+        g.live = live;
         g.v0 = (int)v0;
         g.vocab = (int)V;
         g.out = gm;
@@ -897,6 +934,7 @@ hipError_t launch_loss_backward(const float* dloss, const void* x, const void* w
         h.Q = (int)D;
         h.R = (int)T;
         h.unit = unit;
+        h.live = live;
         h.out = static_cast<uint16_t*>(dw) + v0 * D;
         h.out_pitch = D;
         if (sp.wsplits > 1) {

@@ -626,7 +626,8 @@ fp8_status fp8_attention_backward(const fp8_attention_shape* shape, const fp8_he
  * the head's weight; the logits z = x w^T are never stored.
  *   lse_t = log sum_v exp(z_tv),  loss_t = lse_t - z_t,target(t)
  * A token whose target is outside [0, vocab) (such as -100) has no target: its loss
- * is 0 and it gives no gradient.
+ * is 0 and it gives no gradient, whatever its hidden state is (padding that was never
+ * written may hold a NaN).
  *
  *   x       bf16 [tokens, dim];  weight  bf16 [vocab, dim]
  *   target  int64 [tokens], 8-byte aligned
