@@ -32,7 +32,7 @@
 // operand's end read as zero (the buffer's size, or an offset outside it).
 //
 // g is rounded to bf16, as an operand of the matrix units -- divided by the largest
-// |dloss|, which the products' epilogues multiply in again: with one dloss for all tokens
+// |dloss| of a token with a target, which the products' epilogues multiply in again: with one dloss for all tokens
 // (the mean), its own rounding would be a common error of every gradient, up to 2^-8.
 // z, the statistics and every sum stay in fp32.  The sums are formed in a fixed order: no atomics.
 #include "fp8_device.hpp"
@@ -229,7 +229,7 @@ struct LossArgs {
     const int64_t* target;
     const float* lse;
     const float* dloss;
-    float* unit;                          // the largest |dloss|, found with g and left to its products' epilogues
+    float* unit;                          // the largest |dloss| of a target, found with g and left to its products' epilogues
     float2* stats;                        // [column block][T]: maximum, sum of exponentials
     float* hit;                           // [T]: the target's logit
     uint64_t* live;                       // a bit per token: it has a target (found with g, for dw)
@@ -430,8 +430,9 @@ __global__ void __launch_bounds__(256, loss_per_cu(MI, NJ)) loss_product_kernel(
             }
         }
     };
-    // The largest finite |dloss| (1 if there is none above 0).  g's launches find it, every
-    // workgroup for itself (a launch of its own took 2 to 5 us), and leave it in memory.
+    // The largest finite |dloss| of a token with a target (1 if there is none above 0).  g's
+    // launches find it, every workgroup for itself (a launch of its own took 2 to 5 us), and
+    // leave it in memory.
     float by = 1.0f;
     if (EPI == kGrad) {
         __shared__ uint32_t part[4];
@@ -439,7 +440,8 @@ __global__ void __launch_bounds__(256, loss_per_cu(MI, NJ)) loss_product_kernel(
 #pragma unroll 8
         for (int i = threadIdx.x; i < g.P; i += 256) {
             const uint32_t v = __float_as_uint(g.dloss[i]) & 0x7FFFFFFFu;
-            top = max(top, v < 0x7F800000u ? v : 0u);
+            const bool has = (uint64_t)g.target[i] < (uint64_t)g.vocab;
+            top = max(top, has && v < 0x7F800000u ? v : 0u);
         }
         top = wave_max_u32(top);
         if (lane == 0) part[wave] = top;

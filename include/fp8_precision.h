@@ -646,9 +646,9 @@ fp8_status fp8_linear_cross_entropy_forward(const void* x, const void* weight, c
  * Its gradients: with g_tv = dloss_t (exp(z_tv - lse_t) - [v = target(t)]),
  *   dx = g w,  dweight = g^T x
  * The vocabulary is walked in pieces: a piece's logits are computed again, its g is
- * rounded to bf16 in the workspace (as a fraction of the largest |dloss|, which the
- * sums are multiplied with), and both products are taken from there (dx is summed over
- * the pieces in fp32).
+ * rounded to bf16 in the workspace (as a fraction of the largest |dloss| of a token with
+ * a target, which the sums are multiplied with), and both products are taken from there
+ * (dx is summed over the pieces in fp32).
  *
  *   dloss   fp32 [tokens] (for the mean over n tokens: 1 / n);  lse  from the forward
  *   dx      bf16 [tokens, dim];  dweight  bf16 [vocab, dim]  (written, not added to)

@@ -48,3 +48,17 @@ def test_hidden_states_of_tokens_without_a_target(fp8, T, V, D, value):
     dx2, dw2 = fp8.linear_cross_entropy_backward(d, other, w, t, lse2)
     assert torch.isfinite(dw.float()).all() and dw.any()
     assert torch.equal(dw2, dw) and torch.equal(dx2, dx) and not dx2[gone].any()
+
+
+@pytest.mark.parametrize("T,V,D", SHAPES)
+@pytest.mark.parametrize("value", [float("nan"), float("-inf"), -3e38, 2.0])
+def test_dloss_of_tokens_without_a_target(fp8, T, V, D, value):
+    """It is no measure of the others' gradients, which are held as fractions of the largest."""
+    say("loss backward, dloss of ignored tokens", T, V, D, value)
+    x, w, t, gone, d = make(T, V, D)
+    clean, other = d.clone(), d.clone()
+    clean[gone], other[gone] = 0.0, value
+    _, lse = fp8.linear_cross_entropy(x, w, t)
+    want = fp8.linear_cross_entropy_backward(clean, x, w, t, lse)
+    for a, b in zip(fp8.linear_cross_entropy_backward(other, x, w, t, lse), want):
+        assert b.any() and torch.equal(a, b)
