@@ -416,7 +416,9 @@ __global__ void __launch_bounds__(kAttThreads, 2) attention_forward_kernel(const
     tile.init(lds0);
 
     const float c = a.scale * kLog2e;
-    const float far = 8.0f / c;           // scores may pass the running maximum by 2^8 before a rescale
+    // scores may pass the running maximum by 2^8 before a rescale (any key seen passes the
+    // first maximum, -inf: the step to it is finite however small the scale)
+    const float far = fminf(8.0f / c, 1e38f);
     af32x16 o[DT / 32];
 #pragma unroll
     for (int db = 0; db < DT / 32; ++db) o[db] = af32x16{0};
