@@ -796,8 +796,13 @@ __global__ void __launch_bounds__(64 * keys_waves(DT), DT == 64 ? 3 : 2) attenti
     int t, unit;
     deal(blockIdx.x, a.hk * a.chunks, t, unit);
     const int khead = unit / a.chunks, chunk = unit % a.chunks;
-    const Place pl = find_tile(a, a.tile0 + t, 1, kMine);            // a sequence's first keys are seen by most
+    Place pl = find_tile(a, a.tile0 + t, 1, kMine);        // a sequence's first keys are seen by most
     if (!pl.any) return;
+    // queries that see nothing come first; they are not read, as 0 times whatever they hold
+    // need not be 0
+    const int unseeing = a.causal ? max(0, pl.nq - pl.nk) : 0;
+    pl.q0 += unseeing;
+    pl.nq -= unseeing;
     const int lane = threadIdx.x & 63, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t lds0 = (uint32_t)(uintptr_t)lds, stat0 = lds0 + kRing * 2 * kTile + kOwnTile;

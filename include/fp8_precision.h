@@ -552,8 +552,8 @@ fp8_status fp8_norm_backward(const void* dy, const void* s, fp8_stream_type type
  *   p_ij = exp(s_ij) / sum over the keys seen,  out_i = sum_j p_ij v_j,
  *   lse_i = log sum_j exp(s_ij)
  * A query that sees nothing (an empty key side, or causal with fewer keys than
- * queries) has out = 0, lse = -inf and no gradient.  Query head h uses key head
- * h / (heads_q / heads_k).
+ * queries) has out = 0, lse = -inf and no gradient, whatever it holds.  Query head h
+ * uses key head h / (heads_q / heads_k).
  *
  * A tensor is [tokens, heads, head_dim] bf16 with its own strides, so q, k and v
  * can be the slices of one projection's output, and dq, dk, dv the slices of its
@@ -605,6 +605,8 @@ fp8_status fp8_attention_forward(const fp8_attention_shape* shape, const fp8_hea
  * (delta is taken as dout_i . out_i, the same sum, where a tile of queries sees more
  * than 128 keys).  p and ds are rounded to bf16 for these products; with at most 128 keys
  * (of the tile of queries for dq, of the sequence for dk and dv) to twice its precision.
+ * A NaN or infinity in q, k, v or dout of a query that sees a key, or of a key, may reach
+ * every gradient of its sequence.
  *
  *   dout    as q;  out, lse  from the forward;  dq, dk, dv  as q, k, v
  *   absmax  fp32 scalar or NULL: becomes max(*absmax, max |dq|, max |dk|, max |dv|), as stored
