@@ -372,7 +372,7 @@ constexpr int kKeys = 64;                 // keys per streamed tile, forward and
 // with one running maximum and sum per row.  Operands
 // are read from LDS four instructions ahead of the matrix instruction that takes them.
 // MI355X, causal, heads of 128: 4096 tokens, 32 heads 148 us (0.93 PFLOP/s); 8192 packed
-// tokens, 40 query and 8 key heads 262 us (0.92).  Bound by the two products and the
+// tokens, 40 query and 8 key heads 263 us (0.92).  Bound by the two products and the
 // softmax between them, at the power limit (without a mask the clock falls to 1.83 GHz,
 // where this is half of what the matrix units can do): 32 matrix instructions to 32
 // exponentials and some 120 other vector instructions per step and wave.  Giving a wave
@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(256) attention_forward_join_kernel(const Atten
 // dq: 32 queries per wave, keys and values streamed.  A wave first takes its queries'
 // delta and leaves it for the dk/dv kernel: stats[0][head][token] = lse in powers of two
 // (+inf where the row is empty, so that every p of it is 0), stats[1][head][token] = delta.
-// 4096 causal tokens, 32 heads of 128: 200 us (three products: 1.03 PFLOP/s).
+// 4096 causal tokens, 32 heads of 128: 202 us in a kernel trace (three products: 1.02 PFLOP/s).
 template <int DT>
 __global__ void __launch_bounds__(kAttThreads, 2) attention_dq_kernel(const AttentionArgs a)
 {
@@ -782,7 +782,8 @@ constexpr int keys_waves(int dt) { return dt == 128 ? 8 : 4; }
 // a workgroup is 8 waves: they share each streamed tile, and the LDS of two workgroups of
 // 4 makes room for the ring (with two stages of it, and a barrier to each 32 queries, the
 // waves waited for their loads for half of the time).
-// 4096 causal tokens, 32 heads of 128: 270 us (four products: 1.02 PFLOP/s).
+// 4096 causal tokens, 32 heads of 128: 292 us in a kernel trace (four products: 0.94 PFLOP/s);
+// this and dq's kernel untraced 466 (seven products: 1.03).
 // chunks > 1: the steps are dealt over that many workgroups, each of which leaves fp32
 // partial sums [chunk][dk, dv][token][head][d].
 template <int DT>
@@ -1027,6 +1028,9 @@ static int key_chunks(int64_t tq, int64_t tk, int hq, int hk, int d, int batch)
 // more streamed tiles (256 keys) each.  Unsplit / split, MI355X, heads of 128: 100 queries
 // of 8 heads on 4000 keys, forward 72 / 19 us, backward 107 / 46; one query of 32 heads on
 // 16384 keys 270 / 47 and 493 / 231; 512 queries of 4 heads on 4096 keys 73 / 28 and 124 / 63.
+// The rule goes by averages, and is measured on even batches: one query on 131072 keys among
+// 31 on 500 (32 and 8 heads) is not split and takes 2300 us, 32 queries on as many keys in
+// all, 4577 each, 124.
 static int query_splits(int64_t tq, int64_t tk, int hq, int batch, int group)
 {
     const int64_t tiles = tile_bound(tq * group, batch, kOwn) * (hq / group), cus = device_cu_count();
@@ -1039,7 +1043,9 @@ static int query_splits(int64_t tq, int64_t tk, int hq, int batch, int group)
 // sequence's queries are few (half a tile on average); else each has tiles of its own.
 // MI355X, one query per sequence, heads of 128, apart / together: 64 sequences of 4096 keys,
 // 32 and 8 heads 394 / 193 us (1.07 GB of keys and values, 5.6 TB/s); 8 of 8192, 40 and 8
-// 157 / 61; one of 16384, 40 and 8 36 / 21.
+// 157 / 61; one of 16384, 40 and 8 36 / 21.  By the average again: 63 single queries on 4096 keys
+// each take 191 us (32 and 8 heads), a prompt of 8192 tokens 524, both packed together, where
+// no head is shared, 874.
 static int tile_group(int64_t tq, int hq, int hk, int batch)
 {
     const int group = hq / hk;

@@ -6,8 +6,9 @@
 // and backward, g_tv = dloss_t (exp(z_tv - lse_t) - [v = target(t)]),
 //   dx = g w,   dw = g^T x.
 // A token whose target lies outside [0, V) has no target: loss 0 and no gradient, whatever its
-// x: g's launch leaves a bit per token, by which dw's loads pass over its row (4096 tokens,
-// 32000 x 4096, all three products: 2254 us without, 2273 so).
+// x: g's launch leaves a bit per token, by which dw's loads pass over its row (all three
+// products, without and so: 4096 tokens, 32000 x 4096 2277 and 2297 us, 1001, 40007 x 1600 378
+// and 384).
 //
 // Forward: the logits' product with the row statistics taken in its epilogue -- the
 // maximum and the sum of exponentials of the wave's columns of each row -- and a
@@ -255,8 +256,8 @@ constexpr int loss_per_cu(int mi, int nj) { return mi * nj <= 16 ? 2 : 1; }
 }  // namespace
 
 // MI x NJ blocks of 16 x 16 per wave, GM x GN waves, NS stages.  MI355X: the logits of 4096
-// tokens, 32000 x 4096 735 us (1.46 PFLOP/s; a large library product of the size 720), of
-// 8192, 65521 x 5120 3.73 ms (1.47); the backward's three products 2.23 ms (1.44) and 373 us
+// tokens, 32000 x 4096 748 us (1.44 PFLOP/s; the library's product of the size 718 to 728), of
+// 8192, 65521 x 5120 3.74 ms (1.47); the backward's three products 2.25 ms (1.43) and 383 us
 // for 1001 tokens, 40007 x 1600.  At the power limit; what stands between these and the
 // library is the epilogue and the last round's idle units.
 template <int MI, int NJ, int GM, int GN, int NS, bool LA, bool LB, int EPI>
