@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -57,6 +58,10 @@ _SIGS = {
     "fp8_attention_forward": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
     "fp8_attention_backward_workspace": (_i32, [_vp, _vp]),
     "fp8_attention_backward": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "fp8_kv_cache_write": (_i32, [_vp, _vp, _vp, _vp]),
+    "fp8_kv_cache_read": (_i32, [_vp, _vp, _vp, _vp]),
+    "fp8_attention_cached_workspace": (_i32, [_vp, _i64, _vp]),
+    "fp8_attention_cached": (_i32, [_vp, _vp, _vp, _i64, _i32, ctypes.c_float, _vp, _vp, _vp, _i64, _vp]),
     "fp8_linear_cross_entropy_forward_workspace": (_i32, [_i64, _i64, _i64, _vp]),
     "fp8_linear_cross_entropy_forward": (_i32, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp]),
     "fp8_linear_cross_entropy_backward_workspace": (_i32, [_i64, _i64, _i64, _vp]),
@@ -834,6 +839,116 @@ def attention_backward(dout, q, k, v, out, lse, cu_q=None, cu_k=None, causal: bo
          (dout, q, k, v, out, lse, cu_q, cu_k, dq, dk, dv, absmax, ws), ctypes.byref(shape), hg, hq, hk, hv, ho,
          _ptr(lse), hdq, hdk, hdv, _ptr(absmax), _ptr(ws), ws.numel())
     return dq, dk, dv
+
+
+class KVCache(NamedTuple):
+    """A pool of pages of keys and values in E4M3: k, v uint8 codes [pages, heads,
+    page_tokens, head_dim] and k_scale, v_scale uint8 [pages, heads], a power of two each
+    (the byte e + 127): value = code 2^e.  ``kv_cache`` makes one."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def kv_cache(pages: int, heads: int, head_dim: int, page_tokens: int = 64, device="cuda") -> KVCache:
+    """A pool of ``pages`` pages for ``page_tokens`` (16, 32, 64 or 128) tokens each, not
+    written: a page's first token begins it."""
+    codes = lambda: torch.empty((pages, heads, page_tokens, head_dim), dtype=torch.uint8, device=device)
+    scale = lambda: torch.empty((pages, heads), dtype=torch.uint8, device=device)
+    return KVCache(codes(), codes(), scale(), scale())
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("table", _vp), ("lengths", _vp),
+                ("bounds", _vp), ("pages", _i64), ("heads", _i64), ("page_tokens", _i64), ("head_dim", _i64),
+                ("batch", _i64), ("blocks", _i64), ("tokens", _i64)]
+
+
+def _cache(cache, table, lengths, cu, tokens):
+    """The struct of a call on a cache, its tensors checked: (struct, the tensors)."""
+    k, v, k_scale, v_scale = cache
+    _dev_tensor(k, "cache.k", torch.uint8)
+    _dev_tensor(v, "cache.v", torch.uint8)
+    size = k.shape
+    if len(size) != 4 or v.shape != size:
+        raise ValueError("cache.k and cache.v must be [pages, heads, page_tokens, head_dim]")
+    for t, n in ((k_scale, "cache.k_scale"), (v_scale, "cache.v_scale")):
+        _dev_tensor(t, n, torch.uint8)
+        if t.shape != size[:2]:
+            raise ValueError(f"{n} must be [pages, heads]")
+    _dev_tensor(table, "table", torch.int32)
+    _dev_tensor(lengths, "lengths", torch.int32)
+    if table.dim() != 2 or lengths.shape != table.shape[:1]:
+        raise ValueError("table must be [batch, blocks] and lengths [batch]")
+    batch, blocks = table.shape
+    if cu is not None:
+        _vector(cu, "cu", batch + 1, torch.int32)
+    elif tokens % max(batch, 1):
+        raise ValueError("without cu every sequence has as many tokens")
+    c = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(), lengths.data_ptr(),
+               _ptr(cu), size[0], size[1], size[2], size[3], batch, blocks, tokens)
+    return c, (k, v, k_scale, v_scale, table, lengths, cu)
+
+
+def kv_cache_write(cache, table, lengths, k, v, cu=None) -> None:
+    """Quantise new keys and values (bf16 [tokens, heads, head_dim], tokens and heads with
+    any strides) into a paged cache.
+
+    ``table``: int32 [batch, blocks], the page of each block of page_tokens tokens of a
+    sequence; ``lengths``: int32 [batch], the tokens that each sequence holds, the new ones
+    among them; ``cu``: int32 bounds of the sequences' new tokens ([batch + 1]), or None where
+    all have as many.  Sequence b's n new tokens go to positions lengths[b] - n ..; those
+    whose block has no page of the pool (an entry below 0, say) are left out.  A page that a
+    call writes must stand in the table once.
+    """
+    hk, hv = _heads(k, "k"), _heads(v, "v", k.shape)
+    c, tensors = _cache(cache, table, lengths, cu, k.shape[0])
+    if (k.shape[1], k.shape[2]) != (c.heads, c.head_dim):
+        raise ValueError(f"k and v must be [tokens, {c.heads}, {c.head_dim}]")
+    _run("fp8_kv_cache_write", _lib.fp8_kv_cache_write, tensors + (k, v), ctypes.byref(c), hk, hv)
+
+
+def kv_cache_read(cache, table, lengths, tokens: int, cu=None, k=None, v=None):
+    """The last n tokens' keys and values of each sequence of a paged cache, packed: (k, v)
+    bf16 [tokens, heads, head_dim], exact.  ``table``, ``lengths`` and ``cu`` (whose last bound
+    is at most ``tokens``) as for ``kv_cache_write``: with the bounds of ``lengths`` the whole
+    contexts, as ``attention`` takes them.  Tokens without a page read as zeros."""
+    c, tensors = _cache(cache, table, lengths, cu, tokens)
+    shape = (tokens, c.heads, c.head_dim)
+    k = torch.empty(shape, dtype=torch.bfloat16, device=table.device) if k is None else k
+    v = torch.empty(shape, dtype=torch.bfloat16, device=table.device) if v is None else v
+    hk, hv = _heads(k, "k", shape), _heads(v, "v", shape)
+    _run("fp8_kv_cache_read", _lib.fp8_kv_cache_read, tensors + (k, v), ctypes.byref(c), hk, hv)
+    return k, v
+
+
+def attention_cached(q, cache, table, lengths, cu=None, causal: bool = True, scale: float | None = None, absmax=None,
+                     out=None, lse=None):
+    """Softmax attention of the call's tokens over a paged cache: q bf16 [tokens, heads_q,
+    head_dim] (tokens and heads with any strides), heads_q a multiple of the cache's heads;
+    ``table``, ``lengths`` and ``cu`` as for ``kv_cache_write``, which writes the tokens' own
+    keys and values first.  Query i of a sequence's n stands at position lengths - n + i and,
+    ``causal``, sees the keys up to its own.  ``scale``: head_dim ** -0.5 if not given.
+    ``absmax`` (fp32 [1], holding +0 or an earlier result) becomes max(absmax, max |out|).
+    Returns (out as q, lse fp32 [heads_q, tokens]); a query that sees no key has out 0 and
+    lse -inf."""
+    hq = _heads(q, "q")
+    size = q.shape
+    c, tensors = _cache(cache, table, lengths, cu, size[0])
+    if size[2] != c.head_dim:
+        raise ValueError(f"q must be [tokens, heads_q, {c.head_dim}]")
+    if absmax is not None:
+        _scalar_in(absmax, "absmax")
+    if out is None:
+        out = _new_heads(q)
+    ho = _heads(out, "out", size)
+    lse = _out(lse, "lse", (size[1], size[0]), torch.float32, q.device)
+    ws = _workspace("fp8_attention_cached_workspace", q.device, ctypes.byref(c), size[1])
+    _run("fp8_attention_cached", _lib.fp8_attention_cached, tensors + (q, out, lse, absmax, ws), ctypes.byref(c), hq, ho,
+         size[1], 1 if causal else 0, size[2] ** -0.5 if scale is None else scale, _ptr(lse), _ptr(absmax), _ptr(ws),
+         0 if ws is None else ws.numel())
+    return out, lse
 
 
 def _head(x, weight, target):

@@ -887,6 +887,184 @@ fp8_status fp8_attention_backward(const fp8_attention_shape* shape, const fp8_he
     return FP8_OK;
 }
 
+// ---- keys and values in a paged cache
+
+// The struct's own checks; page_tokens as a power of two in `shift`.
+static fp8_status cache_shape(const char* call, const fp8_kv_cache* c, int& shift)
+{
+    char msg[160];
+    auto no = [&](fp8_status st, const char* what) {
+        std::snprintf(msg, sizeof(msg), "%s: %s", call, what);
+        return fail(st, msg);
+    };
+    if (!c) return no(FP8_ERR_INVALID, "null cache");
+    if (c->pages < 1 || c->heads < 1 || c->head_dim < 1 || c->batch < 1 || c->blocks < 1 || c->tokens < 1 || c->page_tokens < 1)
+        return no(FP8_ERR_INVALID, "pages, heads, page_tokens, head_dim, batch, blocks and tokens must be positive");
+    shift = c->page_tokens == 16 ? 4 : c->page_tokens == 32 ? 5 : c->page_tokens == 64 ? 6 : c->page_tokens == 128 ? 7 : 0;
+    if (!shift) return no(FP8_ERR_UNSUPPORTED, "page_tokens must be 16, 32, 64 or 128");
+    if (c->head_dim % 8 || c->head_dim > 128) return no(FP8_ERR_UNSUPPORTED, "head_dim must be a multiple of 8, at most 128");
+    if (c->pages >= ((int64_t)1 << 31) || c->heads > 65536 || c->batch > (1 << 20) || c->tokens >= ((int64_t)1 << 31))
+        return no(FP8_ERR_UNSUPPORTED, "more than 2^31 - 1 pages or tokens, 2^16 heads or 2^20 sequences");
+    if (c->blocks >= ((int64_t)1 << 31) >> shift) return no(FP8_ERR_UNSUPPORTED, "sequences of 2^31 tokens or more");
+    if (!c->bounds && c->tokens % c->batch)
+        return no(FP8_ERR_INVALID, "tokens must be a multiple of batch without bounds");
+    return FP8_OK;
+}
+
+// The pool, table, lengths and bounds of a call, as byte ranges.
+static void cache_ranges(const fp8_kv_cache& c, Range (&r)[7])
+{
+    const int64_t scales = c.pages * c.heads, codes = scales * c.page_tokens * c.head_dim;
+    const Range all[7] = {{c.k, codes}, {c.v, codes}, {c.k_scale, scales}, {c.v_scale, scales},
+                          {c.table, 4 * c.batch * c.blocks}, {c.lengths, 4 * c.batch}, {c.bounds, 4 * (c.batch + 1)}};
+    for (int i = 0; i < 7; ++i) r[i] = all[i];
+}
+
+static fp8_status cache_pointers(const char* call, const fp8_kv_cache& c)
+{
+    if (!c.k || !c.v || !c.k_scale || !c.v_scale || !c.table || !c.lengths)
+        return fail(FP8_ERR_INVALID, std::string(call) + ": null pointer in the cache");
+    if (!aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(c.table, 4) || !aligned(c.lengths, 4) || !aligned(c.bounds, 4))
+        return fail(FP8_ERR_UNSUPPORTED, std::string(call) + ": misaligned pointer in the cache");
+    return FP8_OK;
+}
+
+static fp8k::CacheArgs cache_args(const fp8_kv_cache& c, int shift)
+{
+    fp8k::CacheArgs a{};
+    a.k = c.k;
+    a.v = c.v;
+    a.k_scale = c.k_scale;
+    a.v_scale = c.v_scale;
+    a.table = c.table;
+    a.lengths = c.lengths;
+    a.cu = c.bounds;
+    a.pages = c.pages;
+    a.tokens = c.tokens;
+    a.heads = (int)c.heads;
+    a.d = (int)c.head_dim;
+    a.shift = shift;
+    a.batch = (int)c.batch;
+    a.blocks = (int)c.blocks;
+    return a;
+}
+
+// Both directions between the call's keys and values and the cache.
+static fp8_status cache_move(const char* call, const fp8_kv_cache* cache, const fp8_head_tensor* k,
+                             const fp8_head_tensor* v, bool write, hipStream_t stream)
+{
+    t_last_error.clear();
+    int shift = 0;
+    fp8_status st = cache_shape(call, cache, shift);
+    if (st != FP8_OK) return st;
+    const fp8_kv_cache& c = *cache;
+    if ((st = cache_pointers(call, c)) != FP8_OK) return st;
+    Heads h[2];
+    if ((st = take_heads(call, "k", k, c.tokens, c.heads, c.head_dim, !write, h[0])) != FP8_OK ||
+        (st = take_heads(call, "v", v, c.tokens, c.heads, c.head_dim, !write, h[1])) != FP8_OK)
+        return st;
+    Range r[7];
+    cache_ranges(c, r);
+    bool bad = !write && heads_overlap(h[0], h[1]);
+    for (int i = 0; i < 7; ++i) {
+        for (const Heads& t : h)
+            if (!write || i < 4) bad = bad || heads_overlap(t, r[i].p, r[i].n);
+        for (int j = 0; write && j < 4; ++j) bad = bad || (i != j && overlap(r[i].p, r[i].n, r[j].p, r[j].n));
+    }
+    if (bad) return fail(FP8_ERR_INVALID, std::string(call) + ": overlapping buffers");
+    fp8k::CacheArgs a = cache_args(c, shift);
+    a.xk = h[0].p; a.xk_row = h[0].row; a.xk_head = h[0].head;
+    a.xv = h[1].p; a.xv_row = h[1].row; a.xv_head = h[1].head;
+    hipError_t e = write ? fp8k::launch_kv_cache_write(a, stream) : fp8k::launch_kv_cache_read(a, stream);
+    if (e != hipSuccess) return fail_hip(call, e);
+    return FP8_OK;
+}
+
+fp8_status fp8_kv_cache_write(const fp8_kv_cache* cache, const fp8_head_tensor* k, const fp8_head_tensor* v,
+                              hipStream_t stream)
+{
+    return cache_move("fp8_kv_cache_write", cache, k, v, true, stream);
+}
+
+fp8_status fp8_kv_cache_read(const fp8_kv_cache* cache, const fp8_head_tensor* k, const fp8_head_tensor* v,
+                             hipStream_t stream)
+{
+    return cache_move("fp8_kv_cache_read", cache, k, v, false, stream);
+}
+
+static fp8_status cached_shape(const char* call, const fp8_kv_cache* c, int64_t heads_q, int& shift)
+{
+    fp8_status st = cache_shape(call, c, shift);
+    if (st != FP8_OK) return st;
+    if (heads_q < 1 || heads_q % c->heads) return fail(FP8_ERR_INVALID, std::string(call) + ": heads_q must be a multiple of heads");
+    if (heads_q > 65536 || c->tokens * heads_q >= ((int64_t)1 << 31) - 256)
+        return fail(FP8_ERR_UNSUPPORTED, std::string(call) + ": more than 2^16 heads or 2^31 rows");
+    return FP8_OK;
+}
+
+static int64_t cached_bytes(const fp8_kv_cache& c, int64_t heads_q, int shift)
+{
+    return fp8k::attention_cached_workspace(c.tokens, (int)heads_q, (int)c.heads, (int)c.head_dim, (int)c.batch, (int)c.blocks,
+                                            shift);
+}
+
+fp8_status fp8_attention_cached_workspace(const fp8_kv_cache* cache, int64_t heads_q, int64_t* bytes)
+{
+    t_last_error.clear();
+    int shift = 0;
+    fp8_status st = cached_shape("fp8_attention_cached_workspace", cache, heads_q, shift);
+    if (st != FP8_OK) return st;
+    if (!bytes) return fail(FP8_ERR_INVALID, "fp8_attention_cached_workspace: null pointer");
+    *bytes = cached_bytes(*cache, heads_q, shift);
+    return FP8_OK;
+}
+
+fp8_status fp8_attention_cached(const fp8_kv_cache* cache, const fp8_head_tensor* q, const fp8_head_tensor* out,
+                                int64_t heads_q, int causal, float scale, float* lse, float* absmax, void* workspace,
+                                int64_t workspace_bytes, hipStream_t stream)
+{
+    t_last_error.clear();
+    const char* call = "fp8_attention_cached";
+    int shift = 0;
+    fp8_status st = cached_shape(call, cache, heads_q, shift);
+    if (st != FP8_OK) return st;
+    const fp8_kv_cache& c = *cache;
+    if ((st = cache_pointers(call, c)) != FP8_OK) return st;
+    if (causal != 0 && causal != 1) return fail(FP8_ERR_INVALID, "fp8_attention_cached: causal must be 0 or 1");
+    if (!(scale > 0.0f) || scale > 3.0e38f)
+        return fail(FP8_ERR_INVALID, "fp8_attention_cached: scale must be positive and finite");
+    Heads h[2];
+    if ((st = take_heads(call, "q", q, c.tokens, heads_q, c.head_dim, false, h[0])) != FP8_OK ||
+        (st = take_heads(call, "out", out, c.tokens, heads_q, c.head_dim, true, h[1])) != FP8_OK)
+        return st;
+    const int64_t need = cached_bytes(c, heads_q, shift);
+    if (!lse) return fail(FP8_ERR_INVALID, "fp8_attention_cached: null lse");
+    if (need > 0 && !workspace) return fail(FP8_ERR_INVALID, "fp8_attention_cached: null workspace");
+    if (workspace_bytes < need) return fail(FP8_ERR_INVALID, "fp8_attention_cached: workspace too small");
+    if (!aligned(lse, 4) || !aligned(absmax, 4) || !aligned(workspace, 16))
+        return fail(FP8_ERR_UNSUPPORTED, "fp8_attention_cached: misaligned lse, absmax or workspace");
+    Range in[7];
+    cache_ranges(c, in);
+    const Range flat[] = {{lse, 4 * heads_q * c.tokens}, {absmax, 4}, {workspace, workspace_bytes}};
+    bool bad = outputs_overlap(flat, 3, in, 7) || heads_overlap(h[1], h[0]);
+    for (const Range& r : flat) bad = bad || heads_overlap(h[0], r.p, r.n) || heads_overlap(h[1], r.p, r.n);
+    for (const Range& r : in) bad = bad || heads_overlap(h[1], r.p, r.n);
+    if (bad) return fail(FP8_ERR_INVALID, "fp8_attention_cached: overlapping buffers");
+    fp8k::CachedAttentionArgs a{};
+    a.c = cache_args(c, shift);
+    a.q = h[0].p; a.q_row = h[0].row; a.q_head = h[0].head;
+    a.out = h[1].p; a.out_row = h[1].row; a.out_head = h[1].head;
+    a.lse = lse;
+    a.absmax = reinterpret_cast<uint32_t*>(absmax);
+    a.hq = (int)heads_q;
+    a.group = (int)(heads_q / c.heads);
+    a.causal = causal;
+    a.scale = scale;
+    hipError_t e = fp8k::launch_attention_cached(a, workspace, stream);
+    if (e != hipSuccess) return fail_hip(call, e);
+    return FP8_OK;
+}
+
 static fp8_status loss_shape(const char* call, int64_t tokens, int64_t vocab, int64_t dim)
 {
     char msg[160];

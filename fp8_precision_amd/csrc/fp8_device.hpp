@@ -72,6 +72,30 @@ __device__ __forceinline__ uint2 quant8(uint4 x, float s)
     return r;
 }
 
+// Two E4M3 codes (bytes 0-1 of w, HI: 2-3) times the power of two s, as two bf16.
+template <bool HI>
+__device__ __forceinline__ uint32_t values2(uint32_t w, float s)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, HI));
+}
+
+// 8 E4M3 codes times the power of two s, as 8 bf16 (exact while they are normal numbers).
+__device__ __forceinline__ uint4 values8(uint2 w, float s)
+{
+    return make_uint4(values2<false>(w.x, s), values2<true>(w.x, s), values2<false>(w.y, s), values2<true>(w.y, s));
+}
+
+// The exponents of a cache's scales (a byte, e + 127), and 2^e.  A byte outside them, which
+// no write leaves, counts as the nearest.
+constexpr int kCacheLeastE = -100, kCacheMostE = 119;
+__device__ __forceinline__ int cache_exponent(uint8_t scale)
+{
+    const int e = (int)scale - 127;
+    return e < kCacheLeastE ? kCacheLeastE : e > kCacheMostE ? kCacheMostE : e;
+}
+__device__ __forceinline__ float two_to(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+__device__ __forceinline__ float cache_scale(uint8_t scale) { return two_to(cache_exponent(scale)); }
+
 // Byte transpose of a 4x4 block held as 4 words (word r = row r, byte c = col c):
 // returns in c0..c3 the columns (word c, byte r = row r).
 __device__ __forceinline__ void transpose4x4(uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3,

@@ -165,6 +165,36 @@ int64_t attention_forward_workspace(int64_t tq, int64_t tk, int hq, int hk, int 
 hipError_t launch_attention_forward(const AttentionArgs& args, void* workspace, hipStream_t stream);
 hipError_t launch_attention_backward(const AttentionArgs& args, hipStream_t stream);
 
+// A paged cache of E4M3 keys and values and the call's tokens (kv_cache.hip,
+// attention_cached.hip).  Strides in elements: _row between tokens, _head between heads.
+struct CacheArgs {
+    uint8_t *k, *v;                       // [pages, heads, 1 << shift, d]
+    uint8_t *k_scale, *v_scale;           // [pages, heads]
+    const int *table, *lengths, *cu;      // [batch, blocks], [batch], [batch + 1] or null (tokens / batch each)
+    int64_t pages, tokens, unit0;
+    int heads, d, shift, batch, blocks;
+    uint16_t *xk, *xv;                    // the call's keys and values (written or read)
+    int64_t xk_row, xk_head, xv_row, xv_head;
+};
+hipError_t launch_kv_cache_write(const CacheArgs& args, hipStream_t stream);
+hipError_t launch_kv_cache_read(const CacheArgs& args, hipStream_t stream);
+
+struct CachedAttentionArgs {
+    CacheArgs c;                          // c.tokens: queries
+    const uint16_t* q;
+    uint16_t* out;
+    int64_t q_row, q_head, out_row, out_head;
+    float* lse;                           // [hq, tokens]
+    uint32_t* absmax;                     // or null
+    float* partial;                       // sums of split work, their maxima and totals, and what to join
+    float2* tops;
+    int4* joins;
+    int hq, group, causal, workers;
+    float scale;
+};
+int64_t attention_cached_workspace(int64_t tokens, int hq, int heads, int d, int batch, int blocks, int shift);
+hipError_t launch_attention_cached(const CachedAttentionArgs& args, void* workspace, hipStream_t stream);
+
 // Cross entropy of a linear head (loss.hip): x [T, D], w [V, D].
 int64_t loss_forward_workspace(int64_t T, int64_t V);
 int64_t loss_backward_workspace(int64_t T, int64_t V, int64_t D);

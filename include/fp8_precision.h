@@ -624,6 +624,79 @@ fp8_status fp8_attention_backward(const fp8_attention_shape* shape, const fp8_he
                                   void* workspace, int64_t workspace_bytes, hipStream_t stream);
 
 /*
+ * Keys and values of generation in a paged cache of E4M3 codes, one scale for each page and
+ * head.  Sequence b's token at position p lies in page table[b][p / page_tokens] at slot
+ * p % page_tokens.  A page's tokens of one head share a power of two for the keys and one for
+ * the values: value = code 2^e, e held to -100 .. 119 and stored as the byte e + 127 (a byte
+ * outside 27 .. 246, which no write leaves, counts as the nearest).
+ *
+ * A call works on `tokens` packed tokens: sequence b's are the last ones that it holds, at
+ * positions lengths[b] - n .. lengths[b] - 1.  So a step of generation adds its tokens to
+ * lengths, writes their keys and values, and attends with their queries, all with one struct.
+ * Bounds and lengths outside what the tensors and the table hold are held to it; a token at
+ * a negative position, or in a block whose table entry is no page of the pool, has no place.
+ * No byte outside the tensors is read or written.
+ */
+typedef struct fp8_kv_cache {
+    uint8_t *k, *v;               /* [pages, heads, page_tokens, head_dim], 16-byte aligned */
+    uint8_t *k_scale, *v_scale;   /* [pages, heads] */
+    const int32_t* table;         /* device int32 [batch, blocks] */
+    const int32_t* lengths;       /* device int32 [batch]: tokens held, the call's own among them */
+    const int32_t* bounds;        /* device int32 [batch + 1]: sequence b's tokens of the call are bounds[b] ..
+                                     bounds[b + 1] - 1 (ascending, within tokens; those outside belong to no
+                                     sequence); NULL: tokens / batch each */
+    int64_t pages;                /* 1 .. 2^31 - 1 */
+    int64_t heads;                /* key heads, 1 .. 2^16 */
+    int64_t page_tokens;          /* 16, 32, 64 or 128 */
+    int64_t head_dim;             /* a multiple of 8, 8 .. 128 */
+    int64_t batch;                /* sequences, 1 .. 2^20 */
+    int64_t blocks;               /* entries of a row of the table, 1 or more; blocks page_tokens below 2^31 */
+    int64_t tokens;               /* of the call, 1 .. 2^31 - 1; a multiple of batch without bounds */
+} fp8_kv_cache;
+
+/*
+ * Quantises the call's keys and values into their pages.  A page that is begun (its slot 0 is
+ * written) takes for e the least with max |x| <= 448 2^e over its new tokens' finite values; a
+ * page that is written on from a later slot takes the larger of that and its own e, and where
+ * e grows its older codes are multiplied by the power of two that lies between, rounded to
+ * nearest even (exact but for those that become subnormal).  Then
+ *   code = encode_e4m3(x 2^-e)   round to nearest even, saturating
+ * A NaN gives a NaN code; an infinity saturates.  Slots behind the last token keep their
+ * codes.  Tokens without a place are left out.  A page that the call writes may stand in the
+ * table of one sequence only, and once; pages that are only read may be shared.
+ *
+ *   k, v    bf16 [tokens, heads, head_dim] with their own strides
+ */
+fp8_status fp8_kv_cache_write(const fp8_kv_cache* cache, const fp8_head_tensor* k, const fp8_head_tensor* v,
+                              hipStream_t stream);
+
+/*
+ * Reads the call's tokens back: k, v bf16 [tokens, heads, head_dim] (written), exact.  Tokens
+ * without a place read as zeros; rows that belong to no sequence are not written.
+ */
+fp8_status fp8_kv_cache_read(const fp8_kv_cache* cache, const fp8_head_tensor* k, const fp8_head_tensor* v,
+                             hipStream_t stream);
+
+/*
+ * Attention of the call's tokens over the cache: query i of a sequence's n stands at position
+ * lengths - n + i and sees the keys at positions up to its own (causal) or all that are held,
+ * as in fp8_attention_forward, whose formulas, head sharing and roundings these are.  A
+ * query that sees nothing has out = 0, lse = -inf.  Keys and values without a place are
+ * zeros (they are seen).  A NaN in a value may reach every query of its sequence.
+ *
+ *   q        bf16 [tokens, heads_q, head_dim] with its own strides;  out  as q
+ *   heads_q  a multiple of the cache's heads, at most 2^16; tokens heads_q below 2^31
+ *   lse      fp32 [heads_q, tokens]
+ *   absmax   fp32 scalar or NULL: becomes max(*absmax, max |out|), out as stored
+ *   workspace, workspace_bytes   device memory, 16-byte aligned, of at least the size that
+ *            fp8_attention_cached_workspace gives on the current device; one call's at a time
+ */
+fp8_status fp8_attention_cached_workspace(const fp8_kv_cache* cache, int64_t heads_q, int64_t* bytes);
+fp8_status fp8_attention_cached(const fp8_kv_cache* cache, const fp8_head_tensor* q, const fp8_head_tensor* out,
+                                int64_t heads_q, int causal, float scale, float* lse, float* absmax, void* workspace,
+                                int64_t workspace_bytes, hipStream_t stream);
+
+/*
  * Cross entropy of a linear head over a large vocabulary, from the hidden states and
  * the head's weight; the logits z = x w^T are never stored.
  *   lse_t = log sum_v exp(z_tv),  loss_t = lse_t - z_t,target(t)
