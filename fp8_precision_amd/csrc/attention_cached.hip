@@ -7,8 +7,17 @@
 // with k and v the codes times the power of two of their page and head.  Codes become bf16
 // exactly on their way into the matrix instructions (the conversion takes the scale), so the
 // only roundings are p's to bf16 and out's.
+//
+// A sequence's rows are its queries of the heads that share a key head (row r: query
+// r / group, head r % group of them).  Sequences of up to 16 rows, the single tokens of a
+// step of generation, are bound by reading the cache: their steps are dealt to the
+// workgroups in equal shares whatever the lengths, and each wave works from registers.
+// Sequences of more rows are bound by the matrix units: tiles of 128 rows, with the keys and
+// values as bf16 tiles in LDS.  Both kinds can be in one launch.
 #include <algorithm>
+#include <type_traits>
 
+#include "attention_tile.hpp"
 #include "fp8_device.hpp"
 #include "fp8_internal.hpp"
 #include "kv_cache.hpp"
@@ -17,35 +26,17 @@ namespace fp8k {
 
 namespace {
 
-typedef __bf16 cb16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 cb16x2 __attribute__((ext_vector_type(2)));
-typedef float cf32x2 __attribute__((ext_vector_type(2)));
-typedef float cf32x4 __attribute__((ext_vector_type(4)));
-typedef unsigned int cu32x4 __attribute__((ext_vector_type(4)));
-typedef unsigned int cu32x2 __attribute__((ext_vector_type(2)));
-typedef const __attribute__((address_space(4))) int const_int;
+typedef unsigned int au32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
 constexpr int kWaves = 4;
-constexpr int kRows = 16;                  // rows of a unit: a query of one head each
-constexpr int kStep = 64;                  // keys a wave takes at a time
-constexpr int kLeastSteps = kWaves;        // a workgroup's share of the work, at least
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kInf = __builtin_inff();
+constexpr int kFew = 16;                   // rows of a sequence that is read in shares
+constexpr int kOwn = 128;                  // rows of a tile: 32 per wave
+constexpr int kLeastSteps = kWaves;        // of a share
+constexpr int kLeastSplit = 4;             // steps of a part of a tile's keys
+constexpr uint32_t kNowhere = 0x7FFFFFF0u; // an offset outside every buffer
 
-union Operand {
-    cu32x4 u;
-    cb16x8 b;
-    uint32_t w[4];
-};
-
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b)
-{
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(cf32x2{a, b}, cb16x2));
-}
-
-__device__ __forceinline__ cf32x4 mma(const Operand& a, const Operand& b, const cf32x4& c)
+__device__ __forceinline__ af32x4 mma16(const Frag& a, const Frag& b, const af32x4& c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.b, b.b, c, 0, 0, 0);
 }
@@ -82,240 +73,303 @@ __device__ __forceinline__ Sequence sequence(const CacheArgs& a, int b)
     return s;
 }
 
-// Steps of unit `u` of one head of a sequence (rows kRows u ..): one at least, for the rows that see nothing.
-__device__ __forceinline__ int unit_steps(const CachedAttentionArgs& a, const Sequence& s, int u)
+__device__ __forceinline__ bool few(const CachedAttentionArgs& a, const Sequence& s) { return s.queries * a.group <= kFew; }
+
+// Steps of one head of a sequence of few rows: one at least, for the rows that see nothing.
+__device__ __forceinline__ int share_steps(const CachedAttentionArgs& a, const Sequence& s)
 {
-    const int last = min((kRows * u + kRows - 1) / a.group, s.queries - 1);
-    const int see = a.causal ? min(s.held, s.held - s.queries + last + 1) : s.held;
-    return max(1, (see + kStep - 1) / kStep);
+    return s.queries == 0 || !few(a, s) ? 0 : max(1, (s.held + kKeys - 1) / kKeys);
 }
 
-__device__ __forceinline__ int units_of(const CachedAttentionArgs& a, const Sequence& s)
+__device__ __forceinline__ int row_tiles(const CachedAttentionArgs& a, const Sequence& s)
 {
-    return (s.queries * a.group + kRows - 1) / kRows;
+    return few(a, s) ? 0 : (s.queries * a.group + kOwn - 1) / kOwn;
 }
 
-__device__ __forceinline__ int64_t head_steps(const CachedAttentionArgs& a, const Sequence& s)
-{
-    const int units = units_of(a, s);
-    int64_t n = 0;
-    for (int u = 0; u < units; ++u) n += unit_steps(a, s, u);
-    return n;
-}
-
-// A wave's codes of 64 keys, as loaded.  Of each block of 16 keys a lane has DT / 4 codes of
-// key lane % 16 (chunk lane / 16), and DT / 16 codes of each of the values 4 (lane / 16) + r.
-template <int DT>
-struct Codes {
-    uint32_t k[4][DT / 16];
-    uint32_t v[4][4][DT / 64];
-    float k_scale[4], v_scale[4];
+// The sums of every thread's (x, y): all threads' in total, the x of those before it in before.
+struct Sums {
+    int64_t before, total, total_y;
 };
 
-// Where the keys 16 x .. of a step lie: the page and head's place in the pool, -1 for none.
-struct Block {
-    int64_t place;
-    int at, rows;        // first row in the page, rows held
+__device__ __forceinline__ Sums block_sums(int64_t x, int64_t y, int64_t (*lds)[2])
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int64_t upto = x;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int64_t o = __shfl_up(upto, off, 64), p = __shfl_xor(y, off, 64);
+        if (lane >= off) upto += o;
+        y += p;
+    }
+    if (lane == 63) {
+        lds[wave][0] = upto;
+        lds[wave][1] = y;
+    }
+    __syncthreads();
+    Sums s{upto - x, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        if (w < wave) s.before += lds[w][0];
+        s.total += lds[w][0];
+        s.total_y += lds[w][1];
+    }
+    return s;
+}
+
+// Where 16 keys of one head lie: their bytes in the pool and how many are held.
+struct Keys16 {
+    int64_t byte;
+    int rows;
+    float k_scale, v_scale;
 };
 
-}  // namespace
+// A sequence's pages and their scales of one head, 64 blocks in the lanes of a wave at a
+// time: this window, the next (its scales on their way) and the one after (its pages).
+struct Pages {
+    const int* table;
+    const uint8_t *k_scale, *v_scale;
+    int64_t pages;
+    int heads, head, held, shift, d;
+    int first;                             // the window's first block
+    int page[3];
+    int scale[2];                          // the lane's two bytes, the values' in the high half
 
-// Rows of one key head (its query heads' queries, 16 to a unit) against its keys.  The steps
-// of all units, in order, are dealt to the workgroups in equal shares, so that one long
-// sequence among short ones is spread like any other; a share's pieces of units that it does
-// not hold whole are left as partial sums and joined.  The four waves take a piece's steps in
-// turn.  Nothing of a step goes through LDS: 16 keys are the rows of a 16x16x32 product with
-// the queries as its columns, in which a lane has 4 keys' scores of one query, and these are
-// the second operand of the product with the values, whose rows are the head dimension: its
-// first operand is 4 + 4 codes of one column, taken from 8 rows by byte permutations.
+    __device__ __forceinline__ int entry(int window) const
+    {
+        const int at = first + 64 * window + (int)(threadIdx.x & 63);
+        return (int64_t)at << shift < held ? table[at] : -1;
+    }
+    __device__ __forceinline__ int scales(int p) const
+    {
+        if (p < 0 || p >= pages) return 127 << 16 | 127;
+        const int64_t at = (int64_t)p * heads + head;
+        return k_scale[at] | v_scale[at] << 16;
+    }
+    __device__ __forceinline__ void init(const CacheArgs& a, int b, int head_, int held_, int key)
+    {
+        table = a.table + (int64_t)b * a.blocks;
+        k_scale = a.k_scale;
+        v_scale = a.v_scale;
+        pages = a.pages;
+        heads = a.heads;
+        head = head_;
+        held = held_;
+        shift = a.shift;
+        d = a.d;
+        first = key >> shift;
+#pragma unroll
+        for (int w = 0; w < 3; ++w) page[w] = entry(w);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) scale[w] = scales(page[w]);
+    }
+    // the keys key .. key + 15 (key: the same in all lanes, a multiple of 16, never falling)
+    __device__ __forceinline__ Keys16 at(int key)
+    {
+        const int block = key >> shift;
+        while (block - first >= 64) {
+            first += 64;
+            page[0] = page[1];
+            page[1] = page[2];
+            scale[0] = scale[1];
+            scale[1] = scales(page[1]);
+            page[2] = entry(2);
+        }
+        const int p = __builtin_amdgcn_readlane(page[0], block - first), s = __builtin_amdgcn_readlane(scale[0], block - first);
+        const bool none = key >= held || p < 0 || p >= pages;
+        Keys16 x;
+        x.byte = none ? 0 : ((((int64_t)p * heads + head) << shift) + (key & ((1 << shift) - 1))) * d;
+        x.rows = none ? 0 : min(held - key, 16);
+        x.k_scale = cache_scale((uint8_t)s);
+        x.v_scale = cache_scale((uint8_t)(s >> 16));
+        return x;
+    }
+};
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const uint8_t* pool, const Keys16& x, int d)
+{
+    return __builtin_amdgcn_make_buffer_rsrc((void*)(pool + x.byte), 0, x.rows * d, 0x00020000);
+}
+
+// What the join takes of a row's sums left in parts.  A part's rows lie 16 to a slot.
+struct Join {
+    int b, head, row, count;               // rows row .. of the sequence; nothing to do below 2 parts
+    int first, second, step, pad;          // the slots: first, second, second + step, ...
+};
+
+template <int DT> constexpr int share_lds() { return kWaves * kFew * (DT + 4 + 2) * 4; }
+template <int DT> constexpr int tile_lds() { return 4 * kKeys * DT * 2; }
+
+// The row's value and its largest magnitude, from unnormalised sums.
+__device__ __forceinline__ float inverse(float l) { return l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l); }   // a NaN sum stays NaN
+
+__device__ __forceinline__ uint32_t top_of(uint32_t w, uint32_t top)
+{
+    return max(max(top, w & 0x7FFF0000u), w << 16 & 0x7FFFFFFFu);
+}
+
+// A share of the steps of all sequences of few rows.  The steps are counted in order (sequence,
+// head, 64 keys) and dealt in equal shares, so that one long sequence among short ones is
+// spread like any other; pieces of a share that are no whole head of a sequence are left as
+// partial sums and joined.  The four waves take a piece's steps in turn.  Nothing of a step
+// goes through LDS: 16 keys are the rows of a 16x16x32 product with the queries as its
+// columns, in which a lane has 4 keys' scores of one query, and these are the second operand
+// of the product with the values, whose rows are the head dimension: its first operand is 4 +
+// 4 codes of one column, taken from 8 rows by byte permutations.  A step's keys are loaded
+// into the registers of the last one's as soon as its scores are there, the values after
+// its output.
 template <int DT, bool FULL>
-__global__ void __launch_bounds__(kThreads, 2) attention_cached_kernel(const CachedAttentionArgs a)
+__device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, int worker, uint8_t* lds, int64_t (*sums)[2], int64_t* found)
 {
     constexpr int kPer = DT / 16;          // values' elements of a lane, and the product's tiles
-    __shared__ float s_out[kWaves][kRows][DT + 4];
-    __shared__ float s_top[kWaves][kRows], s_sum[kWaves][kRows];
-    __shared__ int64_t s_total[kWaves];
-    __shared__ int64_t s_found[2];
+    constexpr int kRow = DT + 4;
+    float* const s_out = reinterpret_cast<float*>(lds);               // [wave][row][kRow]
+    float* const s_top = s_out + kWaves * kFew * kRow;                // [wave][row]
+    float* const s_sum = s_top + kWaves * kFew;
     const CacheArgs& c = a.c;
     const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int worker = blockIdx.x;
+    uint32_t top_out = 0;
 
-    // the share: every thread sums some sequences' steps, in order
+    // the share: every thread counts some sequences' steps, in order
     const int per = (c.batch + kThreads - 1) / kThreads, b0 = threadIdx.x * per, b1 = min(b0 + per, c.batch);
     int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += head_steps(a, sequence(c, b)) * c.heads;
-    int64_t upto = mine;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const int64_t o = __shfl_up(upto, off, 64);
-        if (lane >= off) upto += o;
-    }
-    if (lane == 63) s_total[wave] = upto;
-    __syncthreads();
-    int64_t total = 0, before = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        if (w < wave) before += s_total[w];
-        total += s_total[w];
-    }
-    const int64_t share = max((total + a.workers - 1) / a.workers, (int64_t)kLeastSteps);
+    for (int b = b0; b < b1; ++b) mine += (int64_t)share_steps(a, sequence(c, b)) * c.heads;
+    const Sums all = block_sums(mine, 0, sums);
+    const int64_t share = max((all.total + a.workers - 1) / a.workers, (int64_t)kLeastSteps);
     int64_t at = worker * share;
-    const int64_t end = min(at + share, total);
-    if (threadIdx.x == 0) a.joins[worker] = make_int4(0, 0, 0, 0);
-    if (at >= end) return;
-    before += upto - mine;
-    if (before <= at && at < before + mine) {
-        int64_t left = at - before;
+    const int64_t end = min(at + share, all.total);
+    Join* const joins = reinterpret_cast<Join*>(a.joins);
+    if (threadIdx.x == 0) joins[worker].count = 0;
+    if (at >= end) return 0;
+    if (all.before <= at && at < all.before + mine) {
+        int64_t left = at - all.before;
         int b = b0;
         for (;; ++b) {
-            const int64_t n = head_steps(a, sequence(c, b)) * c.heads;
+            const int64_t n = (int64_t)share_steps(a, sequence(c, b)) * c.heads;
             if (left < n) break;
             left -= n;
         }
-        s_found[0] = b;
-        s_found[1] = left;
+        found[0] = b;
+        found[1] = left;
     }
     __syncthreads();
-    int b = __builtin_amdgcn_readfirstlane((int)s_found[0]);
-    int64_t left = s_found[1];
+    int b = __builtin_amdgcn_readfirstlane((int)found[0]);
     Sequence s = sequence(c, b);
-    int64_t per_head = head_steps(a, s);
-    int head = __builtin_amdgcn_readfirstlane((int)(left / per_head));
-    left -= head * per_head;
-    int u = 0, steps;
-    for (;; ++u) {
-        steps = unit_steps(a, s, u);
-        if (left < steps) break;
-        left -= steps;
-    }
-    int step0 = __builtin_amdgcn_readfirstlane((int)left);
+    int steps = __builtin_amdgcn_readfirstlane(share_steps(a, s));
+    int head = __builtin_amdgcn_readfirstlane((int)(found[1] / steps));
+    int step0 = __builtin_amdgcn_readfirstlane((int)(found[1] - (int64_t)head * steps));
     const float scale2 = a.scale * kLog2e;
-    uint32_t top_out = 0;
+    const float far = fminf(8.0f / scale2, 1e38f);         // scores may pass the running maximum by 2^8 before a rescale
 
     while (true) {
-        b = __builtin_amdgcn_readfirstlane(b);
-        u = __builtin_amdgcn_readfirstlane(u);
-        steps = __builtin_amdgcn_readfirstlane(steps);
         const int from = __builtin_amdgcn_readfirstlane(s.from), queries = __builtin_amdgcn_readfirstlane(s.queries);
         const int held = __builtin_amdgcn_readfirstlane(s.held);
         const int take = __builtin_amdgcn_readfirstlane((int)min((int64_t)(steps - step0), end - at));
-        const int rows = queries * a.group, row = kRows * u + m;
-        const int qi = row / a.group, hq = head * a.group + row - qi * a.group;
-        const bool valid = row < rows;
+        const int rows = queries * a.group, qi = m / a.group, hq = head * a.group + m - qi * a.group;
         const int shift = held - queries;
-        const int see = a.causal ? min(held, qi + shift + 1) : held;
-        const int see_first = a.causal ? min(held, kRows * u / a.group + shift + 1) : held;
+        const int see = a.causal ? min(held, qi + shift + 1) : held, see_first = a.causal ? min(held, shift + 1) : held;
 
         // the queries' operand: lane's column m, elements of chunk g as the keys' lanes have them
-        Operand q[DT / 32];
+        Frag q[DT / 32];
 #pragma unroll
         for (int i = 0; i < DT / 32; ++i) {
-            q[i].u = cu32x4{0, 0, 0, 0};
+            q[i].u = au32x4{0, 0, 0, 0};
             const int e = DT / 4 * g + 8 * i;
-            if (valid && (FULL || e < c.d))
-                q[i].u = *reinterpret_cast<const cu32x4*>(a.q + (int64_t)(from + qi) * a.q_row + (int64_t)hq * a.q_head + e);
+            if (m < rows && (FULL || e < c.d))
+                q[i].u = *reinterpret_cast<const au32x4*>(a.q + (int64_t)(from + qi) * a.q_row + (int64_t)hq * a.q_head + e);
         }
-        cf32x4 o[kPer];
+        af32x4 o[kPer];
 #pragma unroll
-        for (int t = 0; t < kPer; ++t) o[t] = cf32x4{0, 0, 0, 0};
+        for (int t = 0; t < kPer; ++t) o[t] = af32x4{0, 0, 0, 0};
         float top = -kInf, sum = 0.0f;
 
-        const const_int* table = (const const_int*)(uintptr_t)(c.table + (int64_t)b * c.blocks);
-        auto block = [&](int key) __attribute__((always_inline)) {
-            Block x;
-            const int page = key < held ? table[key >> c.shift] : -1;
-            const bool none = page < 0 || page >= c.pages;
-            x.place = none ? -1 : (int64_t)page * c.heads + head;
-            x.at = key & ((1 << c.shift) - 1);
-            x.rows = none ? 0 : min(held - key, 16);
-            return x;
-        };
-        Codes<DT> r;
-        Block bl[4];
-        auto resource = [&](const uint8_t* pool, const Block& x) __attribute__((always_inline)) {
-            const uint8_t* p = pool + (((max(x.place, (int64_t)0) << c.shift) + x.at) * c.d);
-            return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, x.rows * c.d, 0x00020000);
-        };
-        auto load_k = [&]() __attribute__((always_inline)) {
+        // Codes of 64 keys, as loaded.  Of each block of 16 keys a lane has DT / 4 codes of key
+        // m (chunk g), and DT / 16 codes (chunk m) of each of the values 4 g + i.
+        uint32_t ck[4][DT / 16], cv[4][4][DT / 64];
+        Keys16 x[4];
+        float v_scale[4];
+        Pages pages;
+        const int last = step0 + take;
+        auto load_k = [&](int key) __attribute__((always_inline)) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const auto src = resource(c.k, bl[x]);
+            for (int n = 0; n < 4; ++n) {
+                x[n] = pages.at(key + 16 * n);
+                const auto src = rows_of(c.k, x[n], FULL ? DT : c.d);
                 if constexpr (FULL) {
 #pragma unroll
                     for (int i = 0; i < DT / 64; ++i) {
-                        const cu32x4 w = __builtin_amdgcn_raw_buffer_load_b128(src, m * DT + DT / 4 * g + 16 * i, 0, 0);
+                        const au32x4 w = __builtin_amdgcn_raw_buffer_load_b128(src, m * DT + DT / 4 * g + 16 * i, 0, 0);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) r.k[x][4 * i + j] = w[j];
+                        for (int j = 0; j < 4; ++j) ck[n][4 * i + j] = w[j];
                     }
                 } else {
 #pragma unroll
                     for (int i = 0; i < DT / 32; ++i) {
                         const int e = DT / 4 * g + 8 * i;
-                        const cu32x2 w = __builtin_amdgcn_raw_buffer_load_b64(src, e < c.d ? m * c.d + e : 0x7FFFFFF0, 0, 0);
-                        r.k[x][2 * i] = w[0];
-                        r.k[x][2 * i + 1] = w[1];
+                        const au32x2 w = __builtin_amdgcn_raw_buffer_load_b64(src, e < c.d ? m * c.d + e : kNowhere, 0, 0);
+                        ck[n][2 * i] = w[0];
+                        ck[n][2 * i + 1] = w[1];
                     }
                 }
-                r.k_scale[x] = cache_scale(c.k_scale[max(bl[x].place, (int64_t)0)]);
             }
         };
         auto load_v = [&]() __attribute__((always_inline)) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const auto src = resource(c.v, bl[x]);
+            for (int n = 0; n < 4; ++n) {
+                const int d = FULL ? DT : c.d, e = kPer * m;
+                const auto src = rows_of(c.v, x[n], d);
+                v_scale[n] = x[n].v_scale;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int d = FULL ? DT : c.d, e = kPer * m;
-                    const int off = FULL || e < d ? (4 * g + i) * d + e : 0x7FFFFFF0;
+                    const uint32_t off = FULL || e < d ? (uint32_t)((4 * g + i) * d + e) : kNowhere;
                     if constexpr (DT == 128) {
-                        const cu32x2 w = __builtin_amdgcn_raw_buffer_load_b64(src, off, 0, 0);
-                        r.v[x][i][0] = w[0];
-                        r.v[x][i][1] = w[1];
+                        const au32x2 w = __builtin_amdgcn_raw_buffer_load_b64(src, off, 0, 0);
+                        cv[n][i][0] = w[0];
+                        cv[n][i][1] = w[1];
                     } else {
-                        r.v[x][i][0] = __builtin_amdgcn_raw_buffer_load_b32(src, off, 0, 0);
+                        cv[n][i][0] = __builtin_amdgcn_raw_buffer_load_b32(src, off, 0, 0);
                     }
                 }
-                r.v_scale[x] = cache_scale(c.v_scale[max(bl[x].place, (int64_t)0)]);
             }
         };
 
-        const int last = step0 + take;
-        for (int t = step0 + wave; t < last; t += kWaves) {
-            const int j0 = t * kStep;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) bl[x] = block(j0 + 16 * x);
-            load_k();
+        if (step0 + wave < last) {
+            pages.init(c, b, head, held, (step0 + wave) * kKeys);
+            load_k((step0 + wave) * kKeys);
             load_v();
-            cf32x4 p[4];
+        }
+        for (int t = step0 + wave; t < last; t += kWaves) {
+            const int j0 = t * kKeys;
+            const bool more = t + kWaves < last;
+            af32x4 p[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                p[x] = cf32x4{0, 0, 0, 0};
+            for (int n = 0; n < 4; ++n) {
+                p[n] = af32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int i = 0; i < DT / 32; ++i) {
-                    Operand k;
+                    Frag k;
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        k.w[2 * j] = values2<false>(r.k[x][2 * i + j], r.k_scale[x]);
-                        k.w[2 * j + 1] = values2<true>(r.k[x][2 * i + j], r.k_scale[x]);
+                        k.w[2 * j] = values2<false>(ck[n][2 * i + j], x[n].k_scale);
+                        k.w[2 * j + 1] = values2<true>(ck[n][2 * i + j], x[n].k_scale);
                     }
-                    p[x] = mma(k, q[i], p[x]);
+                    p[n] = mma16(k, q[i], p[n]);
                 }
             }
-            if (j0 + kStep > see_first) {
+            if (more) load_k(j0 + kWaves * kKeys);
+            if (j0 + kKeys > see_first) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
+                for (int n = 0; n < 4; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (j0 + 16 * x + 4 * g + i >= see) p[x][i] = -kInf;
+                        if (j0 + 16 * n + 4 * g + i >= see) p[n][i] = -kInf;
             }
-            float up = top;
+            float up = fmaxf(fmaxf(p[0][0], p[0][1]), fmaxf(p[0][2], p[0][3]));
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) up = fmaxf(up, p[x][i]);
+            for (int n = 1; n < 4; ++n) up = fmaxf(up, fmaxf(fmaxf(p[n][0], p[n][1]), fmaxf(p[n][2], p[n][3])));
             up = max4(up);
-            if (__any(up > top)) {
+            if (__any(up > top + far)) {                   // top = -inf: any key seen
+                up = fmaxf(up, top);
                 const float by = up == -kInf ? 1.0f : __builtin_amdgcn_exp2f((top - up) * scale2);
                 sum *= by;
 #pragma unroll
@@ -326,196 +380,432 @@ __global__ void __launch_bounds__(kThreads, 2) attention_cached_kernel(const Cac
             }
             const float use = top == -kInf ? 0.0f : top * scale2;
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
+            for (int n = 0; n < 4; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    p[x][i] = __builtin_amdgcn_exp2f(fmaf(p[x][i], scale2, -use));
-                    sum += p[x][i];
+                    p[n][i] = __builtin_amdgcn_exp2f(fmaf(p[n][i], scale2, -use));
+                    sum += p[n][i];
                 }
 #pragma unroll
-            for (int x = 0; x < 4; x += 2) {
-                Operand f;
-                f.w[0] = bf16_pair(p[x][0], p[x][1]);
-                f.w[1] = bf16_pair(p[x][2], p[x][3]);
-                f.w[2] = bf16_pair(p[x + 1][0], p[x + 1][1]);
-                f.w[3] = bf16_pair(p[x + 1][2], p[x + 1][3]);
+            for (int n = 0; n < 4; n += 2) {
+                Frag f;
+                f.w[0] = bf16_pair(p[n][0], p[n][1]);
+                f.w[1] = bf16_pair(p[n][2], p[n][3]);
+                f.w[2] = bf16_pair(p[n + 1][0], p[n + 1][1]);
+                f.w[3] = bf16_pair(p[n + 1][2], p[n + 1][3]);
 #pragma unroll
                 for (int w = 0; w < DT / 64; ++w) {
                     uint32_t lo[4], hi[4];
-                    transpose4x4(r.v[x][0][w], r.v[x][1][w], r.v[x][2][w], r.v[x][3][w], lo[0], lo[1], lo[2], lo[3]);
-                    transpose4x4(r.v[x + 1][0][w], r.v[x + 1][1][w], r.v[x + 1][2][w], r.v[x + 1][3][w], hi[0], hi[1], hi[2], hi[3]);
+                    transpose4x4(cv[n][0][w], cv[n][1][w], cv[n][2][w], cv[n][3][w], lo[0], lo[1], lo[2], lo[3]);
+                    transpose4x4(cv[n + 1][0][w], cv[n + 1][1][w], cv[n + 1][2][w], cv[n + 1][3][w], hi[0], hi[1], hi[2], hi[3]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        Operand v;
-                        v.w[0] = values2<false>(lo[i], r.v_scale[x]);
-                        v.w[1] = values2<true>(lo[i], r.v_scale[x]);
-                        v.w[2] = values2<false>(hi[i], r.v_scale[x + 1]);
-                        v.w[3] = values2<true>(hi[i], r.v_scale[x + 1]);
-                        o[4 * w + i] = mma(v, f, o[4 * w + i]);
+                        Frag v;
+                        v.w[0] = values2<false>(lo[i], v_scale[n]);
+                        v.w[1] = values2<true>(lo[i], v_scale[n]);
+                        v.w[2] = values2<false>(hi[i], v_scale[n + 1]);
+                        v.w[3] = values2<true>(hi[i], v_scale[n + 1]);
+                        o[4 * w + i] = mma16(v, f, o[4 * w + i]);
                     }
                 }
             }
+            if (more) load_v();
         }
         sum = sum4(sum);
 
         // the waves' sums together: o[t][r] is element kPer (4 g + r) + t of row m
         if (g == 0) {
-            s_top[wave][m] = top;
-            s_sum[wave][m] = sum;
+            s_top[wave * kFew + m] = top;
+            s_sum[wave * kFew + m] = sum;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int t = 0; t < kPer; t += 4)
-                *reinterpret_cast<cf32x4*>(&s_out[wave][m][kPer * (4 * g + i) + t]) =
-                    cf32x4{o[t][i], o[t + 1][i], o[t + 2][i], o[t + 3][i]};
+                *reinterpret_cast<af32x4*>(s_out + (wave * kFew + m) * kRow + kPer * (4 * g + i) + t) =
+                    af32x4{o[t][i], o[t + 1][i], o[t + 2][i], o[t + 3][i]};
         __syncthreads();
-        {
-            const int n = threadIdx.x / 16, e = threadIdx.x % 16 * kPer, r2 = kRows * u + n;
-            const int q2 = r2 / a.group, h2 = head * a.group + r2 - q2 * a.group;
-            float best = -kInf, all = 0.0f, x[kPer];
+        const int n = threadIdx.x / 16, e = threadIdx.x % 16 * kPer;
+        if (n < rows) {
+            const int q2 = n / a.group, h2 = head * a.group + n - q2 * a.group;
+            float best = -kInf, l = 0.0f, y[kPer];
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) best = fmaxf(best, s_top[w][n]);
-            const float use = best == -kInf ? 0.0f : best;
+            for (int w = 0; w < kWaves; ++w) best = fmaxf(best, s_top[w * kFew + n]);
+            const float base = best == -kInf ? 0.0f : best;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) x[i] = 0.0f;
+            for (int i = 0; i < kPer; ++i) y[i] = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) {
-                const float by = __builtin_amdgcn_exp2f((s_top[w][n] - use) * scale2);
-                all = fmaf(s_sum[w][n], by, all);
+                const float by = __builtin_amdgcn_exp2f((s_top[w * kFew + n] - base) * scale2);
+                l = fmaf(s_sum[w * kFew + n], by, l);
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) x[i] = fmaf(s_out[w][n][e + i], by, x[i]);
+                for (int i = 0; i < kPer; ++i) y[i] = fmaf(s_out[(w * kFew + n) * kRow + e + i], by, y[i]);
             }
-            if (r2 < rows) {
-                if (take == steps) {
-                    const float by = all > 0.0f ? 1.0f / all : (all == 0.0f ? 0.0f : all);    // a NaN sum stays NaN
-                    uint32_t w[kPer / 2];
+            if (take == steps) {
+                const float by = inverse(l);
+                uint32_t w[kPer / 2];
+                if (FULL || e < c.d) {
 #pragma unroll
                     for (int i = 0; i < kPer / 2; ++i) {
-                        w[i] = bf16_pair(x[2 * i] * by, x[2 * i + 1] * by);
-                        if (FULL || e < c.d) top_out = max(max(top_out, w[i] & 0x7FFF0000u), w[i] << 16 & 0x7FFFFFFFu);
+                        w[i] = bf16_pair(y[2 * i] * by, y[2 * i + 1] * by);
+                        top_out = top_of(w[i], top_out);
                     }
                     uint16_t* to = a.out + (int64_t)(from + q2) * a.out_row + (int64_t)h2 * a.out_head + e;
-                    if (FULL || e < c.d) {
-                        if constexpr (kPer == 8) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
-                        else *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
-                    }
-                    if (e == 0)
-                        a.lse[(int64_t)h2 * c.tokens + from + q2] =
-                            all == 0.0f ? -kInf : (use * scale2 + __builtin_amdgcn_logf(all)) * kLn2;
-                } else {
-                    const int64_t slot = 2 * (int64_t)worker + (step0 == 0 ? 1 : 0);
-                    float* to = a.partial + (slot * kRows + n) * DT + e;
-#pragma unroll
-                    for (int i = 0; i < kPer; i += 4) *reinterpret_cast<cf32x4*>(to + i) = cf32x4{x[i], x[i + 1], x[i + 2], x[i + 3]};
-                    if (e == 0) a.tops[slot * kRows + n] = make_float2(best == -kInf ? -kInf : best * scale2, all);
+                    if constexpr (kPer == 8) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+                    else *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
                 }
+                if (e == 0)
+                    a.lse[(int64_t)h2 * c.tokens + from + q2] =
+                        l == 0.0f ? -kInf : (base * scale2 + __builtin_amdgcn_logf(l)) * kLn2;
+            } else {
+                const int64_t slot = 2 * (int64_t)worker + (step0 == 0 ? 1 : 0);
+                float* to = a.partial + (slot * 16 + n) * DT + e;
+#pragma unroll
+                for (int i = 0; i < kPer; i += 4) *reinterpret_cast<af32x4*>(to + i) = af32x4{y[i], y[i + 1], y[i + 2], y[i + 3]};
+                if (e == 0) a.tops[slot * 16 + n] = make_float2(best == -kInf ? -kInf : best * scale2, l);
             }
         }
         if (threadIdx.x == 0 && step0 == 0 && take < steps)
-            a.joins[worker] = make_int4(b, head, u, (int)((at + steps - 1) / share) - worker + 1);
-        __syncthreads();
-
+            joins[worker] = Join{b, head, 0, (int)((at + steps - 1) / share) - worker + 1, 2 * worker + 1, 2 * worker + 2, 2, 0};
         at += take;
         if (at >= end) break;
+        __syncthreads();                                   // what is in LDS has been read
         step0 = 0;
-        if (++u == units_of(a, s)) {
-            u = 0;
-            if (++head == c.heads) {
-                head = 0;
-                do s = sequence(c, ++b);
-                while (s.queries == 0);
-            }
+        if (++head == c.heads) {
+            head = 0;
+            do {
+                s = sequence(c, ++b);
+                steps = __builtin_amdgcn_readfirstlane(share_steps(a, s));
+            } while (steps == 0);
         }
-        steps = unit_steps(a, s, u);
     }
-    if (a.absmax) block_max_to_global(top_out, a.absmax);
+    return top_out;
 }
 
-// out and lse of one row of a unit whose steps several workgroups shared: the first's last
-// piece and the following ones' first, in order.
-template <int DT>
-__global__ void __launch_bounds__(256) attention_cached_join_kernel(const CachedAttentionArgs a)
+// 128 rows of one head's sequence of more: attention.hip's forward, whose tiles of keys and
+// values are here made of codes.  Each wave loads 16 of a tile's 64 rows a step ahead and
+// writes them into LDS as bf16.  Where the tiles are few, up to two workgroups per CU share
+// a tile's keys, and the parts are joined.
+template <int DT, bool FULL>
+__device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, int block, uint8_t* lds, int64_t (*sums)[2], int64_t* found)
 {
-    __shared__ float part[256][kRows / 2 + 1];
+    constexpr int kTile = kKeys * DT * 2, kCh = DT / 8, kCodes = DT / 16, kLoads = DT / 64;
     const CacheArgs& c = a.c;
-    const int worker = blockIdx.x, n = blockIdx.y;
-    const int4 job = a.joins[worker];
-    if (job.w <= 1) return;
-    const Sequence s = sequence(c, job.x);
-    const int row = kRows * job.z + n;
-    if (row >= s.queries * a.group) return;
-    constexpr int kPer = 8, kLanes = DT / kPer, kGroups = 256 / kLanes;
-    const int k = threadIdx.x / kLanes, e = threadIdx.x % kLanes * kPer;
-    auto slot = [&](int i) __attribute__((always_inline)) { return (2 * (int64_t)(worker + i) + (i == 0)) * kRows + n; };
-    float m = -kInf, l = 0.0f;
-    for (int i = threadIdx.x & 63; i < job.w; i += 64) m = fmaxf(m, a.tops[slot(i)].x);
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-    const float use = m == -kInf ? 0.0f : m;
-    for (int i = threadIdx.x & 63; i < job.w; i += 64) {
-        const float2 x = a.tops[slot(i)];
-        l = fmaf(x.y, __builtin_amdgcn_exp2f(x.x - use), l);
+    const int lane = threadIdx.x & 63, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+
+    // the tile: every thread counts some sequences', in order
+    const int per = (c.batch + kThreads - 1) / kThreads, b0 = threadIdx.x * per, b1 = min(b0 + per, c.batch);
+    int64_t mine = 0, mine_steps = 0;
+    for (int b = b0; b < b1; ++b) {
+        const Sequence s = sequence(c, b);
+        const int n = row_tiles(a, s);
+        mine += n;
+        mine_steps += (int64_t)n * ((s.held + kKeys - 1) / kKeys);
     }
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) l += __shfl_xor(l, off, 64);
-    float t[kPer] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 4
-    for (int i = k; i < job.w; i += kGroups) {
-        const float by = __builtin_amdgcn_exp2f(a.tops[slot(i)].x - use);
-        const float4* p = reinterpret_cast<const float4*>(a.partial + slot(i) * DT + e);
-        const float4 u = p[0], v = p[1];
-        const float w[kPer] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) t[j] = fmaf(w[j], by, t[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) part[threadIdx.x][j] = t[j];
-    __syncthreads();
-    uint32_t top = 0;
-    if (k == 0 && e < c.d) {
-        for (int i = 1; i < kGroups; ++i)
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) t[j] += part[i * kLanes + threadIdx.x][j];
-        const float by = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-        const int qi = row / a.group, hq = job.y * a.group + row - qi * a.group;
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            w[j] = bf16_pair(t[2 * j] * by, t[2 * j + 1] * by);
-            top = max(max(top, w[j] & 0x7FFF0000u), w[j] << 16 & 0x7FFFFFFFu);
+    const Sums all = block_sums(mine, mine_steps, sums);
+    Join* const joins = reinterpret_cast<Join*>(a.joins) + a.workers;
+    if (threadIdx.x == 0 && block < a.workers) joins[block].count = 0;
+    if (all.total == 0) return 0;
+    const int64_t units = all.total * c.heads;
+    const int splits = (int)max(min((int64_t)a.workers / units, all.total_y / all.total / kLeastSplit), (int64_t)1);
+    const int wide = c.heads * splits;
+    if (block >= all.total * wide) return 0;
+    // blocks are dealt round-robin to the 8 XCDs: each gets whole heads where they divide so
+    const int unit = wide % 8 == 0 ? block % 8 * (wide / 8) + block / 8 % (wide / 8) : block % wide;
+    const int split = unit % splits, head = unit / splits;
+    const int64_t t = all.total - 1 - block / wide;        // a sequence's last (longest) tiles first
+    if (all.before <= t && t < all.before + mine) {
+        int64_t left = t - all.before;
+        int b = b0;
+        for (;; ++b) {
+            const int n = row_tiles(a, sequence(c, b));
+            if (left < n) break;
+            left -= n;
         }
-        *reinterpret_cast<uint4*>(a.out + (int64_t)(s.from + qi) * a.out_row + (int64_t)hq * a.out_head + e) =
-            make_uint4(w[0], w[1], w[2], w[3]);
-        if (e == 0) a.lse[(int64_t)hq * c.tokens + s.from + qi] = l == 0.0f ? -kInf : (use + __builtin_amdgcn_logf(l)) * kLn2;
+        found[0] = b;
+        found[1] = left;
+    }
+    __syncthreads();
+    const int b = __builtin_amdgcn_readfirstlane((int)found[0]);
+    const int first = __builtin_amdgcn_readfirstlane((int)found[1]) * kOwn;
+    const Sequence s = sequence(c, b);
+    const int from = __builtin_amdgcn_readfirstlane(s.from), queries = __builtin_amdgcn_readfirstlane(s.queries);
+    const int held = __builtin_amdgcn_readfirstlane(s.held);
+    const int rows = queries * a.group, r_wave = first + wave * 32, ri = r_wave + (lane & 31);
+    const int q_wave = r_wave / a.group, q_last = (r_wave + 31) / a.group;
+    const int qi = ri / a.group, hq = head * a.group + ri - qi * a.group;
+    const bool valid = ri < rows;
+    const int shift = held - queries;
+    // keys seen: by this lane's query, by the wave's first and last, by the workgroup's last
+    const int see = a.causal ? min(held, qi + shift + 1) : held;
+    const int see_first = a.causal ? min(held, q_wave + shift + 1) : held;
+    const int see_last = r_wave >= rows ? 0 : a.causal ? min(held, q_last + shift + 1) : held;
+    const int end = a.causal ? min(held, min((first + kOwn - 1) / a.group + 1, queries) + shift) : held;
+    const int steps = end > 0 ? (end + kKeys - 1) / kKeys : 0;
+    const int s_begin = (int)((int64_t)steps * split / splits), s_end = (int)((int64_t)steps * (split + 1) / splits);
+
+    Frag q[DT / 16];
+    load_own<DT>(q, a.q + (int64_t)(from + qi) * a.q_row + (int64_t)hq * a.q_head, c.d, valid);
+
+    const float c2 = a.scale * kLog2e;
+    const float far = fminf(8.0f / c2, 1e38f);
+    af32x16 o[DT / 32];
+#pragma unroll
+    for (int db = 0; db < DT / 32; ++db) o[db] = af32x16{0};
+    float m = -kInf, mc = 0.0f, l = 0.0f;
+    Tile<DT> tile;
+    tile.init(lds0);
+
+    // 16-code chunk i of a lane: row (lane + 64 i) / kCodes of the wave's 16, chunk % kCodes; in LDS two chunks of bf16
+    uint32_t off[kLoads][2], put[kLoads][2];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int r = (lane + 64 * i) / kCodes, ch = (lane + 64 * i) % kCodes, row = 16 * wave + r;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int d = FULL ? DT : c.d, e = 16 * ch + 8 * j;
+            off[i][j] = FULL || e < d ? (uint32_t)(r * d + e) : kNowhere;
+            put[i][j] = lds0 + row * (DT * 2) + (((2 * ch + j) ^ spread<kCh>(row)) * 16);
+        }
+    }
+    au32x4 ck[kLoads], cv[kLoads];
+    Keys16 x;
+    Pages pages;
+    auto fetch = [&](int key) __attribute__((always_inline)) {
+        x = pages.at(key);
+        const auto k = rows_of(c.k, x, FULL ? DT : c.d), v = rows_of(c.v, x, FULL ? DT : c.d);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            if constexpr (FULL) {
+                ck[i] = __builtin_amdgcn_raw_buffer_load_b128(k, off[i][0], 0, 0);
+                cv[i] = __builtin_amdgcn_raw_buffer_load_b128(v, off[i][0], 0, 0);
+            } else {
+                const au32x2 k0 = __builtin_amdgcn_raw_buffer_load_b64(k, off[i][0], 0, 0);
+                const au32x2 k1 = __builtin_amdgcn_raw_buffer_load_b64(k, off[i][1], 0, 0);
+                const au32x2 v0 = __builtin_amdgcn_raw_buffer_load_b64(v, off[i][0], 0, 0);
+                const au32x2 v1 = __builtin_amdgcn_raw_buffer_load_b64(v, off[i][1], 0, 0);
+                ck[i] = au32x4{k0[0], k0[1], k1[0], k1[1]};
+                cv[i] = au32x4{v0[0], v0[1], v1[0], v1[1]};
+            }
+        }
+    };
+    auto values = [&](uint32_t a0, uint32_t a1, float by) __attribute__((always_inline)) {
+        return au32x4{values2<false>(a0, by), values2<true>(a0, by), values2<false>(a1, by), values2<true>(a1, by)};
+    };
+    auto step = [&](auto stage, int st) __attribute__((always_inline)) {
+        constexpr int at = stage.value * 2 * kTile;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                lds_u32x4* to = (lds_u32x4*)(uintptr_t)put[i][j];
+                to[at / 16] = values(ck[i][2 * j], ck[i][2 * j + 1], x.k_scale);
+                to[(at + kTile) / 16] = values(cv[i][2 * j], cv[i][2 * j + 1], x.v_scale);
+            }
+        if (st + 1 < s_end) fetch((st + 1) * kKeys + 16 * wave);
+        // tile st is written by all; the other stage was last read in step st - 1, by the waves that are here
+        __syncthreads();
+        const int j0 = st * kKeys;
+        if (j0 < see_last) attend_tile<DT, at>(tile, q, see - j0, j0 + kKeys > see_first, c2, far, o, m, mc, l);
+    };
+    if (s_begin < s_end) {
+        pages.init(c, b, head, held, s_begin * kKeys + 16 * wave);
+        fetch(s_begin * kKeys + 16 * wave);
+    }
+    for (int st = s_begin; st < s_end; st += 2) {
+        step(std::integral_constant<int, 0>{}, st);
+        if (st + 1 < s_end) step(std::integral_constant<int, 1>{}, st + 1);
+    }
+
+    l += partner(l);
+    if (splits > 1) {
+        const int slot0 = 2 * a.workers + (int)((t * c.heads + head) * splits) * (kOwn / 16);
+        const int64_t row = (int64_t)(slot0 + split * (kOwn / 16)) * 16 + wave * 32 + (lane & 31);
+        store_partial<DT>(o, a.partial + row * DT, DT, valid);
+        if (valid && h == 0) a.tops[row] = make_float2(m == -kInf ? -kInf : mc, l);
+        if (split == 0 && threadIdx.x == 0)
+            joins[block] = Join{b, head, first, splits, slot0, slot0 + kOwn / 16, kOwn / 16, 0};
+        return 0;
+    }
+    const uint32_t top = store_own<DT>(o, inverse(l), a.out + (int64_t)(from + qi) * a.out_row + (int64_t)hq * a.out_head, c.d, valid);
+    if (valid && h == 0)
+        a.lse[(int64_t)hq * c.tokens + from + qi] = l == 0.0f ? -kInf : (mc + __builtin_amdgcn_logf(l)) * kLn2;
+    return top;
+}
+
+}  // namespace
+
+// KINDS 1: sequences of few rows alone; 2: of more alone; 3: both, their workgroups in turn, 8
+// by 8 (workgroups are dealt round-robin to the XCDs).
+template <int DT, bool FULL, int KINDS>
+__global__ void __launch_bounds__(kThreads, 2) attention_cached_kernel(const CachedAttentionArgs a)
+{
+    constexpr int kBytes = KINDS == 1 ? share_lds<DT>() : std::max(share_lds<DT>(), tile_lds<DT>());
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kBytes];
+    __shared__ int64_t sums[kWaves][2], found[2];
+    const int i = blockIdx.x, pair = i >> 4;
+    bool share = KINDS == 1;
+    int block = i;
+    if (KINDS == 3) {
+        share = i < 2 * a.workers && !(i & 8);
+        block = i >= 2 * a.workers ? i - a.workers : pair * 8 + (i & 7);
+    }
+    uint32_t top;
+    if (KINDS != 2 && share) top = attend_share<DT, FULL>(a, block, lds, sums, found);
+    else top = attend_rows<DT, FULL>(a, block, lds, sums, found);
+    if (a.absmax) block_max_to_global(top, a.absmax);
+}
+
+// out and lse of rows whose keys several workgroups shared, their parts in order: of few rows a
+// workgroup takes one, its threads side by side over the parts, which may be hundreds; of
+// tiles 16 rows.
+template <int DT>
+__global__ void __launch_bounds__(256) attention_cached_join_kernel(const CachedAttentionArgs a, int share_rows)
+{
+    constexpr int kPer = 8, kLanes = DT / kPer, kGroups = 256 / kLanes;
+    __shared__ float part[256][kPer + 1];
+    const CacheArgs& c = a.c;
+    const int i = blockIdx.x, shares = a.workers * share_rows;
+    const bool share = i < shares;
+    const int entry = share ? i / share_rows : a.workers + (i - shares) / (kOwn / 16);
+    const int group16 = share ? 0 : (i - shares) % (kOwn / 16);
+    const Join job = reinterpret_cast<const Join*>(a.joins)[entry];
+    if (job.count <= 1) return;
+    const Sequence s = sequence(c, job.b);
+    const int k = threadIdx.x / kLanes, e = threadIdx.x % kLanes * kPer;
+    // a row's parts go to kGroups groups of threads, or to one
+    const int rows = s.queries * a.group;
+    const int passes = share ? 1 : (16 + kGroups - 1) / kGroups;
+    uint32_t top = 0;
+    for (int pass = 0; pass < passes; ++pass) {
+        const int n = share ? i % share_rows : pass * kGroups + k, row = job.row + group16 * 16 + n;
+        const bool valid = row < rows && n < 16;
+        if (share && !valid) return;
+        auto slot = [&](int p) __attribute__((always_inline)) {
+            return (int64_t)((p == 0 ? job.first : job.second + (p - 1) * job.step) + group16) * 16 + n;
+        };
+        float m = -kInf, l = 0.0f, t[kPer] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (share) {
+            for (int p = threadIdx.x & 63; p < job.count; p += 64) m = fmaxf(m, a.tops[slot(p)].x);
+#pragma unroll
+            for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+        } else if (valid) {
+            for (int p = 0; p < job.count; ++p) m = fmaxf(m, a.tops[slot(p)].x);
+        }
+        const float use = m == -kInf ? 0.0f : m;
+        if (share) {
+            for (int p = threadIdx.x & 63; p < job.count; p += 64) {
+                const float2 y = a.tops[slot(p)];
+                l = fmaf(y.y, __builtin_amdgcn_exp2f(y.x - use), l);
+            }
+#pragma unroll
+            for (int off = 32; off >= 1; off >>= 1) l += __shfl_xor(l, off, 64);
+        }
+        if (valid)
+#pragma unroll 4
+            for (int p = share ? k : 0; p < job.count; p += share ? kGroups : 1) {
+                const float2 y = a.tops[slot(p)];
+                const float by = __builtin_amdgcn_exp2f(y.x - use);
+                if (!share) l = fmaf(y.y, by, l);
+                const float4* from = reinterpret_cast<const float4*>(a.partial + slot(p) * DT + e);
+                const float4 u = from[0], v = from[1];
+                const float w[kPer] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) t[j] = fmaf(w[j], by, t[j]);
+            }
+        if (share) {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) part[threadIdx.x][j] = t[j];
+            __syncthreads();
+            if (k == 0)
+                for (int g = 1; g < kGroups; ++g)
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j) t[j] += part[g * kLanes + threadIdx.x][j];
+        }
+        if (valid && (!share || k == 0) && e < c.d) {
+            const float by = inverse(l);
+            const int qi = row / a.group, hq = job.head * a.group + row - qi * a.group;
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                w[j] = bf16_pair(t[2 * j] * by, t[2 * j + 1] * by);
+                top = top_of(w[j], top);
+            }
+            *reinterpret_cast<uint4*>(a.out + (int64_t)(s.from + qi) * a.out_row + (int64_t)hq * a.out_head + e) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+            if (e == 0) a.lse[(int64_t)hq * c.tokens + s.from + qi] = l == 0.0f ? -kInf : (use + __builtin_amdgcn_logf(l)) * kLn2;
+        }
     }
     if (a.absmax) block_max_to_global(top, a.absmax);
 }
 
-// Two workgroups per CU share the work.
-static int worker_count() { return 2 * device_cu_count(); }
+namespace {
 
-int64_t attention_cached_workspace(int64_t, int, int, int d, int, int, int)
+// What a call's sequences can be, as far as the host knows.
+struct Plan {
+    int kinds, workers;
+    int64_t tiles;         // of rows, at most
+};
+
+Plan plan(int64_t tokens, int group, int batch, bool bounds)
 {
-    const int64_t workers = worker_count();
-    return workers * (16 + 2 * kRows * (8 + 4 * (d <= 64 ? 64 : 128)));
+    Plan p{};
+    p.workers = (2 * device_cu_count() + 7) / 8 * 8;       // two per CU, whole rounds of the XCDs
+    if (!bounds) p.kinds = tokens / batch * group <= kFew ? 1 : 2;
+    else p.kinds = tokens * group <= kFew ? 1 : 3;
+    if (p.kinds & 2) p.tiles = bounds ? tokens * group / kOwn + std::min<int64_t>(batch, tokens * group / (kFew + 1))
+                                      : batch * ((tokens / batch * group + kOwn - 1) / kOwn);
+    return p;
+}
+
+// Workgroups' tiles of rows: all, or as many as can share them.
+int64_t row_blocks(const Plan& p, int heads) { return std::max<int64_t>(p.tiles * heads, p.workers); }
+
+// Slots of 16 rows that hold parts: two to a share; of tiles, split over `workers` parts at most.
+int64_t slots(const Plan& p) { return p.workers * (2 + (p.kinds & 2 ? kOwn / 16 : 0)); }
+
+template <int DT, bool FULL>
+void (*kernel_of(int kinds))(CachedAttentionArgs)
+{
+    return kinds == 1 ? attention_cached_kernel<DT, FULL, 1> : kinds == 2 ? attention_cached_kernel<DT, FULL, 2>
+                                                                           : attention_cached_kernel<DT, FULL, 3>;
+}
+
+}  // namespace
+
+bool attention_cached_grid_ok(int64_t tokens, int group, int heads, int batch)
+{
+    return tokens * group / kOwn + batch <= 0xFFFFFFFFll / kThreads / 2 / heads;
+}
+
+int64_t attention_cached_workspace(int64_t tokens, int group, int d, int batch, bool bounds)
+{
+    const Plan p = plan(tokens, group, batch, bounds);
+    return 2 * p.workers * (int64_t)sizeof(Join) + slots(p) * 16 * (8 + 4 * (d <= 64 ? 64 : 128));
 }
 
 hipError_t launch_attention_cached(const CachedAttentionArgs& args, void* workspace, hipStream_t stream)
 {
     CachedAttentionArgs a = args;
-    a.workers = worker_count();
-    a.joins = static_cast<int4*>(workspace);
-    a.tops = reinterpret_cast<float2*>(a.joins + a.workers);
-    a.partial = reinterpret_cast<float*>(a.tops + 2 * a.workers * kRows);
-    void (*kernel)(CachedAttentionArgs) =
-        a.c.d == 64 ? attention_cached_kernel<64, true> : a.c.d == 128 ? attention_cached_kernel<128, true>
-        : a.c.d < 64 ? attention_cached_kernel<64, false> : attention_cached_kernel<128, false>;
-    const hipError_t e = launch(kernel, dim3(a.workers), dim3(kThreads), stream, a);
+    const Plan p = plan(a.c.tokens, a.group, a.c.batch, a.c.cu != nullptr);
+    a.workers = p.workers;
+    a.joins = workspace;
+    a.tops = reinterpret_cast<float2*>(static_cast<Join*>(workspace) + 2 * p.workers);
+    a.partial = reinterpret_cast<float*>(a.tops + slots(p) * 16);
+    const int d = a.c.d;
+    const int64_t blocks = (p.kinds & 1 ? p.workers : 0) + (p.kinds & 2 ? row_blocks(p, a.c.heads) : 0);
+    hipError_t e = launch(d == 64 ? kernel_of<64, true>(p.kinds) : d == 128 ? kernel_of<128, true>(p.kinds)
+                          : d < 64 ? kernel_of<64, false>(p.kinds) : kernel_of<128, false>(p.kinds),
+                          dim3((unsigned)blocks), dim3(kThreads), stream, a);
     if (e != hipSuccess) return e;
-    const unsigned rows = (unsigned)std::min<int64_t>(kRows, a.c.tokens * a.group);
-    return launch(a.c.d <= 64 ? attention_cached_join_kernel<64> : attention_cached_join_kernel<128>, dim3(a.workers, rows), dim3(256),
-                  stream, a);
+    // without bounds the tiles are known: more than half as many as workers are not split
+    if (p.kinds == 2 && p.tiles * a.c.heads > p.workers / 2) return e;
+    const int rows = p.kinds & 1 ? (int)std::min<int64_t>(kFew, a.c.tokens * a.group) : 0;
+    const int join_blocks = p.workers * (rows + (p.kinds & 2 ? kOwn / 16 : 0));
+    return launch(d <= 64 ? attention_cached_join_kernel<64> : attention_cached_join_kernel<128>, dim3(join_blocks), dim3(256), stream,
+                  a, rows);
 }
 
 }  // namespace fp8k

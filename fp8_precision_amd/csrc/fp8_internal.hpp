@@ -188,11 +188,12 @@ struct CachedAttentionArgs {
     uint32_t* absmax;                     // or null
     float* partial;                       // sums of split work, their maxima and totals, and what to join
     float2* tops;
-    int4* joins;
-    int hq, group, causal, workers;
+    void* joins;
+    int group, causal, workers;           // group: query heads to a key head
     float scale;
 };
-int64_t attention_cached_workspace(int64_t tokens, int hq, int heads, int d, int batch, int blocks, int shift);
+int64_t attention_cached_workspace(int64_t tokens, int group, int d, int batch, bool bounds);
+bool attention_cached_grid_ok(int64_t tokens, int group, int heads, int batch);
 hipError_t launch_attention_cached(const CachedAttentionArgs& args, void* workspace, hipStream_t stream);
 
 // Cross entropy of a linear head (loss.hip): x [T, D], w [V, D].
