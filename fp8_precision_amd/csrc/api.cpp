@@ -999,8 +999,9 @@ static fp8_status cached_shape(const char* call, const fp8_kv_cache* c, int64_t 
     if (heads_q < 1 || heads_q % c->heads) return fail(FP8_ERR_INVALID, std::string(call) + ": heads_q must be a multiple of heads");
     if (heads_q > 65536 || c->tokens * heads_q >= ((int64_t)1 << 31) - 256)
         return fail(FP8_ERR_UNSUPPORTED, std::string(call) + ": more than 2^16 heads or 2^31 rows");
-    if (!fp8k::attention_cached_grid_ok(c->tokens, (int)(heads_q / c->heads), (int)c->heads, (int)c->batch))
-        return fail(FP8_ERR_UNSUPPORTED, std::string(call) + ": too many rows for one launch");
+    if (!fp8k::attention_cached_grid_ok(c->tokens, (int)(heads_q / c->heads), (int)c->heads, (int)c->batch,
+                                        (int)c->blocks, shift))
+        return fail(FP8_ERR_UNSUPPORTED, std::string(call) + ": too many rows for one launch, or 2^37 keys of all heads");
     return FP8_OK;
 }
 

@@ -33,7 +33,9 @@ constexpr int kWaves = 4;
 constexpr int kFew = 16;                   // rows of a sequence that is read in shares
 constexpr int kOwn = 128;                  // rows of a tile: 32 per wave
 constexpr int kLeastSteps = kWaves;        // of a share
+constexpr int kPiece = 4;                  // what a head of a sequence costs besides its steps, in steps
 constexpr int kLeastSplit = 4;             // steps of a part of a tile's keys
+constexpr int kJoinThreads = 512;
 constexpr uint32_t kNowhere = 0x7FFFFFF0u; // an offset outside every buffer
 
 __device__ __forceinline__ af32x4 mma16(const Frag& a, const Frag& b, const af32x4& c)
@@ -41,17 +43,22 @@ __device__ __forceinline__ af32x4 mma16(const Frag& a, const Frag& b, const af32
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.b, b.b, c, 0, 0, 0);
 }
 
-// Of the four lanes that share lane % 16.
+// Of the four lanes that share lane % 16: a register swapped with itself, by rows of 16 lanes and
+// by halves, gives both sides in every lane.
 __device__ __forceinline__ float max4(float v)
 {
-    v = fmaxf(v, __shfl_xor(v, 16, 64));
-    return fmaxf(v, __shfl_xor(v, 32, 64));
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    const auto t = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(t[0]), __uint_as_float(t[1]));
 }
 
 __device__ __forceinline__ float sum4(float v)
 {
-    v += __shfl_xor(v, 16, 64);
-    return v + __shfl_xor(v, 32, 64);
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    const auto t = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(t[0]) + __uint_as_float(t[1]);
 }
 
 // A sequence's queries and keys.
@@ -75,10 +82,11 @@ __device__ __forceinline__ Sequence sequence(const CacheArgs& a, int b)
 
 __device__ __forceinline__ bool few(const CachedAttentionArgs& a, const Sequence& s) { return s.queries * a.group <= kFew; }
 
-// Steps of one head of a sequence of few rows: one at least, for the rows that see nothing.
+// Steps of one head of a sequence of few rows: kPiece, in which nothing is done, and its keys';
+// one of these at least, for the rows that see nothing.
 __device__ __forceinline__ int share_steps(const CachedAttentionArgs& a, const Sequence& s)
 {
-    return s.queries == 0 || !few(a, s) ? 0 : max(1, (s.held + kKeys - 1) / kKeys);
+    return s.queries == 0 || !few(a, s) ? 0 : kPiece + max(1, (s.held + kKeys - 1) / kKeys);
 }
 
 __device__ __forceinline__ int row_tiles(const CachedAttentionArgs& a, const Sequence& s)
@@ -88,22 +96,26 @@ __device__ __forceinline__ int row_tiles(const CachedAttentionArgs& a, const Seq
 
 // The sums of every thread's (x, y): all threads' in total, the x of those before it in before.
 struct Sums {
-    int64_t before, total, total_y;
+    int before, total;
+    int64_t total_y;
 };
 
-__device__ __forceinline__ Sums block_sums(int64_t x, int64_t y, int64_t (*lds)[2])
+__device__ __forceinline__ Sums block_sums(int x, int64_t y, int (*lds)[4])
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int64_t upto = x;
+    int upto = x;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-        const int64_t o = __shfl_up(upto, off, 64), p = __shfl_xor(y, off, 64);
+        const int o = __shfl_up(upto, off, 64);
         if (lane >= off) upto += o;
-        y += p;
     }
+    if (y != 0 || __any(y != 0))
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) y += __shfl_xor(y, off, 64);
     if (lane == 63) {
         lds[wave][0] = upto;
-        lds[wave][1] = y;
+        lds[wave][2] = (int)y;
+        lds[wave][3] = (int)(y >> 32);
     }
     __syncthreads();
     Sums s{upto - x, 0, 0};
@@ -111,8 +123,9 @@ __device__ __forceinline__ Sums block_sums(int64_t x, int64_t y, int64_t (*lds)[
     for (int w = 0; w < kWaves; ++w) {
         if (w < wave) s.before += lds[w][0];
         s.total += lds[w][0];
-        s.total_y += lds[w][1];
+        s.total_y += (int64_t)lds[w][3] << 32 | (uint32_t)lds[w][2];
     }
+    s.total = __builtin_amdgcn_readfirstlane(s.total);
     return s;
 }
 
@@ -162,11 +175,10 @@ struct Pages {
 #pragma unroll
         for (int w = 0; w < 2; ++w) scale[w] = scales(page[w]);
     }
-    // the keys key .. key + 15 (key: the same in all lanes, a multiple of 16, never falling)
-    __device__ __forceinline__ Keys16 at(int key)
+    // the window holds the blocks of the 64 keys from key on (a multiple of 64, as the first was; never falling)
+    __device__ __forceinline__ void advance(int key)
     {
-        const int block = key >> shift;
-        while (block - first >= 64) {
+        while ((key >> shift) - first >= 64) {
             first += 64;
             page[0] = page[1];
             page[1] = page[2];
@@ -174,11 +186,16 @@ struct Pages {
             scale[1] = scales(page[1]);
             page[2] = entry(2);
         }
-        const int p = __builtin_amdgcn_readlane(page[0], block - first), s = __builtin_amdgcn_readlane(scale[0], block - first);
-        const bool none = key >= held || p < 0 || p >= pages;
+    }
+    // the keys key .. key + 15 within the window (key: the same in all lanes, a multiple of 16), below `limit`
+    __device__ __forceinline__ Keys16 at(int key, int limit) const
+    {
+        const int block = (key >> shift) - first;
+        const int p = __builtin_amdgcn_readlane(page[0], block), s = __builtin_amdgcn_readlane(scale[0], block);
+        const bool none = key >= limit || p < 0 || p >= pages;
         Keys16 x;
-        x.byte = none ? 0 : ((((int64_t)p * heads + head) << shift) + (key & ((1 << shift) - 1))) * d;
-        x.rows = none ? 0 : min(held - key, 16);
+        x.byte = ((((int64_t)(none ? 0 : p) * heads + head) << shift) + (key & ((1 << shift) - 1))) * d;
+        x.rows = none ? 0 : min(limit - key, 16);
         x.k_scale = cache_scale((uint8_t)s);
         x.v_scale = cache_scale((uint8_t)(s >> 16));
         return x;
@@ -218,7 +235,7 @@ __device__ __forceinline__ uint32_t top_of(uint32_t w, uint32_t top)
 // into the registers of the last one's as soon as its scores are there, the values after
 // its output.
 template <int DT, bool FULL>
-__device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, int worker, uint8_t* lds, int64_t (*sums)[2], int64_t* found)
+__device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, int worker, uint8_t* lds, int (*sums)[4], int* found)
 {
     constexpr int kPer = DT / 16;          // values' elements of a lane, and the product's tiles
     constexpr int kRow = DT + 4;
@@ -232,20 +249,19 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
 
     // the share: every thread counts some sequences' steps, in order
     const int per = (c.batch + kThreads - 1) / kThreads, b0 = threadIdx.x * per, b1 = min(b0 + per, c.batch);
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += (int64_t)share_steps(a, sequence(c, b)) * c.heads;
+    int mine = 0;
+    for (int b = b0; b < b1; ++b) mine += share_steps(a, sequence(c, b)) * c.heads;
     const Sums all = block_sums(mine, 0, sums);
-    const int64_t share = max((all.total + a.workers - 1) / a.workers, (int64_t)kLeastSteps);
-    int64_t at = worker * share;
-    const int64_t end = min(at + share, all.total);
+    const int share = max((all.total + a.workers - 1) / a.workers, kLeastSteps);
     Join* const joins = reinterpret_cast<Join*>(a.joins);
     if (threadIdx.x == 0) joins[worker].count = 0;
-    if (at >= end) return 0;
+    if (worker > (all.total - 1) / share || all.total == 0) return 0;
+    int at = worker * share;
+    const int end = min(at + share, all.total);
     if (all.before <= at && at < all.before + mine) {
-        int64_t left = at - all.before;
-        int b = b0;
+        int left = at - all.before, b = b0;
         for (;; ++b) {
-            const int64_t n = (int64_t)share_steps(a, sequence(c, b)) * c.heads;
+            const int n = share_steps(a, sequence(c, b)) * c.heads;
             if (left < n) break;
             left -= n;
         }
@@ -253,18 +269,21 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
         found[1] = left;
     }
     __syncthreads();
-    int b = __builtin_amdgcn_readfirstlane((int)found[0]);
+    int b = __builtin_amdgcn_readfirstlane(found[0]);
     Sequence s = sequence(c, b);
     int steps = __builtin_amdgcn_readfirstlane(share_steps(a, s));
-    int head = __builtin_amdgcn_readfirstlane((int)(found[1] / steps));
-    int step0 = __builtin_amdgcn_readfirstlane((int)(found[1] - (int64_t)head * steps));
+    int head = __builtin_amdgcn_readfirstlane(found[1] / steps);
+    int done = __builtin_amdgcn_readfirstlane(found[1] - head * steps);      // of the head's steps, by other shares
     const float scale2 = a.scale * kLog2e;
     const float far = fminf(8.0f / scale2, 1e38f);         // scores may pass the running maximum by 2^8 before a rescale
 
     while (true) {
         const int from = __builtin_amdgcn_readfirstlane(s.from), queries = __builtin_amdgcn_readfirstlane(s.queries);
         const int held = __builtin_amdgcn_readfirstlane(s.held);
-        const int take = __builtin_amdgcn_readfirstlane((int)min((int64_t)(steps - step0), end - at));
+        const int upto = __builtin_amdgcn_readfirstlane(min(steps, done + end - at));
+        // the piece: the keys' steps step0 .. last - 1 of all
+        const int step0 = max(done - kPiece, 0), last = max(upto - kPiece, 0), all_steps = steps - kPiece;
+        if (last > step0) {
         const int rows = queries * a.group, qi = m / a.group, hq = head * a.group + m - qi * a.group;
         const int shift = held - queries;
         const int see = a.causal ? min(held, qi + shift + 1) : held, see_first = a.causal ? min(held, shift + 1) : held;
@@ -274,44 +293,49 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
 #pragma unroll
         for (int i = 0; i < DT / 32; ++i) {
             q[i].u = au32x4{0, 0, 0, 0};
-            const int e = DT / 4 * g + 8 * i;
+            const int e = 64 * (i / 2) + 16 * g + 8 * (i % 2);
             if (m < rows && (FULL || e < c.d))
                 q[i].u = *reinterpret_cast<const au32x4*>(a.q + (int64_t)(from + qi) * a.q_row + (int64_t)hq * a.q_head + e);
         }
+        // waited for here: at its first use, in the loop, the wait would be one for every load in flight
+#pragma unroll
+        for (int i = 0; i < DT / 32; ++i) asm volatile("" : "+v"(q[i].u));
         af32x4 o[kPer];
 #pragma unroll
         for (int t = 0; t < kPer; ++t) o[t] = af32x4{0, 0, 0, 0};
         float top = -kInf, sum = 0.0f;
 
         // Codes of 64 keys, as loaded.  Of each block of 16 keys a lane has DT / 4 codes of key
-        // m (chunk g), and DT / 16 codes (chunk m) of each of the values 4 g + i.
+        // m (16 of each 64, chunk g), and DT / 16 codes (chunk m) of each of the values 4 g + i.
         uint32_t ck[4][DT / 16], cv[4][4][DT / 64];
         Keys16 x[4];
         float v_scale[4];
         Pages pages;
-        const int last = step0 + take;
+        const int limit = min(held, last * kKeys);
         auto load_k = [&](int key) __attribute__((always_inline)) {
+            pages.advance(key);
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                x[n] = pages.at(key + 16 * n);
+                x[n] = pages.at(key + 16 * n, limit);
                 const auto src = rows_of(c.k, x[n], FULL ? DT : c.d);
                 if constexpr (FULL) {
 #pragma unroll
                     for (int i = 0; i < DT / 64; ++i) {
-                        const au32x4 w = __builtin_amdgcn_raw_buffer_load_b128(src, m * DT + DT / 4 * g + 16 * i, 0, 0);
+                        const au32x4 w = __builtin_amdgcn_raw_buffer_load_b128(src, m * DT + 64 * i + 16 * g, 0, 0);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) ck[n][4 * i + j] = w[j];
                     }
                 } else {
 #pragma unroll
                     for (int i = 0; i < DT / 32; ++i) {
-                        const int e = DT / 4 * g + 8 * i;
+                        const int e = 64 * (i / 2) + 16 * g + 8 * (i % 2);
                         const au32x2 w = __builtin_amdgcn_raw_buffer_load_b64(src, e < c.d ? m * c.d + e : kNowhere, 0, 0);
                         ck[n][2 * i] = w[0];
                         ck[n][2 * i + 1] = w[1];
                     }
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
         };
         auto load_v = [&]() __attribute__((always_inline)) {
 #pragma unroll
@@ -331,6 +355,7 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
                     }
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
         };
 
         if (step0 + wave < last) {
@@ -340,7 +365,6 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
         }
         for (int t = step0 + wave; t < last; t += kWaves) {
             const int j0 = t * kKeys;
-            const bool more = t + kWaves < last;
             af32x4 p[4];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
@@ -356,7 +380,10 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
                     p[n] = mma16(k, q[i], p[n]);
                 }
             }
-            if (more) load_k(j0 + kWaves * kKeys);
+            // (past the last step from buffers of no rows: with loads that some path leaves out, the
+            // compiler would wait for the values together with the next keys)
+            __builtin_amdgcn_sched_barrier(0);
+            load_k(j0 + kWaves * kKeys);
             if (j0 + kKeys > see_first) {
 #pragma unroll
                 for (int n = 0; n < 4; ++n)
@@ -409,7 +436,8 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
                     }
                 }
             }
-            if (more) load_v();
+            __builtin_amdgcn_sched_barrier(0);
+            load_v();
         }
         sum = sum4(sum);
 
@@ -441,7 +469,7 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) y[i] = fmaf(s_out[(w * kFew + n) * kRow + e + i], by, y[i]);
             }
-            if (take == steps) {
+            if (step0 == 0 && last == all_steps) {
                 const float by = inverse(l);
                 uint32_t w[kPer / 2];
                 if (FULL || e < c.d) {
@@ -465,12 +493,13 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
                 if (e == 0) a.tops[slot * 16 + n] = make_float2(best == -kInf ? -kInf : best * scale2, l);
             }
         }
-        if (threadIdx.x == 0 && step0 == 0 && take < steps)
-            joins[worker] = Join{b, head, 0, (int)((at + steps - 1) / share) - worker + 1, 2 * worker + 1, 2 * worker + 2, 2, 0};
-        at += take;
+        if (threadIdx.x == 0 && step0 == 0 && last < all_steps)
+            joins[worker] = Join{b, head, 0, (at - done + steps - 1) / share - worker + 1, 2 * worker + 1, 2 * worker + 2, 2, 0};
+        }
+        at += upto - done;
         if (at >= end) break;
         __syncthreads();                                   // what is in LDS has been read
-        step0 = 0;
+        done = 0;
         if (++head == c.heads) {
             head = 0;
             do {
@@ -487,7 +516,7 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
 // writes them into LDS as bf16.  Where the tiles are few, up to two workgroups per CU share
 // a tile's keys, and the parts are joined.
 template <int DT, bool FULL>
-__device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, int block, uint8_t* lds, int64_t (*sums)[2], int64_t* found)
+__device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, int block, uint8_t* lds, int (*sums)[4], int* found)
 {
     constexpr int kTile = kKeys * DT * 2, kCh = DT / 8, kCodes = DT / 16, kLoads = DT / 64;
     const CacheArgs& c = a.c;
@@ -497,7 +526,8 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
 
     // the tile: every thread counts some sequences', in order
     const int per = (c.batch + kThreads - 1) / kThreads, b0 = threadIdx.x * per, b1 = min(b0 + per, c.batch);
-    int64_t mine = 0, mine_steps = 0;
+    int mine = 0;
+    int64_t mine_steps = 0;
     for (int b = b0; b < b1; ++b) {
         const Sequence s = sequence(c, b);
         const int n = row_tiles(a, s);
@@ -506,19 +536,18 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
     }
     const Sums all = block_sums(mine, mine_steps, sums);
     Join* const joins = reinterpret_cast<Join*>(a.joins) + a.workers;
-    if (threadIdx.x == 0 && block < a.workers) joins[block].count = 0;
+    if (threadIdx.x == 0 && block < a.workers / 2) joins[block].count = 0;   // (more tiles are not split)
     if (all.total == 0) return 0;
-    const int64_t units = all.total * c.heads;
-    const int splits = (int)max(min((int64_t)a.workers / units, all.total_y / all.total / kLeastSplit), (int64_t)1);
+    const int units = all.total * c.heads;
+    const int splits = (int)max(min((int64_t)(a.workers / units), all.total_y / all.total / kLeastSplit), (int64_t)1);
     const int wide = c.heads * splits;
-    if (block >= all.total * wide) return 0;
+    if (block >= (int64_t)all.total * wide) return 0;
     // blocks are dealt round-robin to the 8 XCDs: each gets whole heads where they divide so
     const int unit = wide % 8 == 0 ? block % 8 * (wide / 8) + block / 8 % (wide / 8) : block % wide;
     const int split = unit % splits, head = unit / splits;
-    const int64_t t = all.total - 1 - block / wide;        // a sequence's last (longest) tiles first
+    const int t = all.total - 1 - block / wide;            // a sequence's last (longest) tiles first
     if (all.before <= t && t < all.before + mine) {
-        int64_t left = t - all.before;
-        int b = b0;
+        int left = t - all.before, b = b0;
         for (;; ++b) {
             const int n = row_tiles(a, sequence(c, b));
             if (left < n) break;
@@ -528,8 +557,8 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
         found[1] = left;
     }
     __syncthreads();
-    const int b = __builtin_amdgcn_readfirstlane((int)found[0]);
-    const int first = __builtin_amdgcn_readfirstlane((int)found[1]) * kOwn;
+    const int b = __builtin_amdgcn_readfirstlane(found[0]);
+    const int first = __builtin_amdgcn_readfirstlane(found[1]) * kOwn;
     const Sequence s = sequence(c, b);
     const int from = __builtin_amdgcn_readfirstlane(s.from), queries = __builtin_amdgcn_readfirstlane(s.queries);
     const int held = __builtin_amdgcn_readfirstlane(s.held);
@@ -574,7 +603,8 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
     Keys16 x;
     Pages pages;
     auto fetch = [&](int key) __attribute__((always_inline)) {
-        x = pages.at(key);
+        pages.advance(key);
+        x = pages.at(key + 16 * wave, held);
         const auto k = rows_of(c.k, x, FULL ? DT : c.d), v = rows_of(c.v, x, FULL ? DT : c.d);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
@@ -604,15 +634,15 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
                 to[at / 16] = values(ck[i][2 * j], ck[i][2 * j + 1], x.k_scale);
                 to[(at + kTile) / 16] = values(cv[i][2 * j], cv[i][2 * j + 1], x.v_scale);
             }
-        if (st + 1 < s_end) fetch((st + 1) * kKeys + 16 * wave);
+        if (st + 1 < s_end) fetch((st + 1) * kKeys);
         // tile st is written by all; the other stage was last read in step st - 1, by the waves that are here
         __syncthreads();
         const int j0 = st * kKeys;
         if (j0 < see_last) attend_tile<DT, at>(tile, q, see - j0, j0 + kKeys > see_first, c2, far, o, m, mc, l);
     };
     if (s_begin < s_end) {
-        pages.init(c, b, head, held, s_begin * kKeys + 16 * wave);
-        fetch(s_begin * kKeys + 16 * wave);
+        pages.init(c, b, head, held, s_begin * kKeys);
+        fetch(s_begin * kKeys);
     }
     for (int st = s_begin; st < s_end; st += 2) {
         step(std::integral_constant<int, 0>{}, st);
@@ -621,12 +651,12 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
 
     l += partner(l);
     if (splits > 1) {
-        const int slot0 = 2 * a.workers + (int)((t * c.heads + head) * splits) * (kOwn / 16);
+        const int slot0 = 2 * a.workers + (t * c.heads + head) * splits * (kOwn / 16);
         const int64_t row = (int64_t)(slot0 + split * (kOwn / 16)) * 16 + wave * 32 + (lane & 31);
         store_partial<DT>(o, a.partial + row * DT, DT, valid);
         if (valid && h == 0) a.tops[row] = make_float2(m == -kInf ? -kInf : mc, l);
         if (split == 0 && threadIdx.x == 0)
-            joins[block] = Join{b, head, first, splits, slot0, slot0 + kOwn / 16, kOwn / 16, 0};
+            joins[t * c.heads + head] = Join{b, head, first, splits, slot0, slot0 + kOwn / 16, kOwn / 16, 0};
         return 0;
     }
     const uint32_t top = store_own<DT>(o, inverse(l), a.out + (int64_t)(from + qi) * a.out_row + (int64_t)hq * a.out_head, c.d, valid);
@@ -644,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_cached_kernel(const Cac
 {
     constexpr int kBytes = KINDS == 1 ? share_lds<DT>() : std::max(share_lds<DT>(), tile_lds<DT>());
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kBytes];
-    __shared__ int64_t sums[kWaves][2], found[2];
+    __shared__ int sums[kWaves][4], found[2];
     const int i = blockIdx.x, pair = i >> 4;
     bool share = KINDS == 1;
     int block = i;
@@ -658,85 +688,73 @@ __global__ void __launch_bounds__(kThreads, 2) attention_cached_kernel(const Cac
     if (a.absmax) block_max_to_global(top, a.absmax);
 }
 
-// out and lse of rows whose keys several workgroups shared, their parts in order: of few rows a
-// workgroup takes one, its threads side by side over the parts, which may be hundreds; of
-// tiles 16 rows.
+// out and lse of rows whose keys several workgroups shared: 16 rows to a workgroup, a row's
+// parts dealt to several groups of DT / 8 threads, each with its own running maximum, which
+// are then added in order.
 template <int DT>
-__global__ void __launch_bounds__(256) attention_cached_join_kernel(const CachedAttentionArgs a, int share_rows)
+__global__ void __launch_bounds__(kJoinThreads) attention_cached_join_kernel(const CachedAttentionArgs a, int shares)
 {
-    constexpr int kPer = 8, kLanes = DT / kPer, kGroups = 256 / kLanes;
-    __shared__ float part[256][kPer + 1];
+    constexpr int kPer = 8, kLanes = DT / kPer, kGroups = kJoinThreads / kLanes;
+    __shared__ float s_sum[kGroups][2], s_out[kGroups][DT + 4];
     const CacheArgs& c = a.c;
-    const int i = blockIdx.x, shares = a.workers * share_rows;
-    const bool share = i < shares;
-    const int entry = share ? i / share_rows : a.workers + (i - shares) / (kOwn / 16);
-    const int group16 = share ? 0 : (i - shares) % (kOwn / 16);
+    const int i = blockIdx.x;
+    const int entry = i < shares ? i : a.workers + (i - shares) / (kOwn / 16), group16 = i < shares ? 0 : (i - shares) % (kOwn / 16);
     const Join job = reinterpret_cast<const Join*>(a.joins)[entry];
     if (job.count <= 1) return;
     const Sequence s = sequence(c, job.b);
-    const int k = threadIdx.x / kLanes, e = threadIdx.x % kLanes * kPer;
-    // a row's parts go to kGroups groups of threads, or to one
-    const int rows = s.queries * a.group;
-    const int passes = share ? 1 : (16 + kGroups - 1) / kGroups;
-    uint32_t top = 0;
-    for (int pass = 0; pass < passes; ++pass) {
-        const int n = share ? i % share_rows : pass * kGroups + k, row = job.row + group16 * 16 + n;
-        const bool valid = row < rows && n < 16;
-        if (share && !valid) return;
-        auto slot = [&](int p) __attribute__((always_inline)) {
-            return (int64_t)((p == 0 ? job.first : job.second + (p - 1) * job.step) + group16) * 16 + n;
-        };
-        float m = -kInf, l = 0.0f, t[kPer] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (share) {
-            for (int p = threadIdx.x & 63; p < job.count; p += 64) m = fmaxf(m, a.tops[slot(p)].x);
-#pragma unroll
-            for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-        } else if (valid) {
-            for (int p = 0; p < job.count; ++p) m = fmaxf(m, a.tops[slot(p)].x);
-        }
-        const float use = m == -kInf ? 0.0f : m;
-        if (share) {
-            for (int p = threadIdx.x & 63; p < job.count; p += 64) {
-                const float2 y = a.tops[slot(p)];
-                l = fmaf(y.y, __builtin_amdgcn_exp2f(y.x - use), l);
-            }
-#pragma unroll
-            for (int off = 32; off >= 1; off >>= 1) l += __shfl_xor(l, off, 64);
-        }
-        if (valid)
+    const int rows = min(s.queries * a.group - job.row - 16 * group16, 16);
+    if (rows <= 0) return;
+    const int wide = rows > 8 ? 16 : rows > 4 ? 8 : rows > 2 ? 4 : rows;       // rows side by side
+    const int k = threadIdx.x / kLanes, e = threadIdx.x % kLanes * kPer, n = k % wide, lead = k / wide;
+    auto slot = [&](int p) __attribute__((always_inline)) {
+        return (int64_t)((p == 0 ? job.first : job.second + (p - 1) * job.step) + group16) * 16 + n;
+    };
+    float m = -kInf, l = 0.0f, t[kPer] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (n < rows)
 #pragma unroll 4
-            for (int p = share ? k : 0; p < job.count; p += share ? kGroups : 1) {
-                const float2 y = a.tops[slot(p)];
-                const float by = __builtin_amdgcn_exp2f(y.x - use);
-                if (!share) l = fmaf(y.y, by, l);
-                const float4* from = reinterpret_cast<const float4*>(a.partial + slot(p) * DT + e);
-                const float4 u = from[0], v = from[1];
-                const float w[kPer] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+        for (int p = lead; p < job.count; p += kGroups / wide) {
+            const float2 y = a.tops[slot(p)];
+            const float4* from = reinterpret_cast<const float4*>(a.partial + slot(p) * DT + e);
+            const float4 u = from[0], v = from[1];
+            const float up = fmaxf(m, y.x), base = up == -kInf ? 0.0f : up;
+            const float old = __builtin_amdgcn_exp2f(m - base), by = __builtin_amdgcn_exp2f(y.x - base);
+            const float w[kPer] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+            l = fmaf(y.y, by, l * old);
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) t[j] = fmaf(w[j], by, t[j]);
-            }
-        if (share) {
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) part[threadIdx.x][j] = t[j];
-            __syncthreads();
-            if (k == 0)
-                for (int g = 1; g < kGroups; ++g)
-#pragma unroll
-                    for (int j = 0; j < kPer; ++j) t[j] += part[g * kLanes + threadIdx.x][j];
+            for (int j = 0; j < kPer; ++j) t[j] = fmaf(w[j], by, t[j] * old);
+            m = up;
         }
-        if (valid && (!share || k == 0) && e < c.d) {
-            const float by = inverse(l);
-            const int qi = row / a.group, hq = job.head * a.group + row - qi * a.group;
-            uint32_t w[4];
+    if (e == 0) {
+        s_sum[k][0] = m;
+        s_sum[k][1] = l;
+    }
+    *reinterpret_cast<float4*>(&s_out[k][e]) = make_float4(t[0], t[1], t[2], t[3]);
+    *reinterpret_cast<float4*>(&s_out[k][e + 4]) = make_float4(t[4], t[5], t[6], t[7]);
+    __syncthreads();
+    uint32_t top = 0;
+    if (lead == 0 && n < rows && e < c.d) {
+        float all = -kInf, total = 0.0f;
+        for (int g = n; g < kGroups; g += wide) all = fmaxf(all, s_sum[g][0]);
+        const float base = all == -kInf ? 0.0f : all;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                w[j] = bf16_pair(t[2 * j] * by, t[2 * j + 1] * by);
-                top = top_of(w[j], top);
-            }
-            *reinterpret_cast<uint4*>(a.out + (int64_t)(s.from + qi) * a.out_row + (int64_t)hq * a.out_head + e) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-            if (e == 0) a.lse[(int64_t)hq * c.tokens + s.from + qi] = l == 0.0f ? -kInf : (use + __builtin_amdgcn_logf(l)) * kLn2;
+        for (int j = 0; j < kPer; ++j) t[j] = 0.0f;
+        for (int g = n; g < kGroups; g += wide) {
+            const float by = __builtin_amdgcn_exp2f(s_sum[g][0] - base);
+            total = fmaf(s_sum[g][1], by, total);
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) t[j] = fmaf(s_out[g][e + j], by, t[j]);
         }
+        const float by = inverse(total);
+        const int row = job.row + 16 * group16 + n, qi = row / a.group, hq = job.head * a.group + row - qi * a.group;
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            w[j] = bf16_pair(t[2 * j] * by, t[2 * j + 1] * by);
+            top = top_of(w[j], top);
+        }
+        *reinterpret_cast<uint4*>(a.out + (int64_t)(s.from + qi) * a.out_row + (int64_t)hq * a.out_head + e) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+        if (e == 0) a.lse[(int64_t)hq * c.tokens + s.from + qi] = total == 0.0f ? -kInf : (base + __builtin_amdgcn_logf(total)) * kLn2;
     }
     if (a.absmax) block_max_to_global(top, a.absmax);
 }
@@ -775,9 +793,11 @@ void (*kernel_of(int kinds))(CachedAttentionArgs)
 
 }  // namespace
 
-bool attention_cached_grid_ok(int64_t tokens, int group, int heads, int batch)
+bool attention_cached_grid_ok(int64_t tokens, int group, int heads, int batch, int blocks, int shift)
 {
-    return tokens * group / kOwn + batch <= 0xFFFFFFFFll / kThreads / 2 / heads;
+    // the steps of all sequences of few rows are counted in 32 bits, and so are a launch's threads
+    const int64_t steps = (((int64_t)blocks << shift) + kKeys - 1) / kKeys + kPiece + 1;
+    return batch * steps <= ((int64_t)0x7FFFFFFF - (1 << 20)) / heads && tokens * group / kOwn + batch <= 0xFFFFFFFFll / kThreads / 2 / heads;
 }
 
 int64_t attention_cached_workspace(int64_t tokens, int group, int d, int batch, bool bounds)
@@ -802,10 +822,9 @@ hipError_t launch_attention_cached(const CachedAttentionArgs& args, void* worksp
     if (e != hipSuccess) return e;
     // without bounds the tiles are known: more than half as many as workers are not split
     if (p.kinds == 2 && p.tiles * a.c.heads > p.workers / 2) return e;
-    const int rows = p.kinds & 1 ? (int)std::min<int64_t>(kFew, a.c.tokens * a.group) : 0;
-    const int join_blocks = p.workers * (rows + (p.kinds & 2 ? kOwn / 16 : 0));
-    return launch(d <= 64 ? attention_cached_join_kernel<64> : attention_cached_join_kernel<128>, dim3(join_blocks), dim3(256), stream,
-                  a, rows);
+    const int shares = p.kinds & 1 ? p.workers : 0, joins = shares + (p.kinds & 2 ? p.workers / 2 * (kOwn / 16) : 0);
+    return launch(d <= 64 ? attention_cached_join_kernel<64> : attention_cached_join_kernel<128>, dim3(joins), dim3(kJoinThreads),
+                  stream, a, shares);
 }
 
 }  // namespace fp8k

@@ -193,7 +193,7 @@ struct CachedAttentionArgs {
     float scale;
 };
 int64_t attention_cached_workspace(int64_t tokens, int group, int d, int batch, bool bounds);
-bool attention_cached_grid_ok(int64_t tokens, int group, int heads, int batch);
+bool attention_cached_grid_ok(int64_t tokens, int group, int heads, int batch, int blocks, int shift);
 hipError_t launch_attention_cached(const CachedAttentionArgs& args, void* workspace, hipStream_t stream);
 
 // Cross entropy of a linear head (loss.hip): x [T, D], w [V, D].

@@ -685,7 +685,8 @@ fp8_status fp8_kv_cache_read(const fp8_kv_cache* cache, const fp8_head_tensor* k
  * zeros (they are seen).  A NaN in a value may reach every query of its sequence.
  *
  *   q        bf16 [tokens, heads_q, head_dim] with its own strides;  out  as q
- *   heads_q  a multiple of the cache's heads, at most 2^16; tokens heads_q below 2^31
+ *   heads_q  a multiple of the cache's heads, at most 2^16; tokens heads_q below 2^31, and
+ *            batch heads blocks page_tokens below 2^36
  *   lse      fp32 [heads_q, tokens]
  *   absmax   fp32 scalar or NULL: becomes max(*absmax, max |out|), out as stored
  *   workspace, workspace_bytes   device memory, 16-byte aligned, of at least the size that
