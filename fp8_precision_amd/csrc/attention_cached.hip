@@ -35,7 +35,13 @@ constexpr int kOwn = 128;                  // rows of a tile: 32 per wave
 constexpr int kLeastSteps = kWaves;        // of a share
 constexpr int kPiece = 4;                  // what a head of a sequence costs besides its steps, in steps
 constexpr int kLeastSplit = 4;             // steps of a part of a tile's keys
+constexpr int kSplitFrom = 16;             // steps of a tile, on average, from which on its keys are split
 constexpr int kJoinThreads = 512;
+// Of a buffer load's cache policy: no call reads the keys and values of few rows twice, and
+// before the next call on them a model reads more than the caches hold.  MI355X, without /
+// with: 64 sequences of 4096 keys (0.54 GB) 104 / 94 us, of 16384 394 / 366; but 19.6 / 22.4 for
+// 500 (67 MB), where the last-level cache still has them from the call before.
+constexpr int kNonTemporal = 2;
 constexpr uint32_t kNowhere = 0x7FFFFFF0u; // an offset outside every buffer
 
 __device__ __forceinline__ af32x4 mma16(const Frag& a, const Frag& b, const af32x4& c)
@@ -109,9 +115,10 @@ __device__ __forceinline__ Sums block_sums(int x, int64_t y, int (*lds)[4])
         const int o = __shfl_up(upto, off, 64);
         if (lane >= off) upto += o;
     }
-    if (y != 0 || __any(y != 0))
+    if (__any(y != 0)) {
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1) y += __shfl_xor(y, off, 64);
+    }
     if (lane == 63) {
         lds[wave][0] = upto;
         lds[wave][2] = (int)y;
@@ -321,7 +328,7 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
                 if constexpr (FULL) {
 #pragma unroll
                     for (int i = 0; i < DT / 64; ++i) {
-                        const au32x4 w = __builtin_amdgcn_raw_buffer_load_b128(src, m * DT + 64 * i + 16 * g, 0, 0);
+                        const au32x4 w = __builtin_amdgcn_raw_buffer_load_b128(src, m * DT + 64 * i + 16 * g, 0, kNonTemporal);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) ck[n][4 * i + j] = w[j];
                     }
@@ -329,7 +336,7 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
 #pragma unroll
                     for (int i = 0; i < DT / 32; ++i) {
                         const int e = 64 * (i / 2) + 16 * g + 8 * (i % 2);
-                        const au32x2 w = __builtin_amdgcn_raw_buffer_load_b64(src, e < c.d ? m * c.d + e : kNowhere, 0, 0);
+                        const au32x2 w = __builtin_amdgcn_raw_buffer_load_b64(src, e < c.d ? m * c.d + e : kNowhere, 0, kNonTemporal);
                         ck[n][2 * i] = w[0];
                         ck[n][2 * i + 1] = w[1];
                     }
@@ -347,11 +354,11 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t off = FULL || e < d ? (uint32_t)((4 * g + i) * d + e) : kNowhere;
                     if constexpr (DT == 128) {
-                        const au32x2 w = __builtin_amdgcn_raw_buffer_load_b64(src, off, 0, 0);
+                        const au32x2 w = __builtin_amdgcn_raw_buffer_load_b64(src, off, 0, kNonTemporal);
                         cv[n][i][0] = w[0];
                         cv[n][i][1] = w[1];
                     } else {
-                        cv[n][i][0] = __builtin_amdgcn_raw_buffer_load_b32(src, off, 0, 0);
+                        cv[n][i][0] = __builtin_amdgcn_raw_buffer_load_b32(src, off, 0, kNonTemporal);
                     }
                 }
             }
@@ -532,14 +539,17 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
         const Sequence s = sequence(c, b);
         const int n = row_tiles(a, s);
         mine += n;
-        mine_steps += (int64_t)n * ((s.held + kKeys - 1) / kKeys);
+        mine_steps += (int64_t)n * ((max(s.held - (a.causal ? s.queries / 2 : 0), 0) + kKeys - 1) / kKeys);
     }
     const Sums all = block_sums(mine, mine_steps, sums);
     Join* const joins = reinterpret_cast<Join*>(a.joins) + a.workers;
-    if (threadIdx.x == 0 && block < a.workers / 2) joins[block].count = 0;   // (more tiles are not split)
-    if (all.total == 0) return 0;
     const int units = all.total * c.heads;
-    const int splits = (int)max(min((int64_t)(a.workers / units), all.total_y / all.total / kLeastSplit), (int64_t)1);
+    const int average = units == 0 ? 0 : (int)(all.total_y / all.total);
+    const int splits = average < kSplitFrom ? 1 : max(min(a.workers / units, average / kLeastSplit), 1);
+    // what is to be joined: an entry for each unit if they are split (by its first part, below), else none
+    // (units of more than half the workers are not split)
+    if (threadIdx.x == 0 && block < a.workers / 2 && (splits == 1 || block >= units)) joins[block].count = 0;
+    if (units == 0) return 0;
     const int wide = c.heads * splits;
     if (block >= (int64_t)all.total * wide) return 0;
     // blocks are dealt round-robin to the 8 XCDs: each gets whole heads where they divide so
