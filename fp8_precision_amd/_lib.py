@@ -865,30 +865,52 @@ class _Cache(ctypes.Structure):
                 ("batch", _i64), ("blocks", _i64), ("tokens", _i64)]
 
 
-def _cache(cache, table, lengths, cu, tokens):
-    """The struct of a call on a cache, its tensors checked: (struct, the tensors)."""
-    k, v, k_scale, v_scale = cache
+def _cache_checks(k, v, k_scale, v_scale, table, lengths, cu):
+    """What is wrong with the tensors of a call on a cache."""
     _dev_tensor(k, "cache.k", torch.uint8)
     _dev_tensor(v, "cache.v", torch.uint8)
-    size = k.shape
-    if len(size) != 4 or v.shape != size:
+    if k.dim() != 4 or v.shape != k.shape:
         raise ValueError("cache.k and cache.v must be [pages, heads, page_tokens, head_dim]")
     for t, n in ((k_scale, "cache.k_scale"), (v_scale, "cache.v_scale")):
         _dev_tensor(t, n, torch.uint8)
-        if t.shape != size[:2]:
+        if t.shape != k.shape[:2]:
             raise ValueError(f"{n} must be [pages, heads]")
     _dev_tensor(table, "table", torch.int32)
     _dev_tensor(lengths, "lengths", torch.int32)
     if table.dim() != 2 or lengths.shape != table.shape[:1]:
         raise ValueError("table must be [batch, blocks] and lengths [batch]")
-    batch, blocks = table.shape
     if cu is not None:
-        _vector(cu, "cu", batch + 1, torch.int32)
-    elif tokens % max(batch, 1):
+        _vector(cu, "cu", table.shape[0] + 1, torch.int32)
+
+
+def _cache(cache, table, lengths, cu, tokens):
+    """The struct of a call on a cache, its tensors checked."""
+    k, v, k_scale, v_scale = cache
+    u8, i32 = torch.uint8, torch.int32
+    try:
+        # one test of what a call in a loop passes (a microsecond or two less than one by one)
+        size, (batch, blocks) = k.shape, table.shape
+        fine = (len(size) == 4 and v.shape == size and k_scale.shape == size[:2] == v_scale.shape and lengths.shape == (batch,)
+                and k.dtype is u8 and v.dtype is u8 and k_scale.dtype is u8 and v_scale.dtype is u8
+                and table.dtype is i32 and lengths.dtype is i32 and k.is_cuda
+                and k.get_device() == v.get_device() == k_scale.get_device() == v_scale.get_device() == table.get_device()
+                == lengths.get_device()
+                and k.is_contiguous() and v.is_contiguous() and k_scale.is_contiguous() and v_scale.is_contiguous()
+                and table.is_contiguous() and lengths.is_contiguous()
+                and (cu is None or (cu.dtype is i32 and cu.shape == (batch + 1,) and cu.is_contiguous()
+                                    and cu.get_device() == k.get_device())))
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine:
+        _cache_checks(k, v, k_scale, v_scale, table, lengths, cu)
+        size, (batch, blocks) = k.shape, table.shape
+        for t in (v, k_scale, v_scale, table, lengths, cu):
+            if t is not None and t.device != k.device:
+                raise ValueError(f"all tensors of a cache must be on one device (got {k.device} and {t.device})")
+    if cu is None and tokens % max(batch, 1):
         raise ValueError("without cu every sequence has as many tokens")
-    c = _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(), lengths.data_ptr(),
-               _ptr(cu), size[0], size[1], size[2], size[3], batch, blocks, tokens)
-    return c, (k, v, k_scale, v_scale, table, lengths, cu)
+    return _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(), lengths.data_ptr(),
+                  None if cu is None else cu.data_ptr(), size[0], size[1], size[2], size[3], batch, blocks, tokens)
 
 
 def kv_cache_write(cache, table, lengths, k, v, cu=None) -> None:
@@ -903,10 +925,10 @@ def kv_cache_write(cache, table, lengths, k, v, cu=None) -> None:
     call writes must stand in the table once.
     """
     hk, hv = _heads(k, "k"), _heads(v, "v", k.shape)
-    c, tensors = _cache(cache, table, lengths, cu, k.shape[0])
+    c = _cache(cache, table, lengths, cu, k.shape[0])
     if (k.shape[1], k.shape[2]) != (c.heads, c.head_dim):
         raise ValueError(f"k and v must be [tokens, {c.heads}, {c.head_dim}]")
-    _run("fp8_kv_cache_write", _lib.fp8_kv_cache_write, tensors + (k, v), ctypes.byref(c), hk, hv)
+    _run("fp8_kv_cache_write", _lib.fp8_kv_cache_write, (cache[0], k, v), ctypes.byref(c), hk, hv)
 
 
 def kv_cache_read(cache, table, lengths, tokens: int, cu=None, k=None, v=None):
@@ -914,12 +936,12 @@ def kv_cache_read(cache, table, lengths, tokens: int, cu=None, k=None, v=None):
     bf16 [tokens, heads, head_dim], exact.  ``table``, ``lengths`` and ``cu`` (whose last bound
     is at most ``tokens``) as for ``kv_cache_write``: with the bounds of ``lengths`` the whole
     contexts, as ``attention`` takes them.  Tokens without a page read as zeros."""
-    c, tensors = _cache(cache, table, lengths, cu, tokens)
+    c = _cache(cache, table, lengths, cu, tokens)
     shape = (tokens, c.heads, c.head_dim)
     k = torch.empty(shape, dtype=torch.bfloat16, device=table.device) if k is None else k
     v = torch.empty(shape, dtype=torch.bfloat16, device=table.device) if v is None else v
     hk, hv = _heads(k, "k", shape), _heads(v, "v", shape)
-    _run("fp8_kv_cache_read", _lib.fp8_kv_cache_read, tensors + (k, v), ctypes.byref(c), hk, hv)
+    _run("fp8_kv_cache_read", _lib.fp8_kv_cache_read, (cache[0], k, v), ctypes.byref(c), hk, hv)
     return k, v
 
 
@@ -935,7 +957,7 @@ def attention_cached(q, cache, table, lengths, cu=None, causal: bool = True, sca
     lse -inf."""
     hq = _heads(q, "q")
     size = q.shape
-    c, tensors = _cache(cache, table, lengths, cu, size[0])
+    c = _cache(cache, table, lengths, cu, size[0])
     if size[2] != c.head_dim:
         raise ValueError(f"q must be [tokens, heads_q, {c.head_dim}]")
     if absmax is not None:
@@ -945,7 +967,7 @@ def attention_cached(q, cache, table, lengths, cu=None, causal: bool = True, sca
     ho = _heads(out, "out", size)
     lse = _out(lse, "lse", (size[1], size[0]), torch.float32, q.device)
     ws = _workspace("fp8_attention_cached_workspace", q.device, ctypes.byref(c), size[1])
-    _run("fp8_attention_cached", _lib.fp8_attention_cached, tensors + (q, out, lse, absmax, ws), ctypes.byref(c), hq, ho,
+    _run("fp8_attention_cached", _lib.fp8_attention_cached, (cache[0], q, out, lse, absmax, ws), ctypes.byref(c), hq, ho,
          size[1], 1 if causal else 0, size[2] ** -0.5 if scale is None else scale, _ptr(lse), _ptr(absmax), _ptr(ws),
          0 if ws is None else ws.numel())
     return out, lse

@@ -20,9 +20,13 @@ namespace fp8k {
 
 namespace {
 
+typedef unsigned short ku16x2 __attribute__((ext_vector_type(2)));
+typedef short ki16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 kb16x2 __attribute__((ext_vector_type(2)));
+
 constexpr int kCacheThreads = 256;
 constexpr int kWaveTokens = 4;             // new tokens per sequence, on average, up to which a wave takes a piece
-constexpr int kHeld = 8;                   // 16-byte groups of a piece that a thread keeps in registers
+constexpr int kHeld = 4;                   // 16-byte groups of a piece's keys, and of its values, that a thread keeps in registers
 
 // The scale's exponent for a largest magnitude of these fp32 bits: 448 = 1.75 2^8.
 __device__ __forceinline__ int exponent_for(uint32_t top)
@@ -33,48 +37,69 @@ __device__ __forceinline__ int exponent_for(uint32_t top)
 
 struct Piece {
     CachePiece at;
+    int b;
     int64_t token;      // the first token in the call's tensors
-    int64_t page;       // in the pool; -1: none
 };
 
-// Piece `item` of the call.  Every wave finds its own: 64 sequences are compared at a time.
+// Piece `item` of the call.  Every wave finds its own: 64 sequences are compared at a time,
+// and the last comparison's lanes hold the sequence's bounds and length.
 __device__ __forceinline__ Piece find_piece(const CacheArgs& a, int64_t item)
 {
     const int lane = threadIdx.x & 63;
     Piece p{};
-    int b, from, count;
+    int from, count, length;
     int64_t local;
     if (!a.cu) {
         count = (int)(a.tokens / a.batch);
         const int64_t per = pieces_of(count, a.shift);
-        b = (int)min(item / per, (int64_t)a.batch);
+        p.b = (int)min(item / per, (int64_t)a.batch);
+        if (p.b == a.batch) return p;
         local = item % per;
-        from = (int)min((int64_t)b * count, a.tokens);
+        from = p.b * count;
+        length = a.lengths[p.b];
     } else {
-        int first = 0, width = a.batch;
-        do {
+        int first = 0, width = a.batch, lo = 0, hi = 0, n = 0, l = 0;
+        while (true) {
             const int step = (width + 63) / 64, c = first + lane * step;
-            const bool before = c < first + width && piece_base(min(max(a.cu[c], 0), (int)a.tokens), c, a.shift) <= item;
-            const uint64_t all = __ballot(before);
+            const bool inside = c < first + width;
+            if (inside) {
+                lo = min(max(a.cu[c], 0), (int)a.tokens);
+                hi = min(max(a.cu[c + 1], 0), (int)a.tokens);
+                n = a.lengths[c];
+            }
+            const uint64_t all = __ballot(inside && piece_base(lo, c, a.shift) <= item);
             if (!all) return p;
-            const int l = 63 - __clzll((long long)all);
-            width = min(step, width - l * step);
+            l = 63 - __clzll((long long)all);
             first += l * step;
-        } while (width > 1);
-        b = __builtin_amdgcn_readfirstlane(first);
-        from = min(max(a.cu[b], 0), (int)a.tokens);
-        count = max(min(max(a.cu[b + 1], 0), (int)a.tokens) - from, 0);
-        local = item - piece_base(from, b, a.shift);
+            if (step == 1) break;
+            width = min(step, width - l * step);
+        }
+        p.b = first;
+        from = __builtin_amdgcn_readlane(lo, l);
+        count = max(__builtin_amdgcn_readlane(hi, l) - from, 0);
+        length = __builtin_amdgcn_readlane(n, l);
+        local = item - piece_base(from, p.b, a.shift);
     }
-    if (b >= a.batch) return p;
-    p.at = cache_piece(count, held_tokens(a.lengths[b], a.blocks, a.shift), local, a.shift);
+    p.at = cache_piece(count, held_tokens(length, a.blocks, a.shift), local, a.shift);
     p.token = (int64_t)from + p.at.skip;
-    p.page = -1;
-    if (p.at.count > 0 && p.at.block >= 0) {
-        const int at = a.table[(int64_t)b * a.blocks + p.at.block];
-        if (at >= 0 && at < a.pages) p.page = at;
-    }
     return p;
+}
+
+// Its page in the pool; -1: none.
+__device__ __forceinline__ int64_t page_of(const CacheArgs& a, const Piece& p)
+{
+    if (p.at.block < 0) return -1;
+    const int at = a.table[(int64_t)p.b * a.blocks + p.at.block];
+    return at >= 0 && at < a.pages ? at : -1;
+}
+
+// The larger of m's halves and the magnitudes of 8 bf16 (as 16-bit patterns, NaN above infinity).
+__device__ __forceinline__ ku16x2 raw_top(const uint4& x, ku16x2 m)
+{
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(ku16x2, w[i] & 0x7FFF7FFFu));
+    return m;
 }
 
 // The largest finite magnitude (fp32 bits) of 8 bf16.
@@ -91,6 +116,17 @@ __device__ __forceinline__ uint32_t finite_top(const uint4& x)
     return top;
 }
 
+// The codes of 8 finite bf16 of at most 448 2^e, by = 2^e: the conversion divides by it.
+__device__ __forceinline__ uint2 quant8_finite(const uint4& x, float by)
+{
+    ki16x2 a{0, 0}, b{0, 0};
+    a = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(a, __builtin_bit_cast(kb16x2, x.x), by, false);
+    a = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(a, __builtin_bit_cast(kb16x2, x.y), by, true);
+    b = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(b, __builtin_bit_cast(kb16x2, x.z), by, false);
+    b = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(b, __builtin_bit_cast(kb16x2, x.w), by, true);
+    return make_uint2(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
+}
+
 // 4 codes times a power of two, rounded again.
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float by)
 {
@@ -98,74 +134,110 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float by)
     return enc4<0>(lo[0] * by, lo[1] * by, hi[0] * by, hi[1] * by);
 }
 
-// T threads (a wave, or the workgroup) write one piece of one head's keys or values: its
-// largest magnitude, the page's new exponent, the codes; and where the page was begun
-// before and its exponent grows, its older codes.
+// T threads (a wave, or the workgroup) write one piece of one head's keys and values: the
+// largest magnitudes, the page's new exponents, the codes; and where the page was begun
+// before and an exponent grows, its older codes.  What is finite (one 16-bit maximum per two
+// elements tells) takes one conversion per two elements; the rest is saturated first.
 template <int T>
 __global__ void __launch_bounds__(kCacheThreads) kv_cache_write_kernel(const CacheArgs a)
 {
     constexpr int kUnits = kCacheThreads / T;
-    __shared__ uint32_t part[kCacheThreads / 64];
-    __shared__ int was_e;
+    __shared__ uint32_t part[2][kCacheThreads / 64];
+    __shared__ int was_e[2];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t unit = a.unit0 + (int64_t)blockIdx.x * kUnits + (T == 64 ? wave : 0);
     const int tid = T == 64 ? threadIdx.x & 63 : threadIdx.x;
-    const int head = (int)(unit % a.heads), values = (int)(unit / a.heads % 2);
-    const Piece p = find_piece(a, unit / (2 * a.heads));
-    if (p.at.count <= 0 || p.page < 0) return;
+    const int head = (int)(unit % a.heads);
+    const Piece p = find_piece(a, unit / a.heads);
+    if (p.at.count <= 0) return;
 
     const int d = a.d, per = d / 8, groups = p.at.count * per;
     const uint32_t inverse = (65536 + per - 1) / per;      // i / per for i < 2^12
-    const uint16_t* x = (values ? a.xv : a.xk) + p.token * (values ? a.xv_row : a.xk_row) +
-                        head * (values ? a.xv_head : a.xk_head);
-    const int64_t row = values ? a.xv_row : a.xk_row;
-    const int64_t place = p.page * a.heads + head;
-    uint8_t* codes = (values ? a.v : a.k) + ((place << a.shift) * d);
-    uint8_t* scale = (values ? a.v_scale : a.k_scale) + place;
-
-    auto load = [&](int i) __attribute__((always_inline)) {
+    const uint16_t* const x[2] = {a.xk + p.token * a.xk_row + head * a.xk_head, a.xv + p.token * a.xv_row + head * a.xv_head};
+    const int64_t row[2] = {a.xk_row, a.xv_row};
+    auto load = [&](int values, int i) __attribute__((always_inline)) {
         const int r = (int)(i * inverse >> 16);
-        return *reinterpret_cast<const uint4*>(x + r * row + (i - r * per) * 8);
+        return *reinterpret_cast<const uint4*>(x[values] + r * row[values] + (i - r * per) * 8);
     };
-    uint4 held[kHeld];
-    uint32_t top = 0;
+    uint4 held[2][kHeld];
 #pragma unroll
     for (int h = 0; h < kHeld; ++h)
-        if (tid + h * T < groups) held[h] = load(tid + h * T);
 #pragma unroll
-    for (int h = 0; h < kHeld; ++h)
-        if (tid + h * T < groups) top = max(top, finite_top(held[h]));
-    for (int i = tid + kHeld * T; i < groups; i += T) top = max(top, finite_top(load(i)));
-    top = wave_max_u32(top);
-    int was = kCacheLeastE;
-    if (T == 64) {
-        if (p.at.slot > 0) was = cache_exponent(*scale);
-    } else {
-        if ((threadIdx.x & 63) == 0) part[wave] = top;
-        if (threadIdx.x == 0) was_e = p.at.slot > 0 ? cache_exponent(*scale) : kCacheLeastE;
-        __syncthreads();
-        for (int w = 0; w < kCacheThreads / 64; ++w) top = max(top, part[w]);
-        was = was_e;
-    }
-    const int e = max(exponent_for(top), was);
-    const float s = two_to(-e);
+        for (int v = 0; v < 2; ++v)
+            if (tid + h * T < groups) held[v][h] = load(v, tid + h * T);
+    // (the page is looked up while the tokens are on their way)
+    const int64_t page = page_of(a, p), place = max(page, (int64_t)0) * a.heads + head;
+    if (page < 0) return;
+    uint8_t* const codes[2] = {a.k + (place << a.shift) * d, a.v + (place << a.shift) * d};
+    uint8_t* const scale[2] = {a.k_scale + place, a.v_scale + place};
+    int was[2] = {kCacheLeastE, kCacheLeastE};
+    if (p.at.slot > 0 && (T == 64 || threadIdx.x == 0))
+#pragma unroll
+        for (int v = 0; v < 2; ++v) was[v] = cache_exponent(*scale[v]);
 
-    uint2* to = reinterpret_cast<uint2*>(codes + p.at.slot * d);
+    uint32_t top[2];
 #pragma unroll
-    for (int h = 0; h < kHeld; ++h)
-        if (tid + h * T < groups) to[tid + h * T] = quant8<0>(held[h], s);
-    for (int i = tid + kHeld * T; i < groups; i += T) to[i] = quant8<0>(load(i), s);
-    if (p.at.slot > 0 && e > was) {
-        // 2^-126 and less leave no code but 0
-        const float by = two_to(max(was - e, -126));
-        for (int i = tid; i < p.at.slot * per; i += T) {
-            uint2 w = reinterpret_cast<uint2*>(codes)[i];
-            w.x = rescale4(w.x, by);
-            w.y = rescale4(w.y, by);
-            reinterpret_cast<uint2*>(codes)[i] = w;
-        }
+    for (int v = 0; v < 2; ++v) {
+        ku16x2 raw{0, 0};
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h)
+            if (tid + h * T < groups) raw = raw_top(held[v][h], raw);
+        for (int i = tid + kHeld * T; i < groups; i += T) raw = raw_top(load(v, i), raw);
+        top[v] = (uint32_t)max(raw[0], raw[1]) << 16;
+        top[v] = wave_max_u32(top[v]);
     }
-    if (tid == 0) *scale = (uint8_t)(e + 127);
+    auto whole_max = [&]() __attribute__((always_inline)) {
+        if (T == 64) return;
+        if ((threadIdx.x & 63) == 0) part[0][wave] = top[0], part[1][wave] = top[1];
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+            for (int w = 0; w < kCacheThreads / 64; ++w) top[v] = max(top[v], part[v][w]);
+    };
+    if (T != 64 && threadIdx.x == 0) was_e[0] = was[0], was_e[1] = was[1];
+    whole_max();
+    if (T != 64) was[0] = was_e[0], was[1] = was_e[1];
+    const bool finite = max(top[0], top[1]) < 0x7F800000u;
+    if (!finite) {
+        // the scales are those of the finite values
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            top[v] = 0;
+            for (int i = tid; i < groups; i += T) top[v] = max(top[v], finite_top(load(v, i)));
+            top[v] = wave_max_u32(top[v]);
+        }
+        if (T != 64) __syncthreads();                      // part has been read
+        whole_max();
+    }
+
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+        const int e = max(exponent_for(top[v]), was[v]);
+        const float s = two_to(-e);
+        uint2* to = reinterpret_cast<uint2*>(codes[v] + p.at.slot * d);
+        if (finite && e < kCacheMostE) {
+            const float by = two_to(e);
+#pragma unroll
+            for (int h = 0; h < kHeld; ++h)
+                if (tid + h * T < groups) to[tid + h * T] = quant8_finite(held[v][h], by);
+            for (int i = tid + kHeld * T; i < groups; i += T) to[i] = quant8_finite(load(v, i), by);
+        } else {
+            for (int i = tid; i < groups; i += T) to[i] = quant8<0>(load(v, i), s);
+        }
+        if (p.at.slot > 0 && e > was[v]) {
+            // 2^-126 and less leave no code but 0
+            const float by = two_to(max(was[v] - e, -126));
+            uint2* old = reinterpret_cast<uint2*>(codes[v]);
+            for (int i = tid; i < p.at.slot * per; i += T) {
+                uint2 w = old[i];
+                w.x = rescale4(w.x, by);
+                w.y = rescale4(w.y, by);
+                old[i] = w;
+            }
+        }
+        // (a byte outside e's range that does not grow stays: it counts as was)
+        if (tid == 0 && (p.at.slot == 0 || e > was[v])) *scale[v] = (uint8_t)(e + 127);
+    }
 }
 
 // T threads read one piece of one head's keys or values; tokens with no place read as zeros.
@@ -182,19 +254,18 @@ __global__ void __launch_bounds__(kCacheThreads) kv_cache_read_kernel(const Cach
 
     const int d = a.d, per = d / 8, groups = p.at.count * per;
     const uint32_t inverse = (65536 + per - 1) / per;
-    uint16_t* x = (values ? a.xv : a.xk) + p.token * (values ? a.xv_row : a.xk_row) + head * (values ? a.xv_head : a.xk_head);
+    uint16_t* const x = (values ? a.xv : a.xk) + p.token * (values ? a.xv_row : a.xk_row) + head * (values ? a.xv_head : a.xk_head);
     const int64_t row = values ? a.xv_row : a.xk_row;
-    const int64_t place = max(p.page, (int64_t)0) * a.heads + head;
+    const int64_t page = page_of(a, p), place = max(page, (int64_t)0) * a.heads + head;
     const uint2* codes = reinterpret_cast<const uint2*>((values ? a.v : a.k) + (place << a.shift) * d + p.at.slot * d);
-    const uint8_t byte = p.page < 0 ? 0 : (values ? a.v_scale : a.k_scale)[place];
-    const float s = cache_scale(byte);
+    const float s = page < 0 ? 1.0f : cache_scale((values ? a.v_scale : a.k_scale)[place]);
 
     for (int i0 = tid; i0 < groups; i0 += 4 * T) {
         uint2 w[4];
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
             w[h] = make_uint2(0, 0);
-            if (i0 + h * T < groups && p.page >= 0) w[h] = codes[i0 + h * T];
+            if (i0 + h * T < groups && page >= 0) w[h] = codes[i0 + h * T];
         }
 #pragma unroll
         for (int h = 0; h < 4; ++h)
@@ -207,16 +278,16 @@ __global__ void __launch_bounds__(kCacheThreads) kv_cache_read_kernel(const Cach
 
 }  // namespace
 
-// One unit is a piece of one head's keys, or of its values: a wave where the pieces are short
+// One unit is a piece of one head's keys and values: a wave where the pieces are short
 // (T = 64), a workgroup otherwise.
 template <typename K>
-static hipError_t launch_pieces(K wave_kernel, K block_kernel, const CacheArgs& args, hipStream_t stream)
+static hipError_t launch_pieces(K wave_kernel, K block_kernel, const CacheArgs& args, int sides, hipStream_t stream)
 {
     CacheArgs a = args;
     const int64_t n = a.tokens / a.batch;
     const bool wave = n <= kWaveTokens;
     const int64_t pieces = a.cu ? piece_bound(a.tokens, a.batch, a.shift) : a.batch * pieces_of(n, a.shift);
-    const int64_t units = pieces * 2 * a.heads, per = wave ? kCacheThreads / 64 : 1;
+    const int64_t units = pieces * a.heads * sides, per = wave ? kCacheThreads / 64 : 1;
     const int64_t most = max_workgroups(kCacheThreads) / 2 * per;
     for (a.unit0 = 0; a.unit0 < units; a.unit0 += most) {
         const int64_t blocks = (std::min(most, units - a.unit0) + per - 1) / per;
@@ -228,12 +299,12 @@ static hipError_t launch_pieces(K wave_kernel, K block_kernel, const CacheArgs& 
 
 hipError_t launch_kv_cache_write(const CacheArgs& args, hipStream_t stream)
 {
-    return launch_pieces(kv_cache_write_kernel<64>, kv_cache_write_kernel<256>, args, stream);
+    return launch_pieces(kv_cache_write_kernel<64>, kv_cache_write_kernel<256>, args, 1, stream);
 }
 
 hipError_t launch_kv_cache_read(const CacheArgs& args, hipStream_t stream)
 {
-    return launch_pieces(kv_cache_read_kernel<64>, kv_cache_read_kernel<256>, args, stream);
+    return launch_pieces(kv_cache_read_kernel<64>, kv_cache_read_kernel<256>, args, 2, stream);
 }
 
 }  // namespace fp8k
