@@ -1001,13 +1001,14 @@ static fp8_status cached_shape(const char* call, const fp8_kv_cache* c, int64_t 
         return fail(FP8_ERR_UNSUPPORTED, std::string(call) + ": more than 2^16 heads or 2^31 rows");
     if (!fp8k::attention_cached_grid_ok(c->tokens, (int)(heads_q / c->heads), (int)c->heads, (int)c->batch,
                                         (int)c->blocks, shift))
-        return fail(FP8_ERR_UNSUPPORTED, std::string(call) + ": too many rows for one launch, or 2^37 keys of all heads");
+        return fail(FP8_ERR_UNSUPPORTED, std::string(call) + ": too many rows for one launch, or 2^36 keys of all heads and sequences");
     return FP8_OK;
 }
 
-static int64_t cached_bytes(const fp8_kv_cache& c, int64_t heads_q)
+static int64_t cached_bytes(const fp8_kv_cache& c, int64_t heads_q, int shift)
 {
-    return fp8k::attention_cached_workspace(c.tokens, (int)(heads_q / c.heads), (int)c.head_dim, (int)c.batch, c.bounds != nullptr);
+    return fp8k::attention_cached_workspace(c.tokens, (int)(heads_q / c.heads), (int)c.heads, (int)c.head_dim, (int)c.batch,
+                                            (int)c.blocks, shift, c.bounds != nullptr);
 }
 
 fp8_status fp8_attention_cached_workspace(const fp8_kv_cache* cache, int64_t heads_q, int64_t* bytes)
@@ -1017,7 +1018,7 @@ fp8_status fp8_attention_cached_workspace(const fp8_kv_cache* cache, int64_t hea
     fp8_status st = cached_shape("fp8_attention_cached_workspace", cache, heads_q, shift);
     if (st != FP8_OK) return st;
     if (!bytes) return fail(FP8_ERR_INVALID, "fp8_attention_cached_workspace: null pointer");
-    *bytes = cached_bytes(*cache, heads_q);
+    *bytes = cached_bytes(*cache, heads_q, shift);
     return FP8_OK;
 }
 
@@ -1039,7 +1040,7 @@ fp8_status fp8_attention_cached(const fp8_kv_cache* cache, const fp8_head_tensor
     if ((st = take_heads(call, "q", q, c.tokens, heads_q, c.head_dim, false, h[0])) != FP8_OK ||
         (st = take_heads(call, "out", out, c.tokens, heads_q, c.head_dim, true, h[1])) != FP8_OK)
         return st;
-    const int64_t need = cached_bytes(c, heads_q);
+    const int64_t need = cached_bytes(c, heads_q, shift);
     if (!lse) return fail(FP8_ERR_INVALID, "fp8_attention_cached: null lse");
     if (need > 0 && !workspace) return fail(FP8_ERR_INVALID, "fp8_attention_cached: null workspace");
     if (workspace_bytes < need) return fail(FP8_ERR_INVALID, "fp8_attention_cached: workspace too small");

@@ -35,7 +35,12 @@ constexpr int kOwn = 128;                  // rows of a tile: 32 per wave
 constexpr int kLeastSteps = kWaves;        // of a share
 constexpr int kPiece = 4;                  // what a head of a sequence costs besides its steps, in steps
 constexpr int kLeastSplit = 4;             // steps of a part of a tile's keys
-constexpr int kSplitFrom = 16;             // steps of a tile, on average, from which on its keys are split
+// Steps of a tile, on average, from which on its keys are split over the workgroups that would
+// have none; and in two where there are more tiles than CUs, but not three for two.  MI355X,
+// not split / split: 5 queries on 8005 keys (40 and 8 heads) 158 / 24 us, 512 of 512 22 / 31;
+// 1280 on 8192, no mask (32 heads: 320 tiles) 262 / 231, 1000 on 1500 among 31 single ones (320) 65 / 75.
+constexpr int kSplitFrom = 16, kHalveFrom = 48;
+constexpr int kWholeKeys = 1024;           // that a row of the table holds at most, up to which a head is not shared out
 constexpr int kJoinThreads = 512;
 // Of a buffer load's cache policy: no call reads the keys and values of few rows twice, and
 // before the next call on them a model reads more than the caches hold.  MI355X, without /
@@ -254,33 +259,43 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     uint32_t top_out = 0;
 
-    // the share: every thread counts some sequences' steps, in order
-    const int per = (c.batch + kThreads - 1) / kThreads, b0 = threadIdx.x * per, b1 = min(b0 + per, c.batch);
-    int mine = 0;
-    for (int b = b0; b < b1; ++b) mine += share_steps(a, sequence(c, b)) * c.heads;
-    const Sums all = block_sums(mine, 0, sums);
-    const int share = max((all.total + a.workers - 1) / a.workers, kLeastSteps);
     Join* const joins = reinterpret_cast<Join*>(a.joins);
-    if (threadIdx.x == 0) joins[worker].count = 0;
-    if (worker > (all.total - 1) / share || all.total == 0) return 0;
-    int at = worker * share;
-    const int end = min(at + share, all.total);
-    if (all.before <= at && at < all.before + mine) {
-        int left = at - all.before, b = b0;
-        for (;; ++b) {
-            const int n = share_steps(a, sequence(c, b)) * c.heads;
-            if (left < n) break;
-            left -= n;
+    int b, head, done, at, end, share = 1;                  // done: of the head's steps, by other shares
+    if (a.whole) {
+        b = worker / c.heads;
+        head = worker % c.heads;
+        done = at = 0;
+        end = share_steps(a, sequence(c, b));
+        if (end == 0) return 0;
+    } else {
+        // the share: every thread counts some sequences' steps, in order
+        const int per = (c.batch + kThreads - 1) / kThreads, b0 = threadIdx.x * per, b1 = min(b0 + per, c.batch);
+        int mine = 0;
+        for (int b = b0; b < b1; ++b) mine += share_steps(a, sequence(c, b)) * c.heads;
+        const Sums all = block_sums(mine, 0, sums);
+        share = max((all.total + a.workers - 1) / a.workers, kLeastSteps);
+        if (threadIdx.x == 0) joins[worker].count = 0;
+        if (worker > (all.total - 1) / share || all.total == 0) return 0;
+        at = worker * share;
+        end = min(at + share, all.total);
+        if (all.before <= at && at < all.before + mine) {
+            int left = at - all.before, b = b0;
+            for (;; ++b) {
+                const int n = share_steps(a, sequence(c, b)) * c.heads;
+                if (left < n) break;
+                left -= n;
+            }
+            found[0] = b;
+            found[1] = left;
         }
-        found[0] = b;
-        found[1] = left;
+        __syncthreads();
+        b = __builtin_amdgcn_readfirstlane(found[0]);
+        const int steps = __builtin_amdgcn_readfirstlane(share_steps(a, sequence(c, b)));
+        head = __builtin_amdgcn_readfirstlane(found[1] / steps);
+        done = __builtin_amdgcn_readfirstlane(found[1] - head * steps);
     }
-    __syncthreads();
-    int b = __builtin_amdgcn_readfirstlane(found[0]);
     Sequence s = sequence(c, b);
     int steps = __builtin_amdgcn_readfirstlane(share_steps(a, s));
-    int head = __builtin_amdgcn_readfirstlane(found[1] / steps);
-    int done = __builtin_amdgcn_readfirstlane(found[1] - head * steps);      // of the head's steps, by other shares
     const float scale2 = a.scale * kLog2e;
     const float far = fminf(8.0f / scale2, 1e38f);         // scores may pass the running maximum by 2^8 before a rescale
 
@@ -545,10 +560,12 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
     Join* const joins = reinterpret_cast<Join*>(a.joins) + a.workers;
     const int units = all.total * c.heads;
     const int average = units == 0 ? 0 : (int)(all.total_y / all.total);
-    const int splits = average < kSplitFrom ? 1 : max(min(a.workers / units, average / kLeastSplit), 1);
+    const int parts = 2 * units <= a.workers ? a.workers / units
+                      : 4 * units <= 3 * a.workers && average >= kHalveFrom ? 2 : 1;
+    const int splits = average < kSplitFrom ? 1 : max(min(parts, average / kLeastSplit), 1);
     // what is to be joined: an entry for each unit if they are split (by its first part, below), else none
-    // (units of more than half the workers are not split)
-    if (threadIdx.x == 0 && block < a.workers / 2 && (splits == 1 || block >= units)) joins[block].count = 0;
+    // (more units than workers are not split)
+    if (threadIdx.x == 0 && block < a.workers && (splits == 1 || block >= units)) joins[block].count = 0;
     if (units == 0) return 0;
     const int wide = c.heads * splits;
     if (block >= (int64_t)all.total * wide) return 0;
@@ -774,25 +791,27 @@ namespace {
 // What a call's sequences can be, as far as the host knows.
 struct Plan {
     int kinds, workers;
+    bool whole;            // few rows of short contexts: a workgroup for each head of a sequence, nothing to join
     int64_t tiles;         // of rows, at most
 };
 
-Plan plan(int64_t tokens, int group, int batch, bool bounds)
+Plan plan(int64_t tokens, int group, int heads, int batch, int64_t capacity, bool bounds)
 {
     Plan p{};
     p.workers = (2 * device_cu_count() + 7) / 8 * 8;       // two per CU, whole rounds of the XCDs
     if (!bounds) p.kinds = tokens / batch * group <= kFew ? 1 : 2;
     else p.kinds = tokens * group <= kFew ? 1 : 3;
+    p.whole = p.kinds == 1 && capacity <= kWholeKeys && (int64_t)batch * heads <= 1 << 20;
     if (p.kinds & 2) p.tiles = bounds ? tokens * group / kOwn + std::min<int64_t>(batch, tokens * group / (kFew + 1))
                                       : batch * ((tokens / batch * group + kOwn - 1) / kOwn);
     return p;
 }
 
 // Workgroups' tiles of rows: all, or as many as can share them.
-int64_t row_blocks(const Plan& p, int heads) { return std::max<int64_t>(p.tiles * heads, p.workers); }
+int64_t row_blocks(const Plan& p, int heads) { return std::max<int64_t>(p.tiles * heads, p.workers * 3 / 2); }
 
-// Slots of 16 rows that hold parts: two to a share; of tiles, split over `workers` parts at most.
-int64_t slots(const Plan& p) { return p.workers * (2 + (p.kinds & 2 ? kOwn / 16 : 0)); }
+// Slots of 16 rows that hold parts: two to a share; of tiles, split into 3 / 2 `workers` parts at most.
+int64_t slots(const Plan& p) { return p.whole ? 0 : p.workers * 2 + (p.kinds & 2 ? p.workers * 3 / 2 * (kOwn / 16) : 0); }
 
 template <int DT, bool FULL>
 void (*kernel_of(int kinds))(CachedAttentionArgs)
@@ -810,29 +829,32 @@ bool attention_cached_grid_ok(int64_t tokens, int group, int heads, int batch, i
     return batch * steps <= ((int64_t)0x7FFFFFFF - (1 << 20)) / heads && tokens * group / kOwn + batch <= 0xFFFFFFFFll / kThreads / 2 / heads;
 }
 
-int64_t attention_cached_workspace(int64_t tokens, int group, int d, int batch, bool bounds)
+static int64_t capacity(int blocks, int shift) { return (int64_t)blocks << shift; }
+
+int64_t attention_cached_workspace(int64_t tokens, int group, int heads, int d, int batch, int blocks, int shift, bool bounds)
 {
-    const Plan p = plan(tokens, group, batch, bounds);
-    return 2 * p.workers * (int64_t)sizeof(Join) + slots(p) * 16 * (8 + 4 * (d <= 64 ? 64 : 128));
+    const Plan p = plan(tokens, group, heads, batch, capacity(blocks, shift), bounds);
+    return p.whole ? 0 : 2 * p.workers * (int64_t)sizeof(Join) + slots(p) * 16 * (8 + 4 * (d <= 64 ? 64 : 128));
 }
 
 hipError_t launch_attention_cached(const CachedAttentionArgs& args, void* workspace, hipStream_t stream)
 {
     CachedAttentionArgs a = args;
-    const Plan p = plan(a.c.tokens, a.group, a.c.batch, a.c.cu != nullptr);
+    const int d = a.c.d, heads = a.c.heads;
+    const Plan p = plan(a.c.tokens, a.group, heads, a.c.batch, capacity(a.c.blocks, a.c.shift), a.c.cu != nullptr);
     a.workers = p.workers;
+    a.whole = p.whole;
     a.joins = workspace;
     a.tops = reinterpret_cast<float2*>(static_cast<Join*>(workspace) + 2 * p.workers);
     a.partial = reinterpret_cast<float*>(a.tops + slots(p) * 16);
-    const int d = a.c.d;
-    const int64_t blocks = (p.kinds & 1 ? p.workers : 0) + (p.kinds & 2 ? row_blocks(p, a.c.heads) : 0);
-    hipError_t e = launch(d == 64 ? kernel_of<64, true>(p.kinds) : d == 128 ? kernel_of<128, true>(p.kinds)
-                          : d < 64 ? kernel_of<64, false>(p.kinds) : kernel_of<128, false>(p.kinds),
-                          dim3((unsigned)blocks), dim3(kThreads), stream, a);
-    if (e != hipSuccess) return e;
-    // without bounds the tiles are known: more than half as many as workers are not split
-    if (p.kinds == 2 && p.tiles * a.c.heads > p.workers / 2) return e;
-    const int shares = p.kinds & 1 ? p.workers : 0, joins = shares + (p.kinds & 2 ? p.workers / 2 * (kOwn / 16) : 0);
+    const int64_t blocks = p.whole ? (int64_t)a.c.batch * heads
+                                   : (p.kinds & 1 ? p.workers : 0) + (p.kinds & 2 ? row_blocks(p, heads) : 0);
+    const hipError_t e = launch(d == 64 ? kernel_of<64, true>(p.kinds) : d == 128 ? kernel_of<128, true>(p.kinds)
+                                : d < 64 ? kernel_of<64, false>(p.kinds) : kernel_of<128, false>(p.kinds),
+                                dim3((unsigned)blocks), dim3(kThreads), stream, a);
+    // without bounds the tiles are known, and whether they can be split
+    if (e != hipSuccess || p.whole || (p.kinds == 2 && 4 * p.tiles * heads > 3 * p.workers)) return e;
+    const int shares = p.kinds & 1 ? p.workers : 0, joins = shares + (p.kinds & 2 ? p.workers * 3 / 4 * (kOwn / 16) : 0);
     return launch(d <= 64 ? attention_cached_join_kernel<64> : attention_cached_join_kernel<128>, dim3(joins), dim3(kJoinThreads),
                   stream, a, shares);
 }

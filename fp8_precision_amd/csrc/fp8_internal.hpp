@@ -189,10 +189,10 @@ struct CachedAttentionArgs {
     float* partial;                       // sums of split work, their maxima and totals, and what to join
     float2* tops;
     void* joins;
-    int group, causal, workers;           // group: query heads to a key head
+    int group, causal, workers, whole;    // group: query heads to a key head
     float scale;
 };
-int64_t attention_cached_workspace(int64_t tokens, int group, int d, int batch, bool bounds);
+int64_t attention_cached_workspace(int64_t tokens, int group, int heads, int d, int batch, int blocks, int shift, bool bounds);
 bool attention_cached_grid_ok(int64_t tokens, int group, int heads, int batch, int blocks, int shift);
 hipError_t launch_attention_cached(const CachedAttentionArgs& args, void* workspace, hipStream_t stream);
 

@@ -93,20 +93,23 @@ def test_move(lib, call):
 def test_attention(lib):
     n = i64()
     size = lambda c=None, hq=4: lib.fp8_attention_cached_workspace(c or cache(), hq, ctypes.byref(n))
-    assert size() == OK and n.value > 0
+    assert size() == OK and n.value == 0                 # 14 rows, 256 keys at most: no head of a sequence is shared out
+    assert size(cache(blocks=100)) == OK and n.value > 0
     assert lib.fp8_attention_cached_workspace(None, 4, ctypes.byref(n)) == INVALID
     assert lib.fp8_attention_cached_workspace(cache(), 4, None) == INVALID
     for status, change in SHAPES:
         assert size(cache(**change)) == status, change
     assert size(hq=3) == INVALID and size(hq=0) == INVALID and size(hq=1 << 17) == UNSUPPORTED
     assert size(cache(tokens=(1 << 31) - 1)) == UNSUPPORTED          # 2^33 rows
-    assert size() == OK
+    assert size(cache(batch=1 << 20, blocks=1 << 24)) == UNSUPPORTED and b"2^36" in lib.fp8_last_error()
+    assert size(cache(blocks=100)) == OK
     need = n.value
-    base = dict(cache=cache(), q=tensor(A, token_stride=256), out=tensor(B, token_stride=256), hq=4, causal=1, scale=0.125, lse=LSE,
+    assert need > 0
+    base = dict(cache=cache(blocks=100), q=tensor(A, token_stride=256), out=tensor(B, token_stride=256), hq=4, causal=1, scale=0.125, lse=LSE,
                 absmax=TOP, workspace=WS, bytes=need, stream=None)
     no = lambda **c: lib.fp8_attention_cached(*{**base, **c}.values())
     for status, change in SHAPES + POINTERS:
-        assert no(cache=cache(**change)) == status, change
+        assert no(cache=cache(**{"blocks": 100, **change})) == status, change
     assert no(lse=None) == INVALID and no(workspace=None) == INVALID and no(bytes=need - 1) == INVALID
     assert no(hq=5) == INVALID and no(causal=2) == INVALID
     for bad in (0.0, -1.0, float("nan"), float("inf")):
