@@ -905,7 +905,7 @@ static fp8_status cache_shape(const char* call, const fp8_kv_cache* c, int& shif
     if (c->head_dim % 8 || c->head_dim > 128) return no(FP8_ERR_UNSUPPORTED, "head_dim must be a multiple of 8, at most 128");
     if (c->pages >= ((int64_t)1 << 31) || c->heads > 65536 || c->batch > (1 << 20) || c->tokens >= ((int64_t)1 << 31))
         return no(FP8_ERR_UNSUPPORTED, "more than 2^31 - 1 pages or tokens, 2^16 heads or 2^20 sequences");
-    if (c->blocks >= ((int64_t)1 << 31) >> shift) return no(FP8_ERR_UNSUPPORTED, "sequences of 2^31 tokens or more");
+    if (c->blocks > ((int64_t)1 << 30) >> shift) return no(FP8_ERR_UNSUPPORTED, "rows of the table for more than 2^30 tokens");
     if (!c->bounds && c->tokens % c->batch)
         return no(FP8_ERR_INVALID, "tokens must be a multiple of batch without bounds");
     return FP8_OK;
@@ -1001,7 +1001,7 @@ static fp8_status cached_shape(const char* call, const fp8_kv_cache* c, int64_t 
         return fail(FP8_ERR_UNSUPPORTED, std::string(call) + ": more than 2^16 heads or 2^31 rows");
     if (!fp8k::attention_cached_grid_ok(c->tokens, (int)(heads_q / c->heads), (int)c->heads, (int)c->batch,
                                         (int)c->blocks, shift))
-        return fail(FP8_ERR_UNSUPPORTED, std::string(call) + ": too many rows for one launch, or 2^36 keys of all heads and sequences");
+        return fail(FP8_ERR_UNSUPPORTED, std::string(call) + ": too many rows for one launch, or too many keys of all sequences");
     return FP8_OK;
 }
 

@@ -1,7 +1,7 @@
 // attention_cached.hip -- softmax attention over a paged cache of E4M3 keys and values
 // (kv_cache.hip), for gfx950.
 //
-// Query i of a sequence's n stands at position held - n + i and sees the keys at positions
+// Query i of a sequence's n stands at position length - n + i and sees the keys at positions
 // up to its own (causal) or all that are held:
 //   s = scale q . k,  p = exp(s - lse),  lse = log sum exp(s),  out = sum p v
 // with k and v the codes times the power of two of their page and head.  Codes become bf16
@@ -75,6 +75,7 @@ __device__ __forceinline__ float sum4(float v)
 // A sequence's queries and keys.
 struct Sequence {
     int from, queries, held;
+    int first;                             // the first query's position
 };
 
 __device__ __forceinline__ Sequence sequence(const CacheArgs& a, int b)
@@ -87,8 +88,16 @@ __device__ __forceinline__ Sequence sequence(const CacheArgs& a, int b)
         s.queries = (int)(a.tokens / a.batch);
         s.from = b * s.queries;
     }
-    s.held = held_tokens(a.lengths[b], a.blocks, a.shift);
+    const int length = a.lengths[b];
+    s.held = held_tokens(length, a.blocks, a.shift);
+    s.first = first_position(length, s.queries, a.blocks, a.shift);
     return s;
+}
+
+// Keys that its query i sees.
+__device__ __forceinline__ int seen(const CachedAttentionArgs& a, int held, int first, int i)
+{
+    return a.causal ? (int)min((int64_t)held, (int64_t)first + i + 1) : held;
 }
 
 __device__ __forceinline__ bool few(const CachedAttentionArgs& a, const Sequence& s) { return s.queries * a.group <= kFew; }
@@ -301,14 +310,13 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
 
     while (true) {
         const int from = __builtin_amdgcn_readfirstlane(s.from), queries = __builtin_amdgcn_readfirstlane(s.queries);
-        const int held = __builtin_amdgcn_readfirstlane(s.held);
+        const int held = __builtin_amdgcn_readfirstlane(s.held), first = __builtin_amdgcn_readfirstlane(s.first);
         const int upto = __builtin_amdgcn_readfirstlane(min(steps, done + end - at));
         // the piece: the keys' steps step0 .. last - 1 of all
         const int step0 = max(done - kPiece, 0), last = max(upto - kPiece, 0), all_steps = steps - kPiece;
         if (last > step0) {
         const int rows = queries * a.group, qi = m / a.group, hq = head * a.group + m - qi * a.group;
-        const int shift = held - queries;
-        const int see = a.causal ? min(held, qi + shift + 1) : held, see_first = a.causal ? min(held, shift + 1) : held;
+        const int see = seen(a, held, first, qi), see_first = seen(a, held, first, 0);
 
         // the queries' operand: lane's column m, elements of chunk g as the keys' lanes have them
         Frag q[DT / 32];
@@ -437,11 +445,14 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
                 }
 #pragma unroll
             for (int n = 0; n < 4; n += 2) {
-                Frag f;
-                f.w[0] = bf16_pair(p[n][0], p[n][1]);
-                f.w[1] = bf16_pair(p[n][2], p[n][3]);
-                f.w[2] = bf16_pair(p[n + 1][0], p[n + 1][1]);
-                f.w[3] = bf16_pair(p[n + 1][2], p[n + 1][3]);
+                // p as two bf16, the second what the first's rounding left off: the matrix units have the time
+                Frag f, f2;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float y = p[n + i / 2][2 * (i % 2)], z = p[n + i / 2][2 * (i % 2) + 1];
+                    f.w[i] = bf16_pair(y, z);
+                    f2.w[i] = bf16_pair(y - bf16_lo(f.w[i]), z - bf16_hi(f.w[i]));
+                }
 #pragma unroll
                 for (int w = 0; w < DT / 64; ++w) {
                     uint32_t lo[4], hi[4];
@@ -455,6 +466,7 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
                         v.w[2] = values2<false>(hi[i], v_scale[n + 1]);
                         v.w[3] = values2<true>(hi[i], v_scale[n + 1]);
                         o[4 * w + i] = mma16(v, f, o[4 * w + i]);
+                        o[4 * w + i] = mma16(v, f2, o[4 * w + i]);
                     }
                 }
             }
@@ -554,7 +566,7 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
         const Sequence s = sequence(c, b);
         const int n = row_tiles(a, s);
         mine += n;
-        mine_steps += (int64_t)n * ((max(s.held - (a.causal ? s.queries / 2 : 0), 0) + kKeys - 1) / kKeys);
+        mine_steps += (int64_t)n * ((max(seen(a, s.held, s.first, s.queries / 2), 0) + kKeys - 1) / kKeys);
     }
     const Sums all = block_sums(mine, mine_steps, sums);
     Join* const joins = reinterpret_cast<Join*>(a.joins) + a.workers;
@@ -585,20 +597,20 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
     }
     __syncthreads();
     const int b = __builtin_amdgcn_readfirstlane(found[0]);
-    const int first = __builtin_amdgcn_readfirstlane(found[1]) * kOwn;
+    const int row0 = __builtin_amdgcn_readfirstlane(found[1]) * kOwn;
     const Sequence s = sequence(c, b);
     const int from = __builtin_amdgcn_readfirstlane(s.from), queries = __builtin_amdgcn_readfirstlane(s.queries);
     const int held = __builtin_amdgcn_readfirstlane(s.held);
-    const int rows = queries * a.group, r_wave = first + wave * 32, ri = r_wave + (lane & 31);
+    const int rows = queries * a.group, r_wave = row0 + wave * 32, ri = r_wave + (lane & 31);
     const int q_wave = r_wave / a.group, q_last = (r_wave + 31) / a.group;
     const int qi = ri / a.group, hq = head * a.group + ri - qi * a.group;
     const bool valid = ri < rows;
-    const int shift = held - queries;
+    const int first = __builtin_amdgcn_readfirstlane(s.first);
     // keys seen: by this lane's query, by the wave's first and last, by the workgroup's last
-    const int see = a.causal ? min(held, qi + shift + 1) : held;
-    const int see_first = a.causal ? min(held, q_wave + shift + 1) : held;
-    const int see_last = r_wave >= rows ? 0 : a.causal ? min(held, q_last + shift + 1) : held;
-    const int end = a.causal ? min(held, min((first + kOwn - 1) / a.group + 1, queries) + shift) : held;
+    const int see = seen(a, held, first, qi);
+    const int see_first = seen(a, held, first, q_wave);
+    const int see_last = r_wave >= rows ? 0 : seen(a, held, first, q_last);
+    const int end = seen(a, held, first, min((row0 + kOwn - 1) / a.group, queries - 1));
     const int steps = end > 0 ? (end + kKeys - 1) / kKeys : 0;
     const int s_begin = (int)((int64_t)steps * split / splits), s_end = (int)((int64_t)steps * (split + 1) / splits);
 
@@ -683,7 +695,7 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
         store_partial<DT>(o, a.partial + row * DT, DT, valid);
         if (valid && h == 0) a.tops[row] = make_float2(m == -kInf ? -kInf : mc, l);
         if (split == 0 && threadIdx.x == 0)
-            joins[t * c.heads + head] = Join{b, head, first, splits, slot0, slot0 + kOwn / 16, kOwn / 16, 0};
+            joins[t * c.heads + head] = Join{b, head, row0, splits, slot0, slot0 + kOwn / 16, kOwn / 16, 0};
         return 0;
     }
     const uint32_t top = store_own<DT>(o, inverse(l), a.out + (int64_t)(from + qi) * a.out_row + (int64_t)hq * a.out_head, c.d, valid);

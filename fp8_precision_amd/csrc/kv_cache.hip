@@ -80,7 +80,7 @@ __device__ __forceinline__ Piece find_piece(const CacheArgs& a, int64_t item)
         length = __builtin_amdgcn_readlane(n, l);
         local = item - piece_base(from, p.b, a.shift);
     }
-    p.at = cache_piece(count, held_tokens(length, a.blocks, a.shift), local, a.shift);
+    p.at = cache_piece(count, first_position(length, count, a.blocks, a.shift), local, a.shift);
     p.token = (int64_t)from + p.at.skip;
     return p;
 }
@@ -88,7 +88,7 @@ __device__ __forceinline__ Piece find_piece(const CacheArgs& a, int64_t item)
 // Its page in the pool; -1: none.
 __device__ __forceinline__ int64_t page_of(const CacheArgs& a, const Piece& p)
 {
-    if (p.at.block < 0) return -1;
+    if (p.at.block < 0 || p.at.block >= a.blocks) return -1;
     const int at = a.table[(int64_t)p.b * a.blocks + p.at.block];
     return at >= 0 && at < a.pages ? at : -1;
 }

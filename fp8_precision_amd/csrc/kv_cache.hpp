@@ -2,12 +2,12 @@
 // the kernels' addressing have to agree on, in plain C++ (constexpr functions are the
 // device's too).
 //
-// A sequence holds `held` tokens; a call's `count` tokens of it are the last ones, at the
-// positions held - count .. held - 1 (those below 0 have no place).  They are worked on a
-// block of one page at a time: piece `local` of a sequence is its block floor(first / page)
-// + local.  So that a workgroup finds its sequence without a sum over those before it, the
-// pieces of sequence b begin at (start / page) + 2 b, with start the sequence's first token
-// in the call: n tokens touch at most n / page + 2 pages.
+// The call's `count` tokens of a sequence are the last ones of its length: they stand at the
+// positions first .. first + count - 1.  Those below 0 or past the sequence's row of the table
+// have no place.  They are worked on a block of one page at a time: piece `local` of a
+// sequence is its block floor(first / page) + local.  So that a workgroup finds its sequence
+// without a sum over those before it, the pieces of sequence b begin at (start / page) + 2 b,
+// with start the sequence's first token in the call: n tokens touch at most n / page + 2 pages.
 #pragma once
 #include <stdint.h>
 
@@ -19,11 +19,22 @@ constexpr int64_t piece_bound(int64_t tokens, int64_t batch, int shift) { return
 // Pages that n tokens touch at most, wherever they begin.
 constexpr int64_t pieces_of(int64_t n, int shift) { return ((n + (1 << shift) - 2) >> shift) + 1; }
 
-// Tokens that a sequence holds, whatever `length` says: none, to what its row of the table can.
+// Tokens that a row of the table has places for (2^30 at most).
+constexpr int row_capacity(int blocks, int shift) { return blocks << shift; }
+
+// Of a sequence's tokens, those that can have a place, whatever `length` says.
 constexpr int held_tokens(int length, int blocks, int shift)
 {
-    const int64_t most = (int64_t)blocks << shift;
-    return length < 0 ? 0 : length > most ? (int)most : length;
+    const int most = row_capacity(blocks, shift);
+    return length < 0 ? 0 : length > most ? most : length;
+}
+
+// The position of the first of its `count` tokens in the call; from the end of the row on all
+// are alike, and are counted as there.
+constexpr int first_position(int length, int count, int blocks, int shift)
+{
+    const int most = row_capacity(blocks, shift), first = (length < 0 ? 0 : length) - count;
+    return first > most ? most : first;
 }
 
 struct CachePiece {
@@ -33,11 +44,11 @@ struct CachePiece {
     int skip;           // the first token's number among the call's tokens of this sequence
 };
 
-constexpr CachePiece cache_piece(int count, int held, int64_t local, int shift)
+// Every token of the call has a piece, those without a place too: their block lies outside the row.
+constexpr CachePiece cache_piece(int count, int first, int64_t local, int shift)
 {
-    const int64_t first = (int64_t)held - count, block = (first >> shift) + local;
-    const int64_t a = block << shift, b = a + (1 << shift);
-    const int64_t lo = first > a ? first : a, hi = held < b ? held : b;
+    const int64_t block = ((int64_t)first >> shift) + local, a = block << shift, b = a + (1 << shift);
+    const int64_t end = (int64_t)first + count, lo = first > a ? first : a, hi = end < b ? end : b;
     if (count <= 0 || lo >= hi) return {block, 0, 0, 0};
     return {block, (int)(lo - a), (int)(hi - lo), (int)(lo - first)};
 }

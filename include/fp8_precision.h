@@ -633,9 +633,9 @@ fp8_status fp8_attention_backward(const fp8_attention_shape* shape, const fp8_he
  * A call works on `tokens` packed tokens: sequence b's are the last ones that it holds, at
  * positions lengths[b] - n .. lengths[b] - 1.  So a step of generation adds its tokens to
  * lengths, writes their keys and values, and attends with their queries, all with one struct.
- * Bounds and lengths outside what the tensors and the table hold are held to it; a token at
- * a negative position, or in a block whose table entry is no page of the pool, has no place.
- * No byte outside the tensors is read or written.
+ * Bounds outside [0, tokens] are held to it, and a length below 0 counts as 0.  A token at a
+ * negative position, past the blocks of its row of the table, or in a block whose entry is
+ * no page of the pool, has no place.  No byte outside the tensors is read or written.
  */
 typedef struct fp8_kv_cache {
     uint8_t *k, *v;               /* [pages, heads, page_tokens, head_dim], 16-byte aligned */
@@ -650,7 +650,7 @@ typedef struct fp8_kv_cache {
     int64_t page_tokens;          /* 16, 32, 64 or 128 */
     int64_t head_dim;             /* a multiple of 8, 8 .. 128 */
     int64_t batch;                /* sequences, 1 .. 2^20 */
-    int64_t blocks;               /* entries of a row of the table, 1 or more; blocks page_tokens below 2^31 */
+    int64_t blocks;               /* entries of a row of the table, 1 or more; blocks page_tokens at most 2^30 */
     int64_t tokens;               /* of the call, 1 .. 2^31 - 1; a multiple of batch without bounds */
 } fp8_kv_cache;
 
@@ -680,13 +680,15 @@ fp8_status fp8_kv_cache_read(const fp8_kv_cache* cache, const fp8_head_tensor* k
 /*
  * Attention of the call's tokens over the cache: query i of a sequence's n stands at position
  * lengths - n + i and sees the keys at positions up to its own (causal) or all that are held,
- * as in fp8_attention_forward, whose formulas, head sharing and roundings these are.  A
- * query that sees nothing has out = 0, lse = -inf.  Keys and values without a place are
- * zeros (they are seen).  A NaN in a value may reach every query of its sequence.
+ * as in fp8_attention_forward, whose formulas and head sharing these are.  Probabilities are
+ * rounded to bf16 for the product with v (to twice its precision where a sequence has at most
+ * 16 rows, n heads_q / heads).  A query that sees nothing has out = 0, lse = -inf.  Keys and
+ * values in a block of the row whose entry is no page are zeros, and are seen; past the row
+ * there are none.  A NaN in a key or value may reach every query of its sequence.
  *
  *   q        bf16 [tokens, heads_q, head_dim] with its own strides;  out  as q
  *   heads_q  a multiple of the cache's heads, at most 2^16; tokens heads_q below 2^31, and
- *            batch heads blocks page_tokens below 2^36
+ *            batch heads (blocks page_tokens / 64 + 6) below 2^31 - 2^20
  *   lse      fp32 [heads_q, tokens]
  *   absmax   fp32 scalar or NULL: becomes max(*absmax, max |out|), out as stored
  *   workspace, workspace_bytes   device memory, 16-byte aligned, of at least the size that

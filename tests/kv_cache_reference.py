@@ -24,20 +24,31 @@ def least_exponent(x):
 
 
 def held(lengths, table, page):
+    """Tokens that can have a place."""
     return [min(max(int(n), 0), table.shape[1] * page) for n in lengths]
+
+
+def place(pool, table, b, p):
+    """(page, slot) of position p of sequence b, or None."""
+    page = pool["k"].shape[2]
+    if not 0 <= p < table.shape[1] * page:
+        return None
+    at = int(table[b, p // page])
+    return (at, p % page) if 0 <= at < pool["k"].shape[0] else None
 
 
 def write(pool, table, lengths, news, k, v):
     """pool: dict of CPU tensors k, v, k_scale, v_scale, changed in place; news: new tokens per sequence."""
     pages, heads, page, d = pool["k"].shape
     first = 0
-    for b, (n, total) in enumerate(zip(news, held(lengths, table, page))):
-        places = [(i, total - n + i) for i in range(n) if total - n + i >= 0]
-        for block in sorted({p // page for _, p in places}):
+    for b, (n, total) in enumerate(zip(news, lengths)):
+        places = {}
+        for i in range(n):
+            p = max(int(total), 0) - n + i
+            if place(pool, table, b, p):
+                places.setdefault(p // page, []).append((i, p % page))
+        for block, mine in places.items():
             at = int(table[b, block])
-            if not 0 <= at < pages:
-                continue
-            mine = [(i, p % page) for i, p in places if p // page == block]
             rows, slots = [first + i for i, _ in mine], [s for _, s in mine]
             for name, x in (("k", k), ("v", v)):
                 codes, scale = pool[name], pool[name + "_scale"]
@@ -61,13 +72,12 @@ def read(pool, table, lengths, news, name):
     pages, heads, page, d = pool[name].shape
     out = torch.zeros(sum(news), heads, d, dtype=F64)
     first = 0
-    for b, (n, total) in enumerate(zip(news, held(lengths, table, page))):
+    for b, (n, total) in enumerate(zip(news, lengths)):
         for i in range(n):
-            p = total - n + i
-            at = int(table[b, p // page]) if p >= 0 else -1
-            if 0 <= at < pages:
-                e = (pool[name + "_scale"][at].to(torch.int64) - 127).clamp(-100, 119)
-                out[first + i] = decode(pool[name][at, :, p % page]) * torch.exp2(e.to(F64))[:, None]
+            where = place(pool, table, b, max(int(total), 0) - n + i)
+            if where:
+                e = (pool[name + "_scale"][where[0]].to(torch.int64) - 127).clamp(-100, 119)
+                out[first + i] = decode(pool[name][where[0], :, where[1]]) * torch.exp2(e.to(F64))[:, None]
         first += n
     return out
 

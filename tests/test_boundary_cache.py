@@ -62,7 +62,7 @@ SHAPES = [
     (UNSUPPORTED, dict(page_tokens=48)), (UNSUPPORTED, dict(page_tokens=8)), (UNSUPPORTED, dict(page_tokens=256)),
     (UNSUPPORTED, dict(head_dim=60)), (UNSUPPORTED, dict(head_dim=136)), (UNSUPPORTED, dict(pages=1 << 31)),
     (UNSUPPORTED, dict(heads=1 << 17)), (UNSUPPORTED, dict(batch=(1 << 20) + 1)), (UNSUPPORTED, dict(tokens=1 << 31)),
-    (UNSUPPORTED, dict(blocks=1 << 25)),                 # 2^31 tokens of 64 to a page
+    (UNSUPPORTED, dict(blocks=(1 << 24) + 1)),           # 2^30 tokens and a page of 64
     (INVALID, dict(bounds=None)),                        # 7 tokens of 3 sequences
 ]
 POINTERS = [(INVALID, {n: None}) for n in ("k", "v", "k_scale", "v_scale", "table", "lengths")] + \
@@ -101,7 +101,8 @@ def test_attention(lib):
         assert size(cache(**change)) == status, change
     assert size(hq=3) == INVALID and size(hq=0) == INVALID and size(hq=1 << 17) == UNSUPPORTED
     assert size(cache(tokens=(1 << 31) - 1)) == UNSUPPORTED          # 2^33 rows
-    assert size(cache(batch=1 << 20, blocks=1 << 24)) == UNSUPPORTED and b"2^36" in lib.fp8_last_error()
+    assert size(cache(batch=1 << 20, blocks=1 << 9)) == OK
+    assert size(cache(batch=1 << 20, blocks=1 << 10)) == UNSUPPORTED and b"too many" in lib.fp8_last_error()
     assert size(cache(blocks=100)) == OK
     need = n.value
     assert need > 0

@@ -32,7 +32,7 @@ int main(int, char** argv)
         for (int b = 0; b < batch; ++b) cu[b + 1] = cu[b] + (even ? each : pick(0, 2) ? pick(0, 5) : pick(0, 3 * page));
         int tokens = cu[batch] + (even ? 0 : pick(0, 3));
         if (tokens < 1) tokens = 1;
-        for (int b = 0; b < batch; ++b) len[b] = pick(0, blocks * page);
+        for (int b = 0; b < batch; ++b) len[b] = pick(0, blocks * page + (pick(0, 3) ? 0 : 40));
         if (wild && !even)
             for (int b = 0; b <= batch; ++b) {
                 if (pick(0, 3) == 0) cu[b] = pick(-1000, tokens + 1000);
@@ -59,22 +59,24 @@ int main(int, char** argv)
                 if (count < 0) count = 0;
                 local = item - piece_base(from, b, shift);
             }
-            const int held = held_tokens(len[b], blocks, shift);
-            const CachePiece p = cache_piece(count, held, local, shift);
+            const int first = first_position(len[b], count, blocks, shift), length = len[b] < 0 ? 0 : len[b];
+            const CachePiece p = cache_piece(count, first, local, shift);
             if (p.count <= 0) continue;
-            bad += p.slot < 0 || p.slot + p.count > page || p.block >= blocks || p.skip < 0 || p.skip + p.count > count;
+            bad += p.slot < 0 || p.slot + p.count > page || p.skip < 0 || p.skip + p.count > count;
+            // a token has a place where its position lies in the row, and there alone
+            bad += (p.block >= 0 && p.block < blocks) != (length - count + p.skip >= 0 && length - count + p.skip < blocks * page);
             bad += from + p.skip + p.count > tokens;
             for (int i = 0; i < p.count; ++i) {
                 const int64_t pos = p.block * page + p.slot + i;
-                bad += pos != (int64_t)held - count + p.skip + i;
+                if (p.block >= 0 && p.block < blocks) bad += pos != (int64_t)length - count + p.skip + i;
                 bad += hits[{b, (int)pos}]++ != 0;
                 ++seen;
             }
         }
         if (!wild || even)                                 // nothing is missed
             for (int b = 0; b < batch; ++b) {
-                const int held = held_tokens(len[b], blocks, shift), n = cu[b + 1] - cu[b];
-                for (int pos = held - n; pos < held; ++pos) bad += hits[{b, pos}] != 1;
+                const int n = cu[b + 1] - cu[b];
+                for (int pos = len[b] - n; pos < len[b] && pos < blocks * page; ++pos) bad += hits[{b, pos}] != 1;
             }
     }
     printf("%ld tokens placed, %ld wrong\n", seen, bad);
