@@ -30,7 +30,7 @@ typedef unsigned int au32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
 constexpr int kWaves = 4;
-constexpr int kFew = 16;                   // rows of a sequence that is read in shares
+constexpr int kFew = 16;                   // rows of a sequence that is read in shares, or twice as many (a.few)
 constexpr int kOwn = 128;                  // rows of a tile: 32 per wave
 constexpr int kLeastSteps = kWaves;        // of a share
 constexpr int kPiece = 4;                  // what a head of a sequence costs besides its steps, in steps
@@ -100,7 +100,7 @@ __device__ __forceinline__ int seen(const CachedAttentionArgs& a, int held, int 
     return a.causal ? (int)min((int64_t)held, (int64_t)first + i + 1) : held;
 }
 
-__device__ __forceinline__ bool few(const CachedAttentionArgs& a, const Sequence& s) { return s.queries * a.group <= kFew; }
+__device__ __forceinline__ bool few(const CachedAttentionArgs& a, const Sequence& s) { return s.queries * a.group <= a.few; }
 
 // Steps of one head of a sequence of few rows: kPiece, in which nothing is done, and its keys';
 // one of these at least, for the rows that see nothing.
@@ -255,7 +255,7 @@ __device__ __forceinline__ uint32_t top_of(uint32_t w, uint32_t top)
 // 4 codes of one column, taken from 8 rows by byte permutations.  A step's keys are loaded
 // into the registers of the last one's as soon as its scores are there, the values after
 // its output.
-template <int DT, bool FULL>
+template <int DT, bool FULL, int R>
 __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, int worker, uint8_t* lds, int (*sums)[4], int* found)
 {
     constexpr int kPer = DT / 16;          // values' elements of a lane, and the product's tiles
@@ -315,25 +315,35 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
         // the piece: the keys' steps step0 .. last - 1 of all
         const int step0 = max(done - kPiece, 0), last = max(upto - kPiece, 0), all_steps = steps - kPiece;
         if (last > step0) {
-        const int rows = queries * a.group, qi = m / a.group, hq = head * a.group + m - qi * a.group;
-        const int see = seen(a, held, first, qi), see_first = seen(a, held, first, 0);
+        const int rows = queries * a.group, see_first = seen(a, held, first, 0);
 
-        // the queries' operand: lane's column m, elements of chunk g as the keys' lanes have them
-        Frag q[DT / 32];
+        // the queries' operands: lane's column m, elements of chunk g as the keys' lanes have them
+        Frag q[R][DT / 32];
+        int see[R];
 #pragma unroll
-        for (int i = 0; i < DT / 32; ++i) {
-            q[i].u = au32x4{0, 0, 0, 0};
-            const int e = 64 * (i / 2) + 16 * g + 8 * (i % 2);
-            if (m < rows && (FULL || e < c.d))
-                q[i].u = *reinterpret_cast<const au32x4*>(a.q + (int64_t)(from + qi) * a.q_row + (int64_t)hq * a.q_head + e);
+        for (int r = 0; r < R; ++r) {
+            const int row = 16 * r + m, qi = row / a.group, hq = head * a.group + row - qi * a.group;
+            see[r] = seen(a, held, first, qi);
+#pragma unroll
+            for (int i = 0; i < DT / 32; ++i) {
+                q[r][i].u = au32x4{0, 0, 0, 0};
+                const int e = 64 * (i / 2) + 16 * g + 8 * (i % 2);
+                if (row < rows && (FULL || e < c.d))
+                    q[r][i].u = *reinterpret_cast<const au32x4*>(a.q + (int64_t)(from + qi) * a.q_row + (int64_t)hq * a.q_head + e);
+            }
         }
         // waited for here: at its first use, in the loop, the wait would be one for every load in flight
+        af32x4 o[R][kPer];
+        float top[R], sum[R];
 #pragma unroll
-        for (int i = 0; i < DT / 32; ++i) asm volatile("" : "+v"(q[i].u));
-        af32x4 o[kPer];
+        for (int r = 0; r < R; ++r) {
 #pragma unroll
-        for (int t = 0; t < kPer; ++t) o[t] = af32x4{0, 0, 0, 0};
-        float top = -kInf, sum = 0.0f;
+            for (int i = 0; i < DT / 32; ++i) asm volatile("" : "+v"(q[r][i].u));
+#pragma unroll
+            for (int t = 0; t < kPer; ++t) o[r][t] = af32x4{0, 0, 0, 0};
+            top[r] = -kInf;
+            sum[r] = 0.0f;
+        }
 
         // Codes of 64 keys, as loaded.  Of each block of 16 keys a lane has DT / 4 codes of key
         // m (16 of each 64, chunk g), and DT / 16 codes (chunk m) of each of the values 4 g + i.
@@ -395,10 +405,11 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
         }
         for (int t = step0 + wave; t < last; t += kWaves) {
             const int j0 = t * kKeys;
-            af32x4 p[4];
+            af32x4 p[R][4];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                p[n] = af32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int r = 0; r < R; ++r) p[r][n] = af32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int i = 0; i < DT / 32; ++i) {
                     Frag k;
@@ -407,52 +418,58 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
                         k.w[2 * j] = values2<false>(ck[n][2 * i + j], x[n].k_scale);
                         k.w[2 * j + 1] = values2<true>(ck[n][2 * i + j], x[n].k_scale);
                     }
-                    p[n] = mma16(k, q[i], p[n]);
+#pragma unroll
+                    for (int r = 0; r < R; ++r) p[r][n] = mma16(k, q[r][i], p[r][n]);
                 }
             }
             // (past the last step from buffers of no rows: with loads that some path leaves out, the
             // compiler would wait for the values together with the next keys)
             __builtin_amdgcn_sched_barrier(0);
             load_k(j0 + kWaves * kKeys);
-            if (j0 + kKeys > see_first) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (j0 + kKeys > see_first) {
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (j0 + 16 * n + 4 * g + i >= see[r]) p[r][n][i] = -kInf;
+                }
+                float up = fmaxf(fmaxf(p[r][0][0], p[r][0][1]), fmaxf(p[r][0][2], p[r][0][3]));
+#pragma unroll
+                for (int n = 1; n < 4; ++n) up = fmaxf(up, fmaxf(fmaxf(p[r][n][0], p[r][n][1]), fmaxf(p[r][n][2], p[r][n][3])));
+                up = max4(up);
+                if (__any(up > top[r] + far)) {            // top = -inf: any key seen
+                    up = fmaxf(up, top[r]);
+                    const float by = up == -kInf ? 1.0f : __builtin_amdgcn_exp2f((top[r] - up) * scale2);
+                    sum[r] *= by;
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) o[r][i][j] *= by;
+                    top[r] = up;
+                }
+                const float use = top[r] == -kInf ? 0.0f : top[r] * scale2;
 #pragma unroll
                 for (int n = 0; n < 4; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (j0 + 16 * n + 4 * g + i >= see) p[n][i] = -kInf;
+                    for (int i = 0; i < 4; ++i) {
+                        p[r][n][i] = __builtin_amdgcn_exp2f(fmaf(p[r][n][i], scale2, -use));
+                        sum[r] += p[r][n][i];
+                    }
             }
-            float up = fmaxf(fmaxf(p[0][0], p[0][1]), fmaxf(p[0][2], p[0][3]));
-#pragma unroll
-            for (int n = 1; n < 4; ++n) up = fmaxf(up, fmaxf(fmaxf(p[n][0], p[n][1]), fmaxf(p[n][2], p[n][3])));
-            up = max4(up);
-            if (__any(up > top + far)) {                   // top = -inf: any key seen
-                up = fmaxf(up, top);
-                const float by = up == -kInf ? 1.0f : __builtin_amdgcn_exp2f((top - up) * scale2);
-                sum *= by;
-#pragma unroll
-                for (int i = 0; i < kPer; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) o[i][j] *= by;
-                top = up;
-            }
-            const float use = top == -kInf ? 0.0f : top * scale2;
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    p[n][i] = __builtin_amdgcn_exp2f(fmaf(p[n][i], scale2, -use));
-                    sum += p[n][i];
-                }
 #pragma unroll
             for (int n = 0; n < 4; n += 2) {
-                // p as two bf16, the second what the first's rounding left off: the matrix units have the time
-                Frag f, f2;
+                // p; of 16 rows as two bf16, the second what the first's rounding left off: the matrix units have the time
+                Frag f[R], f2;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float y = p[n + i / 2][2 * (i % 2)], z = p[n + i / 2][2 * (i % 2) + 1];
-                    f.w[i] = bf16_pair(y, z);
-                    f2.w[i] = bf16_pair(y - bf16_lo(f.w[i]), z - bf16_hi(f.w[i]));
-                }
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float y = p[r][n + i / 2][2 * (i % 2)], z = p[r][n + i / 2][2 * (i % 2) + 1];
+                        f[r].w[i] = bf16_pair(y, z);
+                        if (R == 1) f2.w[i] = bf16_pair(y - bf16_lo(f[r].w[i]), z - bf16_hi(f[r].w[i]));
+                    }
 #pragma unroll
                 for (int w = 0; w < DT / 64; ++w) {
                     uint32_t lo[4], hi[4];
@@ -465,70 +482,74 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
                         v.w[1] = values2<true>(lo[i], v_scale[n]);
                         v.w[2] = values2<false>(hi[i], v_scale[n + 1]);
                         v.w[3] = values2<true>(hi[i], v_scale[n + 1]);
-                        o[4 * w + i] = mma16(v, f, o[4 * w + i]);
-                        o[4 * w + i] = mma16(v, f2, o[4 * w + i]);
+#pragma unroll
+                        for (int r = 0; r < R; ++r) o[r][4 * w + i] = mma16(v, f[r], o[r][4 * w + i]);
+                        if (R == 1) o[0][4 * w + i] = mma16(v, f2, o[0][4 * w + i]);
                     }
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
             load_v();
         }
-        sum = sum4(sum);
-
-        // the waves' sums together: o[t][r] is element kPer (4 g + r) + t of row m
-        if (g == 0) {
-            s_top[wave * kFew + m] = top;
-            s_sum[wave * kFew + m] = sum;
-        }
+        // the waves' sums together, 16 rows at a time: o[t][i] is element kPer (4 g + i) + t of row m
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int t = 0; t < kPer; t += 4)
-                *reinterpret_cast<af32x4*>(s_out + (wave * kFew + m) * kRow + kPer * (4 * g + i) + t) =
-                    af32x4{o[t][i], o[t + 1][i], o[t + 2][i], o[t + 3][i]};
-        __syncthreads();
-        const int n = threadIdx.x / 16, e = threadIdx.x % 16 * kPer;
-        if (n < rows) {
-            const int q2 = n / a.group, h2 = head * a.group + n - q2 * a.group;
-            float best = -kInf, l = 0.0f, y[kPer];
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) best = fmaxf(best, s_top[w * kFew + n]);
-            const float base = best == -kInf ? 0.0f : best;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) y[i] = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                const float by = __builtin_amdgcn_exp2f((s_top[w * kFew + n] - base) * scale2);
-                l = fmaf(s_sum[w * kFew + n], by, l);
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) y[i] = fmaf(s_out[(w * kFew + n) * kRow + e + i], by, y[i]);
+        for (int r = 0; r < R; ++r) {
+            if (R > 1 && r > 0) __syncthreads();
+            sum[r] = sum4(sum[r]);
+            if (g == 0) {
+                s_top[wave * kFew + m] = top[r];
+                s_sum[wave * kFew + m] = sum[r];
             }
-            if (step0 == 0 && last == all_steps) {
-                const float by = inverse(l);
-                uint32_t w[kPer / 2];
-                if (FULL || e < c.d) {
 #pragma unroll
-                    for (int i = 0; i < kPer / 2; ++i) {
-                        w[i] = bf16_pair(y[2 * i] * by, y[2 * i + 1] * by);
-                        top_out = top_of(w[i], top_out);
-                    }
-                    uint16_t* to = a.out + (int64_t)(from + q2) * a.out_row + (int64_t)h2 * a.out_head + e;
-                    if constexpr (kPer == 8) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
-                    else *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int t = 0; t < kPer; t += 4)
+                    *reinterpret_cast<af32x4*>(s_out + (wave * kFew + m) * kRow + kPer * (4 * g + i) + t) =
+                        af32x4{o[r][t][i], o[r][t + 1][i], o[r][t + 2][i], o[r][t + 3][i]};
+            __syncthreads();
+            const int n = threadIdx.x / 16, e = threadIdx.x % 16 * kPer;
+            if (16 * r + n < rows) {
+                const int q2 = (16 * r + n) / a.group, h2 = head * a.group + 16 * r + n - q2 * a.group;
+                float best = -kInf, l = 0.0f, y[kPer];
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) best = fmaxf(best, s_top[w * kFew + n]);
+                const float base = best == -kInf ? 0.0f : best;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) y[i] = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) {
+                    const float by = __builtin_amdgcn_exp2f((s_top[w * kFew + n] - base) * scale2);
+                    l = fmaf(s_sum[w * kFew + n], by, l);
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) y[i] = fmaf(s_out[(w * kFew + n) * kRow + e + i], by, y[i]);
                 }
-                if (e == 0)
-                    a.lse[(int64_t)h2 * c.tokens + from + q2] =
-                        l == 0.0f ? -kInf : (base * scale2 + __builtin_amdgcn_logf(l)) * kLn2;
-            } else {
-                const int64_t slot = 2 * (int64_t)worker + (step0 == 0 ? 1 : 0);
-                float* to = a.partial + (slot * 16 + n) * DT + e;
+                if (step0 == 0 && last == all_steps) {
+                    const float by = inverse(l);
+                    uint32_t w[kPer / 2];
+                    if (FULL || e < c.d) {
 #pragma unroll
-                for (int i = 0; i < kPer; i += 4) *reinterpret_cast<af32x4*>(to + i) = af32x4{y[i], y[i + 1], y[i + 2], y[i + 3]};
-                if (e == 0) a.tops[slot * 16 + n] = make_float2(best == -kInf ? -kInf : best * scale2, l);
+                        for (int i = 0; i < kPer / 2; ++i) {
+                            w[i] = bf16_pair(y[2 * i] * by, y[2 * i + 1] * by);
+                            top_out = top_of(w[i], top_out);
+                        }
+                        uint16_t* to = a.out + (int64_t)(from + q2) * a.out_row + (int64_t)h2 * a.out_head + e;
+                        if constexpr (kPer == 8) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+                        else *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+                    }
+                    if (e == 0)
+                        a.lse[(int64_t)h2 * c.tokens + from + q2] =
+                            l == 0.0f ? -kInf : (base * scale2 + __builtin_amdgcn_logf(l)) * kLn2;
+                } else {
+                    const int64_t slot = (2 * (int64_t)worker + (step0 == 0 ? 1 : 0)) * R + r;
+                    float* to = a.partial + (slot * 16 + n) * DT + e;
+#pragma unroll
+                    for (int i = 0; i < kPer; i += 4) *reinterpret_cast<af32x4*>(to + i) = af32x4{y[i], y[i + 1], y[i + 2], y[i + 3]};
+                    if (e == 0) a.tops[slot * 16 + n] = make_float2(best == -kInf ? -kInf : best * scale2, l);
+                }
             }
         }
         if (threadIdx.x == 0 && step0 == 0 && last < all_steps)
-            joins[worker] = Join{b, head, 0, (at - done + steps - 1) / share - worker + 1, 2 * worker + 1, 2 * worker + 2, 2, 0};
+            joins[worker] = Join{b, head, 0, (at - done + steps - 1) / share - worker + 1, (2 * worker + 1) * R, (2 * worker + 2) * R, 2 * R, 0};
         }
         at += upto - done;
         if (at >= end) break;
@@ -708,8 +729,8 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
 
 // KINDS 1: sequences of few rows alone; 2: of more alone; 3: both, their workgroups in turn, 8
 // by 8 (workgroups are dealt round-robin to the XCDs).
-template <int DT, bool FULL, int KINDS>
-__global__ void __launch_bounds__(kThreads, 2) attention_cached_kernel(const CachedAttentionArgs a)
+template <int DT, bool FULL, int KINDS, int R>
+__global__ void __launch_bounds__(kThreads, R == 1 ? 2 : 1) attention_cached_kernel(const CachedAttentionArgs a)
 {
     constexpr int kBytes = KINDS == 1 ? share_lds<DT>() : std::max(share_lds<DT>(), tile_lds<DT>());
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kBytes];
@@ -722,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_cached_kernel(const Cac
         block = i >= 2 * a.workers ? i - a.workers : pair * 8 + (i & 7);
     }
     uint32_t top;
-    if (KINDS != 2 && share) top = attend_share<DT, FULL>(a, block, lds, sums, found);
+    if (KINDS != 2 && share) top = attend_share<DT, FULL, R>(a, block, lds, sums, found);
     else top = attend_rows<DT, FULL>(a, block, lds, sums, found);
     if (a.absmax) block_max_to_global(top, a.absmax);
 }
@@ -737,7 +758,8 @@ __global__ void __launch_bounds__(kJoinThreads) attention_cached_join_kernel(con
     __shared__ float s_sum[kGroups][2], s_out[kGroups][DT + 4];
     const CacheArgs& c = a.c;
     const int i = blockIdx.x;
-    const int entry = i < shares ? i : a.workers + (i - shares) / (kOwn / 16), group16 = i < shares ? 0 : (i - shares) % (kOwn / 16);
+    const int groups = i < shares ? a.few / 16 : kOwn / 16, j = i < shares ? i : i - shares;
+    const int entry = (i < shares ? 0 : a.workers) + j / groups, group16 = j % groups;
     const Join job = reinterpret_cast<const Join*>(a.joins)[entry];
     if (job.count <= 1) return;
     const Sequence s = sequence(c, job.b);
@@ -802,7 +824,7 @@ namespace {
 
 // What a call's sequences can be, as far as the host knows.
 struct Plan {
-    int kinds, workers;
+    int kinds, few, workers;
     bool whole;            // few rows of short contexts: a workgroup for each head of a sequence, nothing to join
     int64_t tiles;         // of rows, at most
 };
@@ -810,9 +832,11 @@ struct Plan {
 Plan plan(int64_t tokens, int group, int heads, int batch, int64_t capacity, bool bounds)
 {
     Plan p{};
-    p.workers = (2 * device_cu_count() + 7) / 8 * 8;       // two per CU, whole rounds of the XCDs
-    if (!bounds) p.kinds = tokens / batch * group <= kFew ? 1 : 2;
-    else p.kinds = tokens * group <= kFew ? 1 : 3;
+    const int64_t rows = (bounds ? tokens : tokens / batch) * group;           // of a sequence, at most
+    p.few = rows <= kFew || rows > 2 * kFew ? kFew : 2 * kFew;
+    p.kinds = rows <= p.few ? 1 : bounds ? 3 : 2;
+    // two per CU (one where the rows take more than half of the registers), whole rounds of the XCDs
+    p.workers = ((p.few == kFew ? 2 : 1) * device_cu_count() + 7) / 8 * 8;
     p.whole = p.kinds == 1 && capacity <= kWholeKeys && (int64_t)batch * heads <= 1 << 20;
     if (p.kinds & 2) p.tiles = bounds ? tokens * group / kOwn + std::min<int64_t>(batch, tokens * group / (kFew + 1))
                                       : batch * ((tokens / batch * group + kOwn - 1) / kOwn);
@@ -823,13 +847,14 @@ Plan plan(int64_t tokens, int group, int heads, int batch, int64_t capacity, boo
 int64_t row_blocks(const Plan& p, int heads) { return std::max<int64_t>(p.tiles * heads, p.workers * 3 / 2); }
 
 // Slots of 16 rows that hold parts: two to a share; of tiles, split into 3 / 2 `workers` parts at most.
-int64_t slots(const Plan& p) { return p.whole ? 0 : p.workers * 2 + (p.kinds & 2 ? p.workers * 3 / 2 * (kOwn / 16) : 0); }
+int64_t slots(const Plan& p) { return p.whole ? 0 : p.workers * 2 * (p.few / 16) + (p.kinds & 2 ? p.workers * 3 / 2 * (kOwn / 16) : 0); }
 
 template <int DT, bool FULL>
-void (*kernel_of(int kinds))(CachedAttentionArgs)
+void (*kernel_of(const Plan& p))(CachedAttentionArgs)
 {
-    return kinds == 1 ? attention_cached_kernel<DT, FULL, 1> : kinds == 2 ? attention_cached_kernel<DT, FULL, 2>
-                                                                           : attention_cached_kernel<DT, FULL, 3>;
+    if (p.kinds == 1)
+        return p.few == kFew ? attention_cached_kernel<DT, FULL, 1, 1> : attention_cached_kernel<DT, FULL, 1, 2>;
+    return p.kinds == 2 ? attention_cached_kernel<DT, FULL, 2, 1> : attention_cached_kernel<DT, FULL, 3, 1>;
 }
 
 }  // namespace
@@ -856,17 +881,18 @@ hipError_t launch_attention_cached(const CachedAttentionArgs& args, void* worksp
     const Plan p = plan(a.c.tokens, a.group, heads, a.c.batch, capacity(a.c.blocks, a.c.shift), a.c.cu != nullptr);
     a.workers = p.workers;
     a.whole = p.whole;
+    a.few = p.few;
     a.joins = workspace;
     a.tops = reinterpret_cast<float2*>(static_cast<Join*>(workspace) + 2 * p.workers);
     a.partial = reinterpret_cast<float*>(a.tops + slots(p) * 16);
     const int64_t blocks = p.whole ? (int64_t)a.c.batch * heads
                                    : (p.kinds & 1 ? p.workers : 0) + (p.kinds & 2 ? row_blocks(p, heads) : 0);
-    const hipError_t e = launch(d == 64 ? kernel_of<64, true>(p.kinds) : d == 128 ? kernel_of<128, true>(p.kinds)
-                                : d < 64 ? kernel_of<64, false>(p.kinds) : kernel_of<128, false>(p.kinds),
+    const hipError_t e = launch(d == 64 ? kernel_of<64, true>(p) : d == 128 ? kernel_of<128, true>(p)
+                                : d < 64 ? kernel_of<64, false>(p) : kernel_of<128, false>(p),
                                 dim3((unsigned)blocks), dim3(kThreads), stream, a);
     // without bounds the tiles are known, and whether they can be split
     if (e != hipSuccess || p.whole || (p.kinds == 2 && 4 * p.tiles * heads > 3 * p.workers)) return e;
-    const int shares = p.kinds & 1 ? p.workers : 0, joins = shares + (p.kinds & 2 ? p.workers * 3 / 4 * (kOwn / 16) : 0);
+    const int shares = p.kinds & 1 ? p.workers * (p.few / 16) : 0, joins = shares + (p.kinds & 2 ? p.workers * 3 / 4 * (kOwn / 16) : 0);
     return launch(d <= 64 ? attention_cached_join_kernel<64> : attention_cached_join_kernel<128>, dim3(joins), dim3(kJoinThreads),
                   stream, a, shares);
 }
