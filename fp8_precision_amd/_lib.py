@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import NamedTuple
 
 import torch
@@ -859,10 +860,9 @@ def kv_cache(pages: int, heads: int, head_dim: int, page_tokens: int = 64, devic
     return KVCache(codes(), codes(), scale(), scale())
 
 
-class _Cache(ctypes.Structure):
-    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("table", _vp), ("lengths", _vp),
-                ("bounds", _vp), ("pages", _i64), ("heads", _i64), ("page_tokens", _i64), ("head_dim", _i64),
-                ("batch", _i64), ("blocks", _i64), ("tokens", _i64)]
+# struct fp8_kv_cache: the pool, table, lengths and bounds; pages, heads, page_tokens, head_dim,
+# batch, blocks, tokens (packed, which takes a third of a ctypes structure's time)
+_pack_cache = struct.Struct("@7P7q").pack
 
 
 def _cache_checks(k, v, k_scale, v_scale, table, lengths, cu):
@@ -884,7 +884,7 @@ def _cache_checks(k, v, k_scale, v_scale, table, lengths, cu):
 
 
 def _cache(cache, table, lengths, cu, tokens):
-    """The struct of a call on a cache, its tensors checked."""
+    """The struct of a call on a cache, its tensors checked: (struct, heads, head_dim)."""
     k, v, k_scale, v_scale = cache
     u8, i32 = torch.uint8, torch.int32
     try:
@@ -909,8 +909,8 @@ def _cache(cache, table, lengths, cu, tokens):
                 raise ValueError(f"all tensors of a cache must be on one device (got {k.device} and {t.device})")
     if cu is None and tokens % max(batch, 1):
         raise ValueError("without cu every sequence has as many tokens")
-    return _Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(), lengths.data_ptr(),
-                  None if cu is None else cu.data_ptr(), size[0], size[1], size[2], size[3], batch, blocks, tokens)
+    return _pack_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(), lengths.data_ptr(),
+                       0 if cu is None else cu.data_ptr(), *size, batch, blocks, tokens), size[1], size[3]
 
 
 def kv_cache_write(cache, table, lengths, k, v, cu=None) -> None:
@@ -925,10 +925,10 @@ def kv_cache_write(cache, table, lengths, k, v, cu=None) -> None:
     call writes must stand in the table once.
     """
     hk, hv = _heads(k, "k"), _heads(v, "v", k.shape)
-    c = _cache(cache, table, lengths, cu, k.shape[0])
-    if (k.shape[1], k.shape[2]) != (c.heads, c.head_dim):
-        raise ValueError(f"k and v must be [tokens, {c.heads}, {c.head_dim}]")
-    _run("fp8_kv_cache_write", _lib.fp8_kv_cache_write, (cache[0], k, v), ctypes.byref(c), hk, hv)
+    c, heads, head_dim = _cache(cache, table, lengths, cu, k.shape[0])
+    if k.shape[1:] != (heads, head_dim):
+        raise ValueError(f"k and v must be [tokens, {heads}, {head_dim}]")
+    _run("fp8_kv_cache_write", _lib.fp8_kv_cache_write, (cache[0], k, v), c, hk, hv)
 
 
 def kv_cache_read(cache, table, lengths, tokens: int, cu=None, k=None, v=None):
@@ -936,12 +936,12 @@ def kv_cache_read(cache, table, lengths, tokens: int, cu=None, k=None, v=None):
     bf16 [tokens, heads, head_dim], exact.  ``table``, ``lengths`` and ``cu`` (whose last bound
     is at most ``tokens``) as for ``kv_cache_write``: with the bounds of ``lengths`` the whole
     contexts, as ``attention`` takes them.  Tokens without a page read as zeros."""
-    c = _cache(cache, table, lengths, cu, tokens)
-    shape = (tokens, c.heads, c.head_dim)
+    c, heads, head_dim = _cache(cache, table, lengths, cu, tokens)
+    shape = (tokens, heads, head_dim)
     k = torch.empty(shape, dtype=torch.bfloat16, device=table.device) if k is None else k
     v = torch.empty(shape, dtype=torch.bfloat16, device=table.device) if v is None else v
     hk, hv = _heads(k, "k", shape), _heads(v, "v", shape)
-    _run("fp8_kv_cache_read", _lib.fp8_kv_cache_read, (cache[0], k, v), ctypes.byref(c), hk, hv)
+    _run("fp8_kv_cache_read", _lib.fp8_kv_cache_read, (cache[0], k, v), c, hk, hv)
     return k, v
 
 
@@ -957,17 +957,17 @@ def attention_cached(q, cache, table, lengths, cu=None, causal: bool = True, sca
     lse -inf."""
     hq = _heads(q, "q")
     size = q.shape
-    c = _cache(cache, table, lengths, cu, size[0])
-    if size[2] != c.head_dim:
-        raise ValueError(f"q must be [tokens, heads_q, {c.head_dim}]")
+    c, _, head_dim = _cache(cache, table, lengths, cu, size[0])
+    if size[2] != head_dim:
+        raise ValueError(f"q must be [tokens, heads_q, {head_dim}]")
     if absmax is not None:
         _scalar_in(absmax, "absmax")
     if out is None:
         out = _new_heads(q)
     ho = _heads(out, "out", size)
     lse = _out(lse, "lse", (size[1], size[0]), torch.float32, q.device)
-    ws = _workspace("fp8_attention_cached_workspace", q.device, ctypes.byref(c), size[1])
-    _run("fp8_attention_cached", _lib.fp8_attention_cached, (cache[0], q, out, lse, absmax, ws), ctypes.byref(c), hq, ho,
+    ws = _workspace("fp8_attention_cached_workspace", q.device, c, size[1])
+    _run("fp8_attention_cached", _lib.fp8_attention_cached, (cache[0], q, out, lse, absmax, ws), c, hq, ho,
          size[1], 1 if causal else 0, size[2] ** -0.5 if scale is None else scale, _ptr(lse), _ptr(absmax), _ptr(ws),
          0 if ws is None else ws.numel())
     return out, lse

@@ -34,6 +34,7 @@ constexpr int kFew = 16;                   // rows of a sequence that is read in
 constexpr int kOwn = 128;                  // rows of a tile: 32 per wave
 constexpr int kLeastSteps = kWaves;        // of a share
 constexpr int kPiece = 4;                  // what a head of a sequence costs besides its steps, in steps
+constexpr int kMostTiles = (1 << 23) - 1;   // that a thread counts: no call has more in all
 constexpr int kLeastSplit = 4;             // steps of a part of a tile's keys
 // Steps of a tile, on average, from which on its keys are split over the workgroups that would
 // have none; and in two where there are more tiles than CUs, but not three for two.  MI355X,
@@ -154,7 +155,6 @@ __device__ __forceinline__ Sums block_sums(int x, int64_t y, int (*lds)[4])
 struct Keys16 {
     int64_t byte;
     int rows;
-    float k_scale, v_scale;
 };
 
 // A sequence's pages and their scales of one head, 64 blocks in the lanes of a wave at a
@@ -166,18 +166,22 @@ struct Pages {
     int heads, head, held, shift, d;
     int first;                             // the window's first block
     int page[3];
-    int scale[2];                          // the lane's two bytes, the values' in the high half
+    int k_byte[2], v_byte[2];              // their scales
 
     __device__ __forceinline__ int entry(int window) const
     {
         const int at = first + 64 * window + (int)(threadIdx.x & 63);
         return (int64_t)at << shift < held ? table[at] : -1;
     }
-    __device__ __forceinline__ int scales(int p) const
+    __device__ __forceinline__ void scales(int window)
     {
-        if (p < 0 || p >= pages) return 127 << 16 | 127;
-        const int64_t at = (int64_t)p * heads + head;
-        return k_scale[at] | v_scale[at] << 16;
+        const int p = page[window];
+        k_byte[window] = v_byte[window] = 127;
+        if (p >= 0 && p < pages) {
+            const int64_t at = (int64_t)p * heads + head;
+            k_byte[window] = k_scale[at];
+            v_byte[window] = v_scale[at];
+        }
     }
     __device__ __forceinline__ void init(const CacheArgs& a, int b, int head_, int held_, int key)
     {
@@ -194,7 +198,7 @@ struct Pages {
 #pragma unroll
         for (int w = 0; w < 3; ++w) page[w] = entry(w);
 #pragma unroll
-        for (int w = 0; w < 2; ++w) scale[w] = scales(page[w]);
+        for (int w = 0; w < 2; ++w) scales(w);
     }
     // the window holds the blocks of the 64 keys from key on (a multiple of 64, as the first was; never falling)
     __device__ __forceinline__ void advance(int key)
@@ -203,8 +207,9 @@ struct Pages {
             first += 64;
             page[0] = page[1];
             page[1] = page[2];
-            scale[0] = scale[1];
-            scale[1] = scales(page[1]);
+            k_byte[0] = k_byte[1];
+            v_byte[0] = v_byte[1];
+            scales(1);
             page[2] = entry(2);
         }
     }
@@ -212,14 +217,19 @@ struct Pages {
     __device__ __forceinline__ Keys16 at(int key, int limit) const
     {
         const int block = (key >> shift) - first;
-        const int p = __builtin_amdgcn_readlane(page[0], block), s = __builtin_amdgcn_readlane(scale[0], block);
+        const int p = __builtin_amdgcn_readlane(page[0], block);
         const bool none = key >= limit || p < 0 || p >= pages;
         Keys16 x;
         x.byte = ((((int64_t)(none ? 0 : p) * heads + head) << shift) + (key & ((1 << shift) - 1))) * d;
         x.rows = none ? 0 : min(limit - key, 16);
-        x.k_scale = cache_scale((uint8_t)s);
-        x.v_scale = cache_scale((uint8_t)(s >> 16));
         return x;
+    }
+    // their scales (asked for when the codes are here, so that the codes do not wait for them)
+    __device__ __forceinline__ float scale_k(int key) const { return lane_scale(k_byte[0], key); }
+    __device__ __forceinline__ float scale_v(int key) const { return lane_scale(v_byte[0], key); }
+    __device__ __forceinline__ float lane_scale(int byte, int key) const
+    {
+        return cache_scale((uint8_t)__builtin_amdgcn_readlane(byte, (key >> shift) - first));
     }
 };
 
@@ -228,18 +238,20 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const uint8_t* pool, c
     return __builtin_amdgcn_make_buffer_rsrc((void*)(pool + x.byte), 0, x.rows * d, 0x00020000);
 }
 
-// What the join takes of a row's sums left in parts.  A part's rows lie 16 to a slot.
+// What is to be joined: rows of a sequence whose sums are left in parts, 16 rows to a slot.
 struct Join {
-    int b, head, row, count;               // rows row .. of the sequence; nothing to do below 2 parts
-    int first, second, step, pad;          // the slots: first, second, second + step, ...
+    int from, head, row, rows;             // the sequence's first query; rows row .. rows - 1 of it
+    int count;                             // parts; nothing to do below 2
+    int first, second, step;               // their slots: first, second, second + step, ...
 };
 
 template <int DT> constexpr int share_lds() { return kWaves * kFew * (DT + 4 + 2) * 4; }
 template <int DT> constexpr int tile_lds() { return 4 * kKeys * DT * 2; }
 
-// The row's value and its largest magnitude, from unnormalised sums.
-__device__ __forceinline__ float inverse(float l) { return l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l); }   // a NaN sum stays NaN
+// What a row's sums are multiplied with: 0 for one that sees nothing; a NaN sum stays NaN.
+__device__ __forceinline__ float inverse(float l) { return l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l); }
 
+// The larger of `top` and the magnitudes (fp32 bits) of two bf16.
 __device__ __forceinline__ uint32_t top_of(uint32_t w, uint32_t top)
 {
     return max(max(top, w & 0x7FFF0000u), w << 16 & 0x7FFFFFFFu);
@@ -276,8 +288,27 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
         done = at = 0;
         end = share_steps(a, sequence(c, b));
         if (end == 0) return 0;
+    } else if (c.batch <= 64) {
+        // the share: every lane counts a sequence's steps
+        const int mine = lane < c.batch ? share_steps(a, sequence(c, lane)) * c.heads : 0;
+        int sum = mine;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int o = __shfl_up(sum, off, 64);
+            if (lane >= off) sum += o;
+        }
+        const int total = __builtin_amdgcn_readlane(sum, 63);
+        share = max((total + a.workers - 1) / a.workers, kLeastSteps);
+        if (threadIdx.x == 0) joins[worker].count = 0;
+        if (total == 0 || worker > (total - 1) / share) return 0;
+        at = worker * share;
+        end = min(at + share, total);
+        b = __ffsll((unsigned long long)__ballot(sum > at)) - 1;
+        const int left = at - __builtin_amdgcn_readlane(sum - mine, b), steps = __builtin_amdgcn_readlane(mine, b) / c.heads;
+        head = __builtin_amdgcn_readfirstlane(left / steps);
+        done = __builtin_amdgcn_readfirstlane(left - head * steps);
     } else {
-        // the share: every thread counts some sequences' steps, in order
+        // more sequences: every thread counts some, in order
         const int per = (c.batch + kThreads - 1) / kThreads, b0 = threadIdx.x * per, b1 = min(b0 + per, c.batch);
         int mine = 0;
         for (int b = b0; b < b1; ++b) mine += share_steps(a, sequence(c, b)) * c.heads;
@@ -315,241 +346,246 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
         // the piece: the keys' steps step0 .. last - 1 of all
         const int step0 = max(done - kPiece, 0), last = max(upto - kPiece, 0), all_steps = steps - kPiece;
         if (last > step0) {
-        const int rows = queries * a.group, see_first = seen(a, held, first, 0);
+            const int rows = queries * a.group, see_first = seen(a, held, first, 0);
 
-        // the queries' operands: lane's column m, elements of chunk g as the keys' lanes have them
-        Frag q[R][DT / 32];
-        int see[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int row = 16 * r + m, qi = row / a.group, hq = head * a.group + row - qi * a.group;
-            see[r] = seen(a, held, first, qi);
-#pragma unroll
-            for (int i = 0; i < DT / 32; ++i) {
-                q[r][i].u = au32x4{0, 0, 0, 0};
-                const int e = 64 * (i / 2) + 16 * g + 8 * (i % 2);
-                if (row < rows && (FULL || e < c.d))
-                    q[r][i].u = *reinterpret_cast<const au32x4*>(a.q + (int64_t)(from + qi) * a.q_row + (int64_t)hq * a.q_head + e);
-            }
-        }
-        // waited for here: at its first use, in the loop, the wait would be one for every load in flight
-        af32x4 o[R][kPer];
-        float top[R], sum[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-#pragma unroll
-            for (int i = 0; i < DT / 32; ++i) asm volatile("" : "+v"(q[r][i].u));
-#pragma unroll
-            for (int t = 0; t < kPer; ++t) o[r][t] = af32x4{0, 0, 0, 0};
-            top[r] = -kInf;
-            sum[r] = 0.0f;
-        }
-
-        // Codes of 64 keys, as loaded.  Of each block of 16 keys a lane has DT / 4 codes of key
-        // m (16 of each 64, chunk g), and DT / 16 codes (chunk m) of each of the values 4 g + i.
-        uint32_t ck[4][DT / 16], cv[4][4][DT / 64];
-        Keys16 x[4];
-        float v_scale[4];
-        Pages pages;
-        const int limit = min(held, last * kKeys);
-        auto load_k = [&](int key) __attribute__((always_inline)) {
-            pages.advance(key);
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                x[n] = pages.at(key + 16 * n, limit);
-                const auto src = rows_of(c.k, x[n], FULL ? DT : c.d);
-                if constexpr (FULL) {
-#pragma unroll
-                    for (int i = 0; i < DT / 64; ++i) {
-                        const au32x4 w = __builtin_amdgcn_raw_buffer_load_b128(src, m * DT + 64 * i + 16 * g, 0, kNonTemporal);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) ck[n][4 * i + j] = w[j];
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < DT / 32; ++i) {
-                        const int e = 64 * (i / 2) + 16 * g + 8 * (i % 2);
-                        const au32x2 w = __builtin_amdgcn_raw_buffer_load_b64(src, e < c.d ? m * c.d + e : kNowhere, 0, kNonTemporal);
-                        ck[n][2 * i] = w[0];
-                        ck[n][2 * i + 1] = w[1];
-                    }
-                }
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        };
-        auto load_v = [&]() __attribute__((always_inline)) {
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const int d = FULL ? DT : c.d, e = kPer * m;
-                const auto src = rows_of(c.v, x[n], d);
-                v_scale[n] = x[n].v_scale;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t off = FULL || e < d ? (uint32_t)((4 * g + i) * d + e) : kNowhere;
-                    if constexpr (DT == 128) {
-                        const au32x2 w = __builtin_amdgcn_raw_buffer_load_b64(src, off, 0, kNonTemporal);
-                        cv[n][i][0] = w[0];
-                        cv[n][i][1] = w[1];
-                    } else {
-                        cv[n][i][0] = __builtin_amdgcn_raw_buffer_load_b32(src, off, 0, kNonTemporal);
-                    }
-                }
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        };
-
-        if (step0 + wave < last) {
-            pages.init(c, b, head, held, (step0 + wave) * kKeys);
-            load_k((step0 + wave) * kKeys);
-            load_v();
-        }
-        for (int t = step0 + wave; t < last; t += kWaves) {
-            const int j0 = t * kKeys;
-            af32x4 p[R][4];
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-#pragma unroll
-                for (int r = 0; r < R; ++r) p[r][n] = af32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int i = 0; i < DT / 32; ++i) {
-                    Frag k;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        k.w[2 * j] = values2<false>(ck[n][2 * i + j], x[n].k_scale);
-                        k.w[2 * j + 1] = values2<true>(ck[n][2 * i + j], x[n].k_scale);
-                    }
-#pragma unroll
-                    for (int r = 0; r < R; ++r) p[r][n] = mma16(k, q[r][i], p[r][n]);
-                }
-            }
-            // (past the last step from buffers of no rows: with loads that some path leaves out, the
-            // compiler would wait for the values together with the next keys)
-            __builtin_amdgcn_sched_barrier(0);
-            load_k(j0 + kWaves * kKeys);
+            // the queries' operands: lane's column m, elements of chunk g as the keys' lanes have them
+            Frag q[R][DT / 32];
+            int see[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                if (j0 + kKeys > see_first) {
+                const int row = 16 * r + m, qi = row / a.group, hq = head * a.group + row - qi * a.group;
+                see[r] = seen(a, held, first, qi);
+#pragma unroll
+                for (int i = 0; i < DT / 32; ++i) {
+                    q[r][i].u = au32x4{0, 0, 0, 0};
+                    const int e = 64 * (i / 2) + 16 * g + 8 * (i % 2);
+                    if (row < rows && (FULL || e < c.d))
+                        q[r][i].u = *reinterpret_cast<const au32x4*>(a.q + (int64_t)(from + qi) * a.q_row + (int64_t)hq * a.q_head + e);
+                }
+            }
+            // waited for here: at its first use, in the loop, the wait would be one for every load in flight
+            af32x4 o[R][kPer];
+            float top[R], sum[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+#pragma unroll
+                for (int i = 0; i < DT / 32; ++i) asm volatile("" : "+v"(q[r][i].u));
+#pragma unroll
+                for (int t = 0; t < kPer; ++t) o[r][t] = af32x4{0, 0, 0, 0};
+                top[r] = -kInf;
+                sum[r] = 0.0f;
+            }
+
+            // Codes of 64 keys, as loaded.  Of each block of 16 keys a lane has DT / 4 codes of key
+            // m (16 of each 64, chunk g), and DT / 16 codes (chunk m) of each of the values 4 g + i.
+            uint32_t ck[4][DT / 16], cv[4][4][DT / 64];
+            Keys16 x[4];
+            Pages pages;
+            const int limit = min(held, last * kKeys);
+            auto load_k = [&](int key) __attribute__((always_inline)) {
+                pages.advance(key);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    x[n] = pages.at(key + 16 * n, limit);
+                    const auto src = rows_of(c.k, x[n], FULL ? DT : c.d);
+                    if constexpr (FULL) {
+#pragma unroll
+                        for (int i = 0; i < DT / 64; ++i) {
+                            const au32x4 w = __builtin_amdgcn_raw_buffer_load_b128(src, m * DT + 64 * i + 16 * g, 0, kNonTemporal);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) ck[n][4 * i + j] = w[j];
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < DT / 32; ++i) {
+                            const int e = 64 * (i / 2) + 16 * g + 8 * (i % 2);
+                            const au32x2 w = __builtin_amdgcn_raw_buffer_load_b64(src, e < c.d ? m * c.d + e : kNowhere, 0, kNonTemporal);
+                            ck[n][2 * i] = w[0];
+                            ck[n][2 * i + 1] = w[1];
+                        }
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            auto load_v = [&]() __attribute__((always_inline)) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const int d = FULL ? DT : c.d, e = kPer * m;
+                    const auto src = rows_of(c.v, x[n], d);
+    #pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t off = FULL || e < d ? (uint32_t)((4 * g + i) * d + e) : kNowhere;
+                        if constexpr (DT == 128) {
+                            const au32x2 w = __builtin_amdgcn_raw_buffer_load_b64(src, off, 0, kNonTemporal);
+                            cv[n][i][0] = w[0];
+                            cv[n][i][1] = w[1];
+                        } else {
+                            cv[n][i][0] = __builtin_amdgcn_raw_buffer_load_b32(src, off, 0, kNonTemporal);
+                        }
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            };
+
+            if (step0 + wave < last) {
+                pages.init(c, b, head, held, (step0 + wave) * kKeys);
+                load_k((step0 + wave) * kKeys);
+                load_v();
+            }
+            for (int t = step0 + wave; t < last; t += kWaves) {
+                const int j0 = t * kKeys;
+                float k_scale[4], v_scale[4];              // before the window moves on to the next step
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    k_scale[n] = pages.scale_k(j0 + 16 * n);
+                    v_scale[n] = pages.scale_v(j0 + 16 * n);
+                }
+                af32x4 p[R][4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r) p[r][n] = af32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int i = 0; i < DT / 32; ++i) {
+                        Frag k;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            k.w[2 * j] = values2<false>(ck[n][2 * i + j], k_scale[n]);
+                            k.w[2 * j + 1] = values2<true>(ck[n][2 * i + j], k_scale[n]);
+                        }
+#pragma unroll
+                        for (int r = 0; r < R; ++r) p[r][n] = mma16(k, q[r][i], p[r][n]);
+                    }
+                }
+                // (past the last step from buffers of no rows: with loads that some path leaves out, the
+                // compiler would wait for the values together with the next keys)
+                __builtin_amdgcn_sched_barrier(0);
+                load_k(j0 + kWaves * kKeys);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    if (j0 + kKeys > see_first) {
+#pragma unroll
+                        for (int n = 0; n < 4; ++n)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (j0 + 16 * n + 4 * g + i >= see[r]) p[r][n][i] = -kInf;
+                    }
+                    float up = fmaxf(fmaxf(p[r][0][0], p[r][0][1]), fmaxf(p[r][0][2], p[r][0][3]));
+#pragma unroll
+                    for (int n = 1; n < 4; ++n) up = fmaxf(up, fmaxf(fmaxf(p[r][n][0], p[r][n][1]), fmaxf(p[r][n][2], p[r][n][3])));
+                    up = max4(up);
+                    if (__any(up > top[r] + far)) {            // top = -inf: any key seen
+                        up = fmaxf(up, top[r]);
+                        const float by = up == -kInf ? 1.0f : __builtin_amdgcn_exp2f((top[r] - up) * scale2);
+                        sum[r] *= by;
+#pragma unroll
+                        for (int i = 0; i < kPer; ++i)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) o[r][i][j] *= by;
+                        top[r] = up;
+                    }
+                    const float use = top[r] == -kInf ? 0.0f : top[r] * scale2;
 #pragma unroll
                     for (int n = 0; n < 4; ++n)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (j0 + 16 * n + 4 * g + i >= see[r]) p[r][n][i] = -kInf;
-                }
-                float up = fmaxf(fmaxf(p[r][0][0], p[r][0][1]), fmaxf(p[r][0][2], p[r][0][3]));
-#pragma unroll
-                for (int n = 1; n < 4; ++n) up = fmaxf(up, fmaxf(fmaxf(p[r][n][0], p[r][n][1]), fmaxf(p[r][n][2], p[r][n][3])));
-                up = max4(up);
-                if (__any(up > top[r] + far)) {            // top = -inf: any key seen
-                    up = fmaxf(up, top[r]);
-                    const float by = up == -kInf ? 1.0f : __builtin_amdgcn_exp2f((top[r] - up) * scale2);
-                    sum[r] *= by;
-#pragma unroll
-                    for (int i = 0; i < kPer; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) o[r][i][j] *= by;
-                    top[r] = up;
-                }
-                const float use = top[r] == -kInf ? 0.0f : top[r] * scale2;
-#pragma unroll
-                for (int n = 0; n < 4; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        p[r][n][i] = __builtin_amdgcn_exp2f(fmaf(p[r][n][i], scale2, -use));
-                        sum[r] += p[r][n][i];
-                    }
-            }
-#pragma unroll
-            for (int n = 0; n < 4; n += 2) {
-                // p; of 16 rows as two bf16, the second what the first's rounding left off: the matrix units have the time
-                Frag f[R], f2;
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float y = p[r][n + i / 2][2 * (i % 2)], z = p[r][n + i / 2][2 * (i % 2) + 1];
-                        f[r].w[i] = bf16_pair(y, z);
-                        if (R == 1) f2.w[i] = bf16_pair(y - bf16_lo(f[r].w[i]), z - bf16_hi(f[r].w[i]));
-                    }
-#pragma unroll
-                for (int w = 0; w < DT / 64; ++w) {
-                    uint32_t lo[4], hi[4];
-                    transpose4x4(cv[n][0][w], cv[n][1][w], cv[n][2][w], cv[n][3][w], lo[0], lo[1], lo[2], lo[3]);
-                    transpose4x4(cv[n + 1][0][w], cv[n + 1][1][w], cv[n + 1][2][w], cv[n + 1][3][w], hi[0], hi[1], hi[2], hi[3]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        Frag v;
-                        v.w[0] = values2<false>(lo[i], v_scale[n]);
-                        v.w[1] = values2<true>(lo[i], v_scale[n]);
-                        v.w[2] = values2<false>(hi[i], v_scale[n + 1]);
-                        v.w[3] = values2<true>(hi[i], v_scale[n + 1]);
-#pragma unroll
-                        for (int r = 0; r < R; ++r) o[r][4 * w + i] = mma16(v, f[r], o[r][4 * w + i]);
-                        if (R == 1) o[0][4 * w + i] = mma16(v, f2, o[0][4 * w + i]);
-                    }
-                }
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            load_v();
-        }
-        // the waves' sums together, 16 rows at a time: o[t][i] is element kPer (4 g + i) + t of row m
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            if (R > 1 && r > 0) __syncthreads();
-            sum[r] = sum4(sum[r]);
-            if (g == 0) {
-                s_top[wave * kFew + m] = top[r];
-                s_sum[wave * kFew + m] = sum[r];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int t = 0; t < kPer; t += 4)
-                    *reinterpret_cast<af32x4*>(s_out + (wave * kFew + m) * kRow + kPer * (4 * g + i) + t) =
-                        af32x4{o[r][t][i], o[r][t + 1][i], o[r][t + 2][i], o[r][t + 3][i]};
-            __syncthreads();
-            const int n = threadIdx.x / 16, e = threadIdx.x % 16 * kPer;
-            if (16 * r + n < rows) {
-                const int q2 = (16 * r + n) / a.group, h2 = head * a.group + 16 * r + n - q2 * a.group;
-                float best = -kInf, l = 0.0f, y[kPer];
-#pragma unroll
-                for (int w = 0; w < kWaves; ++w) best = fmaxf(best, s_top[w * kFew + n]);
-                const float base = best == -kInf ? 0.0f : best;
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) y[i] = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kWaves; ++w) {
-                    const float by = __builtin_amdgcn_exp2f((s_top[w * kFew + n] - base) * scale2);
-                    l = fmaf(s_sum[w * kFew + n], by, l);
-#pragma unroll
-                    for (int i = 0; i < kPer; ++i) y[i] = fmaf(s_out[(w * kFew + n) * kRow + e + i], by, y[i]);
-                }
-                if (step0 == 0 && last == all_steps) {
-                    const float by = inverse(l);
-                    uint32_t w[kPer / 2];
-                    if (FULL || e < c.d) {
-#pragma unroll
-                        for (int i = 0; i < kPer / 2; ++i) {
-                            w[i] = bf16_pair(y[2 * i] * by, y[2 * i + 1] * by);
-                            top_out = top_of(w[i], top_out);
+                        for (int i = 0; i < 4; ++i) {
+                            p[r][n][i] = __builtin_amdgcn_exp2f(fmaf(p[r][n][i], scale2, -use));
+                            sum[r] += p[r][n][i];
                         }
-                        uint16_t* to = a.out + (int64_t)(from + q2) * a.out_row + (int64_t)h2 * a.out_head + e;
-                        if constexpr (kPer == 8) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
-                        else *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
-                    }
-                    if (e == 0)
-                        a.lse[(int64_t)h2 * c.tokens + from + q2] =
-                            l == 0.0f ? -kInf : (base * scale2 + __builtin_amdgcn_logf(l)) * kLn2;
-                } else {
-                    const int64_t slot = (2 * (int64_t)worker + (step0 == 0 ? 1 : 0)) * R + r;
-                    float* to = a.partial + (slot * 16 + n) * DT + e;
+                }
 #pragma unroll
-                    for (int i = 0; i < kPer; i += 4) *reinterpret_cast<af32x4*>(to + i) = af32x4{y[i], y[i + 1], y[i + 2], y[i + 3]};
-                    if (e == 0) a.tops[slot * 16 + n] = make_float2(best == -kInf ? -kInf : best * scale2, l);
+                for (int n = 0; n < 4; n += 2) {
+                    // p; of 16 rows as two bf16, the second what the first's rounding left off: the matrix units have the time
+                    Frag f[R], f2;
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float y = p[r][n + i / 2][2 * (i % 2)], z = p[r][n + i / 2][2 * (i % 2) + 1];
+                            f[r].w[i] = bf16_pair(y, z);
+                            if (R == 1) f2.w[i] = bf16_pair(y - bf16_lo(f[r].w[i]), z - bf16_hi(f[r].w[i]));
+                        }
+#pragma unroll
+                    for (int w = 0; w < DT / 64; ++w) {
+                        uint32_t lo[4], hi[4];
+                        transpose4x4(cv[n][0][w], cv[n][1][w], cv[n][2][w], cv[n][3][w], lo[0], lo[1], lo[2], lo[3]);
+                        transpose4x4(cv[n + 1][0][w], cv[n + 1][1][w], cv[n + 1][2][w], cv[n + 1][3][w], hi[0], hi[1], hi[2], hi[3]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            Frag v;
+                            v.w[0] = values2<false>(lo[i], v_scale[n]);
+                            v.w[1] = values2<true>(lo[i], v_scale[n]);
+                            v.w[2] = values2<false>(hi[i], v_scale[n + 1]);
+                            v.w[3] = values2<true>(hi[i], v_scale[n + 1]);
+#pragma unroll
+                            for (int r = 0; r < R; ++r) o[r][4 * w + i] = mma16(v, f[r], o[r][4 * w + i]);
+                            if (R == 1) o[0][4 * w + i] = mma16(v, f2, o[0][4 * w + i]);
+                        }
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                load_v();
+            }
+            // the waves' sums together, 16 rows at a time: o[t][i] is element kPer (4 g + i) + t of row m
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (R > 1 && r > 0) __syncthreads();
+                sum[r] = sum4(sum[r]);
+                if (g == 0) {
+                    s_top[wave * kFew + m] = top[r];
+                    s_sum[wave * kFew + m] = sum[r];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int t = 0; t < kPer; t += 4)
+                        *reinterpret_cast<af32x4*>(s_out + (wave * kFew + m) * kRow + kPer * (4 * g + i) + t) =
+                            af32x4{o[r][t][i], o[r][t + 1][i], o[r][t + 2][i], o[r][t + 3][i]};
+                __syncthreads();
+                const int n = threadIdx.x / 16, e = threadIdx.x % 16 * kPer;
+                if (16 * r + n < rows) {
+                    const int q2 = (16 * r + n) / a.group, h2 = head * a.group + 16 * r + n - q2 * a.group;
+                    float best = -kInf, l = 0.0f, y[kPer];
+#pragma unroll
+                    for (int w = 0; w < kWaves; ++w) best = fmaxf(best, s_top[w * kFew + n]);
+                    const float base = best == -kInf ? 0.0f : best;
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) y[i] = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < kWaves; ++w) {
+                        const float by = __builtin_amdgcn_exp2f((s_top[w * kFew + n] - base) * scale2);
+                        l = fmaf(s_sum[w * kFew + n], by, l);
+#pragma unroll
+                        for (int i = 0; i < kPer; ++i) y[i] = fmaf(s_out[(w * kFew + n) * kRow + e + i], by, y[i]);
+                    }
+                    if (step0 == 0 && last == all_steps) {
+                        const float by = inverse(l);
+                        uint32_t w[kPer / 2];
+                        if (FULL || e < c.d) {
+#pragma unroll
+                            for (int i = 0; i < kPer / 2; ++i) {
+                                w[i] = bf16_pair(y[2 * i] * by, y[2 * i + 1] * by);
+                                top_out = top_of(w[i], top_out);
+                            }
+                            uint16_t* to = a.out + (int64_t)(from + q2) * a.out_row + (int64_t)h2 * a.out_head + e;
+                            if constexpr (kPer == 8) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+                            else *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+                        }
+                        if (e == 0)
+                            a.lse[(int64_t)h2 * c.tokens + from + q2] =
+                                l == 0.0f ? -kInf : (base * scale2 + __builtin_amdgcn_logf(l)) * kLn2;
+                    } else {
+                        const int64_t slot = (2 * (int64_t)worker + (step0 == 0 ? 1 : 0)) * R + r;
+                        float* to = a.partial + (slot * 16 + n) * DT + e;
+#pragma unroll
+                        for (int i = 0; i < kPer; i += 4) *reinterpret_cast<af32x4*>(to + i) = af32x4{y[i], y[i + 1], y[i + 2], y[i + 3]};
+                        if (e == 0) a.tops[slot * 16 + n] = make_float2(best == -kInf ? -kInf : best * scale2, l);
+                    }
                 }
             }
-        }
-        if (threadIdx.x == 0 && step0 == 0 && last < all_steps)
-            joins[worker] = Join{b, head, 0, (at - done + steps - 1) / share - worker + 1, (2 * worker + 1) * R, (2 * worker + 2) * R, 2 * R, 0};
+            if (threadIdx.x == 0 && step0 == 0 && last < all_steps)
+                joins[worker] = Join{from, head, 0, rows, (at - done + steps - 1) / share - worker + 1, (2 * worker + 1) * R,
+                                     (2 * worker + 2) * R, 2 * R};
         }
         at += upto - done;
         if (at >= end) break;
@@ -581,15 +617,17 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
 
     // the tile: every thread counts some sequences', in order
     const int per = (c.batch + kThreads - 1) / kThreads, b0 = threadIdx.x * per, b1 = min(b0 + per, c.batch);
+    // (held to what the launch has room for, should bounds overlap)
     int mine = 0;
     int64_t mine_steps = 0;
-    for (int b = b0; b < b1; ++b) {
+    for (int b = b0; b < b1 && mine < kMostTiles; ++b) {
         const Sequence s = sequence(c, b);
-        const int n = row_tiles(a, s);
+        const int n = min(row_tiles(a, s), kMostTiles - mine);
         mine += n;
         mine_steps += (int64_t)n * ((max(seen(a, s.held, s.first, s.queries / 2), 0) + kKeys - 1) / kKeys);
     }
-    const Sums all = block_sums(mine, mine_steps, sums);
+    Sums all = block_sums(mine, mine_steps, sums);
+    all.total = min(all.total, a.tiles);
     Join* const joins = reinterpret_cast<Join*>(a.joins) + a.workers;
     const int units = all.total * c.heads;
     const int average = units == 0 ? 0 : (int)(all.total_y / all.total);
@@ -660,11 +698,10 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
         }
     }
     au32x4 ck[kLoads], cv[kLoads];
-    Keys16 x;
     Pages pages;
     auto fetch = [&](int key) __attribute__((always_inline)) {
         pages.advance(key);
-        x = pages.at(key + 16 * wave, held);
+        const Keys16 x = pages.at(key + 16 * wave, held);
         const auto k = rows_of(c.k, x, FULL ? DT : c.d), v = rows_of(c.v, x, FULL ? DT : c.d);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
@@ -686,13 +723,14 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
     };
     auto step = [&](auto stage, int st) __attribute__((always_inline)) {
         constexpr int at = stage.value * 2 * kTile;
+        const float k_scale = pages.scale_k(st * kKeys + 16 * wave), v_scale = pages.scale_v(st * kKeys + 16 * wave);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 lds_u32x4* to = (lds_u32x4*)(uintptr_t)put[i][j];
-                to[at / 16] = values(ck[i][2 * j], ck[i][2 * j + 1], x.k_scale);
-                to[(at + kTile) / 16] = values(cv[i][2 * j], cv[i][2 * j + 1], x.v_scale);
+                to[at / 16] = values(ck[i][2 * j], ck[i][2 * j + 1], k_scale);
+                to[(at + kTile) / 16] = values(cv[i][2 * j], cv[i][2 * j + 1], v_scale);
             }
         if (st + 1 < s_end) fetch((st + 1) * kKeys);
         // tile st is written by all; the other stage was last read in step st - 1, by the waves that are here
@@ -716,7 +754,7 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
         store_partial<DT>(o, a.partial + row * DT, DT, valid);
         if (valid && h == 0) a.tops[row] = make_float2(m == -kInf ? -kInf : mc, l);
         if (split == 0 && threadIdx.x == 0)
-            joins[t * c.heads + head] = Join{b, head, row0, splits, slot0, slot0 + kOwn / 16, kOwn / 16, 0};
+            joins[t * c.heads + head] = Join{from, head, row0, rows, splits, slot0, slot0 + kOwn / 16, kOwn / 16};
         return 0;
     }
     const uint32_t top = store_own<DT>(o, inverse(l), a.out + (int64_t)(from + qi) * a.out_row + (int64_t)hq * a.out_head, c.d, valid);
@@ -762,8 +800,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_cached_join_kernel(con
     const int entry = (i < shares ? 0 : a.workers) + j / groups, group16 = j % groups;
     const Join job = reinterpret_cast<const Join*>(a.joins)[entry];
     if (job.count <= 1) return;
-    const Sequence s = sequence(c, job.b);
-    const int rows = min(s.queries * a.group - job.row - 16 * group16, 16);
+    const int rows = min(job.rows - job.row - 16 * group16, 16);
     if (rows <= 0) return;
     const int wide = rows > 8 ? 16 : rows > 4 ? 8 : rows > 2 ? 4 : rows;       // rows side by side
     const int k = threadIdx.x / kLanes, e = threadIdx.x % kLanes * kPer, n = k % wide, lead = k / wide;
@@ -813,9 +850,9 @@ __global__ void __launch_bounds__(kJoinThreads) attention_cached_join_kernel(con
             w[j] = bf16_pair(t[2 * j] * by, t[2 * j + 1] * by);
             top = top_of(w[j], top);
         }
-        *reinterpret_cast<uint4*>(a.out + (int64_t)(s.from + qi) * a.out_row + (int64_t)hq * a.out_head + e) =
+        *reinterpret_cast<uint4*>(a.out + (int64_t)(job.from + qi) * a.out_row + (int64_t)hq * a.out_head + e) =
             make_uint4(w[0], w[1], w[2], w[3]);
-        if (e == 0) a.lse[(int64_t)hq * c.tokens + s.from + qi] = total == 0.0f ? -kInf : (base + __builtin_amdgcn_logf(total)) * kLn2;
+        if (e == 0) a.lse[(int64_t)hq * c.tokens + job.from + qi] = total == 0.0f ? -kInf : (base + __builtin_amdgcn_logf(total)) * kLn2;
     }
     if (a.absmax) block_max_to_global(top, a.absmax);
 }
@@ -882,6 +919,7 @@ hipError_t launch_attention_cached(const CachedAttentionArgs& args, void* worksp
     a.workers = p.workers;
     a.whole = p.whole;
     a.few = p.few;
+    a.tiles = (int)p.tiles;
     a.joins = workspace;
     a.tops = reinterpret_cast<float2*>(static_cast<Join*>(workspace) + 2 * p.workers);
     a.partial = reinterpret_cast<float*>(a.tops + slots(p) * 16);

@@ -189,7 +189,8 @@ struct CachedAttentionArgs {
     float* partial;                       // sums of split work, their maxima and totals, and what to join
     float2* tops;
     void* joins;
-    int group, causal, few, workers, whole;   // group: query heads to a key head
+    int group, causal;                    // group: query heads to a key head
+    int few, workers, whole, tiles;       // the launch's plan
     float scale;
 };
 int64_t attention_cached_workspace(int64_t tokens, int group, int heads, int d, int batch, int blocks, int shift, bool bounds);

@@ -149,6 +149,22 @@ def test_bounds_in_no_order(fp8):
         assert ((out[i].to(F64) - p @ v[:n]).abs() <= 2 * U * (p @ v[:n].abs()) + 2 * E * (p @ v[:n].abs())).all()
 
 
+@pytest.mark.parametrize("batch", [2, 400])
+def test_bounds_that_overlap(fp8, batch):
+    """Every second sequence claims all tokens: more rows than the call has; nothing outside is touched."""
+    say("overlapping bounds", batch)
+    pool, table, lengths = setup([1] * batch, [70] * batch, 1, 64, 16, 2)
+    cu = torch.tensor(([0, 300] * batch)[:batch + 1], dtype=torch.int32).cuda()
+    q = torch.randn(300, 4, 64, generator=torch.Generator().manual_seed(1)).to(BF16).cuda()
+    out = torch.full((310, 4, 64), 7.0, dtype=BF16, device="cuda")
+    cache = ref.on_gpu(fp8, pool)
+    fp8.attention_cached(q, cache, table.cuda(), torch.tensor(lengths, dtype=torch.int32).cuda(), cu=cu, out=out[:300])
+    torch.cuda.synchronize()
+    assert (out[300:] == 7).all()
+    for t, n in zip(cache, ("k", "v", "k_scale", "v_scale")):
+        assert torch.equal(t.cpu(), pool[n])
+
+
 @pytest.mark.parametrize("slices", ["fused", "head_major"])
 def test_strides(fp8, slices):
     news, past, hq, hk, d = [3, 1, 40], [50, 200, 7], 8, 2, 64
