@@ -39,7 +39,8 @@ constexpr int kLeastSplit = 4;             // steps of a part of a tile's keys
 // Steps of a tile, on average, from which on its keys are split over the workgroups that would
 // have none; and in two where there are more tiles than CUs, but not three for two.  MI355X,
 // not split / split: 5 queries on 8005 keys (40 and 8 heads) 158 / 24 us, 512 of 512 22 / 31;
-// 1280 on 8192, no mask (32 heads: 320 tiles) 262 / 231, 1000 on 1500 among 31 single ones (320) 65 / 75.
+// 1280 on 8192, no mask (32 heads: 320 tiles) 262 / 231, 1000 on 1500 among 31 single ones (320) 65 / 75
+// (with the workgroups in turn).
 constexpr int kSplitFrom = 16, kHalveFrom = 48;
 constexpr int kWholeKeys = 1024;           // that a row of the table holds at most, up to which a head is not shared out
 constexpr int kJoinThreads = 512;
@@ -765,24 +766,21 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
 
 }  // namespace
 
-// KINDS 1: sequences of few rows alone; 2: of more alone; 3: both, their workgroups in turn, 8
-// by 8 (workgroups are dealt round-robin to the XCDs).
+// KINDS 1: sequences of few rows alone; 2: of more alone; 3: both, the tiles' workgroups first, so
+// that the shares run in what room they leave (1000 queries on 1500 keys among 31 single ones,
+// 40 and 8 heads: 51 us, the tiles alone 49, the shares alone 22; in turn, 8 by 8, 70).
 template <int DT, bool FULL, int KINDS, int R>
 __global__ void __launch_bounds__(kThreads, R == 1 ? 2 : 1) attention_cached_kernel(const CachedAttentionArgs a)
 {
     constexpr int kBytes = KINDS == 1 ? share_lds<DT>() : std::max(share_lds<DT>(), tile_lds<DT>());
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kBytes];
     __shared__ int sums[kWaves][4], found[2];
-    const int i = blockIdx.x, pair = i >> 4;
-    bool share = KINDS == 1;
-    int block = i;
-    if (KINDS == 3) {
-        share = i < 2 * a.workers && !(i & 8);
-        block = i >= 2 * a.workers ? i - a.workers : pair * 8 + (i & 7);
-    }
-    uint32_t top;
+    const int shares = KINDS == 1 ? gridDim.x : KINDS == 2 ? 0 : a.workers, tiles = gridDim.x - shares;
+    const bool share = (int)blockIdx.x >= tiles;
+    const int block = share ? blockIdx.x - tiles : blockIdx.x;
+    uint32_t top = 0;
     if (KINDS != 2 && share) top = attend_share<DT, FULL, R>(a, block, lds, sums, found);
-    else top = attend_rows<DT, FULL>(a, block, lds, sums, found);
+    else if constexpr (KINDS != 1) top = attend_rows<DT, FULL>(a, block, lds, sums, found);
     if (a.absmax) block_max_to_global(top, a.absmax);
 }
 
