@@ -8,8 +8,10 @@
 // are multiplied by a power of two, exact except where they become subnormal and are rounded
 // once more.  The scale stays a byte, e + 127, as the block-scaled formats have it.
 //
-// Bound by memory, 2 bytes read and 1 written per element (or the reverse); for a single new
-// token per sequence by the launch and three dependent reads (bounds, table, token).
+// Bound by memory, 2 bytes read and 1 written per element (or the reverse): 8192 tokens of 8
+// heads of 128 are written in 11.4 us (4.4 TB/s; the kernel begins with dependent reads: bounds
+// and length, then table and tokens, then the page's scale), 32768 read in 34 (5.9).  For a
+// single new token per sequence that chain and the launch are all: 3.4 us in a chain of calls.
 #include <algorithm>
 
 #include "fp8_device.hpp"
@@ -23,9 +25,14 @@ namespace {
 typedef unsigned short ku16x2 __attribute__((ext_vector_type(2)));
 typedef short ki16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 kb16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int ku32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kCacheThreads = 256;
-constexpr int kWaveTokens = 4;             // new tokens per sequence, on average, up to which a wave takes a piece
+// New tokens per sequence, on average, up to which a wave takes a piece; beyond, a workgroup does.
+// 512 sequences, 8 heads of 128, in a chain of calls, a wave / a workgroup: written, 1 token each
+// 5.2 / 13.0 us, 16 13.3 / 23.5, 32 25.0 / 24.5, 64 41.0 / 35.2; read 1 6.3 / 15.4, 32 26.5 / 41.1; of
+// 64 sequences, 64 tokens each, 9.6 / 8.7.
+constexpr int kWriteWave = 16, kReadWave = 32;
 constexpr int kHeld = 4;                   // 16-byte groups of a piece's keys, and of its values, that a thread keeps in registers
 
 // The scale's exponent for a largest magnitude of these fp32 bits: 448 = 1.75 2^8.
@@ -240,7 +247,17 @@ __global__ void __launch_bounds__(kCacheThreads) kv_cache_write_kernel(const Cac
     }
 }
 
-// T threads read one piece of one head's keys or values; tokens with no place read as zeros.
+__device__ __forceinline__ uint2 read_past(const uint2* p)
+{
+    const ku32x2 w = __builtin_nontemporal_load(reinterpret_cast<const ku32x2*>(p));
+    return make_uint2(w[0], w[1]);
+}
+
+// T threads read one piece of one head's keys or values; tokens with no place read as zeros.  The
+// codes are read past the caches, which are left to what is written: MI355X, 32768 tokens of 8
+// heads of 128 (134 MB out) 34 us (5.9 TB/s) and 65 with attention of 8 queries over them after
+// it, with ordinary loads 44 and 67, with ordinary loads and stores past the caches 32 and 74;
+// 16384 tokens, whose codes the last-level cache still has from the call before, 21 (18).
 template <int T>
 __global__ void __launch_bounds__(kCacheThreads) kv_cache_read_kernel(const CacheArgs a)
 {
@@ -265,7 +282,7 @@ __global__ void __launch_bounds__(kCacheThreads) kv_cache_read_kernel(const Cach
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
             w[h] = make_uint2(0, 0);
-            if (i0 + h * T < groups && page >= 0) w[h] = codes[i0 + h * T];
+            if (i0 + h * T < groups && page >= 0) w[h] = read_past(codes + i0 + h * T);
         }
 #pragma unroll
         for (int h = 0; h < 4; ++h)
@@ -278,14 +295,15 @@ __global__ void __launch_bounds__(kCacheThreads) kv_cache_read_kernel(const Cach
 
 }  // namespace
 
-// One unit is a piece of one head's keys and values: a wave where the pieces are short
-// (T = 64), a workgroup otherwise.
+// One unit is a piece of one head's keys and values (written) or of one of them (read, which has
+// more to write: `sides` 2).
 template <typename K>
-static hipError_t launch_pieces(K wave_kernel, K block_kernel, const CacheArgs& args, int sides, hipStream_t stream)
+static hipError_t launch_pieces(K wave_kernel, K block_kernel, int wave_tokens, const CacheArgs& args, int sides,
+                                hipStream_t stream)
 {
     CacheArgs a = args;
     const int64_t n = a.tokens / a.batch;
-    const bool wave = n <= kWaveTokens;
+    const bool wave = n <= wave_tokens;
     const int64_t pieces = a.cu ? piece_bound(a.tokens, a.batch, a.shift) : a.batch * pieces_of(n, a.shift);
     const int64_t units = pieces * a.heads * sides, per = wave ? kCacheThreads / 64 : 1;
     const int64_t most = max_workgroups(kCacheThreads) / 2 * per;
@@ -299,12 +317,12 @@ static hipError_t launch_pieces(K wave_kernel, K block_kernel, const CacheArgs& 
 
 hipError_t launch_kv_cache_write(const CacheArgs& args, hipStream_t stream)
 {
-    return launch_pieces(kv_cache_write_kernel<64>, kv_cache_write_kernel<256>, args, 1, stream);
+    return launch_pieces(kv_cache_write_kernel<64>, kv_cache_write_kernel<256>, kWriteWave, args, 1, stream);
 }
 
 hipError_t launch_kv_cache_read(const CacheArgs& args, hipStream_t stream)
 {
-    return launch_pieces(kv_cache_read_kernel<64>, kv_cache_read_kernel<256>, args, 2, stream);
+    return launch_pieces(kv_cache_read_kernel<64>, kv_cache_read_kernel<256>, kReadWave, args, 2, stream);
 }
 
 }  // namespace fp8k
