@@ -37,11 +37,12 @@ constexpr int kPiece = 4;                  // what a head of a sequence costs be
 constexpr int kMostTiles = (1 << 23) - 1;   // that a thread counts: no call has more in all
 constexpr int kLeastSplit = 4;             // steps of a part of a tile's keys
 // Steps of a tile, on average, from which on its keys are split over the workgroups that would
-// have none; and in two where there are more tiles than CUs, but not three for two.  MI355X,
-// not split / split: 5 queries on 8005 keys (40 and 8 heads) 158 / 24 us, 512 of 512 22 / 31;
-// 1280 on 8192, no mask (32 heads: 320 tiles) 262 / 231, 1000 on 1500 among 31 single ones (320) 65 / 75
-// (with the workgroups in turn).
-constexpr int kSplitFrom = 16, kHalveFrom = 48;
+// have none; in two where there are more tiles than CUs, but not three for two; and of many
+// tiles, those behind the last whole round of the workgroups.  MI355X, not split / split: 5
+// queries on 8005 keys (40 and 8 heads) 158 / 24 us, 512 of 512 22 / 31; 1280 on 8192, no mask (32
+// heads: 320 tiles) 262 / 231, 1000 on 1500 among 31 single ones (320) 65 / 75; 2048 on 8192 (40
+// and 8: 640) 370 / 347, 1100 on 8100 (64 and 8: 552) 383 / 306, 4096 of 4096 (40 and 8: 1280) 211 / 217.
+constexpr int kSplitFrom = 16, kHalveFrom = 48, kTailFrom = 48;
 constexpr int kWholeKeys = 1024;           // that a row of the table holds at most, up to which a head is not shared out
 constexpr int kJoinThreads = 512;
 // Of a buffer load's cache policy: no call reads the keys and values of few rows twice, and
@@ -630,21 +631,33 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
     Sums all = block_sums(mine, mine_steps, sums);
     all.total = min(all.total, a.tiles);
     Join* const joins = reinterpret_cast<Join*>(a.joins) + a.workers;
-    const int units = all.total * c.heads;
-    const int average = units == 0 ? 0 : (int)(all.total_y / all.total);
-    const int parts = 2 * units <= a.workers ? a.workers / units
-                      : 4 * units <= 3 * a.workers && average >= kHalveFrom ? 2 : 1;
-    const int splits = average < kSplitFrom ? 1 : max(min(parts, average / kLeastSplit), 1);
-    // what is to be joined: an entry for each unit if they are split (by its first part, below), else none
-    // (more units than workers are not split)
-    if (threadIdx.x == 0 && block < a.workers && (splits == 1 || block >= units)) joins[block].count = 0;
-    if (units == 0) return 0;
-    const int wide = c.heads * splits;
-    if (block >= (int64_t)all.total * wide) return 0;
-    // blocks are dealt round-robin to the 8 XCDs: each gets whole heads where they divide so
-    const int unit = wide % 8 == 0 ? block % 8 * (wide / 8) + block / 8 % (wide / 8) : block % wide;
-    const int split = unit % splits, head = unit / splits;
-    const int t = all.total - 1 - block / wide;            // a sequence's last (longest) tiles first
+    const int units = all.total * c.heads, average = units == 0 ? 0 : (int)(all.total_y / all.total);
+    // the first `whole` units are not split, the others in `splits`
+    int whole = units, splits = 1;
+    if (units < a.workers && average >= kSplitFrom) {
+        const int parts = 2 * units <= a.workers ? a.workers / units
+                          : 4 * units <= 3 * a.workers && average >= kHalveFrom ? 2 : 1;
+        splits = max(min(parts, average / kLeastSplit), 1);
+    } else if (units > a.workers && average >= kTailFrom) {
+        const int rest = units % a.workers;
+        if (rest > 0 && 2 * rest <= a.workers) splits = min(a.workers / rest, average / kLeastSplit);
+    }
+    if (splits > 1) whole = units < a.workers ? 0 : units / a.workers * a.workers;
+    const int joined = splits > 1 ? units - whole : 0;
+    // what is to be joined: an entry for each unit that is split (by its first part, below), no others
+    if (threadIdx.x == 0 && block < a.workers && block >= joined) joins[block].count = 0;
+    if (block >= whole + (int64_t)(units - whole) * splits) return 0;
+    const bool part = block >= whole;
+    const int parts = part ? splits : 1, index = part ? block - whole : block, wide = c.heads * parts;
+    // a row of tiles after another (of all heads), each head's parts side by side; blocks are dealt
+    // round-robin to the 8 XCDs: each gets whole heads where they divide so
+    int unit = whole * part + index / parts, split = index % parts;
+    if (wide % 8 == 0 && (!part || whole % c.heads == 0)) {
+        const int at = index % 8 * (wide / 8) + index / 8 % (wide / 8);
+        unit = whole * part + index / wide * c.heads + at / parts;
+        split = at % parts;
+    }
+    const int head = unit % c.heads, t = all.total - 1 - unit / c.heads;   // a sequence's last (longest) tiles first
     if (all.before <= t && t < all.before + mine) {
         int left = t - all.before, b = b0;
         for (;; ++b) {
@@ -672,7 +685,7 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
     const int see_last = r_wave >= rows ? 0 : seen(a, held, first, q_last);
     const int end = seen(a, held, first, min((row0 + kOwn - 1) / a.group, queries - 1));
     const int steps = end > 0 ? (end + kKeys - 1) / kKeys : 0;
-    const int s_begin = (int)((int64_t)steps * split / splits), s_end = (int)((int64_t)steps * (split + 1) / splits);
+    const int s_begin = (int)((int64_t)steps * split / parts), s_end = (int)((int64_t)steps * (split + 1) / parts);
 
     Frag q[DT / 16];
     load_own<DT>(q, a.q + (int64_t)(from + qi) * a.q_row + (int64_t)hq * a.q_head, c.d, valid);
@@ -749,13 +762,13 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
     }
 
     l += partner(l);
-    if (splits > 1) {
-        const int slot0 = 2 * a.workers + (t * c.heads + head) * splits * (kOwn / 16);
+    if (parts > 1) {
+        const int slot0 = 2 * a.workers + (unit - whole) * parts * (kOwn / 16);
         const int64_t row = (int64_t)(slot0 + split * (kOwn / 16)) * 16 + wave * 32 + (lane & 31);
         store_partial<DT>(o, a.partial + row * DT, DT, valid);
         if (valid && h == 0) a.tops[row] = make_float2(m == -kInf ? -kInf : mc, l);
         if (split == 0 && threadIdx.x == 0)
-            joins[t * c.heads + head] = Join{from, head, row0, rows, splits, slot0, slot0 + kOwn / 16, kOwn / 16};
+            joins[unit - whole] = Join{from, head, row0, rows, parts, slot0, slot0 + kOwn / 16, kOwn / 16};
         return 0;
     }
     const uint32_t top = store_own<DT>(o, inverse(l), a.out + (int64_t)(from + qi) * a.out_row + (int64_t)hq * a.out_head, c.d, valid);
@@ -879,7 +892,11 @@ Plan plan(int64_t tokens, int group, int heads, int batch, int64_t capacity, boo
 }
 
 // Workgroups' tiles of rows: all, or as many as can share them.
-int64_t row_blocks(const Plan& p, int heads) { return std::max<int64_t>(p.tiles * heads, p.workers * 3 / 2); }
+int64_t row_blocks(const Plan& p, int heads)
+{
+    const int64_t units = p.tiles * heads;
+    return units > p.workers ? units + p.workers : p.workers * 3 / 2;
+}
 
 // Slots of 16 rows that hold parts: two to a share; of tiles, split into 3 / 2 `workers` parts at most.
 int64_t slots(const Plan& p) { return p.whole ? 0 : p.workers * 2 * (p.few / 16) + (p.kinds & 2 ? p.workers * 3 / 2 * (kOwn / 16) : 0); }
@@ -927,7 +944,10 @@ hipError_t launch_attention_cached(const CachedAttentionArgs& args, void* worksp
                                 : d < 64 ? kernel_of<64, false>(p) : kernel_of<128, false>(p),
                                 dim3((unsigned)blocks), dim3(kThreads), stream, a);
     // without bounds the tiles are known, and whether they can be split
-    if (e != hipSuccess || p.whole || (p.kinds == 2 && 4 * p.tiles * heads > 3 * p.workers)) return e;
+    const int64_t units = p.tiles * heads, rest = units % p.workers, steps = (capacity(a.c.blocks, a.c.shift) + kKeys - 1) / kKeys;
+    const bool split = p.kinds != 2 || (units > p.workers ? rest > 0 && 2 * rest <= p.workers && steps >= kTailFrom
+                                                          : 4 * units <= 3 * p.workers && steps >= kSplitFrom);
+    if (e != hipSuccess || p.whole || !split) return e;
     const int shares = p.kinds & 1 ? p.workers * (p.few / 16) : 0, joins = shares + (p.kinds & 2 ? p.workers * 3 / 4 * (kOwn / 16) : 0);
     return launch(d <= 64 ? attention_cached_join_kernel<64> : attention_cached_join_kernel<128>, dim3(joins), dim3(kJoinThreads),
                   stream, a, shares);
