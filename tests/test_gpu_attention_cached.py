@@ -293,6 +293,56 @@ def test_replays(fp8, kind):
             assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8)), (rep, i)
 
 
+def test_pool_of_more_than_4_gib(fp8):
+    """The last pages of a pool of 4.6 GB of keys and as many of values: the bytes that a small pool gives."""
+    heads, d, page, news = 8, 128, 64, [130, 1, 40]
+    say("large pool")
+    g = torch.Generator().manual_seed(4)
+    qkv = torch.randn(sum(news), 3 * heads, d, generator=g).to(BF16).cuda()
+    q, k, v = qkv[:, :heads], qkv[:, heads:2 * heads], qkv[:, 2 * heads:]
+    small, lengths = torch.tensor([[0, 1, 2], [3, 4, 5], [6, 7, 8]], dtype=torch.int32), torch.tensor([130, 1, 40], dtype=torch.int32).cuda()
+    got = []
+    for pages in (9, 70000):
+        cache = fp8.kv_cache(pages, heads, d, page)
+        table = (small + (pages - 9)).cuda()
+        fp8.kv_cache_write(cache, table, lengths, k, v, cu=ref.bounds(news))
+        out = fp8.attention_cached(q, cache, table, lengths, cu=ref.bounds(news))
+        last = fp8.attention_cached(q[:3], cache, table, lengths)
+        got.append([*fp8.kv_cache_read(cache, table, lengths, sum(news), cu=ref.bounds(news)), *out, *last])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+def test_two_streams(fp8):
+    """Calls on two streams at once, each with its own cache and what its stream made just before."""
+    news, past, hq, hk, d, page = [1] * 24, [157 * i % 900 for i in range(24)], 8, 2, 128, 64
+    say("two streams")
+    pools = [setup(news, past, hk, d, page, 40 + i) for i in range(2)]
+    make = [torch.randn(24, hq + 2 * hk, d, generator=torch.Generator().manual_seed(i)).to(BF16).cuda() for i in range(2)]
+    n = torch.tensor(pools[0][2], dtype=torch.int32).cuda()
+    tables = [p[1].cuda() for p in pools]
+
+    def chain(i, cache):
+        outs = []
+        for step in range(6):
+            qkv = make[i] * (1 + step)                     # made on this stream
+            fp8.kv_cache_write(cache, tables[i], n, qkv[:, hq:hq + hk], qkv[:, hq + hk:])
+            outs += fp8.attention_cached(qkv[:, :hq], cache, tables[i], n)
+        return outs
+
+    want = [chain(i, ref.on_gpu(fp8, pools[i][0])) for i in range(2)]
+    caches = [ref.on_gpu(fp8, pools[i][0]) for i in range(2)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [None, None]
+    for i, s in enumerate(streams):
+        with torch.cuda.stream(s):
+            got[i] = chain(i, caches[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        for a, b in zip(got[i], want[i]):
+            assert torch.equal(a, b)
+
+
 def test_refusals(fp8):
     cache = fp8.kv_cache(4, 2, 64, 16)
     table, lengths = torch.zeros(2, 2, dtype=torch.int32).cuda(), torch.zeros(2, dtype=torch.int32).cuda()
