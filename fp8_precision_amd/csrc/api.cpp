@@ -941,6 +941,7 @@ static fp8k::CacheArgs cache_args(const fp8_kv_cache& c, int shift)
     a.cu = c.bounds;
     a.pages = c.pages;
     a.tokens = c.tokens;
+    a.each = (int)(c.tokens / c.batch);
     a.heads = (int)c.heads;
     a.d = (int)c.head_dim;
     a.shift = shift;

@@ -84,14 +84,15 @@ struct Sequence {
 __device__ __forceinline__ Sequence sequence(const CacheArgs& a, int b)
 {
     Sequence s;
+    const int length = a.lengths[b];
     if (a.cu) {
-        s.from = min(max(a.cu[b], 0), (int)a.tokens);
-        s.queries = max(min(max(a.cu[b + 1], 0), (int)a.tokens) - s.from, 0);
+        const int from = a.cu[b], to = a.cu[b + 1];
+        s.from = min(max(from, 0), (int)a.tokens);
+        s.queries = max(min(max(to, 0), (int)a.tokens) - s.from, 0);
     } else {
-        s.queries = (int)(a.tokens / a.batch);
+        s.queries = a.each;
         s.from = b * s.queries;
     }
-    const int length = a.lengths[b];
     s.held = held_tokens(length, a.blocks, a.shift);
     s.first = first_position(length, s.queries, a.blocks, a.shift);
     return s;
@@ -199,6 +200,10 @@ struct Pages {
         first = key >> shift;
 #pragma unroll
         for (int w = 0; w < 3; ++w) page[w] = entry(w);
+    }
+    // the first scales: they need the pages
+    __device__ __forceinline__ void start()
+    {
 #pragma unroll
         for (int w = 0; w < 2; ++w) scales(w);
     }
@@ -287,16 +292,19 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
     uint32_t top_out = 0;
 
     Join* const joins = reinterpret_cast<Join*>(a.joins);
-    int b, head, done, at, end, share = 1;                  // done: of the head's steps, by other shares
+    int b, head, done, at, end, share = 1, steps;           // done: of the head's steps, by other shares
+    Sequence s;
     if (a.whole) {
         b = worker / c.heads;
         head = worker % c.heads;
         done = at = 0;
-        end = share_steps(a, sequence(c, b));
+        s = sequence(c, b);
+        end = steps = __builtin_amdgcn_readfirstlane(share_steps(a, s));
         if (end == 0) return 0;
     } else if (c.batch <= 64) {
         // the share: every lane counts a sequence's steps
-        const int mine = lane < c.batch ? share_steps(a, sequence(c, lane)) * c.heads : 0;
+        const Sequence own = sequence(c, min(lane, c.batch - 1));
+        const int one = lane < c.batch ? share_steps(a, own) : 0, mine = one * c.heads;
         int sum = mine;
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1) {
@@ -310,7 +318,10 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
         at = worker * share;
         end = min(at + share, total);
         b = __ffsll((unsigned long long)__ballot(sum > at)) - 1;
-        const int left = at - __builtin_amdgcn_readlane(sum - mine, b), steps = __builtin_amdgcn_readlane(mine, b) / c.heads;
+        const int left = at - __builtin_amdgcn_readlane(sum - mine, b);
+        steps = __builtin_amdgcn_readlane(one, b);
+        s = Sequence{__builtin_amdgcn_readlane(own.from, b), __builtin_amdgcn_readlane(own.queries, b),
+                     __builtin_amdgcn_readlane(own.held, b), __builtin_amdgcn_readlane(own.first, b)};
         head = __builtin_amdgcn_readfirstlane(left / steps);
         done = __builtin_amdgcn_readfirstlane(left - head * steps);
     } else {
@@ -336,12 +347,11 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
         }
         __syncthreads();
         b = __builtin_amdgcn_readfirstlane(found[0]);
-        const int steps = __builtin_amdgcn_readfirstlane(share_steps(a, sequence(c, b)));
+        s = sequence(c, b);
+        steps = __builtin_amdgcn_readfirstlane(share_steps(a, s));
         head = __builtin_amdgcn_readfirstlane(found[1] / steps);
         done = __builtin_amdgcn_readfirstlane(found[1] - head * steps);
     }
-    Sequence s = sequence(c, b);
-    int steps = __builtin_amdgcn_readfirstlane(share_steps(a, s));
     const float scale2 = a.scale * kLog2e;
     const float far = fminf(8.0f / scale2, 1e38f);         // scores may pass the running maximum by 2^8 before a rescale
 
@@ -369,7 +379,9 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
                         q[r][i].u = *reinterpret_cast<const au32x4*>(a.q + (int64_t)(from + qi) * a.q_row + (int64_t)hq * a.q_head + e);
                 }
             }
-            // waited for here: at its first use, in the loop, the wait would be one for every load in flight
+            Pages pages;
+            if (step0 + wave < last) pages.init(c, b, head, held, (step0 + wave) * kKeys);
+            // waited for here, with the pages: at its first use, in the loop, the wait would be one for every load in flight
             af32x4 o[R][kPer];
             float top[R], sum[R];
 #pragma unroll
@@ -386,10 +398,8 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
             // m (16 of each 64, chunk g), and DT / 16 codes (chunk m) of each of the values 4 g + i.
             uint32_t ck[4][DT / 16], cv[4][4][DT / 64];
             Keys16 x[4];
-            Pages pages;
             const int limit = min(held, last * kKeys);
             auto load_k = [&](int key) __attribute__((always_inline)) {
-                pages.advance(key);
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
                     x[n] = pages.at(key + 16 * n, limit);
@@ -434,7 +444,7 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
             };
 
             if (step0 + wave < last) {
-                pages.init(c, b, head, held, (step0 + wave) * kKeys);
+                pages.start();
                 load_k((step0 + wave) * kKeys);
                 load_v();
             }
@@ -466,6 +476,7 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
                 // (past the last step from buffers of no rows: with loads that some path leaves out, the
                 // compiler would wait for the values together with the next keys)
                 __builtin_amdgcn_sched_barrier(0);
+                pages.advance(j0 + kWaves * kKeys);
                 load_k(j0 + kWaves * kKeys);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
@@ -723,7 +734,6 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
     au32x4 ck[kLoads], cv[kLoads];
     Pages pages;
     auto fetch = [&](int key) __attribute__((always_inline)) {
-        pages.advance(key);
         const Keys16 x = pages.at(key + 16 * wave, held);
         const auto k = rows_of(c.k, x, FULL ? DT : c.d), v = rows_of(c.v, x, FULL ? DT : c.d);
 #pragma unroll
@@ -755,7 +765,10 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
                 to[at / 16] = values(ck[i][2 * j], ck[i][2 * j + 1], k_scale);
                 to[(at + kTile) / 16] = values(cv[i][2 * j], cv[i][2 * j + 1], v_scale);
             }
-        if (st + 1 < s_end) fetch((st + 1) * kKeys);
+        if (st + 1 < s_end) {
+            pages.advance((st + 1) * kKeys);
+            fetch((st + 1) * kKeys);
+        }
         // tile st is written by all; the other stage was last read in step st - 1, by the waves that are here
         __syncthreads();
         const int j0 = st * kKeys;
@@ -763,6 +776,7 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
     };
     if (s_begin < s_end) {
         pages.init(c, b, head, held, s_begin * kKeys);
+        pages.start();
         fetch(s_begin * kKeys);
     }
     for (int st = s_begin; st < s_end; st += 2) {
@@ -852,11 +866,14 @@ __global__ void __launch_bounds__(kJoinThreads) attention_cached_join_kernel(con
     uint32_t top = 0;
     if (lead == 0 && n < rows && e < c.d) {
         float all = -kInf, total = 0.0f;
-        for (int g = n; g < kGroups; g += wide) all = fmaxf(all, s_sum[g][0]);
+        const int upto = min(kGroups, n + job.count * wide);            // groups that had a part
+#pragma unroll 8
+        for (int g = n; g < upto; g += wide) all = fmaxf(all, s_sum[g][0]);
         const float base = all == -kInf ? 0.0f : all;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) t[j] = 0.0f;
-        for (int g = n; g < kGroups; g += wide) {
+#pragma unroll 4
+        for (int g = n; g < upto; g += wide) {
             const float by = __builtin_amdgcn_exp2f(s_sum[g][0] - base);
             total = fmaf(s_sum[g][1], by, total);
 #pragma unroll

@@ -173,6 +173,7 @@ struct CacheArgs {
     const int *table, *lengths, *cu;      // [batch, blocks], [batch], [batch + 1] or null (tokens / batch each)
     int64_t pages, tokens, unit0;
     int heads, d, shift, batch, blocks;
+    int each;                             // new tokens of a sequence, on average: of every one without bounds
     uint16_t *xk, *xv;                    // the call's keys and values (written or read)
     int64_t xk_row, xk_head, xv_row, xv_head;
 };

@@ -57,7 +57,7 @@ __device__ __forceinline__ Piece find_piece(const CacheArgs& a, int64_t item)
     int from, count, length;
     int64_t local;
     if (!a.cu) {
-        count = (int)(a.tokens / a.batch);
+        count = a.each;
         const int64_t per = pieces_of(count, a.shift);
         p.b = (int)min(item / per, (int64_t)a.batch);
         if (p.b == a.batch) return p;
@@ -302,9 +302,8 @@ static hipError_t launch_pieces(K wave_kernel, K block_kernel, int wave_tokens, 
                                 hipStream_t stream)
 {
     CacheArgs a = args;
-    const int64_t n = a.tokens / a.batch;
-    const bool wave = n <= wave_tokens;
-    const int64_t pieces = a.cu ? piece_bound(a.tokens, a.batch, a.shift) : a.batch * pieces_of(n, a.shift);
+    const bool wave = a.each <= wave_tokens;
+    const int64_t pieces = a.cu ? piece_bound(a.tokens, a.batch, a.shift) : a.batch * pieces_of(a.each, a.shift);
     const int64_t units = pieces * a.heads * sides, per = wave ? kCacheThreads / 64 : 1;
     const int64_t most = max_workgroups(kCacheThreads) / 2 * per;
     for (a.unit0 = 0; a.unit0 < units; a.unit0 += most) {
