@@ -96,6 +96,8 @@ def _ptr(t: torch.Tensor | None):
 # around it (a microsecond a call) where this torch has the accessor.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+# The current device's index (half of the time of torch.cuda.current_device).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _run(call: str, fn, tensors, *args) -> None:
@@ -111,7 +113,7 @@ def _run(call: str, fn, tensors, *args) -> None:
             first, index = t, i
         elif i != index or (i < 0 and t.device != first.device):
             raise ValueError(f"{call}: all tensors must be on one device (got {first.device} and {t.device})")
-    if index >= 0 and index == torch.cuda.current_device():
+    if index >= 0 and index == _current_device():
         _check(call, fn(*args, _raw_stream(index)))
         return
     with torch.cuda.device(first.device):
@@ -642,7 +644,7 @@ def _workspace(call, device, *args):
     on ``device`` (the torch allocator's, so stream-ordered like any tensor); None
     where none is needed."""
     size = _i64()
-    if device.index == torch.cuda.current_device():
+    if device.index == _current_device():
         _check(call, getattr(_lib, call)(*args, ctypes.byref(size)))
     else:
         with torch.cuda.device(device):
@@ -741,8 +743,8 @@ def norm_backward(dy, s, weight, mean, rstd, dres=None, want_dbias: bool = False
     return dx, dweight, dbias
 
 
-class _HeadTensor(ctypes.Structure):
-    _fields_ = [("data", _vp), ("token_stride", _i64), ("head_stride", _i64)]
+# struct fp8_head_tensor: data, strides of tokens and heads (packed: half of a ctypes structure's time)
+_pack_heads = struct.Struct("@Pqq").pack
 
 
 class _AttentionShape(ctypes.Structure):
@@ -762,7 +764,7 @@ def _heads(t, name, shape=None):
         raise ValueError(f"{name} must be " + ("[tokens, heads, head_dim]" if shape is None else f"{tuple(shape)}"))
     if step[2] != 1 and size[2] > 1:
         raise ValueError(f"{name} must be contiguous along head_dim")
-    return ctypes.byref(_HeadTensor(t.data_ptr(), step[0], step[1]))
+    return _pack_heads(t.data_ptr(), step[0], step[1])
 
 
 def _new_heads(like):
