@@ -36,10 +36,12 @@ constexpr int kLeastSteps = kWaves;        // of a share
 constexpr int kPiece = 4;                  // what a head of a sequence costs besides its steps, in steps
 constexpr int kMostTiles = (1 << 23) - 1;   // that a thread counts: no call has more in all
 constexpr int kLeastSplit = 4;             // steps of a part of a tile's keys
-// Steps of a tile, on average, from which on its keys are split over the workgroups that would
-// have none; in two where there are more tiles than CUs, but not three for two; and of many
-// tiles, those behind the last whole round of the workgroups.  MI355X, not split / split: 5
-// queries on 8005 keys (40 and 8 heads) 158 / 24 us, 512 of 512 22 / 31; 1280 on 8192, no mask (32
+// Where at most half of the workgroups have a tile: steps of a sequence's longest tile from which on
+// its keys are split (twice as many where it would be in two parts only).  MI355X, not split /
+// split: 5 queries on 8005 keys (40 and 8 heads) 158 / 21 us, 1425 of 1425, 38 on 2035 and 122 on 158
+// (one head) 50 / 21, 1024 causal ones of 8 heads 31 / 26, of 32 (in two, of 8 steps) 32 / 38.  With more
+// tiles, steps on average: in two where there are more tiles than CUs, but not three for two; and
+// of many tiles, those behind the last whole round of the workgroups: 1280 on 8192, no mask (32
 // heads: 320 tiles) 262 / 231, 1000 on 1500 among 31 single ones (320) 65 / 75; 2048 on 8192 (40
 // and 8: 640) 370 / 347, 1100 on 8100 (64 and 8: 552) 383 / 306, 4096 of 4096 (40 and 8: 1280) 211 / 217.
 constexpr int kSplitFrom = 16, kHalveFrom = 48, kTailFrom = 48;
@@ -118,6 +120,12 @@ __device__ __forceinline__ int row_tiles(const CachedAttentionArgs& a, const Seq
     return few(a, s) ? 0 : (s.queries * a.group + kOwn - 1) / kOwn;
 }
 
+// Steps of the keys that query i of a sequence sees.
+__device__ __forceinline__ int tile_steps(const CachedAttentionArgs& a, const Sequence& s, int i)
+{
+    return (max(seen(a, s.held, s.first, i), 0) + kKeys - 1) / kKeys;
+}
+
 // The sums of every thread's (x, y): all threads' in total, the x of those before it in before.
 struct Sums {
     int before, total;
@@ -152,6 +160,31 @@ __device__ __forceinline__ Sums block_sums(int x, int64_t y, int (*lds)[4])
     }
     s.total = __builtin_amdgcn_readfirstlane(s.total);
     return s;
+}
+
+// The sum of the threads' before this one, and of all.
+__device__ __forceinline__ void block_scan(uint64_t x, int (*lds)[4], uint64_t& before, uint64_t& total)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint64_t upto = x;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const uint64_t o = __shfl_up(upto, off, 64);
+        if (lane >= off) upto += o;
+    }
+    if (lane == 63) {
+        lds[wave][0] = (int)upto;
+        lds[wave][1] = (int)(upto >> 32);
+    }
+    __syncthreads();
+    before = upto - x;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        const uint64_t y = (uint64_t)(uint32_t)lds[w][1] << 32 | (uint32_t)lds[w][0];
+        if (w < wave) before += y;
+        total += y;
+    }
 }
 
 // Where 16 keys of one head lie: their bytes in the pool and how many are held.
@@ -646,49 +679,112 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
         const Sequence s = sequence(c, b);
         const int n = min(row_tiles(a, s), kMostTiles - mine);
         mine += n;
-        mine_steps += (int64_t)n * ((max(seen(a, s.held, s.first, s.queries / 2), 0) + kKeys - 1) / kKeys);
+        mine_steps += (int64_t)n * tile_steps(a, s, s.queries / 2);
     }
     Sums all = block_sums(mine, mine_steps, sums);
+    const bool fits = all.total <= a.tiles;
     all.total = min(all.total, a.tiles);
     Join* const joins = reinterpret_cast<Join*>(a.joins) + a.workers;
-    const int units = all.total * c.heads, average = units == 0 ? 0 : (int)(all.total_y / all.total);
-    // the first `whole` units are not split, the others in `splits`
-    int whole = units, splits = 1;
-    if (units < a.workers && average >= kSplitFrom) {
-        const int parts = 2 * units <= a.workers ? a.workers / units
-                          : 4 * units <= 3 * a.workers && average >= kHalveFrom ? 2 : 1;
-        splits = max(min(parts, average / kLeastSplit), 1);
-    } else if (units > a.workers && average >= kTailFrom) {
-        const int rest = units % a.workers;
-        if (rest > 0 && 2 * rest <= a.workers) splits = min(a.workers / rest, average / kLeastSplit);
-    }
-    if (splits > 1) whole = units < a.workers ? 0 : units / a.workers * a.workers;
-    const int joined = splits > 1 ? units - whole : 0;
-    // what is to be joined: an entry for each unit that is split (by its first part, below), no others
-    if (threadIdx.x == 0 && block < a.workers && block >= joined) joins[block].count = 0;
-    if (block >= whole + (int64_t)(units - whole) * splits) return 0;
-    const bool part = block >= whole;
-    const int parts = part ? splits : 1, index = part ? block - whole : block, wide = c.heads * parts;
-    // a row of tiles after another (of all heads), each head's parts side by side; blocks are dealt
-    // round-robin to the 8 XCDs: each gets whole heads where they divide so
-    int unit = whole * part + index / parts, split = index % parts;
-    if (wide % 8 == 0 && (!part || whole % c.heads == 0)) {
-        const int at = index % 8 * (wide / 8) + index / 8 % (wide / 8);
-        unit = whole * part + index / wide * c.heads + at / parts;
-        split = at % parts;
-    }
-    const int head = unit % c.heads, t = all.total - 1 - unit / c.heads;   // a sequence's last (longest) tiles first
-    if (all.before <= t && t < all.before + mine) {
-        int left = t - all.before, b = b0;
-        for (;; ++b) {
-            const int n = row_tiles(a, sequence(c, b));
-            if (left < n) break;
-            left -= n;
+    const int units = all.total * c.heads;
+    int head, split, parts, entry, slot0, slot_step;                       // of the unit's parts: what to join, and their sums' slots
+    if (fits && units > 0 && 2 * units <= a.workers && all.total <= 256) {
+        // few: each sequence's tiles in parts of the same number of steps, the least of three with which there are no
+        // more parts than workgroups, or in two; counted for all of these at once (16 bits: 256 tiles of 255 parts)
+        const int share = (int)min((all.total_y * c.heads + a.workers - 1) / a.workers, (int64_t)1 << 24);
+        auto parts_of = [&](const Sequence& s, int k) __attribute__((always_inline)) {
+            const int steps = tile_steps(a, s, s.queries - 1), size = max(share * (2 + k) / 2, kLeastSplit);
+            const int n = k == 3 ? 2 : min((steps + size - 1) / size, 255);
+            return steps < (n > 2 ? kSplitFrom : 2 * kSplitFrom) ? 1 : n;
+        };
+        uint64_t own = 0;
+        for (int b = b0; b < b1; ++b) {
+            const Sequence s = sequence(c, b);
+            const int n = row_tiles(a, s);
+            if (n > 0)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) own += (uint64_t)(n * parts_of(s, k)) << 16 * k;
         }
-        found[0] = b;
-        found[1] = left;
+        __syncthreads();
+        uint64_t before, total;
+        block_scan(own, sums, before, total);
+        int k = 0, pieces = 0;
+        for (; k < 4; ++k) {
+            pieces = __builtin_amdgcn_readfirstlane((int)(total >> 16 * k & 0xFFFF));
+            if (k == 3 || pieces * c.heads <= a.workers) break;
+        }
+        if (threadIdx.x == 0 && block < a.workers && block >= units) joins[block].count = 0;
+        if (block >= pieces * c.heads) return 0;
+        const int at = pieces - 1 - block / c.heads;                       // a sequence's last (longest) tiles first
+        head = block % c.heads;                                            // (blocks are dealt round-robin to the 8 XCDs)
+        int left = at - (int)(before >> 16 * k & 0xFFFF);
+        if (0 <= left && left < (int)(own >> 16 * k & 0xFFFF)) {
+            int tile = all.before, b = b0, each;
+            for (;; ++b) {
+                const Sequence s = sequence(c, b);
+                const int n = row_tiles(a, s);
+                if (n == 0) continue;
+                each = parts_of(s, k);
+                if (left < n * each) break;
+                left -= n * each;
+                tile += n;
+            }
+            found[0] = b;
+            found[1] = left / each;
+            found[2] = left % each;
+            found[3] = each;
+            found[4] = tile + left / each;
+        }
+        __syncthreads();
+        split = __builtin_amdgcn_readfirstlane(found[2]);
+        parts = __builtin_amdgcn_readfirstlane(found[3]);
+        entry = __builtin_amdgcn_readfirstlane(found[4]) * c.heads + head;
+        slot0 = 2 * a.workers + ((at - split) * c.heads + head) * (kOwn / 16);
+        slot_step = c.heads * (kOwn / 16);
+        if (parts == 1 && threadIdx.x == 0) joins[entry].count = 0;
+    } else {
+        const int average = units == 0 ? 0 : (int)(all.total_y / all.total);
+        // the first `whole` units are not split, the others in `splits`
+        int whole = units, splits = 1;
+        if (units < a.workers) {
+            if (4 * units <= 3 * a.workers && average >= kHalveFrom) splits = 2;
+        } else if (units > a.workers && average >= kTailFrom) {
+            const int rest = units % a.workers;
+            if (rest > 0 && 2 * rest <= a.workers) splits = min(a.workers / rest, average / kLeastSplit);
+        }
+        if (splits > 1) whole = units < a.workers ? 0 : units / a.workers * a.workers;
+        const int joined = splits > 1 ? units - whole : 0;
+        // what is to be joined: an entry for each unit that is split (by its first part, below), no others
+        if (threadIdx.x == 0 && block < a.workers && block >= joined) joins[block].count = 0;
+        if (block >= whole + (int64_t)(units - whole) * splits) return 0;
+        const bool part = block >= whole;
+        parts = part ? splits : 1;
+        const int index = part ? block - whole : block, wide = c.heads * parts;
+        // a row of tiles after another (of all heads), each head's parts side by side; blocks are dealt
+        // round-robin to the 8 XCDs: each gets whole heads where they divide so
+        int unit = whole * part + index / parts;
+        split = index % parts;
+        if (wide % 8 == 0 && (!part || whole % c.heads == 0)) {
+            const int at = index % 8 * (wide / 8) + index / 8 % (wide / 8);
+            unit = whole * part + index / wide * c.heads + at / parts;
+            split = at % parts;
+        }
+        head = unit % c.heads;
+        const int t = all.total - 1 - unit / c.heads;                      // a sequence's last (longest) tiles first
+        if (all.before <= t && t < all.before + mine) {
+            int left = t - all.before, b = b0;
+            for (;; ++b) {
+                const int n = row_tiles(a, sequence(c, b));
+                if (left < n) break;
+                left -= n;
+            }
+            found[0] = b;
+            found[1] = left;
+        }
+        __syncthreads();
+        entry = unit - whole;
+        slot0 = 2 * a.workers + entry * parts * (kOwn / 16);
+        slot_step = kOwn / 16;
     }
-    __syncthreads();
     const int b = __builtin_amdgcn_readfirstlane(found[0]);
     const int row0 = __builtin_amdgcn_readfirstlane(found[1]) * kOwn;
     const Sequence s = sequence(c, b);
@@ -786,12 +882,10 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
 
     l += partner(l);
     if (parts > 1) {
-        const int slot0 = 2 * a.workers + (unit - whole) * parts * (kOwn / 16);
-        const int64_t row = (int64_t)(slot0 + split * (kOwn / 16)) * 16 + wave * 32 + (lane & 31);
+        const int64_t row = (int64_t)(slot0 + split * slot_step) * 16 + wave * 32 + (lane & 31);
         store_partial<DT>(o, a.partial + row * DT, DT, valid);
         if (valid && h == 0) a.tops[row] = make_float2(m == -kInf ? -kInf : mc, l);
-        if (split == 0 && threadIdx.x == 0)
-            joins[unit - whole] = Join{from, head, row0, rows, parts, slot0, slot0 + kOwn / 16, kOwn / 16};
+        if (split == 0 && threadIdx.x == 0) joins[entry] = Join{from, head, row0, rows, parts, slot0, slot0 + slot_step, slot_step};
         return 0;
     }
     const uint32_t top = store_own<DT>(o, inverse(l), a.out + (int64_t)(from + qi) * a.out_row + (int64_t)hq * a.out_head, c.d, valid);
@@ -810,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? 2 : 1) attention_cached_ker
 {
     constexpr int kBytes = KINDS == 1 ? share_lds<DT>() : std::max(share_lds<DT>(), tile_lds<DT>());
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kBytes];
-    __shared__ int sums[kWaves][4], found[2];
+    __shared__ int sums[kWaves][4], found[5];
     const int shares = KINDS == 1 ? gridDim.x : KINDS == 2 ? 0 : a.workers, tiles = gridDim.x - shares;
     const bool share = (int)blockIdx.x >= tiles;
     const int block = share ? blockIdx.x - tiles : blockIdx.x;

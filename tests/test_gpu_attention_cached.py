@@ -105,6 +105,31 @@ def test_against_float64(fp8, case):
     assert torch.equal(again, out) and torch.equal(lse3, lse)
 
 
+UNEVEN = [
+    # few tiles, each sequence's split as its own length has it: 1 to 16 parts a tile, then 2, 3 and none
+    ([122, 38, 1, 425, 2, 2], [36, 1997, 105, 0, 3990, 488], 1, 1, 128, 64, True),
+    ([44, 5, 137, 2, 1], [1923, 2, 270, 13, 11], 64, 8, 104, 64, True),
+    ([900, 533, 53], [6260, 3769, 1086], 36, 18, 64, 128, True),
+    ([17, 129], [69000, 0], 1, 1, 64, 128, False),       # as many parts as there can be
+    ([2000, 3], [-900, 40], 1, 1, 64, 16, True),         # the middle query of the longest sees nothing
+    ([18] * 70, [3] * 69 + [5000], 1, 1, 64, 32, True),  # more sequences than a wave has lanes
+]
+
+
+@pytest.mark.parametrize("case", range(len(UNEVEN)))
+def test_uneven_tiles(fp8, case):
+    news, past, hq, hk, d, page, causal = UNEVEN[case]
+    say("uneven", UNEVEN[case])
+    pool, table, lengths = setup(news, past, hk, d, page, 50 + case)
+    q = torch.randn(sum(news), hq, d, generator=torch.Generator().manual_seed(case)).to(BF16).cuda()
+    n = torch.tensor(lengths, dtype=torch.int32).cuda()
+    call = lambda: fp8.attention_cached(q, ref.on_gpu(fp8, pool), table.cuda(), n, cu=ref.bounds(news), causal=causal)
+    out, lse = call()
+    check(q, out, lse, pool, table, lengths, news, causal, d ** -0.5)
+    again, lse2 = call()
+    assert torch.equal(again, out) and torch.equal(lse2, lse)
+
+
 @pytest.mark.parametrize("scale", [1e-30, 1e-3, 3.0])
 def test_scales(fp8, scale):
     say("scale", scale)
