@@ -36,15 +36,19 @@ constexpr int kLeastSteps = kWaves;        // of a share
 constexpr int kPiece = 4;                  // what a head of a sequence costs besides its steps, in steps
 constexpr int kMostTiles = (1 << 23) - 1;   // that a thread counts: no call has more in all
 constexpr int kLeastSplit = 4;             // steps of a part of a tile's keys
-// Where at most half of the workgroups have a tile: steps of a sequence's longest tile from which on
-// its keys are split (twice as many where it would be in two parts only).  MI355X, not split /
-// split: 5 queries on 8005 keys (40 and 8 heads) 158 / 21 us, 1425 of 1425, 38 on 2035 and 122 on 158
-// (one head) 50 / 21, 1024 causal ones of 8 heads 31 / 26, of 32 (in two, of 8 steps) 32 / 38.  With more
-// tiles, steps on average: in two where there are more tiles than CUs, but not three for two; and
-// of many tiles, those behind the last whole round of the workgroups: 1280 on 8192, no mask (32
+// Where at most half of the workgroups have a tile: steps of the longest from which on all tiles'
+// keys are split into parts of the same size, into two only from twice as many on; the fewer
+// tiles, the sooner: the sums of the parts are less.  MI355X, not split / split: 5 queries on 8005 keys
+// (40 and 8 heads) 158 / 21 us; 1425 of 1425, 38 on 2035 and 122 on 158 (one head) 50 / 20; 1024
+// causal ones of 8 heads 31 / 26, of 32 (in two, of 8 steps) 32 / 38; 64 on 704, 16 heads (16
+// tiles of 11 steps) 21.7 / 18.0; 500 on 700, 32 and 8 (128 of 11) 24 / 32.
+constexpr int kSplitFrom = 16, kSplitFewFrom = 10;
+constexpr bool few_tiles(int64_t tiles, int workers) { return 8 * tiles <= workers; }
+// With more tiles, steps on average: in two where there are more tiles than CUs, but not three for
+// two; and of many, those behind the last whole round of the workgroups: 1280 on 8192, no mask (32
 // heads: 320 tiles) 262 / 231, 1000 on 1500 among 31 single ones (320) 65 / 75; 2048 on 8192 (40
 // and 8: 640) 370 / 347, 1100 on 8100 (64 and 8: 552) 383 / 306, 4096 of 4096 (40 and 8: 1280) 211 / 217.
-constexpr int kSplitFrom = 16, kHalveFrom = 48, kTailFrom = 48;
+constexpr int kHalveFrom = 48, kTailFrom = 48;
 constexpr int kWholeKeys = 1024;           // that a row of the table holds at most, up to which a head is not shared out
 constexpr int kJoinThreads = 512;
 // Of a buffer load's cache policy: no call reads the keys and values of few rows twice, and
@@ -126,13 +130,15 @@ __device__ __forceinline__ int tile_steps(const CachedAttentionArgs& a, const Se
     return (max(seen(a, s.held, s.first, i), 0) + kKeys - 1) / kKeys;
 }
 
-// The sums of every thread's (x, y): all threads' in total, the x of those before it in before.
+// The sums of every thread's (x, y): all threads' in total, the x of those before it in before; and
+// which bits of the waves' `marks` are set in any.
 struct Sums {
     int before, total;
     int64_t total_y;
+    int marks;
 };
 
-__device__ __forceinline__ Sums block_sums(int x, int64_t y, int (*lds)[4])
+__device__ __forceinline__ Sums block_sums(int x, int64_t y, int (*lds)[4], int marks = 0)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int upto = x;
@@ -147,18 +153,21 @@ __device__ __forceinline__ Sums block_sums(int x, int64_t y, int (*lds)[4])
     }
     if (lane == 63) {
         lds[wave][0] = upto;
+        lds[wave][1] = marks;
         lds[wave][2] = (int)y;
         lds[wave][3] = (int)(y >> 32);
     }
     __syncthreads();
-    Sums s{upto - x, 0, 0};
+    Sums s{upto - x, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
         if (w < wave) s.before += lds[w][0];
         s.total += lds[w][0];
+        s.marks |= lds[w][1];
         s.total_y += (int64_t)lds[w][3] << 32 | (uint32_t)lds[w][2];
     }
     s.total = __builtin_amdgcn_readfirstlane(s.total);
+    s.marks = __builtin_amdgcn_readfirstlane(s.marks);
     return s;
 }
 
@@ -673,28 +682,30 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
     // the tile: every thread counts some sequences', in order
     const int per = (c.batch + kThreads - 1) / kThreads, b0 = threadIdx.x * per, b1 = min(b0 + per, c.batch);
     // (held to what the launch has room for, should bounds overlap)
-    int mine = 0;
+    int mine = 0, longest = 0;
     int64_t mine_steps = 0;
     for (int b = b0; b < b1 && mine < kMostTiles; ++b) {
         const Sequence s = sequence(c, b);
         const int n = min(row_tiles(a, s), kMostTiles - mine);
         mine += n;
         mine_steps += (int64_t)n * tile_steps(a, s, s.queries / 2);
+        if (n > 0) longest = max(longest, tile_steps(a, s, s.queries - 1));
     }
-    Sums all = block_sums(mine, mine_steps, sums);
+    const int marks = (__any(longest >= kSplitFewFrom) ? 1 : 0) | (__any(longest >= kSplitFrom) ? 2 : 0) | (__any(longest >= 2 * kSplitFrom) ? 4 : 0);
+    Sums all = block_sums(mine, mine_steps, sums, marks);
     const bool fits = all.total <= a.tiles;
     all.total = min(all.total, a.tiles);
     Join* const joins = reinterpret_cast<Join*>(a.joins) + a.workers;
     const int units = all.total * c.heads;
     int head, split, parts, entry, slot0, slot_step;                       // of the unit's parts: what to join, and their sums' slots
-    if (fits && units > 0 && 2 * units <= a.workers && all.total <= 256) {
-        // few: each sequence's tiles in parts of the same number of steps, the least of three with which there are no
-        // more parts than workgroups, or in two; counted for all of these at once (16 bits: 256 tiles of 255 parts)
+    if (fits && units > 0 && 2 * units <= a.workers && all.total <= 256 && (all.marks & (few_tiles(units, a.workers) ? 1 : 2))) {
+        // few: all tiles in parts of so many steps, the least of three with which there are no more parts than
+        // workgroups, or in two; counted for all of these at once (16 bits: 256 tiles of 255 parts)
         const int share = (int)min((all.total_y * c.heads + a.workers - 1) / a.workers, (int64_t)1 << 24);
         auto parts_of = [&](const Sequence& s, int k) __attribute__((always_inline)) {
             const int steps = tile_steps(a, s, s.queries - 1), size = max(share * (2 + k) / 2, kLeastSplit);
-            const int n = k == 3 ? 2 : min((steps + size - 1) / size, 255);
-            return steps < (n > 2 ? kSplitFrom : 2 * kSplitFrom) ? 1 : n;
+            const int n = k == 3 ? min(steps, 2) : min((steps + size - 1) / size, 255);
+            return n < 2 || (n == 2 && !(all.marks & 4)) ? 1 : n;
         };
         uint64_t own = 0;
         for (int b = b0; b < b1; ++b) {
@@ -704,9 +715,8 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
 #pragma unroll
                 for (int k = 0; k < 4; ++k) own += (uint64_t)(n * parts_of(s, k)) << 16 * k;
         }
-        __syncthreads();
         uint64_t before, total;
-        block_scan(own, sums, before, total);
+        block_scan(own, sums + kWaves, before, total);
         int k = 0, pieces = 0;
         for (; k < 4; ++k) {
             pieces = __builtin_amdgcn_readfirstlane((int)(total >> 16 * k & 0xFFFF));
@@ -904,7 +914,7 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? 2 : 1) attention_cached_ker
 {
     constexpr int kBytes = KINDS == 1 ? share_lds<DT>() : std::max(share_lds<DT>(), tile_lds<DT>());
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kBytes];
-    __shared__ int sums[kWaves][4], found[5];
+    __shared__ int sums[2 * kWaves][4], found[5];
     const int shares = KINDS == 1 ? gridDim.x : KINDS == 2 ? 0 : a.workers, tiles = gridDim.x - shares;
     const bool share = (int)blockIdx.x >= tiles;
     const int block = share ? blockIdx.x - tiles : blockIdx.x;
@@ -1066,7 +1076,7 @@ hipError_t launch_attention_cached(const CachedAttentionArgs& args, void* worksp
     // without bounds the tiles are known, and whether they can be split
     const int64_t units = p.tiles * heads, rest = units % p.workers, steps = (capacity(a.c.blocks, a.c.shift) + kKeys - 1) / kKeys;
     const bool split = p.kinds != 2 || (units > p.workers ? rest > 0 && 2 * rest <= p.workers && steps >= kTailFrom
-                                                          : 4 * units <= 3 * p.workers && steps >= kSplitFrom);
+                                                          : 4 * units <= 3 * p.workers && steps >= (few_tiles(units, p.workers) ? kSplitFewFrom : kSplitFrom));
     if (e != hipSuccess || p.whole || !split) return e;
     const int shares = p.kinds & 1 ? p.workers * (p.few / 16) : 0, joins = shares + (p.kinds & 2 ? p.workers * 3 / 4 * (kOwn / 16) : 0);
     return launch(d <= 64 ? attention_cached_join_kernel<64> : attention_cached_join_kernel<128>, dim3(joins), dim3(kJoinThreads),

@@ -78,11 +78,13 @@ CASES = [
     ([130, 1, 64], [70, 900, 0], 4, 2, 128, 64, True), ([257], [0], 3, 3, 128, 16, True),
     ([65, 40, 1, 0, 300], [0, 90, 600, 5, 1], 5, 1, 80, 32, True), ([200], [313], 8, 8, 64, 128, False),
     ([31, 40, 7], [1, 90, 333], 6, 2, 8, 16, True), ([9], [3], 40, 8, 120, 64, True),
-    ([40], [968], 8, 1, 64, 16, True),                   # few tiles, split from 16 steps on: the last of them part of one
+    ([40], [968], 8, 1, 64, 16, True),                   # few tiles, split: the last step part of one
     ([1100], [3000], 64, 8, 128, 64, True),              # 552 tiles: those behind the first 512 are split
     ([6] * 3, [40, 2000, 300], 5, 1, 128, 64, True),     # 30 rows, in shares where all have as many
     ([4] * 5, [0, 5000, 77, 1, 900], 16, 2, 72, 32, False),
     ([1] * 300, [i % 50 for i in range(300)], 2, 1, 64, 16, True), ([600, 1, 500], [1500, 3000, 0], 10, 2, 128, 64, True),
+    ([40], [568], 8, 1, 64, 16, True),                   # split from 10 steps on, and from 16 with more tiles: the last part of one
+    ([520], [488], 16, 16, 64, 16, True),
 ]
 
 
