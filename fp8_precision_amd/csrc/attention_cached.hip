@@ -49,7 +49,13 @@ constexpr bool few_tiles(int64_t tiles, int workers) { return 8 * tiles <= worke
 // heads: 320 tiles) 262 / 231, 1000 on 1500 among 31 single ones (320) 65 / 75; 2048 on 8192 (40
 // and 8: 640) 370 / 347, 1100 on 8100 (64 and 8: 552) 383 / 306, 4096 of 4096 (40 and 8: 1280) 211 / 217.
 constexpr int kHalveFrom = 48, kTailFrom = 48;
-constexpr int kWholeKeys = 1024;           // that a row of the table holds at most, up to which a head is not shared out
+// Keys that a row of the table holds at most, up to which a head is not shared out; as many times more as the heads of
+// all sequences fill two workgroups a CU, up to four.  MI355X, 32 and 8 heads, a chain of calls, whole / shared out:
+// 100 keys of one sequence 5.6 / 7.8 us, 1000 10.3 / 9.9, of 64 23.4 / 25.5; of rows for 2048, 128 sequences of
+// 2048 82 / 88, of 1 to 2048 59 / 56, one of 2048 and the others 256 22 / 28, but 64 like these 20.6 / 18.5; of
+// rows for 4096, 64 sequences of 32 heads, 4096 315 / 331, 1 to 4096 193 / 192, one 4096 and the others 512
+// 54 / 65, but 32 like these 41 / 40 and 64 of 8 38 / 24.
+constexpr int kWholeKeys = 1024, kMostWhole = 4;
 constexpr int kJoinThreads = 512;
 // Of a buffer load's cache policy: no call reads the keys and values of few rows twice, and
 // before the next call on them a model reads more than the caches hold.  MI355X, without /
@@ -317,8 +323,8 @@ __device__ __forceinline__ uint32_t top_of(uint32_t w, uint32_t top)
 // into the registers of the last one's as soon as its scores are there, the values after
 // its output.  R blocks of 16 rows.
 // Bound by reading: MI355X, one query each of 64 sequences, 40 and 8 heads of 128, 4096 keys 94
-// us (5.7 TB/s), 16384 365 (5.9, a large copy's rate); one on 16384 keys of 32 heads 27 and
-// a join of 5; one of 65536 keys among 31 of 500 34 and 5.  8 waves to a CU and 4 read at the same
+// us (5.7 TB/s), 16384 365 (5.9, a large copy's rate); one on 16384 keys of 32 heads 26 and
+// a join of 4; one of 65536 keys among 31 of 500 34 and 5.  8 waves to a CU and 4 read at the same
 // rate, 12 slower.
 template <int DT, bool FULL, int R>
 __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, int worker, uint8_t* lds, int (*sums)[4], int* found)
@@ -1011,11 +1017,15 @@ Plan plan(int64_t tokens, int group, int heads, int batch, int64_t capacity, boo
 {
     Plan p{};
     const int64_t rows = (bounds ? tokens : tokens / batch) * group;           // of a sequence, at most
+    // (up to 32 in shares where no sequence has more, MI355X, shares / tiles: 4 queries of 64 heads on 4096 keys of 8, 64
+    // sequences 107 / 108 us, 5 of 32 on 65535 among 31 times on 505 50 / 67, 5 of 10 on 1000 keys of 2, 8 times 16.6 / 17.9)
     p.few = rows <= kFew || rows > 2 * kFew ? kFew : 2 * kFew;
     p.kinds = rows <= p.few ? 1 : bounds ? 3 : 2;
     // two per CU (one where the rows take more than half of the registers), whole rounds of the XCDs
-    p.workers = ((p.few == kFew ? 2 : 1) * device_cu_count() + 7) / 8 * 8;
-    p.whole = p.kinds == 1 && capacity <= kWholeKeys && (int64_t)batch * heads <= 1 << 20;
+    const int cus = device_cu_count();
+    p.workers = ((p.few == kFew ? 2 : 1) * cus + 7) / 8 * 8;
+    const int64_t all = (int64_t)batch * heads, times = std::min<int64_t>(std::max<int64_t>(all / (2 * cus), 1), kMostWhole);
+    p.whole = p.kinds == 1 && capacity <= kWholeKeys * times && all <= 1 << 20;
     if (p.kinds & 2) p.tiles = bounds ? tokens * group / kOwn + std::min<int64_t>(batch, tokens * group / (kFew + 1))
                                       : batch * ((tokens / batch * group + kOwn - 1) / kOwn);
     return p;

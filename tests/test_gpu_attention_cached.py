@@ -132,6 +132,19 @@ def test_uneven_tiles(fp8, case):
     assert torch.equal(again, out) and torch.equal(lse2, lse)
 
 
+@pytest.mark.parametrize("batch, heads, longest", [(128, 8, 2048), (127, 8, 2048), (128, 8, 2049), (64, 32, 4096)])
+def test_many_heads(fp8, batch, heads, longest):
+    """Many heads' rows are each read by one workgroup up to some length of the table's rows, else shared out."""
+    say("many heads", batch, heads, longest)
+    past = [longest - 1] + [37 * i % 300 for i in range(batch - 1)]
+    pool, table, lengths = setup([1] * batch, past, heads, 64, 64, 3)
+    q = torch.randn(batch, heads, 64, generator=torch.Generator().manual_seed(1)).to(BF16).cuda()
+    top = torch.zeros(1, device="cuda")
+    out, lse = fp8.attention_cached(q, ref.on_gpu(fp8, pool), table.cuda(), torch.tensor(lengths, dtype=torch.int32).cuda(), absmax=top)
+    check(q, out, lse, pool, table, lengths, [1] * batch, True, 0.125)
+    assert top.item() == out.float().abs().max().item()
+
+
 @pytest.mark.parametrize("scale", [1e-30, 1e-3, 3.0])
 def test_scales(fp8, scale):
     say("scale", scale)
