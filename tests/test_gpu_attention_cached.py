@@ -85,6 +85,8 @@ CASES = [
     ([1] * 300, [i % 50 for i in range(300)], 2, 1, 64, 16, True), ([600, 1, 500], [1500, 3000, 0], 10, 2, 128, 64, True),
     ([40], [568], 8, 1, 64, 16, True),                   # split from 10 steps on, and from 16 with more tiles: the last part of one
     ([520], [488], 16, 16, 64, 16, True),
+    ([6] * 3, [40, 800, 300], 5, 1, 128, 64, True),      # 30 rows, each head by one workgroup where all have as many
+    ([8] * 2, [0, 100], 8, 2, 72, 16, False),
 ]
 
 
