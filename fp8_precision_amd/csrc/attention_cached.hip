@@ -476,7 +476,7 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
                 for (int n = 0; n < 4; ++n) {
                     const int d = FULL ? DT : c.d, e = kPer * m;
                     const auto src = rows_of(c.v, x[n], d);
-    #pragma unroll
+#pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t off = FULL || e < d ? (uint32_t)((4 * g + i) * d + e) : kNowhere;
                         if constexpr (DT == 128) {
@@ -697,7 +697,8 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
         mine_steps += (int64_t)n * tile_steps(a, s, s.queries / 2);
         if (n > 0) longest = max(longest, tile_steps(a, s, s.queries - 1));
     }
-    const int marks = (__any(longest >= kSplitFewFrom) ? 1 : 0) | (__any(longest >= kSplitFrom) ? 2 : 0) | (__any(longest >= 2 * kSplitFrom) ? 4 : 0);
+    const int marks = (__any(longest >= kSplitFewFrom) ? 1 : 0) | (__any(longest >= kSplitFrom) ? 2 : 0)
+                    | (__any(longest >= 2 * kSplitFrom) ? 4 : 0);
     Sums all = block_sums(mine, mine_steps, sums, marks);
     const bool fits = all.total <= a.tiles;
     all.total = min(all.total, a.tiles);
@@ -1085,8 +1086,9 @@ hipError_t launch_attention_cached(const CachedAttentionArgs& args, void* worksp
                                 dim3((unsigned)blocks), dim3(kThreads), stream, a);
     // without bounds the tiles are known, and whether they can be split
     const int64_t units = p.tiles * heads, rest = units % p.workers, steps = (capacity(a.c.blocks, a.c.shift) + kKeys - 1) / kKeys;
+    const int from = few_tiles(units, p.workers) ? kSplitFewFrom : kSplitFrom;
     const bool split = p.kinds != 2 || (units > p.workers ? rest > 0 && 2 * rest <= p.workers && steps >= kTailFrom
-                                                          : 4 * units <= 3 * p.workers && steps >= (few_tiles(units, p.workers) ? kSplitFewFrom : kSplitFrom));
+                                                          : 4 * units <= 3 * p.workers && steps >= from);
     if (e != hipSuccess || p.whole || !split) return e;
     const int shares = p.kinds & 1 ? p.workers * (p.few / 16) : 0, joins = shares + (p.kinds & 2 ? p.workers * 3 / 4 * (kOwn / 16) : 0);
     return launch(d <= 64 ? attention_cached_join_kernel<64> : attention_cached_join_kernel<128>, dim3(joins), dim3(kJoinThreads),
