@@ -18,6 +18,7 @@
 #include <type_traits>
 
 #include "attention_tile.hpp"
+#include "cached_tiles.hpp"
 #include "fp8_device.hpp"
 #include "fp8_internal.hpp"
 #include "kv_cache.hpp"
@@ -35,7 +36,6 @@ constexpr int kOwn = 128;                  // rows of a tile: 32 per wave
 constexpr int kLeastSteps = kWaves;        // of a share
 constexpr int kPiece = 4;                  // what a head of a sequence costs besides its steps, in steps
 constexpr int kMostTiles = (1 << 23) - 1;   // that a thread counts: no call has more in all
-constexpr int kLeastSplit = 4;             // steps of a part of a tile's keys
 // Where at most half of the workgroups have a tile: steps of the longest from which on all tiles'
 // keys are split into parts of the same size, into two only from twice as many on; the fewer
 // tiles, the sooner: the sums of the parts are less.  MI355X, not split / split: 5 queries on 8005 keys
@@ -44,11 +44,6 @@ constexpr int kLeastSplit = 4;             // steps of a part of a tile's keys
 // tiles of 11 steps) 21.7 / 18.0; 500 on 700, 32 and 8 (128 of 11) 24 / 32.
 constexpr int kSplitFrom = 16, kSplitFewFrom = 10;
 constexpr bool few_tiles(int64_t tiles, int workers) { return 8 * tiles <= workers; }
-// With more tiles, steps on average: in two where there are more tiles than CUs, but not three for
-// two; and of many, those behind the last whole round of the workgroups: 1280 on 8192, no mask (32
-// heads: 320 tiles) 262 / 231, 1000 on 1500 among 31 single ones (320) 65 / 75; 2048 on 8192 (40
-// and 8: 640) 370 / 347, 1100 on 8100 (64 and 8: 552) 383 / 306, 4096 of 4096 (40 and 8: 1280) 211 / 217.
-constexpr int kHalveFrom = 48, kTailFrom = 48;
 // Keys that a row of the table holds at most, up to which a head is not shared out; as many times more as the heads of
 // all sequences fill two workgroups a CU, up to four.  MI355X, 32 and 8 heads, a chain of calls, whole / shared out:
 // 100 keys of one sequence 5.6 / 7.8 us, 1000 10.3 / 9.9, of 64 23.4 / 25.5; of rows for 2048, 128 sequences of
@@ -760,33 +755,16 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
         if (parts == 1 && threadIdx.x == 0) joins[entry].count = 0;
     } else {
         const int average = units == 0 ? 0 : (int)(all.total_y / all.total);
-        // the first `whole` units are not split, the others in `splits`
-        int whole = units, splits = 1;
-        if (units < a.workers) {
-            if (4 * units <= 3 * a.workers && average >= kHalveFrom) splits = 2;
-        } else if (units > a.workers && average >= kTailFrom) {
-            const int rest = units % a.workers;
-            if (rest > 0 && 2 * rest <= a.workers) splits = min(a.workers / rest, average / kLeastSplit);
-        }
-        if (splits > 1) whole = units < a.workers ? 0 : units / a.workers * a.workers;
-        const int joined = splits > 1 ? units - whole : 0;
+        const TileSplit how = tile_split(units, a.workers, average);
+        const int joined = how.splits > 1 ? units - how.whole : 0;
         // what is to be joined: an entry for each unit that is split (by its first part, below), no others
         if (threadIdx.x == 0 && block < a.workers && block >= joined) joins[block].count = 0;
-        if (block >= whole + (int64_t)(units - whole) * splits) return 0;
-        const bool part = block >= whole;
-        parts = part ? splits : 1;
-        const int index = part ? block - whole : block, wide = c.heads * parts;
-        // a row of tiles after another (of all heads), each head's parts side by side; blocks are dealt
-        // round-robin to the 8 XCDs: each gets whole heads where they divide so
-        int unit = whole * part + index / parts;
-        split = index % parts;
-        if (wide % 8 == 0 && (!part || whole % c.heads == 0)) {
-            const int at = index % 8 * (wide / 8) + index / 8 % (wide / 8);
-            unit = whole * part + index / wide * c.heads + at / parts;
-            split = at % parts;
-        }
-        head = unit % c.heads;
-        const int t = all.total - 1 - unit / c.heads;                      // a sequence's last (longest) tiles first
+        if (block >= tile_blocks(how, units)) return 0;
+        const TilePart taken = tile_part(block, units, c.heads, how);
+        split = taken.split;
+        parts = taken.parts;
+        head = taken.unit % c.heads;
+        const int t = all.total - 1 - taken.unit / c.heads;                // a sequence's last (longest) tiles first
         if (all.before <= t && t < all.before + mine) {
             int left = t - all.before, b = b0;
             for (;; ++b) {
@@ -798,7 +776,7 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
             found[1] = left;
         }
         __syncthreads();
-        entry = unit - whole;
+        entry = taken.unit - how.whole;
         slot0 = 2 * a.workers + entry * parts * (kOwn / 16);
         slot_step = kOwn / 16;
     }
