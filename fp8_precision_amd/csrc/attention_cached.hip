@@ -33,17 +33,10 @@ constexpr int kThreads = 256;
 constexpr int kWaves = 4;
 constexpr int kFew = 16;                   // rows of a sequence that is read in shares, or twice as many (a.few)
 constexpr int kOwn = 128;                  // rows of a tile: 32 per wave
+static_assert(kOwn == 16 * kTileSlots, "a tile's slots");
 constexpr int kLeastSteps = kWaves;        // of a share
 constexpr int kPiece = 4;                  // what a head of a sequence costs besides its steps, in steps
 constexpr int kMostTiles = (1 << 23) - 1;   // that a thread counts: no call has more in all
-// Where at most half of the workgroups have a tile: steps of the longest from which on all tiles'
-// keys are split into parts of the same size, into two only from twice as many on; the fewer
-// tiles, the sooner: the sums of the parts are less.  MI355X, not split / split: 5 queries on 8005 keys
-// (40 and 8 heads) 158 / 21 us; 1425 of 1425, 38 on 2035 and 122 on 158 (one head) 50 / 20; 1024
-// causal ones of 8 heads 31 / 26, of 32 (in two, of 8 steps) 32 / 38; 64 on 704, 16 heads (16
-// tiles of 11 steps) 21.7 / 18.0; 500 on 700, 32 and 8 (128 of 11) 24 / 32.
-constexpr int kSplitFrom = 16, kSplitFewFrom = 10;
-constexpr bool few_tiles(int64_t tiles, int workers) { return 8 * tiles <= workers; }
 // Keys that a row of the table holds at most, up to which a head is not shared out; as many times more as the heads of
 // all sequences fill two workgroups a CU, up to four.  MI355X, 32 and 8 heads, a chain of calls, whole / shared out:
 // 100 keys of one sequence 5.6 / 7.8 us, 1000 10.3 / 9.9, of 64 23.4 / 25.5; of rows for 2048, 128 sequences of
@@ -692,22 +685,21 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
         mine_steps += (int64_t)n * tile_steps(a, s, s.queries / 2);
         if (n > 0) longest = max(longest, tile_steps(a, s, s.queries - 1));
     }
-    const int marks = (__any(longest >= kSplitFewFrom) ? 1 : 0) | (__any(longest >= kSplitFrom) ? 2 : 0)
-                    | (__any(longest >= 2 * kSplitFrom) ? 4 : 0);
+    int marks = 0;
+#pragma unroll
+    for (int bit = 1; bit <= 4; bit <<= 1) marks |= __any(step_marks(longest) & bit) ? bit : 0;
     Sums all = block_sums(mine, mine_steps, sums, marks);
     const bool fits = all.total <= a.tiles;
     all.total = min(all.total, a.tiles);
     Join* const joins = reinterpret_cast<Join*>(a.joins) + a.workers;
     const int units = all.total * c.heads;
     int head, split, parts, entry, slot0, slot_step;                       // of the unit's parts: what to join, and their sums' slots
-    if (fits && units > 0 && 2 * units <= a.workers && all.total <= 256 && (all.marks & (few_tiles(units, a.workers) ? 1 : 2))) {
+    if (fits && few_split(units, all.total, a.workers, all.marks)) {
         // few: all tiles in parts of so many steps, the least of three with which there are no more parts than
-        // workgroups, or in two; counted for all of these at once (16 bits: 256 tiles of 255 parts)
-        const int share = (int)min((all.total_y * c.heads + a.workers - 1) / a.workers, (int64_t)1 << 24);
+        // workgroups, or in two; counted for all of these at once
+        const int share = few_share(all.total_y * c.heads, a.workers);
         auto parts_of = [&](const Sequence& s, int k) __attribute__((always_inline)) {
-            const int steps = tile_steps(a, s, s.queries - 1), size = max(share * (2 + k) / 2, kLeastSplit);
-            const int n = k == 3 ? min(steps, 2) : min((steps + size - 1) / size, 255);
-            return n < 2 || (n == 2 && !(all.marks & 4)) ? 1 : n;
+            return few_parts(tile_steps(a, s, s.queries - 1), share, k, all.marks);
         };
         uint64_t own = 0;
         for (int b = b0; b < b1; ++b) {
@@ -715,21 +707,17 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
             const int n = row_tiles(a, s);
             if (n > 0)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) own += (uint64_t)(n * parts_of(s, k)) << 16 * k;
+                for (int k = 0; k < kFewChoices; ++k) own += (uint64_t)(n * parts_of(s, k)) << 16 * k;
         }
         uint64_t before, total;
         block_scan(own, sums + kWaves, before, total);
-        int k = 0, pieces = 0;
-        for (; k < 4; ++k) {
-            pieces = __builtin_amdgcn_readfirstlane((int)(total >> 16 * k & 0xFFFF));
-            if (k == 3 || pieces * c.heads <= a.workers) break;
-        }
+        const int k = few_choice(total, c.heads, a.workers), pieces = __builtin_amdgcn_readfirstlane(few_parts_of_all(total, k));
         if (threadIdx.x == 0 && block < a.workers && block >= units) joins[block].count = 0;
         if (block >= pieces * c.heads) return 0;
         const int at = pieces - 1 - block / c.heads;                       // a sequence's last (longest) tiles first
         head = block % c.heads;                                            // (blocks are dealt round-robin to the 8 XCDs)
-        int left = at - (int)(before >> 16 * k & 0xFFFF);
-        if (0 <= left && left < (int)(own >> 16 * k & 0xFFFF)) {
+        int left = at - few_parts_of_all(before, k);
+        if (0 <= left && left < few_parts_of_all(own, k)) {
             int tile = all.before, b = b0, each;
             for (;; ++b) {
                 const Sequence s = sequence(c, b);
@@ -750,8 +738,8 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
         split = __builtin_amdgcn_readfirstlane(found[2]);
         parts = __builtin_amdgcn_readfirstlane(found[3]);
         entry = __builtin_amdgcn_readfirstlane(found[4]) * c.heads + head;
-        slot0 = 2 * a.workers + ((at - split) * c.heads + head) * (kOwn / 16);
-        slot_step = c.heads * (kOwn / 16);
+        slot0 = few_slot0(a.workers, at, split, c.heads, head);
+        slot_step = few_step(c.heads);
         if (parts == 1 && threadIdx.x == 0) joins[entry].count = 0;
     } else {
         const int average = units == 0 ? 0 : (int)(all.total_y / all.total);
@@ -777,8 +765,8 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
         }
         __syncthreads();
         entry = taken.unit - how.whole;
-        slot0 = 2 * a.workers + entry * parts * (kOwn / 16);
-        slot_step = kOwn / 16;
+        slot0 = tile_slot0(a.workers, entry, parts);
+        slot_step = kTileSlots;
     }
     const int b = __builtin_amdgcn_readfirstlane(found[0]);
     const int row0 = __builtin_amdgcn_readfirstlane(found[1]) * kOwn;
@@ -1010,15 +998,8 @@ Plan plan(int64_t tokens, int group, int heads, int batch, int64_t capacity, boo
     return p;
 }
 
-// Workgroups' tiles of rows: all, or as many as can share them.
-int64_t row_blocks(const Plan& p, int heads)
-{
-    const int64_t units = p.tiles * heads;
-    return units > p.workers ? units + p.workers : p.workers * 3 / 2;
-}
-
-// Slots of 16 rows that hold parts: two to a share; of tiles, split into 3 / 2 `workers` parts at most.
-int64_t slots(const Plan& p) { return p.whole ? 0 : p.workers * 2 * (p.few / 16) + (p.kinds & 2 ? p.workers * 3 / 2 * (kOwn / 16) : 0); }
+// Slots of 16 rows that hold parts: two to a share, and the tiles'.
+int64_t slots(const Plan& p) { return p.whole ? 0 : p.workers * 2 * (p.few / 16) + (p.kinds & 2 ? split_parts(p.workers) * kTileSlots : 0); }
 
 template <int DT, bool FULL>
 void (*kernel_of(const Plan& p))(CachedAttentionArgs)
@@ -1058,17 +1039,15 @@ hipError_t launch_attention_cached(const CachedAttentionArgs& args, void* worksp
     a.tops = reinterpret_cast<float2*>(static_cast<Join*>(workspace) + 2 * p.workers);
     a.partial = reinterpret_cast<float*>(a.tops + slots(p) * 16);
     const int64_t blocks = p.whole ? (int64_t)a.c.batch * heads
-                                   : (p.kinds & 1 ? p.workers : 0) + (p.kinds & 2 ? row_blocks(p, heads) : 0);
+                                   : (p.kinds & 1 ? p.workers : 0) + (p.kinds & 2 ? row_blocks(p.tiles * heads, p.workers) : 0);
     const hipError_t e = launch(d == 64 ? kernel_of<64, true>(p) : d == 128 ? kernel_of<128, true>(p)
                                 : d < 64 ? kernel_of<64, false>(p) : kernel_of<128, false>(p),
                                 dim3((unsigned)blocks), dim3(kThreads), stream, a);
     // without bounds the tiles are known, and whether they can be split
-    const int64_t units = p.tiles * heads, rest = units % p.workers, steps = (capacity(a.c.blocks, a.c.shift) + kKeys - 1) / kKeys;
-    const int from = few_tiles(units, p.workers) ? kSplitFewFrom : kSplitFrom;
-    const bool split = p.kinds != 2 || (units > p.workers ? rest > 0 && 2 * rest <= p.workers && steps >= kTailFrom
-                                                          : 4 * units <= 3 * p.workers && steps >= from);
+    const int64_t steps = (capacity(a.c.blocks, a.c.shift) + kKeys - 1) / kKeys;
+    const bool split = p.kinds != 2 || may_split(p.tiles * heads, p.workers, steps);
     if (e != hipSuccess || p.whole || !split) return e;
-    const int shares = p.kinds & 1 ? p.workers * (p.few / 16) : 0, joins = shares + (p.kinds & 2 ? p.workers * 3 / 4 * (kOwn / 16) : 0);
+    const int shares = p.kinds & 1 ? p.workers * (p.few / 16) : 0, joins = shares + (p.kinds & 2 ? joined_units(p.workers) * kTileSlots : 0);
     return launch(d <= 64 ? attention_cached_join_kernel<64> : attention_cached_join_kernel<128>, dim3(joins), dim3(kJoinThreads),
                   stream, a, shares);
 }
