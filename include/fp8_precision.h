@@ -681,8 +681,10 @@ fp8_status fp8_kv_cache_read(const fp8_kv_cache* cache, const fp8_head_tensor* k
  * Attention of the call's tokens over the cache: query i of a sequence's n stands at position
  * lengths - n + i and sees the keys at positions up to its own (causal) or all that are held,
  * as in fp8_attention_forward, whose formulas and head sharing these are.  Probabilities are
- * rounded to bf16 for the product with v (to twice its precision where a sequence has at most
- * 16 rows, n heads_q / heads).  A query that sees nothing has out = 0, lse = -inf.  Keys and
+ * rounded to bf16 for the product with v; to twice its precision in a sequence of at most 16
+ * rows (n heads_q / heads), and in one of at most 32 where the call's tokens (without bounds:
+ * tokens / batch) come to no more than 32 rows.  So out may differ in its rounding with what
+ * else is in the call.  A query that sees nothing has out = 0, lse = -inf.  Keys and
  * values in a block of the row whose entry is no page are zeros, and are seen; past the row
  * there are none.  A NaN in a key or value may reach every query of its sequence.
  *
