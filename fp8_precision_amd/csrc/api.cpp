@@ -1035,8 +1035,8 @@ fp8_status fp8_attention_cached(const fp8_kv_cache* cache, const fp8_head_tensor
     const fp8_kv_cache& c = *cache;
     if ((st = cache_pointers(call, c)) != FP8_OK) return st;
     if (causal != 0 && causal != 1) return fail(FP8_ERR_INVALID, "fp8_attention_cached: causal must be 0 or 1");
-    if (!(scale > 0.0f) || scale > 3.0e38f)
-        return fail(FP8_ERR_INVALID, "fp8_attention_cached: scale must be positive and finite");
+    if (!(scale > 0.0f) || scale > 2.3e38f)                    // times log2 e it is finite
+        return fail(FP8_ERR_INVALID, "fp8_attention_cached: scale must be positive and at most 2.3e38");
     Heads h[2];
     if ((st = take_heads(call, "q", q, c.tokens, heads_q, c.head_dim, false, h[0])) != FP8_OK ||
         (st = take_heads(call, "out", out, c.tokens, heads_q, c.head_dim, true, h[1])) != FP8_OK)

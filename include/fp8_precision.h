@@ -691,6 +691,7 @@ fp8_status fp8_kv_cache_read(const fp8_kv_cache* cache, const fp8_head_tensor* k
  *   q        bf16 [tokens, heads_q, head_dim] with its own strides;  out  as q
  *   heads_q  a multiple of the cache's heads, at most 2^16; tokens heads_q below 2^31, and
  *            batch heads (blocks page_tokens / 64 + 6) below 2^31 - 2^20
+ *   causal   0 or 1;  scale  > 0, at most 2.3e38
  *   lse      fp32 [heads_q, tokens]
  *   absmax   fp32 scalar or NULL: becomes max(*absmax, max |out|), out as stored
  *   workspace, workspace_bytes   device memory, 16-byte aligned, of at least the size that

@@ -120,3 +120,16 @@ def test_attention(lib):
     assert no(lse=K) == INVALID and no(absmax=LSE) == INVALID and no(workspace=V) == INVALID and no(lse=A) == INVALID
     assert no(out=tensor(B, token_stride=256, head_stride=0)) == INVALID       # heads on top of one another
     assert no(q=tensor(A + 8, token_stride=256)) == UNSUPPORTED
+
+
+def test_attention_scale(lib):
+    """The kernel works with scale log2 e, which has to be finite (a score of 0 would be a NaN)."""
+    n = i64()
+    c = cache(blocks=100)
+    assert lib.fp8_attention_cached_workspace(c, 4, ctypes.byref(n)) == OK
+    call = lambda scale, out: lib.fp8_attention_cached(c, tensor(A, token_stride=256), out, 4, 1, scale, LSE, TOP, WS, n.value, None)
+    bad_out = tensor(B + 8, token_stride=256)            # refused after the scale: nothing is launched
+    for scale in (2.4e38, 2.5e38, 3.0e38, 3.4e38):
+        assert call(scale, bad_out) == INVALID and b"scale" in lib.fp8_last_error(), scale
+    for scale in (1e-45, 1.0, 2.3e38):
+        assert call(scale, bad_out) == UNSUPPORTED and b"scale" not in lib.fp8_last_error(), scale

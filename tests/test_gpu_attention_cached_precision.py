@@ -73,3 +73,14 @@ def test_probabilities(fp8, case):
             once = p.to(torch.float32).to(BF16).to(F64) @ z / total
             worse += int(((once.to(torch.float32).to(BF16).to(F64) - o).abs() > bound).sum())
     assert worse > 0
+
+
+@pytest.mark.parametrize("news", [[1, 1], [40, 1]])
+def test_largest_scale(fp8, news):
+    """Queries of zeros: every score is 0 whatever the scale, out the mean of the values."""
+    say("largest scale", news)
+    pool, table, lengths = cached.setup(news, [20, 50], 1, 64, 16, 7)
+    q = torch.zeros(sum(news), 2, 64, dtype=BF16, device="cuda")
+    n = torch.tensor(lengths, dtype=torch.int32).cuda()
+    out, lse = fp8.attention_cached(q, ref.on_gpu(fp8, pool), table.cuda(), n, cu=ref.bounds(news), causal=False, scale=2.3e38)
+    cached.check(q, out, lse, pool, table, lengths, news, False, 1.0)
