@@ -662,7 +662,7 @@ __device__ __forceinline__ uint32_t attend_share(const CachedAttentionArgs& a, i
 // writes them into LDS as bf16.  Where the tiles are few, up to two workgroups per CU share
 // a tile's keys, and the parts are joined.
 // Bound by the matrix units and the softmax: MI355X, heads of 128, 4096 causal queries of 32 heads
-// 158 us (0.87 PFLOP/s; from bf16 keys 150), 4096 on 8192 without a mask 0.95; 35% of the cycles
+// 152 to 158 us (0.87 to 0.90 PFLOP/s; from bf16 keys 150), 4096 on 8192 without a mask 541 (1.02); 35% of the cycles
 // are the matrix units', at 2.06 GHz.  A tile's conversion is 32 of a wave's 219 vector instructions a step.
 // p is rounded to bf16 once: with what that leaves off as a second operand, as in a share, the error is
 // out's own rounding (2.2e-3 -> 1.7e-3 of its norm), but the 4096 take 154 -> 197 us, 2048 on 8192 328 -> 423.
@@ -883,7 +883,7 @@ __device__ __forceinline__ uint32_t attend_rows(const CachedAttentionArgs& a, in
 
 // KINDS 1: sequences of few rows alone; 2: of more alone; 3: both, the tiles' workgroups first, so
 // that the shares run in what room they leave (1000 queries on 1500 keys among 31 single ones,
-// 40 and 8 heads: 51 us, the tiles alone 49, the shares alone 22; in turn, 8 by 8, 70).
+// 40 and 8 heads: 47.5 us, the tiles alone 45.5, the shares alone 18; with both in turn, 8 by 8, 70 where this order took 49).
 template <int DT, bool FULL, int KINDS, int R>
 __global__ void __launch_bounds__(kThreads, R == 1 ? 2 : 1) attention_cached_kernel(const CachedAttentionArgs a)
 {

@@ -70,9 +70,10 @@ constexpr int few_slot0(int workers, int at, int split, int heads, int head)
 constexpr int few_step(int heads) { return heads * kTileSlots; }
 
 // With more tiles than few, steps on average: in two where there are more tiles than CUs, but not three for
-// two; and of many, those behind the last whole round of the workgroups: 1280 on 8192, no mask (32
-// heads: 320 tiles) 262 / 231, 1000 on 1500 among 31 single ones (320) 65 / 75; 2048 on 8192 (40
-// and 8: 640) 370 / 347, 1100 on 8100 (64 and 8: 552) 383 / 306, 4096 of 4096 (40 and 8: 1280) 211 / 217.
+// two; and of many, those behind the last whole round of the workgroups.  MI355X, not split / split, in us:
+// 320 tiles: 1280 queries on 8192 keys without a mask, 32 heads (128 steps) 267 / 226, 1200 on 3700, 32 heads (49)
+// 107.5 / 101, 1000 on 2500 among 31 single ones, 40 and 8 (32) 77.5 / 80, on 1500 (16) 47.5 / 63; 640: 2048 on
+// 8192, 40 and 8 (112) 355 / 328; 552: 1100 on 8100, 64 and 8 (118) 369 / 286; 1280: 4096 of 4096, 40 and 8 (32) 189 / 198.
 constexpr int kHalveFrom = 48, kTailFrom = 48;
 
 struct TileSplit {

@@ -31,7 +31,9 @@ constexpr int kCacheThreads = 256;
 // New tokens per sequence, on average, up to which a wave takes a piece; beyond, a workgroup does.
 // 512 sequences, 8 heads of 128, in a chain of calls, a wave / a workgroup: written, 1 token each
 // 5.2 / 13.0 us, 16 13.3 / 23.5, 32 25.0 / 24.5, 64 41.0 / 35.2; read 1 6.3 / 15.4, 32 26.5 / 41.1; of
-// 64 sequences, 64 tokens each, 9.6 / 8.7.
+// 64 sequences, 64 tokens each, 9.6 / 8.7.  Uneven ones are told by their average too, which a prompt's full pages among
+// few single tokens pay for: written, 500 tokens among 31 single ones 12.7 / 4.8, 2000 among 127 13.2 / 7.7, 8000 among
+// 511 23.9 / 25.3; read 4.6 / 4.0, 5.8 / 9.5, 18.2 / 35.7.
 constexpr int kWriteWave = 16, kReadWave = 32;
 constexpr int kHeld = 4;                   // 16-byte groups of a piece's keys, and of its values, that a thread keeps in registers
 
